@@ -270,17 +270,17 @@ def _run_assign(st):
     grows = n >= 0
     add = n.clamp(min=0)
     held = (o + ps - 1) // ps
-    upto = torch.where(grows, (o + add + ps - 1) // ps, held)
-    want = (upto.clamp(max=P) - held).clamp(min=0)
-    base = torch.cumsum(want, 0) - want
+    upto = (o + add + ps - 1) // ps
+    fits = grows & (upto <= P)
+    want = torch.where(fits, upto - held, 0)
+    need = torch.cumsum(want, 0)
+    base = need - want
     head, tail = cursor[0], cursor[1]
-    avail = tail - head
+    placed = fits & ((want == 0) | (need <= tail - head))  # in the requests' order, all of its pages or none
     col = torch.arange(P, device=o.device)
     j = col[None] - held[:, None]
-    k = base[:, None] + j
-    fresh = torch.where(k < avail, ring[(head + k) % cap], -1)
-    takes = (j >= 0) & (j < want[:, None])
-    table.copy_(torch.where(takes, fresh, table))
+    takes = (j >= 0) & (j < want[:, None]) & placed[:, None]
+    table.copy_(torch.where(takes, ring[(head + base[:, None] + j) % cap], table))
     gone = torch.where(grows, 0, held)
     gbase = torch.cumsum(gone, 0) - gone
     to = torch.where(col[None] < gone[:, None], (tail + gbase[:, None] + col[None]) % cap, cap)
@@ -288,19 +288,16 @@ def _run_assign(st):
     cu = torch.cat([torch.zeros(1, device=o.device, dtype=torch.int64), torch.cumsum(add, 0)])
     t = torch.arange(T, device=o.device)
     req = torch.searchsorted(cu, t, right=True) - 1
-    live = req < o.shape[0]
     rq = req.clamp(max=o.shape[0] - 1)
+    live = (req < o.shape[0]) & placed[rq]
     pos = o[rq] + t - cu[rq]
-    at = pos // ps
-    page = torch.where(at < P, table[rq, at.clamp(max=P - 1)].long(), -1)
-    slot = torch.where(live & (page >= 0), page * ps + pos % ps, -1)
-    total = want.sum()
-    taken = torch.minimum(total, avail)
-    counts = torch.stack([cu[-1], taken, (upto - held).sum() - taken, gone.sum()])
+    page = table[rq, (pos // ps).clamp(max=P - 1)].long()
+    taken = torch.where(placed & (want > 0), need, 0).amax()
+    counts = torch.stack([torch.where(placed, add, 0).sum(), taken, (grows & ~placed).sum(), gone.sum()])
     return {"table": table, "ring": ring, "cursor": torch.stack([head + taken, tail + gone.sum()]),
-            "seq_len": torch.where(grows, o + add, 0).int(), "cu_len": cu.int(), "slot": slot,
-            "req": torch.where(live, req, -1).int(), "pos": torch.where(live, pos, 0).int(),
-            "len": torch.where(live, pos + 1, 0).int(), "counts": counts.int()}
+            "seq_len": torch.where(placed, o + add, torch.where(grows, o, 0)).int(), "cu_len": cu.int(),
+            "slot": torch.where(live, page * ps + pos % ps, -1), "req": torch.where(live, req, -1).int(),
+            "pos": torch.where(live, pos, 0).int(), "len": torch.where(live, pos + 1, 0).int(), "counts": counts.int()}
 
 
 def _split(y, c):
