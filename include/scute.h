@@ -316,6 +316,183 @@ scute_status scute_layer_forward_noalloc(scute_layer* layer, const int32_t* toke
  * count < 0; SCUTE_E_HIP if the launch fails. */
 scute_status scute_silu_gate(const float* g, const float* u, float* h, int64_t count, void* stream);
 
+/* ---- between the adapter layers of a decoder block ----------------------- */
+
+/* The operators that run from the q / k / v layer's output to the output
+ * projection's input and from one block's output to the next layer's x. They
+ * belong to no layer: each names its device, launches on `stream` (null: that
+ * device's default stream) with that device current, allocates nothing, keeps
+ * nothing between calls and may be captured into a graph. Pointers are DEVICE
+ * pointers on that device, borrowed for the call, and outputs overlap no
+ * input unless stated. Every call checks its arguments before it touches the
+ * device. */
+
+/* A paged key-value cache: n_pages pages of page_size positions. Element
+ * (page p, position i of the page, head g, dim j) of K and of V lies
+ * p page_stride + i token_stride + g head_stride + j elements from k and v
+ * (so [page][position][head][dim] and [page][head][position][dim] are both
+ * served). A slot names one position of the cache: page * page_size + i. */
+typedef struct scute_kv_cache {
+  int32_t device;
+  int32_t dtype;      /* SCUTE_BF16 or SCUTE_F32                             */
+  int32_t page_size;  /* positions of a page, 1 .. 65536                     */
+  int32_t n_kv_heads; /* 1 .. 1024                                           */
+  int32_t head_dim;   /* a multiple of 8, 8 .. 256                           */
+  int32_t reserved;   /* 0                                                   */
+  int64_t n_pages;    /* 1 .. 2^31 - 1                                       */
+  int64_t page_stride, token_stride, head_stride; /* multiples of 8, 8 .. 2^40
+                         (token_stride below 2^24)                           */
+  void* k;            /* 16-byte aligned                                     */
+  void* v;
+} scute_kv_cache;
+
+/* Pages and slots of one step's tokens from the requests' lengths, without
+ * the host: request r holds old_len[r] positions of the cache, its pages in
+ * table[r][0 .. ceil(old_len[r] / page_size)); it brings new_len[r] tokens
+ * (0: none), or ends (new_len[r] < 0). The free pages lie in a ring of
+ * ring_size entries from cursor[0] (head) up to cursor[1] (tail), both
+ * counted on without wrapping (entry c is ring[c mod ring_size]).
+ *   - In the requests' order each takes the pages its new positions need from
+ *     the head of the ring into its row of the table. A request gets all of
+ *     them or none: when the free pages do not suffice, or its pages would
+ *     pass the table's width, it is refused and keeps old_len; those after it
+ *     that need pages are refused too when the ring ran out.
+ *   - The pages of a request that ends go back to the tail of the ring and
+ *     may be taken from the next step on; its row of the table is left as
+ *     it is.
+ * Tokens stand in the requests' order. Token t of a request's new tokens gets
+ * its position (len - 1 = pos), its request, and its slot; tokens of a refused
+ * request and every row past the last token up to max_tokens get slot -1,
+ * request -1, pos 0 and len 0, which the operators below skip, so a captured
+ * step may hold fewer tokens than rows.
+ * Lengths, token and page totals may be at most 2^30; negative old lengths
+ * count as 0. Errors: SCUTE_E_INVALID for null or misaligned pointers or an
+ * output that is also an input, SCUTE_E_SHAPE for sizes out of range. */
+typedef struct scute_cache_assign_args {
+  int32_t device;
+  int32_t n_requests;   /* 0 .. 65536                                        */
+  int32_t table_width;  /* pages of a request at most, 1 .. 2^24             */
+  int32_t page_size;    /* 1 .. 65536                                        */
+  int32_t ring_size;    /* 1 .. 2^30                                         */
+  int32_t max_tokens;   /* rows of slot, req, pos and len, 0 .. 2^30         */
+  int64_t table_stride; /* entries between rows of the table, >= table_width */
+  const int32_t* old_len; /* [n_requests]                                    */
+  const int32_t* new_len; /* [n_requests]                                    */
+  int32_t* table;         /* [n_requests][table_stride], updated             */
+  int32_t* ring;          /* [ring_size], updated                            */
+  const int64_t* cursor;  /* [2] head, tail                                  */
+  int64_t* cursor_out;    /* [2] head and tail after the step                */
+  int32_t* seq_len;       /* [n_requests] positions held after the step (0:
+                             the request ended)                              */
+  int32_t* cu_len;        /* [n_requests + 1] first token of each request,
+                             and the tokens in all                           */
+  int64_t* slot;          /* [max_tokens]                                    */
+  int32_t* req;           /* [max_tokens]                                    */
+  int32_t* pos;           /* [max_tokens]                                    */
+  int32_t* len;           /* [max_tokens]                                    */
+  int32_t* counts;        /* [4] tokens placed, pages taken, requests refused,
+                             pages returned                                  */
+} scute_cache_assign_args;
+
+scute_status scute_cache_assign(const scute_cache_assign_args* args, void* stream);
+
+/* Rotary positions: pair i of a head's first rot_dim elements is turned by
+ * the angle pos[axis[i]][t] * freq[i] (one axis for text; time, height and
+ * width for images and video). The angle is reduced in 64 bits, so far
+ * positions lose nothing. Elements past rot_dim stay as they are. */
+typedef struct scute_rotary {
+  int32_t head_dim;
+  int32_t rot_dim;      /* even, 0 .. head_dim                               */
+  int32_t n_axes;       /* 1 .. 8                                            */
+  int32_t interleaved;  /* 0: pair i is (i, i + rot_dim / 2); 1: (2i, 2i + 1) */
+  const double* freq;   /* [rot_dim / 2] radians a position                  */
+  const int32_t* axis;  /* [rot_dim / 2] axis of each pair, 0 .. n_axes - 1
+                           (others count as axis 0); null: all axis 0        */
+} scute_rotary;
+
+/* Rotate q and k of n_tokens tokens, store k and v in the cache. q
+ * [n_tokens][n_heads][head_dim], k and v [n_tokens][n_kv_heads][head_dim] in
+ * src_dtype (SCUTE_F32: a layer's y, each a range of its columns; or
+ * SCUTE_BF16), their rows q_stride, k_stride and v_stride elements apart.
+ * pos [n_axes][n_tokens], its axes pos_stride elements apart. slot
+ * [n_tokens]: a token whose slot is negative or past the cache is not
+ * stored; slots that repeat leave one of their tokens, whichever. q_out
+ * [n_tokens][n_heads][head_dim] in the cache's type, its rows q_out_stride
+ * apart. Products are fp32, rounded once to the cache's type.
+ * Errors: SCUTE_E_INVALID for null or misaligned pointers (each to its
+ * element) or a bad dtype, SCUTE_E_SHAPE for sizes out of range. */
+scute_status scute_rotary_store(const scute_rotary* rotary, const scute_kv_cache* cache, const void* q,
+                                int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, int32_t src_dtype, const int32_t* pos,
+                                int64_t pos_stride, const int64_t* slot, int32_t n_tokens,
+                                int32_t n_heads, void* q_out, int64_t q_out_stride, void* stream);
+
+/* Bytes of workspace that scute_paged_attention may use on `device` for
+ * heads of head_dim elements. */
+scute_status scute_paged_attention_workspace(int32_t device, int32_t head_dim, int64_t* bytes);
+
+/* Attention of new tokens over the paged cache. Row i belongs to request
+ * req[i] (null: request i) and sees that request's positions
+ * max(0, n - window) .. n - 1, n = len[i] (window 0: all of them); position t
+ * lies in page table[request][t / page_size].
+ *   out[i][h] = sum_t softmax_t(scale q[i][h] . K[t][g]) V[t][g]
+ * with g = h / (n_heads / n_kv_heads). A row that sees nothing (len <= 0, or a
+ * request outside 0 .. n_requests - 1) gives zeros; positions past the
+ * table's width, or whose page lies outside the cache, are not seen.
+ * q and out [n_rows][n_heads][head_dim] in the cache's type, rows q_stride and
+ * out_stride elements apart (multiples of 8, 16-byte aligned pointers).
+ * Several rows of one request (its new tokens, each with its own length) are
+ * several rows of one call. Scores, the softmax and the sums are fp32; the
+ * weights are rounded once to bf16 for a bf16 cache. The result depends on
+ * n_rows and the lengths only, never on the order in which work-groups end.
+ * workspace: `workspace_bytes` (at least what scute_paged_attention_workspace
+ * says), 256-byte aligned, zeroed once by the caller before its first use;
+ * every call leaves its counters zero. Calls that may overlap in time need
+ * workspaces of their own.
+ * Errors: SCUTE_E_INVALID for null or misaligned pointers, a workspace that
+ * is too small, or a scale that is not finite; SCUTE_E_SHAPE for sizes out of
+ * range. */
+scute_status scute_paged_attention(const scute_kv_cache* cache, const void* q, int64_t q_stride,
+                                   int32_t n_heads, const int32_t* table, int64_t table_stride,
+                                   int32_t n_requests, int32_t table_width, const int32_t* len,
+                                   const int32_t* req, int32_t n_rows, float scale, int32_t window,
+                                   void* out, int64_t out_stride, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+
+/* The norms around a block's residual:
+ *   h' = h_scale h + y_scale (gate (.) N_post(y))     x = N_pre(h')
+ * N(v) = v / sqrt(mean(v^2) + eps) (.) w + b (SCUTE_NORM_RMS), or the same of
+ * v - mean(v) (SCUTE_NORM_LAYER). */
+typedef enum scute_norm_kind { SCUTE_NORM_RMS = 0, SCUTE_NORM_LAYER = 1 } scute_norm_kind;
+
+typedef struct scute_norm {
+  int32_t device;
+  int32_t kind;         /* scute_norm_kind                                   */
+  int32_t d;            /* 1 .. 32768                                        */
+  int32_t post;         /* 0: y enters as it is; 1: through N_post           */
+  float eps;
+  float h_scale, y_scale;
+  int32_t reserved;     /* 0                                                 */
+  const float* post_w;  /* [d] each, null: ones (weights), zeros (biases)    */
+  const float* post_b;
+  const float* pre_w;
+  const float* pre_b;
+} scute_norm;
+
+/* y [n_rows][d] (a layer's output; null: h' = h_scale h), h [n_rows][d], gate
+ * null, [d] (gate_stride 0) or [n_rows][d] float32; h_out [n_rows][d] in h's
+ * type (null: not written; may be h itself), x [n_rows][d] (null: no N_pre).
+ * Types SCUTE_F32 or SCUTE_BF16, rows *_stride elements apart. x is computed
+ * from h' before it is rounded to h's type. Sums are fp32; the variance is
+ * summed about the mean.
+ * Errors: SCUTE_E_INVALID for null or misaligned pointers (each to its
+ * element), a bad dtype, x that is also h, y or h_out, or neither output;
+ * SCUTE_E_SHAPE for sizes out of range. */
+scute_status scute_residual_norm(const scute_norm* norm, const void* y, int32_t y_dtype, int64_t y_stride,
+                                 const void* h, int32_t h_dtype, int64_t h_stride, const float* gate,
+                                 int64_t gate_stride, void* h_out, int64_t h_out_stride, void* x,
+                                 int32_t x_dtype, int64_t x_stride, int32_t n_rows, void* stream);
+
 /* Algorithmic bytes / FLOPs / launches of one forward with this plan. */
 scute_status scute_cost_model(const scute_layer* layer, const scute_batch* batch,
                               scute_cost* out);

@@ -70,6 +70,41 @@ class KernelTime(C.Structure):
     _fields_ = [("name", C.c_char * 32), ("launches", C.c_int32), ("total_ms", C.c_double)]
 
 
+class KVCacheDesc(C.Structure):
+    """scute_kv_cache"""
+    _fields_ = [("device", C.c_int32), ("dtype", C.c_int32), ("page_size", C.c_int32),
+                ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("reserved", C.c_int32),
+                ("n_pages", C.c_int64), ("page_stride", C.c_int64), ("token_stride", C.c_int64),
+                ("head_stride", C.c_int64), ("k", C.c_void_p), ("v", C.c_void_p)]
+
+
+class CacheAssignArgs(C.Structure):
+    _fields_ = [("device", C.c_int32), ("n_requests", C.c_int32), ("table_width", C.c_int32),
+                ("page_size", C.c_int32), ("ring_size", C.c_int32), ("max_tokens", C.c_int32),
+                ("table_stride", C.c_int64), ("old_len", C.c_void_p), ("new_len", C.c_void_p),
+                ("table", C.c_void_p), ("ring", C.c_void_p), ("cursor", C.c_void_p),
+                ("cursor_out", C.c_void_p), ("seq_len", C.c_void_p), ("cu_len", C.c_void_p),
+                ("slot", C.c_void_p), ("req", C.c_void_p), ("pos", C.c_void_p), ("len", C.c_void_p),
+                ("counts", C.c_void_p)]
+
+
+class RotaryDesc(C.Structure):
+    """scute_rotary"""
+    _fields_ = [("head_dim", C.c_int32), ("rot_dim", C.c_int32), ("n_axes", C.c_int32),
+                ("interleaved", C.c_int32), ("freq", C.c_void_p), ("axis", C.c_void_p)]
+
+
+class NormDesc(C.Structure):
+    """scute_norm"""
+    _fields_ = [("device", C.c_int32), ("kind", C.c_int32), ("d", C.c_int32), ("post", C.c_int32),
+                ("eps", C.c_float), ("h_scale", C.c_float), ("y_scale", C.c_float),
+                ("reserved", C.c_int32), ("post_w", C.c_void_p), ("post_b", C.c_void_p),
+                ("pre_w", C.c_void_p), ("pre_b", C.c_void_p)]
+
+
+NORM_RMS, NORM_LAYER = 0, 1
+
+
 # exported symbols and their signatures (must match include/scute.h)
 _P = C.c_void_p
 SIGNATURES = {
@@ -97,6 +132,17 @@ SIGNATURES = {
                                        C.POINTER(C.c_int32)]),
     "scute_launch_empty": (C.c_int32, [C.c_int32, _P]),
     "scute_silu_gate": (C.c_int32, [_P, _P, _P, C.c_int64, _P]),
+    "scute_cache_assign": (C.c_int32, [C.POINTER(CacheAssignArgs), _P]),
+    "scute_rotary_store": (C.c_int32, [C.POINTER(RotaryDesc), C.POINTER(KVCacheDesc), _P, C.c_int64,
+                                       _P, C.c_int64, _P, C.c_int64, C.c_int32, _P, C.c_int64, _P,
+                                       C.c_int32, C.c_int32, _P, C.c_int64, _P]),
+    "scute_paged_attention_workspace": (C.c_int32, [C.c_int32, C.c_int32, C.POINTER(C.c_int64)]),
+    "scute_paged_attention": (C.c_int32, [C.POINTER(KVCacheDesc), _P, C.c_int64, C.c_int32, _P,
+                                          C.c_int64, C.c_int32, C.c_int32, _P, _P, C.c_int32,
+                                          C.c_float, C.c_int32, _P, C.c_int64, _P, C.c_int64, _P]),
+    "scute_residual_norm": (C.c_int32, [C.POINTER(NormDesc), _P, C.c_int32, C.c_int64, _P, C.c_int32,
+                                        C.c_int64, _P, C.c_int64, _P, C.c_int64, _P, C.c_int32,
+                                        C.c_int64, C.c_int32, _P]),
     "scute_last_error": (C.c_char_p, []),
     "scute_version": (C.c_char_p, []),
 }
@@ -222,6 +268,40 @@ def scute_silu_gate(g, u, h, count=None, stream=None) -> None:
     """h = silu(g) (.) u on device float32 tensors."""
     n = int(h.numel() if count is None else count)
     _check(lib.scute_silu_gate(_ptr(g), _ptr(u), _ptr(h), n, _stream_ptr(stream)))
+
+
+def scute_cache_assign(args: CacheAssignArgs, stream=None) -> None:
+    _check(lib.scute_cache_assign(C.byref(args), _stream_ptr(stream)))
+
+
+def scute_rotary_store(rotary: RotaryDesc, cache: KVCacheDesc, q, q_stride, k, k_stride, v, v_stride,
+                       src_dtype, pos, pos_stride, slot, n_tokens, n_heads, q_out, q_out_stride,
+                       stream=None) -> None:
+    _check(lib.scute_rotary_store(rotary, cache, _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
+                                  src_dtype, _ptr(pos), pos_stride, _ptr(slot), n_tokens, n_heads,
+                                  _ptr(q_out), q_out_stride, _stream_ptr(stream)))
+
+
+def scute_paged_attention_workspace(device: int, head_dim: int) -> int:
+    out = C.c_int64(0)
+    _check(lib.scute_paged_attention_workspace(device, head_dim, C.byref(out)))
+    return out.value
+
+
+def scute_paged_attention(cache: KVCacheDesc, q, q_stride, n_heads, table, table_stride, n_requests,
+                          table_width, len, req, n_rows, scale, window, out, out_stride, workspace,
+                          workspace_bytes, stream=None) -> None:
+    _check(lib.scute_paged_attention(cache, _ptr(q), q_stride, n_heads, _ptr(table), table_stride,
+                                     n_requests, table_width, _ptr(len), _ptr(req), n_rows, scale, window,
+                                     _ptr(out), out_stride, _ptr(workspace), workspace_bytes,
+                                     _stream_ptr(stream)))
+
+
+def scute_residual_norm(norm: NormDesc, y, y_dtype, y_stride, h, h_dtype, h_stride, gate, gate_stride,
+                        h_out, h_out_stride, x, x_dtype, x_stride, n_rows, stream=None) -> None:
+    _check(lib.scute_residual_norm(norm, _ptr(y), y_dtype, y_stride, _ptr(h), h_dtype, h_stride,
+                                   _ptr(gate), gate_stride, _ptr(h_out), h_out_stride, _ptr(x), x_dtype,
+                                   x_stride, n_rows, _stream_ptr(stream)))
 
 
 def scute_launch_empty(count: int, stream=None) -> None:
