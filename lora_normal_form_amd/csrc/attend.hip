@@ -2,6 +2,9 @@
 
 #include <math.h>
 
+#include <algorithm>
+#include <atomic>
+
 #include "block.h"
 #include "kernels.h"
 
@@ -11,70 +14,527 @@ struct AttArgs {
   const void *q, *k, *v;
   void* out;
   const int32_t *table, *len, *req;
+  float* part;     // partial results, two pieces a work-group
+  int32_t* count;  // arrivals at a split piece's first work-group
   int64_t q_stride, out_stride, page_stride, token_stride, head_stride, table_stride, n_pages;
-  int32_t n_heads, group, head_dim, page_size, table_width, n_requests, window;
-  float scale_log2;  // scale * log2(e): the softmax runs on powers of two
+  uint32_t part_bytes, ps_mul;  // t / page_size = t ps_mul >> 31 + ps_shift
+  int32_t n_rows, n_kv, q_tiles, group, head_dim, page_size, ps_shift, table_width, n_requests, window;
+  float scale_log2;  // scale log2(e): the softmax runs on powers of two
 };
 
-template <typename T>
-__device__ __forceinline__ float att_ld(const T* p) {
-  if constexpr (sizeof(T) == 4)
-    return ldg(p);
-  else
-    return bf2f(ldg(p));
+// How the work is cut. A unit is one tile of positions (32 of bf16, 16 of
+// fp32) of one row, key head and tile of 16 query heads; units are numbered
+// row by row, key head by key head. W work-groups take equal contiguous
+// ranges of them, so that ragged lengths cost no balance and a few long rows
+// use the whole chip; a range's part of one (row, head) is a piece, its four
+// waves on every fourth tile. A piece that holds all of its (row, head) writes
+// the output; the others write partial results, and the last of them to arrive
+// adds them in the pieces' order. Every work-group finds its range from the
+// lengths by itself (4 bytes a row), so nothing is planned on the host and a
+// captured launch follows the lengths.
+struct AttRow {
+  int n, lo, first, tiles, req;  // positions seen: lo .. n - 1, in `tiles` tiles from tile `first`
+};
+
+template <int TILE>
+__device__ __forceinline__ AttRow att_row(const AttArgs& A, int row) {
+  AttRow r;
+  r.req = A.req ? ldg(A.req + row) : row;
+  const int64_t reach = min((int64_t)A.table_width * A.page_size, (int64_t)1 << 30);
+  const int n = r.req >= 0 && r.req < A.n_requests ? max(0, ldg(A.len + row)) : 0;
+  r.n = n < reach ? n : (int)reach;
+  r.lo = A.window > 0 && r.n > A.window ? r.n - A.window : 0;
+  r.first = r.lo / TILE;
+  r.tiles = max(1, (r.n + TILE - 1) / TILE - r.first);  // (an empty row writes its zeros)
+  return r;
 }
 
-// One work-group per (row, query head), its four waves on every fourth
-// position, a lane on dims lane, lane + 64, ...; running maximum and sum per
-// wave, the four joined in LDS.
-template <typename T>
-__global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
-  __shared__ float sm[4], sl[4], so[4][256];
-  const int row = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int rq = A.req ? A.req[row] : row, D = A.head_dim;
-  const int64_t reach = (int64_t)A.table_width * A.page_size;
-  int n = rq >= 0 && rq < A.n_requests ? A.len[row] : 0;
-  n = (int)(n < reach ? n : reach);
-  const int lo = A.window > 0 && n > A.window ? n - A.window : 0;
-  const T* q = (const T*)A.q + row * A.q_stride + (int64_t)h * D;
-  const int64_t head = (h / A.group) * A.head_stride;
-  float qv[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-  for (int i = 0; i < 4; ++i) qv[i] = lane + 64 * i < D ? att_ld(q + lane + 64 * i) : 0.f;
-  for (int t = lo + w; t < n; t += 4) {
-    const int at = t / A.page_size;
-    const int page = A.table[rq * A.table_stride + at];
-    if (page < 0 || page >= A.n_pages) continue;
-    const int64_t off = page * A.page_stride + (t - at * A.page_size) * A.token_stride + head;
-    float s = 0.f;
-    for (int i = 0; i < 4; ++i)
-      if (lane + 64 * i < D) s += qv[i] * att_ld((const T*)A.k + off + lane + 64 * i);
-    s = wave_sum(s) * A.scale_log2;
-    const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
-    const float f = exp2f(m - ref), p = exp2f(s - ref);
-    m = mn;
-    l = l * f + p;
-    for (int i = 0; i < 4; ++i)
-      if (lane + 64 * i < D) o[i] = o[i] * f + p * att_ld((const T*)A.v + off + lane + 64 * i);
+__device__ __forceinline__ int64_t uni64(int64_t v) {
+  return (int64_t)(((uint64_t)(uint32_t)uni((int)(v >> 32)) << 32) | (uint32_t)uni((int)(uint32_t)v));
+}
+__device__ __forceinline__ float max_over_quarters(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16, 64));
+  return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+__device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_frag(a), as_frag(b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma4(uint32_t a, uint32_t b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a), __uint_as_float(b), c, 0, 0, 0);
+}
+__device__ __forceinline__ uint4 ldg_b16(const char* p, uint32_t off) {
+  const u32x4 v = *(const GLOBAL u32x4*)(p + off);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+__device__ __forceinline__ uint32_t dword(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// Geometry of one instantiation: heads of up to DP elements of type T.
+template <typename T, int DP>
+struct AttGeo {
+  static constexpr int ES = sizeof(T);
+  static constexpr int SUB = ES == 2 ? 2 : 1;   // blocks of 16 positions in a tile
+  static constexpr int TILE = 16 * SUB;
+  static constexpr int NC = DP * ES / 64;       // 64-byte chunks of a K row
+  static constexpr int VB = ES == 2 && DP == 64 ? 8 : 16;  // bytes of a V row a lane loads at once
+  static constexpr int VD = VB / ES;            // elements of them
+  static constexpr int NG = DP / (16 * VD);     // loads that cover a V row over 16 lanes
+};
+
+// One tile's products. Scores: S^T = K Q^T, K rows as the A operand (lane
+// (m, g): row m of 16, the 16 bytes g of every 64-byte chunk; Q is laid out
+// alike, so the order of the contraction does not matter), so a lane holds
+// query m and positions 4 g + 0..3 of each 16. Output: O^T = V^T P^T with the
+// contraction index permuted so that a lane's own scores are its P operand
+// (nothing crosses lanes); V is loaded in rows, VD elements of rows
+// 4 g + 0..3 per lane, and the V^T operand of element i is a permutation of
+// bytes inside the lane. Output rows (dims) of lane (m, g), element i of load
+// ng, register r: 16 VD ng + VD (4 g + r) + i; its column is query m again,
+// so the softmax factors need no exchange either.
+template <typename T, int DP, bool EXACT>
+struct AttTile {
+  using G = AttGeo<T, DP>;
+  uint4 k[G::SUB][G::NC];
+  uint32_t v[G::SUB][4][G::NG][G::VB / 4];
+
+  __device__ __forceinline__ void load_v(const char* p, uint32_t off, int s, int j, int ng) {
+    if constexpr (G::VB == 16) {
+      const uint4 x = ldg_b16(p, off);
+      v[s][j][ng][0] = x.x, v[s][j][ng][1] = x.y, v[s][j][ng][2] = x.z, v[s][j][ng][3] = x.w;
+    } else {
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      const u32x2 x = *(const GLOBAL u32x2*)(p + off);
+      v[s][j][ng][0] = x.x, v[s][j][ng][1] = x.y;
+    }
   }
-  if (lane == 0) sm[w] = m, sl[w] = l;
-  for (int i = 0; i < 4; ++i) so[w][lane + 64 * i] = o[i];
+  __device__ __forceinline__ void scores(const uint4 (&q)[G::NC], f32x4 (&sc)[G::SUB], int gq, int row_bytes) {
+#pragma unroll
+    for (int s = 0; s < G::SUB; ++s) {
+      sc[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < G::NC; ++c) {
+        uint4 kk = k[s][c];
+        if constexpr (!EXACT)  // past the head's end: other elements, which may hold anything
+          if (64 * c + 16 * gq >= row_bytes) kk = make_uint4(0, 0, 0, 0);
+        if constexpr (G::ES == 2) {
+          sc[s] = mfma16(kk, q[c], sc[s]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[s] = mfma4(dword(kk, e), dword(q[c], e), sc[s]);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void clear_v(int s, int j) {
+#pragma unroll
+    for (int ng = 0; ng < G::NG; ++ng)
+#pragma unroll
+      for (int e = 0; e < G::VB / 4; ++e) v[s][j][ng][e] = 0;
+  }
+  __device__ __forceinline__ void weigh(const f32x4 (&p)[G::SUB], f32x4 (&acc)[G::NG][G::VD]) {
+    if constexpr (G::ES == 2) {
+      uint4 b;  // the weights, rounded once to bf16 (relative 2^-8, as the values they multiply)
+      b.x = pack_bf2(__float_as_uint(p[0][0]), __float_as_uint(p[0][1]));
+      b.y = pack_bf2(__float_as_uint(p[0][2]), __float_as_uint(p[0][3]));
+      b.z = pack_bf2(__float_as_uint(p[1][0]), __float_as_uint(p[1][1]));
+      b.w = pack_bf2(__float_as_uint(p[1][2]), __float_as_uint(p[1][3]));
+#pragma unroll
+      for (int ng = 0; ng < G::NG; ++ng)
+#pragma unroll
+        for (int i = 0; i < G::VD; ++i) {
+          const uint32_t sel = i & 1 ? 0x07060302u : 0x05040100u;
+          uint4 a;
+          a.x = __builtin_amdgcn_perm(v[0][1][ng][i / 2], v[0][0][ng][i / 2], sel);
+          a.y = __builtin_amdgcn_perm(v[0][3][ng][i / 2], v[0][2][ng][i / 2], sel);
+          a.z = __builtin_amdgcn_perm(v[1][1][ng][i / 2], v[1][0][ng][i / 2], sel);
+          a.w = __builtin_amdgcn_perm(v[1][3][ng][i / 2], v[1][2][ng][i / 2], sel);
+          acc[ng][i] = mfma16(a, b, acc[ng][i]);
+        }
+    } else {
+#pragma unroll
+      for (int ng = 0; ng < G::NG; ++ng)
+#pragma unroll
+        for (int i = 0; i < G::VD; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[ng][i] = mfma4(v[0][j][ng][i], __float_as_uint(p[0][j]), acc[ng][i]);
+    }
+  }
+};
+
+// Work-groups a compute unit, by the registers a wave needs (K and V of a
+// tile, the output, Q).
+template <typename T, int DP>
+constexpr int att_groups() {
+  return sizeof(T) == 2 ? (DP <= 128 ? 3 : 2) : (DP <= 64 ? 3 : DP <= 128 ? 2 : 1);
+}
+constexpr int ATT_MIN_UNITS = 4;  // tiles a work-group takes at least: one a wave
+
+// PAGE16: pages hold multiples of 16 positions, so the 16 of a block lie in
+// one page and their place is one scalar; else every position is looked up.
+// EXACT: the head dimension is DP.
+template <typename T, int DP, bool PAGE16, bool EXACT>
+__global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(AttArgs A) {
+  using G = AttGeo<T, DP>;
+  constexpr int TILE = G::TILE, SUB = G::SUB, OS = DP + 4;
+  __shared__ float s_ml[4][16][2];
+  __shared__ __align__(16) float s_o[2][16][OS];
+  __shared__ int64_t s_wsum[4], s_before;
+  __shared__ int s_row, s_last;
+  const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6), m16 = lane & 15, gq = lane >> 4;
+  const int H = A.n_kv * A.q_tiles, D = EXACT ? DP : A.head_dim, row_bytes = D * G::ES;
+
+  // this work-group's range of units
+  const int per = (A.n_rows + 255) / 256, r0 = min(A.n_rows, tid * per), r1 = min(A.n_rows, r0 + per);
+  int64_t own = 0;
+  for (int r = r0; r < r1; ++r) own += att_row<TILE>(A, r).tiles;
+  int64_t inc = own;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t x = __shfl_up(inc, o, 64);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 63) s_wsum[w] = inc;
   __syncthreads();
-  const float mx = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3])), ref = mx == -INFINITY ? 0.f : mx;
-  float sum = 0.f, acc = 0.f;
-  for (int i = 0; i < 4; ++i) {
-    const float f = exp2f(sm[i] - ref);
-    sum += sl[i] * f;
-    acc += so[i][threadIdx.x] * f;
+  int64_t pre = inc - own, U = 0;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    if (x < w) pre += s_wsum[x];
+    U += s_wsum[x];
   }
-  if ((int)threadIdx.x < D) {
-    const float r[1] = {sum == 0.f ? 0.f : acc / sum};
-    T* out = (T*)A.out + row * A.out_stride + (int64_t)h * D + threadIdx.x;
-    if constexpr (sizeof(T) == 4)
-      *out = r[0];
-    else
-      *out = (T)pack_bf2(__float_as_uint(r[0]), 0);
+  U = uni64(U * H);
+  const int64_t want = (U + ATT_MIN_UNITS - 1) / ATT_MIN_UNITS;
+  const int64_t W = want < (int64_t)gridDim.x ? want : (int64_t)gridDim.x, wg = blockIdx.x;
+  if (wg >= W) return;
+  const int64_t u_begin = wg * U / W, u_end = (wg + 1) * U / W;
+  if (pre * H <= u_begin && u_begin < (pre + own) * H) {
+    int r = r0;
+    for (int64_t t = att_row<TILE>(A, r).tiles; (pre + t) * H <= u_begin; t = att_row<TILE>(A, r).tiles) {
+      pre += t;
+      ++r;
+    }
+    s_row = r;
+    s_before = pre;
+  }
+  __syncthreads();
+  int row = uni(s_row);
+  int64_t base = uni64(s_before) * H;  // first unit of the row
+  const rsrc_t part = make_rsrc(A.part, A.part_bytes);
+  constexpr uint32_t SLOT = 16 * (DP + 4) * 4;  // bytes of a partial result: 16 x (DP values, m, l, unused)
+
+  for (int64_t u = u_begin; u < u_end;) {
+    AttRow R = att_row<TILE>(A, row);
+    R.n = uni(R.n), R.lo = uni(R.lo), R.first = uni(R.first), R.tiles = uni(R.tiles), R.req = uni(R.req);
+    const int hh = uni((int)((u - base) / R.tiles)), t0 = uni((int)((u - base) - (int64_t)hh * R.tiles));
+    const int cnt = (int)min((int64_t)(R.tiles - t0), u_end - u);
+    const int kvh = hh / A.q_tiles, h0 = kvh * A.group + (hh - kvh * A.q_tiles) * 16;
+    const int nq = min(16, (kvh + 1) * A.group - h0);
+
+    // ---- the wave's tiles t0 + w, t0 + w + 4, ... ----
+    float mx = -INFINITY, l = 0.f;
+    f32x4 acc[G::NG][G::VD];
+#pragma unroll
+    for (int ng = 0; ng < G::NG; ++ng)
+#pragma unroll
+      for (int i = 0; i < G::VD; ++i) acc[ng][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (R.n > 0 && w < cnt) {
+      uint4 q[G::NC];
+      {
+        const char* qp = (const char*)A.q + ((int64_t)row * A.q_stride + (int64_t)(h0 + min(m16, nq - 1)) * D) * G::ES;
+#pragma unroll
+        for (int c = 0; c < G::NC; ++c) {
+          const bool in = m16 < nq && (EXACT || 64 * c + 16 * gq < row_bytes);
+          q[c] = ldg_b16(qp, EXACT ? 64 * c + 16 * gq : min(64 * c + 16 * gq, row_bytes - 16));
+          if (!in) q[c] = make_uint4(0, 0, 0, 0);
+        }
+      }
+      const char *kb = (const char*)A.k, *vb = (const char*)A.v;
+      const int32_t* tab = A.table + (int64_t)R.req * A.table_stride;
+      const int64_t head = (int64_t)kvh * A.head_stride * G::ES;
+      const uint32_t tok = (uint32_t)A.token_stride * G::ES;
+      const int trips = (cnt - w + 3) >> 2, tb = R.first + t0 + w;  // tile of trip i: tb + 4 i
+      const auto page_of = [&](int t) { return (int)(((uint64_t)(uint32_t)t * A.ps_mul) >> (31 + A.ps_shift)); };
+
+      AttTile<T, DP, EXACT> tile;
+      // places of the next 64 trips' blocks, a trip a lane (PAGE16): bytes from
+      // k and v, -1 for a page outside the cache
+      int32_t place_lo[SUB], place_hi[SUB];
+      // the next trip's pages, a position of each block a lane (otherwise)
+      int32_t page_next[SUB];
+      const auto look_up = [&](int trip) {
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) {
+          if constexpr (PAGE16) {
+            const int t = min((tb + 4 * (trip + lane)) * TILE + 16 * s, (R.n - 1) & ~15);
+            const int at = page_of(t), page = ldg(tab + at);
+            const int64_t off = ((int64_t)page * A.page_stride + (int64_t)(t - at * A.page_size) * A.token_stride) * G::ES + head;
+            const bool ok = page >= 0 && page < A.n_pages;
+            place_lo[s] = ok ? (int32_t)(uint32_t)off : -1;
+            place_hi[s] = ok ? (int32_t)(off >> 32) : -1;
+          } else {
+            const int t = min((tb + 4 * trip) * TILE + 16 * s + m16, R.n - 1);
+            page_next[s] = ldg(tab + page_of(t));
+          }
+        }
+      };
+      int64_t off[SUB];       // PAGE16: of the block; else of this lane's position m16
+      uint32_t bad[SUB];      // bits of the positions whose page is outside the cache
+      const auto locate = [&](int trip) {
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) {
+          if constexpr (PAGE16) {
+            const int src = trip & 63;
+            const int64_t o = (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane(place_hi[s], src) << 32) |
+                                        (uint32_t)__builtin_amdgcn_readlane(place_lo[s], src));
+            bad[s] = o < 0 ? 0xFFFFu : 0u;
+            off[s] = o < 0 ? head : o;
+          } else {
+            const int t = min((tb + 4 * trip) * TILE + 16 * s + m16, R.n - 1), page = page_next[s];
+            const bool ok = page >= 0 && page < A.n_pages;
+            off[s] = (ok ? ((int64_t)page * A.page_stride + (int64_t)(t - page_of(t) * A.page_size) * A.token_stride) * G::ES
+                         : 0) + head;
+            bad[s] = (uint32_t)(__ballot(!ok) & 0xFFFFu);
+          }
+        }
+      };
+      const auto load_k = [&]() {
+#pragma unroll
+        for (int s = 0; s < SUB; ++s)
+#pragma unroll
+          for (int c = 0; c < G::NC; ++c) {
+            const uint32_t at = EXACT ? 64 * c + 16 * gq : min(64 * c + 16 * gq, row_bytes - 16);
+            tile.k[s][c] = PAGE16 ? ldg_b16(kb + off[s], m16 * tok + at) : ldg_b16(kb + off[s], at);
+          }
+      };
+      const auto load_v = [&]() {
+#pragma unroll
+        for (int s = 0; s < SUB; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const char* p = vb + off[s];
+            uint32_t o = (4 * gq + j) * tok;
+            if constexpr (!PAGE16) {
+              const int src = 4 * gq + j;
+              const uint32_t lo = __shfl((int)(uint32_t)off[s], src, 64), hi = __shfl((int)(off[s] >> 32), src, 64);
+              p = vb + (int64_t)(((uint64_t)hi << 32) | lo);
+              o = 0;
+            }
+#pragma unroll
+            for (int ng = 0; ng < G::NG; ++ng) {
+              const int at = (16 * ng + m16) * G::VB;
+              tile.load_v(p, o + (EXACT ? at : min(at, row_bytes - G::VB)), s, j, ng);
+            }
+          }
+      };
+
+      look_up(0);
+      locate(0);
+      load_k();
+      load_v();
+      if constexpr (!PAGE16) look_up(min(1, trips - 1));
+      for (int i = 0; i < trips; ++i) {
+        const int t = (tb + 4 * i) * TILE;
+        uint32_t gone[SUB];
+        bool cut = t < R.lo || t + TILE > R.n;
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) {
+          gone[s] = bad[s];
+          cut = cut || bad[s] != 0;
+        }
+        f32x4 sc[SUB];
+        tile.scores(q, sc, gq, row_bytes);
+        const bool more = i + 1 < trips;
+        if (more) {
+          if constexpr (PAGE16) {
+            if (((i + 1) & 63) == 0) look_up(i + 1);
+          }
+          locate(i + 1);
+          load_k();
+          if constexpr (!PAGE16) look_up(min(i + 2, trips - 1));
+        }
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) sc[s] *= A.scale_log2;
+        if (cut) {
+#pragma unroll
+          for (int s = 0; s < SUB; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int at = t + 16 * s + 4 * gq + j;
+              // (a position that is not seen: no weight, and its value, which may be anything, is cleared)
+              if (at < R.lo || at >= R.n || ((gone[s] >> (4 * gq + j)) & 1)) {
+                sc[s][j] = -INFINITY;
+                tile.clear_v(s, j);
+              }
+            }
+        }
+        float tm = sc[0][0];
+#pragma unroll
+        for (int s = 0; s < SUB; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tm = fmaxf(tm, sc[s][j]);
+        const float mn = fmaxf(mx, max_over_quarters(tm));
+        if (__any(mn > mx)) {
+          const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mx - mn);
+          l *= f;
+#pragma unroll
+          for (int ng = 0; ng < G::NG; ++ng)
+#pragma unroll
+            for (int e = 0; e < G::VD; ++e) acc[ng][e] *= f;
+          mx = mn;
+        }
+        const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+        for (int s = 0; s < SUB; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sc[s][j] = __builtin_amdgcn_exp2f(sc[s][j] - ref);
+            l += sc[s][j];
+          }
+        tile.weigh(sc, acc);
+        if (more) load_v();
+      }
+    }
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+
+    // ---- the four waves' results joined in LDS ----
+    if (gq == 0) s_ml[w][m16][0] = mx, s_ml[w][m16][1] = l;
+    __syncthreads();
+    float M = s_ml[0][m16][0];
+#pragma unroll
+    for (int x = 1; x < 4; ++x) M = fmaxf(M, s_ml[x][m16][0]);
+    const float f = mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx - M);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if ((w >> 1) == half && m16 < nq) {
+#pragma unroll
+        for (int ng = 0; ng < G::NG; ++ng)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < G::VD; i += 4) {
+              f32x4* o = (f32x4*)&s_o[w & 1][m16][16 * G::VD * ng + G::VD * (4 * gq + r) + i];
+              f32x4 x = f32x4{acc[ng][i][r], acc[ng][i + 1][r], acc[ng][i + 2][r], acc[ng][i + 3][r]} * f;
+              if (half) x += *o;
+              *o = x;
+            }
+      }
+      __syncthreads();
+    }
+    const bool whole = cnt == R.tiles;
+    const int E = nq * D / 4;  // groups of four elements of the piece's output
+    const auto put = [&](int g, int d, f32x4 o, float L) {
+      const f32x4 x = L == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : o / L;
+      const int64_t at = (int64_t)row * A.out_stride + (int64_t)(h0 + g) * D + d;
+      if constexpr (G::ES == 4) {
+        stg4((float*)A.out + at, x);
+      } else {
+        typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+        *(GLOBAL u32x2*)((uint16_t*)A.out + at) = u32x2{pack_bf2(__float_as_uint(x.x), __float_as_uint(x.y)),
+                                                       pack_bf2(__float_as_uint(x.z), __float_as_uint(x.w))};
+      }
+    };
+    const int64_t slot = 2 * wg + (u == u_begin ? 0 : 1);
+    for (int e = tid; e < E; e += 256) {
+      const int g = e / (D / 4), d = 4 * (e - g * (D / 4));
+      float gm = s_ml[0][g][0];
+#pragma unroll
+      for (int x = 1; x < 4; ++x) gm = fmaxf(gm, s_ml[x][g][0]);
+      float L = 0.f;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        L += s_ml[x][g][1] * (s_ml[x][g][0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(s_ml[x][g][0] - gm));
+      const f32x4 o = *(const f32x4*)&s_o[0][g][d] + *(const f32x4*)&s_o[1][g][d];
+      if (whole) {
+        put(g, d, o, L);
+      } else {
+        const uint32_t at = (uint32_t)slot * SLOT + g * (DP + 4) * 4;
+        st_sys4(part, at + d * 4, o);
+        if (d == 0) st_sys4(part, at + DP * 4, f32x4{gm, L, 0.f, 0.f});
+      }
+    }
+    if (!whole) {
+      // pieces of this (row, head): one in each of the work-groups w0 .. w1
+      const int64_t a = u - t0, b = a + R.tiles - 1;
+      const int64_t w0 = ((a + 1) * W - 1) / U, w1 = ((b + 1) * W - 1) / U;
+      wait_vm_all();
+      __syncthreads();
+      if (tid == 0) s_last = arrive(A.count + w0) == (int)(w1 - w0);
+      __syncthreads();
+      if (s_last) {
+        if (tid == 0) reset_counter(A.count + w0);
+        // a's piece is its work-group's first one only where its range begins there
+        const uint32_t first = (uint32_t)(2 * w0 + (w0 * U / W == a ? 0 : 1));
+        const int np = (int)(w1 - w0) + 1, sets = E < 256 ? 256 / E : 1;
+        float* jo = &s_o[0][0][0];
+        for (int e0 = 0; e0 < E; e0 += 256) {
+          const int set = sets > 1 ? tid / E : 0, e = sets > 1 ? tid - set * E : e0 + tid;
+          const bool on = set < sets && e < E;
+          const int g = on ? e / (D / 4) : 0, d = on ? 4 * (e - g * (D / 4)) : 0;
+          float gm = -INFINITY, L = 0.f;
+          f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (on) {
+#pragma unroll 4
+            for (int x = set; x < np; x += sets) {
+              const uint32_t at = (x == 0 ? first : (uint32_t)(2 * (w0 + x))) * SLOT + g * (DP + 4) * 4;
+              const f32x4 ml = ld_sys4(part, at + DP * 4), po = ld_sys4(part, at + d * 4);
+              const float mn = fmaxf(gm, ml.x), ref = mn == -INFINITY ? 0.f : mn;
+              const float fa = __builtin_amdgcn_exp2f(gm - ref), fb = __builtin_amdgcn_exp2f(ml.x - ref);
+              o = o * fa + po * fb;
+              L = L * fa + ml.y * fb;
+              gm = mn;
+            }
+          }
+          if (sets > 1) {  // the sets' sums in the sets' order
+            if (on) {
+              *(f32x4*)&jo[4 * tid] = o;
+              jo[1024 + 2 * tid] = gm, jo[1024 + 2 * tid + 1] = L;
+            }
+            __syncthreads();
+            if (on && set == 0) {
+              for (int x = 1; x < sets; ++x) {
+                const float xm = jo[1024 + 2 * (tid + x * E)], mn = fmaxf(gm, xm), ref = mn == -INFINITY ? 0.f : mn;
+                const float fa = __builtin_amdgcn_exp2f(gm - ref), fb = __builtin_amdgcn_exp2f(xm - ref);
+                o = o * fa + *(const f32x4*)&jo[4 * (tid + x * E)] * fb;
+                L = L * fa + jo[1024 + 2 * (tid + x * E) + 1] * fb;
+                gm = mn;
+              }
+            }
+          }
+          if (on && set == 0) put(g, d, o, L);
+        }
+      }
+    }
+    __syncthreads();  // (the next piece reuses the LDS)
+    u += cnt;
+    if (u == base + (int64_t)R.tiles * H) base = u, ++row;
   }
 }
+
+template <typename T, int DP>
+void att_launch(const AttArgs& A, int blocks, hipStream_t s) {
+  if (A.page_size % 16)
+    hipLaunchKernelGGL((k_paged_attention<T, DP, false, false>), dim3(blocks), dim3(256), 0, s, A);
+  else if (A.head_dim == DP)
+    hipLaunchKernelGGL((k_paged_attention<T, DP, true, true>), dim3(blocks), dim3(256), 0, s, A);
+  else
+    hipLaunchKernelGGL((k_paged_attention<T, DP, true, false>), dim3(blocks), dim3(256), 0, s, A);
+}
+
+// compute units of `device`, asked once a device (a negative answer is an error)
+int device_units(int device) {
+  static std::atomic<int> known[64];
+  const bool keep = device >= 0 && device < 64;
+  int n = keep ? known[device].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, device) != hipSuccess || n < 1) return -1;
+    if (keep) known[device].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
+constexpr int ATT_GROUPS_MOST = 3;
+int att_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
+int64_t att_counter_bytes(int units) { return ((int64_t)units * ATT_GROUPS_MOST * 4 + 255) / 256 * 256; }
 
 }  // namespace scute
 
@@ -85,7 +545,9 @@ extern "C" scute_status scute_paged_attention_workspace(int32_t device, int32_t 
   if (device < 0) return fail(SCUTE_E_INVALID, "scute_paged_attention_workspace: device must be >= 0");
   if (head_dim < 8 || head_dim > 256 || head_dim % 8)
     return fail(SCUTE_E_SHAPE, "scute_paged_attention_workspace: head_dim must be a multiple of 8 in [8, 256]");
-  *bytes = 256;
+  const int units = device_units(device);
+  if (units < 0) return fail(SCUTE_E_INVALID, "scute_paged_attention_workspace: no such HIP device");
+  *bytes = att_counter_bytes(units) + (int64_t)units * ATT_GROUPS_MOST * 2 * 16 * (att_dim(head_dim) + 4) * 4;
   return SCUTE_OK;
 }
 
@@ -124,15 +586,29 @@ extern "C" scute_status scute_paged_attention(const scute_kv_cache* C, const voi
   int64_t need = 0;
   if ((st = scute_paged_attention_workspace(C->device, C->head_dim, &need)) != SCUTE_OK) return st;
   if (workspace_bytes < need) return fail(SCUTE_E_INVALID, "scute_paged_attention: the workspace is too small");
-  const AttArgs A{q, C->k, C->v, out, table, len, req, q_stride, out_stride, C->page_stride, C->token_stride,
-                  C->head_stride, table_stride, C->n_pages, n_heads, n_heads / C->n_kv_heads, C->head_dim,
-                  C->page_size, table_width, n_requests, window, scale * 1.4426950408889634f};
-  const dim3 grid((unsigned)n_rows, (unsigned)n_heads);
+  const int units = device_units(C->device), dp = att_dim(C->head_dim);
+  const int64_t counters = att_counter_bytes(units);
+  // t / page_size for 0 <= t < 2^31: multiply by ceil(2^(31 + shift) / page_size), shift = ceil(log2 page_size)
+  int shift = 0;
+  while ((1 << shift) < C->page_size) ++shift;
+  const uint64_t mul = (((uint64_t)1 << (31 + shift)) + C->page_size - 1) / C->page_size;
+  const int group = n_heads / C->n_kv_heads;
+  AttArgs A{q, C->k, C->v, out, table, len, req, (float*)((char*)workspace + counters), (int32_t*)workspace, q_stride,
+            out_stride, C->page_stride, C->token_stride, C->head_stride, table_stride, C->n_pages,
+            (uint32_t)(need - counters), (uint32_t)mul, n_rows, C->n_kv_heads, (group + 15) / 16, group, C->head_dim,
+            C->page_size, shift, table_width, n_requests, window, scale * 1.4426950408889634f};
   const hipStream_t s = (hipStream_t)stream;
-  if (C->dtype == SCUTE_F32)
-    hipLaunchKernelGGL(k_paged_attention<float>, grid, dim3(256), 0, s, A);
-  else
-    hipLaunchKernelGGL(k_paged_attention<uint16_t>, grid, dim3(256), 0, s, A);
+#define ATT(T, DP) att_launch<T, DP>(A, units * att_groups<T, DP>(), s)
+  if (C->dtype == SCUTE_F32) {
+    if (dp == 64) ATT(float, 64);
+    else if (dp == 128) ATT(float, 128);
+    else ATT(float, 256);
+  } else {
+    if (dp == 64) ATT(uint16_t, 64);
+    else if (dp == 128) ATT(uint16_t, 128);
+    else ATT(uint16_t, 256);
+  }
+#undef ATT
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SCUTE_OK : hip_fail(e, fn);
 }

@@ -65,12 +65,11 @@ __device__ __forceinline__ int asg_find(const uint32_t* b, uint32_t x) {
 
 __global__ __launch_bounds__(ASG_THREADS) void k_cache_assign(scute_cache_assign_args A) {
   __shared__ uint32_t ctok[ASG_THREADS], cpage[ASG_THREADS], cgone[ASG_THREADS];
-  __shared__ uint32_t wsum[3][ASG_THREADS / 64];
-  __shared__ uint32_t s_tot[3], s_taken, s_placed, s_refused;
+  __shared__ uint32_t wsum[3][ASG_THREADS / 64], wout[3][ASG_THREADS / 64];
+  __shared__ uint32_t s_tot[3];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int R = A.n_requests, per = (R + ASG_THREADS - 1) / ASG_THREADS;
   const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
-  if (tid == 0) s_taken = s_placed = s_refused = 0;
 
   uint32_t own[3] = {0, 0, 0};
   for (int r = r0; r < r1; ++r) {
@@ -129,28 +128,26 @@ __global__ __launch_bounds__(ASG_THREADS) void k_cache_assign(scute_cache_assign
       tok = sat_add(tok, q.add);
       page = need;
     }
-    if (taken) atomicMax(&s_taken, taken);
-    if (blockIdx.x == 0) {
-      if (refused) atomicAdd(&s_refused, refused);
-      // (threads add at most 2^30 each: saturate against the sum so far)
-      if (placed) {
-        uint32_t seen = s_placed, was;
-        do {
-          was = seen;
-          seen = atomicCAS(&s_placed, was, sat_add(was, placed));
-        } while (seen != was);
-      }
+    for (int o = 32; o > 0; o >>= 1) {
+      taken = max(taken, (uint32_t)__shfl_xor((int)taken, o, 64));
+      placed = sat_add(placed, (uint32_t)__shfl_xor((int)placed, o, 64));
+      refused += (uint32_t)__shfl_xor((int)refused, o, 64);
     }
+    if (lane == 0) wout[0][wv] = taken, wout[1][wv] = placed, wout[2][wv] = refused;
   }
   __syncthreads();
-  const uint32_t tokens = s_tot[0], taken = s_taken, gone = s_tot[2];
+  uint32_t taken = 0;
+  for (int w = 0; w < ASG_THREADS / 64; ++w) taken = max(taken, wout[0][w]);
+  const uint32_t tokens = s_tot[0], gone = s_tot[2];
   if (blockIdx.x == 0 && tid == 0) {
+    uint32_t placed = 0, refused = 0;
+    for (int w = 0; w < ASG_THREADS / 64; ++w) placed = sat_add(placed, wout[1][w]), refused += wout[2][w];
     A.cu_len[R] = (int32_t)tokens;
     A.cursor_out[0] = head + taken;
     A.cursor_out[1] = tail + gone;
-    A.counts[0] = (int32_t)s_placed;
+    A.counts[0] = (int32_t)placed;
     A.counts[1] = (int32_t)taken;
-    A.counts[2] = (int32_t)s_refused;
+    A.counts[2] = (int32_t)refused;
     A.counts[3] = (int32_t)gone;
   }
 
