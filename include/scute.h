@@ -438,7 +438,7 @@ scute_status scute_paged_attention_workspace(int32_t device, int32_t head_dim, i
  *   out[i][h] = sum_t softmax_t(scale q[i][h] . K[t][g]) V[t][g]
  * with g = h / (n_heads / n_kv_heads). A row that sees nothing (len <= 0, or a
  * request outside 0 .. n_requests - 1) gives zeros; positions past the
- * table's width or from 2^30 on, or whose page lies outside the cache, are not
+ * table's width or from 2^29 on, or whose page lies outside the cache, are not
  * seen.
  * q and out [n_rows][n_heads][head_dim] in the cache's type, rows q_stride and
  * out_stride elements apart (multiples of 8, 16-byte aligned pointers).

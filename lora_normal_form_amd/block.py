@@ -40,9 +40,15 @@ def _bad(what):
     raise ValueError(what)
 
 
-def _stream(stream, device):
+# torch's current stream of a device as an address (its accessor without the
+# Stream object, which costs more than a launch's other checks together)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _stream(stream, index):
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -50,26 +56,27 @@ def _gpu(device, *tensors):
     """Every tensor (None passes) on `device`, a GPU."""
     if device.type != "cuda":
         _bad(f"the tensors must be on a GPU, got {device}")
+    index = device.index
     for t in tensors:
-        if t is not None and t.device != device:
+        if t is not None and t.get_device() != index:
             _bad(f"tensors on {t.device} and {device} in one call")
 
 
 def _vector(t, n, dtype, name):
-    """A contiguous one-dimensional tensor of n elements."""
-    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    """A contiguous one-dimensional tensor of n elements; its address."""
+    if t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
         _bad(f"{name} must be a contiguous {dtype} tensor of {n} elements")
-    return t
+    return t.data_ptr()
 
 
 def _heads(t, n, heads, dim, name):
     """[n][heads][dim] with the heads of a row contiguous; its row stride."""
-    if t.dim() != 3 or t.shape != (n, heads, dim):
+    if t.shape != (n, heads, dim):
         _bad(f"{name} must be [{n}][{heads}][{dim}], got {tuple(t.shape)}")
-    s = t.stride()
-    if s[2] != 1 or (heads > 1 and s[1] != dim):
+    a, b, c = t.stride()
+    if c != 1 or (b != dim and heads > 1):
         _bad(f"{name}: the heads of a row must be contiguous")
-    return s[0]
+    return a
 
 
 # ---- the cache -----------------------------------------------------------------------------------
@@ -94,7 +101,7 @@ class KVCache:
             _bad("the last axis of k and v must be contiguous")
         _gpu(k.device, v)
         self.k, self.v = k, v
-        self.device = k.device
+        self.device, self.index = k.device, k.device.index
         self.dtype, self.page_size, self.n_kv_heads, self.head_dim = k.dtype, ps, heads, dim
         self.desc = scute.KVCacheDesc(k.device.index, _DTYPES[k.dtype], ps, heads, dim, 0, n_pages,
                                       *strides, k.data_ptr(), v.data_ptr())
@@ -134,20 +141,18 @@ def assign_pages(old_len, new_len, table, ring, cursor, page_size, rows, stream=
     rows.cursor as old_len and cursor and another Rows (inputs and outputs may
     not be the same tensors)."""
     R = rows.n_requests
-    _vector(old_len, R, _I32, "old_len")
-    _vector(new_len, R, _I32, "new_len")
-    _vector(ring, ring.shape[0], _I32, "ring")
-    _vector(cursor, 2, _I64, "cursor")
-    if table.dtype != _I32 or table.dim() != 2 or table.shape[0] != R or (table.shape[1] > 1 and table.stride(1) != 1):
-        _bad(f"table must be int32 [{R}][pages] with contiguous rows")
-    dev = rows.device
-    _gpu(dev, old_len, new_len, table, ring, cursor)
     a = rows.args
-    a.table_width, a.page_size, a.ring_size = table.shape[1], page_size, ring.shape[0]
-    a.table_stride = table.stride(0) if R > 1 else table.shape[1]
-    a.old_len, a.new_len, a.table = old_len.data_ptr(), new_len.data_ptr(), table.data_ptr()
-    a.ring, a.cursor = ring.data_ptr(), cursor.data_ptr()
-    scute._check(scute.lib.scute_cache_assign(a, _stream(stream, dev)))
+    a.old_len, a.new_len = _vector(old_len, R, _I32, "old_len"), _vector(new_len, R, _I32, "new_len")
+    if table.dtype != _I32 or table.dim() != 2 or table.shape[0] != R:
+        _bad(f"table must be int32 [{R}][pages] with contiguous rows")
+    P, (ts, tc) = table.shape[1], table.stride()
+    if tc != 1 and P > 1:
+        _bad(f"table must be int32 [{R}][pages] with contiguous rows")
+    a.ring_size = size = ring.shape[0]
+    a.ring, a.cursor = _vector(ring, size, _I32, "ring"), _vector(cursor, 2, _I64, "cursor")
+    _gpu(rows.device, old_len, new_len, table, ring, cursor)
+    a.table_width, a.page_size, a.table_stride, a.table = P, page_size, ts if R > 1 else P, table.data_ptr()
+    scute._check(scute.lib.scute_cache_assign(a, _stream(stream, rows.device.index)))
     return rows
 
 
@@ -190,16 +195,17 @@ class Rotary:
             _bad("q_out must have the cache's type")
         qs, ks = _heads(q, T, H, D, "q"), _heads(k, T, cache.n_kv_heads, D, "k")
         vs, os = _heads(v, T, cache.n_kv_heads, D, "v"), _heads(q_out, T, H, D, "q_out")
-        _vector(slot, T, _I64, "slot")
-        if pos.dtype != _I32 or pos.shape != ((self.n_axes, T) if pos.dim() == 2 else (T,)) or \
-                (pos.dim() == 1 and self.n_axes != 1) or (T > 1 and pos.stride(-1) != 1):
+        sp = _vector(slot, T, _I64, "slot")
+        if pos.dim() == 2:
+            ok, (ps, pc) = pos.shape == (self.n_axes, T), pos.stride()
+        else:
+            ok, ps, pc = pos.shape == (T,) and self.n_axes == 1, 0, 1 if pos.is_contiguous() else 0
+        if not ok or pos.dtype != _I32 or (pc != 1 and T > 1):
             _bad(f"pos must be int32 [{self.n_axes}][{T}] with contiguous rows")
-        dev = cache.device
-        _gpu(dev, self.freq, q, k, v, pos, slot, q_out)
+        _gpu(cache.device, self.freq, q, k, v, pos, slot, q_out)
         scute._check(scute.lib.scute_rotary_store(
             self.desc, cache.desc, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPES[dt],
-            pos.data_ptr(), pos.stride(0) if pos.dim() == 2 else 0, slot.data_ptr(), T, H,
-            q_out.data_ptr(), os, _stream(stream, dev)))
+            pos.data_ptr(), ps, sp, T, H, q_out.data_ptr(), os, _stream(stream, cache.index)))
         return q_out
 
 
@@ -234,21 +240,22 @@ class PagedAttention:
         qs, os = _heads(q, N, H, D, "q"), _heads(out, N, H, D, "out")
         if q.dtype != c.dtype or out.dtype != c.dtype:
             _bad("q and out must have the cache's type")
-        if table.dtype != _I32 or table.dim() != 2 or (table.shape[1] > 1 and table.stride(1) != 1):
+        if table.dtype != _I32 or table.dim() != 2:
             _bad("table must be int32 [n_requests][pages] with contiguous rows")
-        R, P = table.shape
-        _vector(row_len, N, _I32, "row_len")
+        (R, P), (ts, tc) = table.shape, table.stride()
+        if tc != 1 and P > 1:
+            _bad("table must be int32 [n_requests][pages] with contiguous rows")
+        lp, rp = _vector(row_len, N, _I32, "row_len"), None
         if row_req is not None:
-            _vector(row_req, N, _I32, "row_req")
+            rp = _vector(row_req, N, _I32, "row_req")
         elif N > R:
             _bad("more rows than requests: row_req says whose they are")
-        dev = c.device
-        _gpu(dev, q, table, row_len, out, row_req)
+        _gpu(c.device, q, table, row_len, out, row_req)
+        ws = self.workspace
         scute._check(scute.lib.scute_paged_attention(
-            c.desc, q.data_ptr(), qs if N > 1 else 0, H, table.data_ptr(), table.stride(0) if R > 1 else P, R, P,
-            row_len.data_ptr(), None if row_req is None else row_req.data_ptr(), N, self.scale, self.window,
-            out.data_ptr(), os if N > 1 else 0, self.workspace.data_ptr(), self.workspace.shape[0],
-            _stream(stream, dev)))
+            c.desc, q.data_ptr(), qs if N > 1 else 0, H, table.data_ptr(), ts if R > 1 else P, R, P, lp, rp, N,
+            self.scale, self.window, out.data_ptr(), os if N > 1 else 0, ws.data_ptr(), ws.shape[0],
+            _stream(stream, c.index)))
         return out
 
 
@@ -281,11 +288,15 @@ class ResidualNorm:
                                    *[None if t is None else t.data_ptr() for t in vecs])
 
     def _rows(self, t, n, name):
-        if t.dim() != 2 or t.shape[0] != n or t.shape[1] != self.d or (self.d > 1 and t.stride(1) != 1):
-            _bad(f"{name} must be [{n}][{self.d}] with contiguous rows")
-        if t.dtype not in _DTYPES:
+        if t.shape != (n, self.d):
+            _bad(f"{name} must be [{n}][{self.d}]")
+        a, b = t.stride()
+        if b != 1 and self.d > 1:
+            _bad(f"{name} must have contiguous rows")
+        dt = _DTYPES.get(t.dtype)
+        if dt is None:
             _bad(f"{name} must be float32 or bfloat16")
-        return t.data_ptr(), _DTYPES[t.dtype], t.stride(0) if n > 1 else 0
+        return t.data_ptr(), dt, a if n > 1 else 0
 
     def forward(self, y, h, h_out, x=None, gate=None, stream=None):
         """y [T][d] (a layer's output; None: h' = h_scale h), h [T][d], gate
@@ -303,17 +314,15 @@ class ResidualNorm:
         gp, gs = None, 0
         if gate is not None:
             if gate.dim() == 1:
-                _vector(gate, self.d, _F32, "gate")
-                gp = gate.data_ptr()
+                gp = _vector(gate, self.d, _F32, "gate")
             else:
                 gp, gt, gs = self._rows(gate, n, "gate")
                 if gt != scute.F32:
                     _bad("gate must be float32")
             if y is None:
                 _bad("a gate without y")
-        dev = self.device
-        _gpu(dev, y, h, h_out, x, gate)
+        _gpu(self.device, y, h, h_out, x, gate)
         scute._check(scute.lib.scute_residual_norm(
             self.desc, yp[0], yp[1], yp[2], hp[0], hp[1], hp[2], gp, gs, op[0], op[2], xp[0], xp[1], xp[2], n,
-            _stream(stream, dev)))
+            _stream(stream, self.device.index)))
         return h_out, x

@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "block.h"
 #include "kernels.h"
@@ -17,40 +18,50 @@ struct AttArgs {
   float* part;     // partial results, two pieces a work-group
   int32_t* count;  // arrivals at a split piece's first work-group
   int64_t q_stride, out_stride, page_stride, token_stride, head_stride, table_stride, n_pages;
+  int32_t once;  // no two rows or query tiles read the same positions
+  int32_t row0;  // the launch's first row (a request's own number where req is null)
   uint32_t part_bytes, ps_mul;  // t / page_size = t ps_mul >> 31 + ps_shift
   int32_t n_rows, n_kv, q_tiles, group, head_dim, page_size, ps_shift, table_width, n_requests, window;
   float scale_log2;  // scale log2(e): the softmax runs on powers of two
 };
 
-// How the work is cut. A unit is one tile of positions (32 of bf16, 16 of
-// fp32) of one row, key head and tile of 16 query heads; units are numbered
-// row by row, key head by key head. W work-groups take equal contiguous
-// ranges of them, so that ragged lengths cost no balance and a few long rows
-// use the whole chip; a range's part of one (row, head) is a piece, its four
-// waves on every fourth tile. A piece that holds all of its (row, head) writes
+// How the work is cut. A unit is four tiles of positions, one for each wave (a
+// tile: 32 of bf16, 16 of fp32), of one row, key head and tile of 16 query
+// heads; units are numbered row by row, key head by key head. W work-groups
+// take equal contiguous ranges of them, so that ragged lengths cost no balance
+// and a few long rows use the whole chip; a range's part of one (row, head) is
+// a piece. A piece that holds all of its (row, head) writes
 // the output; the others write partial results, and the last of them to arrive
 // adds them in the pieces' order. Every work-group finds its range from the
 // lengths by itself (4 bytes a row), so nothing is planned on the host and a
 // captured launch follows the lengths.
 struct AttRow {
-  int n, lo, first, tiles, req;  // positions seen: lo .. n - 1, in `tiles` tiles from tile `first`
+  int n, lo, first, units, req;  // positions seen: lo .. n - 1, in `units` units from tile `first`
 };
 
 template <int TILE>
 __device__ __forceinline__ AttRow att_row(const AttArgs& A, int row) {
   AttRow r;
-  r.req = A.req ? ldg(A.req + row) : row;
-  const int64_t reach = min((int64_t)A.table_width * A.page_size, (int64_t)1 << 30);
+  r.req = A.req ? ldg(A.req + row) : A.row0 + row;
+  const int64_t reach = min((int64_t)A.table_width * A.page_size, (int64_t)1 << 29);
   const int n = r.req >= 0 && r.req < A.n_requests ? max(0, ldg(A.len + row)) : 0;
   r.n = n < reach ? n : (int)reach;
   r.lo = A.window > 0 && r.n > A.window ? r.n - A.window : 0;
   r.first = r.lo / TILE;
-  r.tiles = max(1, (r.n + TILE - 1) / TILE - r.first);  // (an empty row writes its zeros)
+  r.units = max(1, ((r.n + TILE - 1) / TILE - r.first + 3) >> 2);  // (an empty row writes its zeros)
   return r;
 }
 
-__device__ __forceinline__ int64_t uni64(int64_t v) {
-  return (int64_t)(((uint64_t)(uint32_t)uni((int)(v >> 32)) << 32) | (uint32_t)uni((int)(uint32_t)v));
+__device__ __forceinline__ int lane_of(int v, int src) { return __builtin_amdgcn_readlane(v, src); }
+// inclusive sum over the wave's lanes, on row shifts and row broadcasts
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);
+  return v;
 }
 __device__ __forceinline__ float max_over_quarters(float v) {
   v = fmaxf(v, __shfl_xor(v, 16, 64));
@@ -62,8 +73,10 @@ __device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
 __device__ __forceinline__ f32x4 mfma4(uint32_t a, uint32_t b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a), __uint_as_float(b), c, 0, 0, 0);
 }
-__device__ __forceinline__ uint4 ldg_b16(const char* p, uint32_t off) {
-  const u32x4 v = *(const GLOBAL u32x4*)(p + off);
+// once: the bytes are read by this wave only (evicted first from the caches)
+__device__ __forceinline__ uint4 ldg_b16(const char* p, uint32_t off, bool once = false) {
+  const GLOBAL u32x4* a = (const GLOBAL u32x4*)(p + off);
+  const u32x4 v = once ? __builtin_nontemporal_load(a) : *a;
   return make_uint4(v.x, v.y, v.z, v.w);
 }
 __device__ __forceinline__ uint32_t dword(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
@@ -96,13 +109,14 @@ struct AttTile {
   uint4 k[G::SUB][G::NC];
   uint32_t v[G::SUB][4][G::NG][G::VB / 4];
 
-  __device__ __forceinline__ void load_v(const char* p, uint32_t off, int s, int j, int ng) {
+  __device__ __forceinline__ void load_v(const char* p, uint32_t off, int s, int j, int ng, bool once) {
     if constexpr (G::VB == 16) {
-      const uint4 x = ldg_b16(p, off);
+      const uint4 x = ldg_b16(p, off, once);
       v[s][j][ng][0] = x.x, v[s][j][ng][1] = x.y, v[s][j][ng][2] = x.z, v[s][j][ng][3] = x.w;
     } else {
       typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-      const u32x2 x = *(const GLOBAL u32x2*)(p + off);
+      const GLOBAL u32x2* a = (const GLOBAL u32x2*)(p + off);
+      const u32x2 x = once ? __builtin_nontemporal_load(a) : *a;
       v[s][j][ng][0] = x.x, v[s][j][ng][1] = x.y;
     }
   }
@@ -165,9 +179,8 @@ struct AttTile {
 // tile, the output, Q).
 template <typename T, int DP>
 constexpr int att_groups() {
-  return sizeof(T) == 2 ? (DP <= 128 ? 3 : 2) : (DP <= 64 ? 3 : DP <= 128 ? 2 : 1);
+  return sizeof(T) == 2 ? 2 : (DP <= 64 ? 3 : DP <= 128 ? 2 : 1);
 }
-constexpr int ATT_MIN_UNITS = 4;  // tiles a work-group takes at least: one a wave
 
 // PAGE16: pages hold multiples of 16 positions, so the 16 of a block lie in
 // one page and their place is one scalar; else every position is looked up.
@@ -177,56 +190,85 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
   using G = AttGeo<T, DP>;
   constexpr int TILE = G::TILE, SUB = G::SUB, OS = DP + 4;
   __shared__ float s_ml[4][16][2];
-  __shared__ __align__(16) float s_o[2][16][OS];
-  __shared__ int64_t s_wsum[4], s_before;
+  __shared__ __align__(16) float s_o[4][16][OS];
+  __shared__ uint32_t s_wsum[4], s_before;
   __shared__ int s_row, s_last;
   const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6), m16 = lane & 15, gq = lane >> 4;
   const int H = A.n_kv * A.q_tiles, D = EXACT ? DP : A.head_dim, row_bytes = D * G::ES;
 
-  // this work-group's range of units
-  const int per = (A.n_rows + 255) / 256, r0 = min(A.n_rows, tid * per), r1 = min(A.n_rows, r0 + per);
-  int64_t own = 0;
-  for (int r = r0; r < r1; ++r) own += att_row<TILE>(A, r).tiles;
-  int64_t inc = own;
+  // This work-group's range of units, the row it begins in and that row's first
+  // unit (all below 2^31: the host cuts the rows into launches for that). Up
+  // to 64 rows: a row a lane, every wave for itself.
+  const uint32_t wg = blockIdx.x;
+  const bool few = A.n_rows <= 64;
+  AttRow mine = {0, 0, 0, 0, 0};
+  int row;
+  uint32_t before, W, quot, rem, u_begin, u_end;
+  // U units in W ranges: the first `rem` hold quot + 1 units, the others quot
+  const auto cut_ranges = [&](uint32_t U) {
+    W = min(U, gridDim.x);
+    quot = U / W;
+    rem = U - quot * W;
+    u_begin = wg * quot + min(wg, rem);
+    u_end = u_begin + quot + (wg < rem ? 1 : 0);
+  };
+  if (few) {
+    if (lane < A.n_rows) mine = att_row<TILE>(A, lane);
+    const uint32_t inc = wave_scan((uint32_t)mine.units);
+    cut_ranges((uint32_t)lane_of((int)inc, 63) * H);
+    if (wg >= W) return;
+    row = (int)__popcll(__ballot(inc * H <= u_begin));  // (rows that end before: their lanes come first)
+    before = row ? (uint32_t)lane_of((int)inc, row - 1) : 0;
+  } else {
+    const int per = (A.n_rows + 255) / 256, r0 = min(A.n_rows, tid * per), r1 = min(A.n_rows, r0 + per);
+    uint32_t own = 0;
+    for (int r = r0; r < r1; ++r) own += (uint32_t)att_row<TILE>(A, r).units;
+    const uint32_t inc = wave_scan(own);
+    if (lane == 63) s_wsum[w] = inc;
+    __syncthreads();
+    uint32_t pre = inc - own, U = 0;
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int64_t x = __shfl_up(inc, o, 64);
-    if (lane >= o) inc += x;
-  }
-  if (lane == 63) s_wsum[w] = inc;
-  __syncthreads();
-  int64_t pre = inc - own, U = 0;
-#pragma unroll
-  for (int x = 0; x < 4; ++x) {
-    if (x < w) pre += s_wsum[x];
-    U += s_wsum[x];
-  }
-  U = uni64(U * H);
-  const int64_t want = (U + ATT_MIN_UNITS - 1) / ATT_MIN_UNITS;
-  const int64_t W = want < (int64_t)gridDim.x ? want : (int64_t)gridDim.x, wg = blockIdx.x;
-  if (wg >= W) return;
-  const int64_t u_begin = wg * U / W, u_end = (wg + 1) * U / W;
-  if (pre * H <= u_begin && u_begin < (pre + own) * H) {
-    int r = r0;
-    for (int64_t t = att_row<TILE>(A, r).tiles; (pre + t) * H <= u_begin; t = att_row<TILE>(A, r).tiles) {
-      pre += t;
-      ++r;
+    for (int x = 0; x < 4; ++x) {
+      if (x < w) pre += s_wsum[x];
+      U += s_wsum[x];
     }
-    s_row = r;
-    s_before = pre;
+    cut_ranges((uint32_t)uni((int)U) * H);
+    if (wg >= W) return;
+    if (pre * H <= u_begin && u_begin < (pre + own) * H) {
+      int r = r0;
+      for (uint32_t t = att_row<TILE>(A, r).units; (pre + t) * H <= u_begin; t = att_row<TILE>(A, r).units) {
+        pre += t;
+        ++r;
+      }
+      s_row = r;
+      s_before = pre;
+    }
+    __syncthreads();
+    row = uni(s_row);
+    before = (uint32_t)uni((int)s_before);
   }
-  __syncthreads();
-  int row = uni(s_row);
-  int64_t base = uni64(s_before) * H;  // first unit of the row
+  const auto range_of = [&](uint32_t unit) {  // the work-group whose range holds a unit
+    const uint32_t longer = rem * (quot + 1);
+    return unit < longer ? unit / (quot + 1) : rem + (unit - longer) / quot;
+  };
+  uint32_t base = before * H;  // first unit of the row
   const rsrc_t part = make_rsrc(A.part, A.part_bytes);
   constexpr uint32_t SLOT = 16 * (DP + 4) * 4;  // bytes of a partial result: 16 x (DP values, m, l, unused)
 
-  for (int64_t u = u_begin; u < u_end;) {
-    AttRow R = att_row<TILE>(A, row);
-    R.n = uni(R.n), R.lo = uni(R.lo), R.first = uni(R.first), R.tiles = uni(R.tiles), R.req = uni(R.req);
-    const int hh = uni((int)((u - base) / R.tiles)), t0 = uni((int)((u - base) - (int64_t)hh * R.tiles));
-    const int cnt = (int)min((int64_t)(R.tiles - t0), u_end - u);
-    const int kvh = hh / A.q_tiles, h0 = kvh * A.group + (hh - kvh * A.q_tiles) * 16;
+  for (uint32_t u = u_begin; u < u_end;) {
+    AttRow R;
+    if (few) {
+      R = {lane_of(mine.n, row), lane_of(mine.lo, row), lane_of(mine.first, row), lane_of(mine.units, row),
+           lane_of(mine.req, row)};
+    } else {
+      R = att_row<TILE>(A, row);
+      R.n = uni(R.n), R.lo = uni(R.lo), R.first = uni(R.first), R.units = uni(R.units), R.req = uni(R.req);
+    }
+    const uint32_t hh = (u - base) / (uint32_t)R.units, v0 = u - base - hh * R.units;
+    const uint32_t units = min(R.units - v0, u_end - u);
+    // the piece's tiles of the row: t0 .. t0 + cnt - 1 from the row's first
+    const int t0 = 4 * (int)v0, cnt = min(4 * (int)units, (R.n + TILE - 1) / TILE - R.first - t0);
+    const int kvh = A.q_tiles == 1 ? hh : hh / A.q_tiles, h0 = kvh * A.group + (hh - kvh * A.q_tiles) * 16;
     const int nq = min(16, (kvh + 1) * A.group - h0);
 
     // ---- the wave's tiles t0 + w, t0 + w + 4, ... ----
@@ -236,17 +278,7 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
     for (int ng = 0; ng < G::NG; ++ng)
 #pragma unroll
       for (int i = 0; i < G::VD; ++i) acc[ng][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (R.n > 0 && w < cnt) {
-      uint4 q[G::NC];
-      {
-        const char* qp = (const char*)A.q + ((int64_t)row * A.q_stride + (int64_t)(h0 + min(m16, nq - 1)) * D) * G::ES;
-#pragma unroll
-        for (int c = 0; c < G::NC; ++c) {
-          const bool in = m16 < nq && (EXACT || 64 * c + 16 * gq < row_bytes);
-          q[c] = ldg_b16(qp, EXACT ? 64 * c + 16 * gq : min(64 * c + 16 * gq, row_bytes - 16));
-          if (!in) q[c] = make_uint4(0, 0, 0, 0);
-        }
-      }
+    if (w < cnt) {  // (an empty row has none)
       const char *kb = (const char*)A.k, *vb = (const char*)A.v;
       const int32_t* tab = A.table + (int64_t)R.req * A.table_stride;
       const int64_t head = (int64_t)kvh * A.head_stride * G::ES;
@@ -296,16 +328,16 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
           }
         }
       };
-      const auto load_k = [&]() {
+      const auto load_k_as = [&](auto once) {
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
 #pragma unroll
           for (int c = 0; c < G::NC; ++c) {
             const uint32_t at = EXACT ? 64 * c + 16 * gq : min(64 * c + 16 * gq, row_bytes - 16);
-            tile.k[s][c] = PAGE16 ? ldg_b16(kb + off[s], m16 * tok + at) : ldg_b16(kb + off[s], at);
+            tile.k[s][c] = ldg_b16(kb + off[s], PAGE16 ? m16 * tok + at : at, once);
           }
       };
-      const auto load_v = [&]() {
+      const auto load_v_as = [&](auto once) {
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
 #pragma unroll
@@ -321,12 +353,25 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
 #pragma unroll
             for (int ng = 0; ng < G::NG; ++ng) {
               const int at = (16 * ng + m16) * G::VB;
-              tile.load_v(p, o + (EXACT ? at : min(at, row_bytes - G::VB)), s, j, ng);
+              tile.load_v(p, o + (EXACT ? at : min(at, row_bytes - G::VB)), s, j, ng, once);
             }
           }
       };
 
+      const auto load_k = [&]() { A.once ? load_k_as(std::true_type()) : load_k_as(std::false_type()); };
+      const auto load_v = [&]() { A.once ? load_v_as(std::true_type()) : load_v_as(std::false_type()); };
+
       look_up(0);
+      uint4 q[G::NC];
+      {
+        const char* qp = (const char*)A.q + ((int64_t)row * A.q_stride + (int64_t)(h0 + min(m16, nq - 1)) * D) * G::ES;
+#pragma unroll
+        for (int c = 0; c < G::NC; ++c) {
+          const bool in = m16 < nq && (EXACT || 64 * c + 16 * gq < row_bytes);
+          q[c] = ldg_b16(qp, EXACT ? 64 * c + 16 * gq : min(64 * c + 16 * gq, row_bytes - 16));
+          if (!in) q[c] = make_uint4(0, 0, 0, 0);
+        }
+      }
       locate(0);
       load_k();
       load_v();
@@ -397,30 +442,20 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
     l += __shfl_xor(l, 32, 64);
 
     // ---- the four waves' results joined in LDS ----
-    if (gq == 0) s_ml[w][m16][0] = mx, s_ml[w][m16][1] = l;
-    __syncthreads();
-    float M = s_ml[0][m16][0];
+    const int waves = max(0, min(cnt, 4));  // those with tiles
+    if (w < waves && m16 < nq) {
+      if (gq == 0) s_ml[w][m16][0] = mx, s_ml[w][m16][1] = l;
 #pragma unroll
-    for (int x = 1; x < 4; ++x) M = fmaxf(M, s_ml[x][m16][0]);
-    const float f = mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx - M);
+      for (int ng = 0; ng < G::NG; ++ng)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if ((w >> 1) == half && m16 < nq) {
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int ng = 0; ng < G::NG; ++ng)
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int i = 0; i < G::VD; i += 4) {
-              f32x4* o = (f32x4*)&s_o[w & 1][m16][16 * G::VD * ng + G::VD * (4 * gq + r) + i];
-              f32x4 x = f32x4{acc[ng][i][r], acc[ng][i + 1][r], acc[ng][i + 2][r], acc[ng][i + 3][r]} * f;
-              if (half) x += *o;
-              *o = x;
-            }
-      }
-      __syncthreads();
+          for (int i = 0; i < G::VD; i += 4)
+            *(f32x4*)&s_o[w][m16][16 * G::VD * ng + G::VD * (4 * gq + r) + i] =
+                f32x4{acc[ng][i][r], acc[ng][i + 1][r], acc[ng][i + 2][r], acc[ng][i + 3][r]};
     }
-    const bool whole = cnt == R.tiles;
+    __syncthreads();
+    const bool whole = units == (uint32_t)R.units;
     const int E = nq * D / 4;  // groups of four elements of the piece's output
     const auto put = [&](int g, int d, f32x4 o, float L) {
       const f32x4 x = L == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : o / L;
@@ -433,29 +468,28 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
                                                        pack_bf2(__float_as_uint(x.z), __float_as_uint(x.w))};
       }
     };
-    const int64_t slot = 2 * wg + (u == u_begin ? 0 : 1);
+    const uint32_t slot = 2 * wg + (u == u_begin ? 0 : 1);
     for (int e = tid; e < E; e += 256) {
       const int g = e / (D / 4), d = 4 * (e - g * (D / 4));
-      float gm = s_ml[0][g][0];
-#pragma unroll
-      for (int x = 1; x < 4; ++x) gm = fmaxf(gm, s_ml[x][g][0]);
-      float L = 0.f;
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        L += s_ml[x][g][1] * (s_ml[x][g][0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(s_ml[x][g][0] - gm));
-      const f32x4 o = *(const f32x4*)&s_o[0][g][d] + *(const f32x4*)&s_o[1][g][d];
+      float gm = -INFINITY, L = 0.f;
+      f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int x = 0; x < waves; ++x) gm = fmaxf(gm, s_ml[x][g][0]);
+      for (int x = 0; x < waves; ++x) {
+        const float f = gm == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(s_ml[x][g][0] - gm);
+        L += s_ml[x][g][1] * f;
+        o += *(const f32x4*)&s_o[x][g][d] * f;
+      }
       if (whole) {
         put(g, d, o, L);
       } else {
-        const uint32_t at = (uint32_t)slot * SLOT + g * (DP + 4) * 4;
+        const uint32_t at = slot * SLOT + g * (DP + 4) * 4;
         st_sys4(part, at + d * 4, o);
         if (d == 0) st_sys4(part, at + DP * 4, f32x4{gm, L, 0.f, 0.f});
       }
     }
     if (!whole) {
       // pieces of this (row, head): one in each of the work-groups w0 .. w1
-      const int64_t a = u - t0, b = a + R.tiles - 1;
-      const int64_t w0 = ((a + 1) * W - 1) / U, w1 = ((b + 1) * W - 1) / U;
+      const uint32_t a = u - v0, b = a + R.units - 1, w0 = range_of(a), w1 = range_of(b);
       wait_vm_all();
       __syncthreads();
       if (tid == 0) s_last = arrive(A.count + w0) == (int)(w1 - w0);
@@ -463,7 +497,7 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
       if (s_last) {
         if (tid == 0) reset_counter(A.count + w0);
         // a's piece is its work-group's first one only where its range begins there
-        const uint32_t first = (uint32_t)(2 * w0 + (w0 * U / W == a ? 0 : 1));
+        const uint32_t first = 2 * w0 + (w0 * quot + min(w0, rem) == a ? 0 : 1);
         const int np = (int)(w1 - w0) + 1, sets = E < 256 ? 256 / E : 1;
         float* jo = &s_o[0][0][0];
         for (int e0 = 0; e0 < E; e0 += 256) {
@@ -473,15 +507,24 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
           float gm = -INFINITY, L = 0.f;
           f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
           if (on) {
-#pragma unroll 4
-            for (int x = set; x < np; x += sets) {
-              const uint32_t at = (x == 0 ? first : (uint32_t)(2 * (w0 + x))) * SLOT + g * (DP + 4) * 4;
-              const f32x4 ml = ld_sys4(part, at + DP * 4), po = ld_sys4(part, at + d * 4);
-              const float mn = fmaxf(gm, ml.x), ref = mn == -INFINITY ? 0.f : mn;
-              const float fa = __builtin_amdgcn_exp2f(gm - ref), fb = __builtin_amdgcn_exp2f(ml.x - ref);
-              o = o * fa + po * fb;
-              L = L * fa + ml.y * fb;
-              gm = mn;
+            for (int x = set; x < np; x += 4 * sets) {  // (four pieces' loads in flight)
+              f32x4 ml[4], po[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int y = min(x + i * sets, np - 1);
+                const uint32_t at = (y == 0 ? first : 2 * (w0 + y)) * SLOT + g * (DP + 4) * 4;
+                ml[i] = ld_sys4(part, at + DP * 4);
+                po[i] = ld_sys4(part, at + d * 4);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if (x + i * sets >= np) break;
+                const float mn = fmaxf(gm, ml[i].x), ref = mn == -INFINITY ? 0.f : mn;
+                const float fa = __builtin_amdgcn_exp2f(gm - ref), fb = __builtin_amdgcn_exp2f(ml[i].x - ref);
+                o = o * fa + po[i] * fb;
+                L = L * fa + ml[i].y * fb;
+                gm = mn;
+              }
             }
           }
           if (sets > 1) {  // the sets' sums in the sets' order
@@ -505,8 +548,8 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
       }
     }
     __syncthreads();  // (the next piece reuses the LDS)
-    u += cnt;
-    if (u == base + (int64_t)R.tiles * H) base = u, ++row;
+    u += units;
+    if (u == base + (uint32_t)(R.units * H)) base = u, ++row;
   }
 }
 
@@ -595,18 +638,32 @@ extern "C" scute_status scute_paged_attention(const scute_kv_cache* C, const voi
   const int group = n_heads / C->n_kv_heads;
   AttArgs A{q, C->k, C->v, out, table, len, req, (float*)((char*)workspace + counters), (int32_t*)workspace, q_stride,
             out_stride, C->page_stride, C->token_stride, C->head_stride, table_stride, C->n_pages,
+            !req && group <= 16, 0,
             (uint32_t)(need - counters), (uint32_t)mul, n_rows, C->n_kv_heads, (group + 15) / 16, group, C->head_dim,
             C->page_size, shift, table_width, n_requests, window, scale * 1.4426950408889634f};
+  // rows of one launch: their units, at the table's whole width, stay below 2^31
+  const int64_t es = C->dtype == SCUTE_F32 ? 4 : 2, unit = es == 4 ? 64 : 128;
+  const int64_t reach = std::min<int64_t>((int64_t)table_width * C->page_size, (int64_t)1 << 29);
+  const int64_t most = (((int64_t)1 << 31) - 1) / ((int64_t)A.n_kv * A.q_tiles * (reach / unit + 2));
+  if (most < 1) return fail(SCUTE_E_SHAPE, "scute_paged_attention: too many heads for a table this wide");
   const hipStream_t s = (hipStream_t)stream;
 #define ATT(T, DP) att_launch<T, DP>(A, units * att_groups<T, DP>(), s)
-  if (C->dtype == SCUTE_F32) {
-    if (dp == 64) ATT(float, 64);
-    else if (dp == 128) ATT(float, 128);
-    else ATT(float, 256);
-  } else {
-    if (dp == 64) ATT(uint16_t, 64);
-    else if (dp == 128) ATT(uint16_t, 128);
-    else ATT(uint16_t, 256);
+  for (int64_t r = 0; r < n_rows; r += most) {
+    A.row0 = (int32_t)r;
+    A.n_rows = (int32_t)std::min<int64_t>(most, n_rows - r);
+    A.q = (const char*)q + r * q_stride * es;
+    A.out = (char*)out + r * out_stride * es;
+    A.len = len + r;
+    A.req = req ? req + r : nullptr;
+    if (es == 4) {
+      if (dp == 64) ATT(float, 64);
+      else if (dp == 128) ATT(float, 128);
+      else ATT(float, 256);
+    } else {
+      if (dp == 64) ATT(uint16_t, 64);
+      else if (dp == 128) ATT(uint16_t, 128);
+      else ATT(uint16_t, 256);
+    }
   }
 #undef ATT
   const hipError_t e = hipGetLastError();
