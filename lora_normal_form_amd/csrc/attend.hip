@@ -15,26 +15,37 @@ struct AttArgs {
   const void *q, *k, *v;
   void* out;
   const int32_t *table, *len, *req;
-  float* part;     // partial results, two pieces a work-group
-  int32_t* count;  // arrivals at a split piece's first work-group
+  float* part;  // partial results, two pieces a slice
+  int32_t* count;
   int64_t q_stride, out_stride, page_stride, token_stride, head_stride, table_stride, n_pages;
-  int32_t once;  // no two rows or query tiles read the same positions
   int32_t row0;  // the launch's first row (a request's own number where req is null)
   uint32_t part_bytes, ps_mul;  // t / page_size = t ps_mul >> 31 + ps_shift
-  int32_t n_rows, n_kv, q_tiles, group, head_dim, page_size, ps_shift, table_width, n_requests, window;
+  int32_t n_rows, n_kv, q_tiles, group, head_dim, page_size, ps_shift, reach, n_requests, window;
   float scale_log2;  // scale log2(e): the softmax runs on powers of two
 };
 
 // How the work is cut. A unit is four tiles of positions, one for each wave (a
 // tile: 32 of bf16, 16 of fp32), of one row, key head and tile of 16 query
-// heads; units are numbered row by row, key head by key head. W work-groups
-// take equal contiguous ranges of them, so that ragged lengths cost no balance
-// and a few long rows use the whole chip; a range's part of one (row, head) is
-// a piece. A piece that holds all of its (row, head) writes
-// the output; the others write partial results, and the last of them to arrive
-// adds them in the pieces' order. Every work-group finds its range from the
-// lengths by itself (4 bytes a row), so nothing is planned on the host and a
-// captured launch follows the lengths.
+// heads; units are numbered row by row, key head by key head, and cut into
+// slices of consecutive units, whatever rows and heads they cross: one slice a
+// work-group, all alike, and where each has 64 units or more a tail of short
+// slices (1/16 of the units, 1/8 from 128 on) that the work-groups take from a
+// counter as they get done: work-groups with equal work differ by a quarter in
+// time, by their die and its distance to the memory.
+// A slice's part of one (row, head) is a piece. A piece that holds all of its
+// (row, head) writes the output; the others write partial results, and the
+// last of them to arrive adds them in the pieces' order (32 at a time where
+// they are more), so the result does not depend on who took which slice. Every
+// work-group finds the slices from the lengths by itself (4 bytes a row), so
+// nothing is planned on the host and a captured launch follows the lengths.
+constexpr int ATT_FAN = 32;
+// places of partial results a work-group: two a slice, at most 1 + 143 / 64
+// slices a work-group and one more
+constexpr int ATT_PLACES = 2 * 4;
+// counters of the workspace: slices taken, work-groups done, and from
+// ATT_ARRIVALS on the arrivals at each partial result's place, for groups of
+// pieces and for all of them
+constexpr int ATT_QUEUE = 0, ATT_DONE = 32, ATT_ARRIVALS = 64;
 struct AttRow {
   int n, lo, first, units, req;  // positions seen: lo .. n - 1, in `units` units from tile `first`
 };
@@ -42,10 +53,9 @@ struct AttRow {
 template <int TILE>
 __device__ __forceinline__ AttRow att_row(const AttArgs& A, int row) {
   AttRow r;
+  const int len = ldg(A.len + row);  // (asked for before req is known: one trip to memory, not two)
   r.req = A.req ? ldg(A.req + row) : A.row0 + row;
-  const int64_t reach = min((int64_t)A.table_width * A.page_size, (int64_t)1 << 29);
-  const int n = r.req >= 0 && r.req < A.n_requests ? max(0, ldg(A.len + row)) : 0;
-  r.n = n < reach ? n : (int)reach;
+  r.n = (uint32_t)r.req < (uint32_t)A.n_requests ? min(max(len, 0), A.reach) : 0;
   r.lo = A.window > 0 && r.n > A.window ? r.n - A.window : 0;
   r.first = r.lo / TILE;
   r.units = max(1, ((r.n + TILE - 1) / TILE - r.first + 3) >> 2);  // (an empty row writes its zeros)
@@ -73,10 +83,17 @@ __device__ __forceinline__ f32x4 mfma16(uint4 a, uint4 b, f32x4 c) {
 __device__ __forceinline__ f32x4 mfma4(uint32_t a, uint32_t b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a), __uint_as_float(b), c, 0, 0, 0);
 }
-// once: the bytes are read by this wave only (evicted first from the caches)
-__device__ __forceinline__ uint4 ldg_b16(const char* p, uint32_t off, bool once = false) {
-  const GLOBAL u32x4* a = (const GLOBAL u32x4*)(p + off);
-  const u32x4 v = once ? __builtin_nontemporal_load(a) : *a;
+// ONCE: the bytes are read by this wave only (evicted first from the caches)
+template <bool ONCE, typename V>
+__device__ __forceinline__ V ldg_at(const char* p, uint32_t off) {
+  if constexpr (ONCE)
+    return __builtin_nontemporal_load((const GLOBAL V*)(p + off));
+  else
+    return *(const GLOBAL V*)(p + off);
+}
+template <bool ONCE>
+__device__ __forceinline__ uint4 ldg_b16(const char* p, uint32_t off) {
+  const u32x4 v = ldg_at<ONCE, u32x4>(p, off);
   return make_uint4(v.x, v.y, v.z, v.w);
 }
 __device__ __forceinline__ uint32_t dword(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
@@ -109,16 +126,12 @@ struct AttTile {
   uint4 k[G::SUB][G::NC];
   uint32_t v[G::SUB][4][G::NG][G::VB / 4];
 
-  __device__ __forceinline__ void load_v(const char* p, uint32_t off, int s, int j, int ng, bool once) {
-    if constexpr (G::VB == 16) {
-      const uint4 x = ldg_b16(p, off, once);
-      v[s][j][ng][0] = x.x, v[s][j][ng][1] = x.y, v[s][j][ng][2] = x.z, v[s][j][ng][3] = x.w;
-    } else {
-      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-      const GLOBAL u32x2* a = (const GLOBAL u32x2*)(p + off);
-      const u32x2 x = once ? __builtin_nontemporal_load(a) : *a;
-      v[s][j][ng][0] = x.x, v[s][j][ng][1] = x.y;
-    }
+  template <bool ONCE>
+  __device__ __forceinline__ void load_v(const char* p, uint32_t off, int s, int j, int ng) {
+    typedef uint32_t vec __attribute__((ext_vector_type(G::VB / 4)));
+    const vec x = ldg_at<ONCE, vec>(p, off);
+#pragma unroll
+    for (int e = 0; e < G::VB / 4; ++e) v[s][j][ng][e] = x[e];
   }
   __device__ __forceinline__ void scores(const uint4 (&q)[G::NC], f32x4 (&sc)[G::SUB], int gq, int row_bytes) {
 #pragma unroll
@@ -175,87 +188,95 @@ struct AttTile {
   }
 };
 
-// Work-groups a compute unit, by the registers a wave needs (K and V of a
-// tile, the output, Q).
-template <typename T, int DP>
-constexpr int att_groups() {
-  return sizeof(T) == 2 ? 2 : (DP <= 64 ? 3 : DP <= 128 ? 2 : 1);
-}
-
 // PAGE16: pages hold multiples of 16 positions, so the 16 of a block lie in
 // one page and their place is one scalar; else every position is looked up.
-// EXACT: the head dimension is DP.
-template <typename T, int DP, bool PAGE16, bool EXACT>
-__global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(AttArgs A) {
+// EXACT: the head dimension is DP. ONCE: no two rows or query tiles read the
+// same positions, so K and V are loaded past the caches (64 rows of 16384
+// positions: 5.9 TB/s without, 6.4 with; rows that share positions lose: four
+// drafted tokens a request 48 us with it, 39 without).
+// One work-group a compute unit: four waves with a tile of K and V each in
+// flight (64 KB at 128 elements) already fill the memory's queues, and fewer
+// streams at once run faster than more (64 rows of 16384 positions: 674 us
+// with one, 712 with two).
+template <typename T, int DP, bool PAGE16, bool EXACT, bool ONCE>
+__global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
   using G = AttGeo<T, DP>;
   constexpr int TILE = G::TILE, SUB = G::SUB, OS = DP + 4;
   __shared__ float s_ml[4][16][2];
   __shared__ __align__(16) float s_o[4][16][OS];
   __shared__ uint32_t s_wsum[4], s_before;
+  __shared__ uint32_t s_next;
   __shared__ int s_row, s_last;
   const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6), m16 = lane & 15, gq = lane >> 4;
   const int H = A.n_kv * A.q_tiles, D = EXACT ? DP : A.head_dim, row_bytes = D * G::ES;
 
-  // This work-group's range of units, the row it begins in and that row's first
-  // unit (all below 2^31: the host cuts the rows into launches for that). Up
-  // to 64 rows: a row a lane, every wave for itself.
-  const uint32_t wg = blockIdx.x;
+  // Units (all below 2^31: the host cuts the rows into launches for that) and
+  // where the rows' begin. Up to 64 rows: a row a lane, every wave for itself.
   const bool few = A.n_rows <= 64;
   AttRow mine = {0, 0, 0, 0, 0};
-  int row;
-  uint32_t before, W, quot, rem, u_begin, u_end;
-  // U units in W ranges: the first `rem` hold quot + 1 units, the others quot
-  const auto cut_ranges = [&](uint32_t U) {
-    W = min(U, gridDim.x);
-    quot = U / W;
-    rem = U - quot * W;
-    u_begin = wg * quot + min(wg, rem);
-    u_end = u_begin + quot + (wg < rem ? 1 : 0);
-  };
+  const int per = (A.n_rows + 255) / 256, r0 = min(A.n_rows, tid * per), r1 = min(A.n_rows, r0 + per);
+  uint32_t own = 0, upto;  // units of one head: of this lane's rows, and up to them
+  uint32_t U;
   if (few) {
     if (lane < A.n_rows) mine = att_row<TILE>(A, lane);
-    const uint32_t inc = wave_scan((uint32_t)mine.units);
-    cut_ranges((uint32_t)lane_of((int)inc, 63) * H);
-    if (wg >= W) return;
-    row = (int)__popcll(__ballot(inc * H <= u_begin));  // (rows that end before: their lanes come first)
-    before = row ? (uint32_t)lane_of((int)inc, row - 1) : 0;
+    upto = wave_scan((uint32_t)mine.units);
+    U = (uint32_t)lane_of((int)upto, 63) * H;
   } else {
-    const int per = (A.n_rows + 255) / 256, r0 = min(A.n_rows, tid * per), r1 = min(A.n_rows, r0 + per);
-    uint32_t own = 0;
     for (int r = r0; r < r1; ++r) own += (uint32_t)att_row<TILE>(A, r).units;
-    const uint32_t inc = wave_scan(own);
-    if (lane == 63) s_wsum[w] = inc;
+    upto = wave_scan(own);
+    if (lane == 63) s_wsum[w] = upto;
     __syncthreads();
-    uint32_t pre = inc - own, U = 0;
+    U = 0;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      if (x < w) pre += s_wsum[x];
+      if (x < w) upto += s_wsum[x];
       U += s_wsum[x];
     }
-    cut_ranges((uint32_t)uni((int)U) * H);
-    if (wg >= W) return;
-    if (pre * H <= u_begin && u_begin < (pre + own) * H) {
-      int r = r0;
-      for (uint32_t t = att_row<TILE>(A, r).units; (pre + t) * H <= u_begin; t = att_row<TILE>(A, r).units) {
-        pre += t;
-        ++r;
-      }
-      s_row = r;
-      s_before = pre;
-    }
-    __syncthreads();
-    row = uni(s_row);
-    before = (uint32_t)uni((int)s_before);
+    U = (uint32_t)uni((int)U) * H;
   }
-  const auto range_of = [&](uint32_t unit) {  // the work-group whose range holds a unit
-    const uint32_t longer = rem * (quot + 1);
-    return unit < longer ? unit / (quot + 1) : rem + (unit - longer) / quot;
+  // slices: `workers` of quot or quot + 1 units (the first `longer`), then from
+  // unit `fixed` on of `step` units each
+  const uint32_t workers = min(U, gridDim.x), each = U / workers;
+  const uint32_t tail = each >= 128 ? U / 8 : each >= 64 ? U / 16 : 0, step = max(4u, each / 16);
+  const uint32_t fixed = U - tail, quot = tail ? fixed / workers : each, longer = fixed - quot * workers;
+  const uint32_t slices = workers + (tail ? (tail + step - 1) / step : 0);
+  const auto slice_of = [&](uint32_t unit) {  // the slice that holds a unit
+    const uint32_t edge = longer * (quot + 1);
+    if (unit >= fixed) return workers + (unit - fixed) / step;
+    return unit < edge ? unit / (quot + 1) : longer + (unit - edge) / quot;
   };
-  uint32_t base = before * H;  // first unit of the row
+  const auto slice_begin = [&](uint32_t i) {
+    return i < workers ? i * quot + min(i, longer) : min(U, fixed + (i - workers) * step);
+  };
   const rsrc_t part = make_rsrc(A.part, A.part_bytes);
-  constexpr uint32_t SLOT = 16 * (DP + 4) * 4;  // bytes of a partial result: 16 x (DP values, m, l, unused)
+  constexpr uint32_t SLOT = 16 * (DP + 4) * 4;  // bytes of a partial result: 16 x (DP values, m, l, a group's m, l)
 
-  for (uint32_t u = u_begin; u < u_end;) {
+  uint32_t slice = blockIdx.x, u_begin = 0, u = 0, u_end = 0, base = 0;
+  int row = 0;
+  if (slice >= slices) return;
+  for (;;) {
+    if (u == u_end) {  // the slice's units, the row they begin in and that row's first unit
+      u = u_begin = slice_begin(slice);
+      u_end = slice_begin(slice + 1);
+      if (few) {
+        row = (int)__popcll(__ballot(upto * H <= u));  // (rows that end before: their lanes come first)
+        base = row ? (uint32_t)lane_of((int)upto, row - 1) * H : 0;
+      } else {
+        uint32_t pre = upto - own;
+        if (pre * H <= u && u < upto * H) {
+          int r = r0;
+          for (uint32_t t = att_row<TILE>(A, r).units; (pre + t) * H <= u; t = att_row<TILE>(A, r).units) {
+            pre += t;
+            ++r;
+          }
+          s_row = r;
+          s_before = pre;
+        }
+        __syncthreads();
+        row = uni(s_row);
+        base = (uint32_t)uni((int)s_before) * H;
+      }
+    }
     AttRow R;
     if (few) {
       R = {lane_of(mine.n, row), lane_of(mine.lo, row), lane_of(mine.first, row), lane_of(mine.units, row),
@@ -292,35 +313,35 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
       int32_t place_lo[SUB], place_hi[SUB];
       // the next trip's pages, a position of each block a lane (otherwise)
       int32_t page_next[SUB];
-      const auto look_up = [&](int trip) {
+      const auto look_up = [&](int i) {
 #pragma unroll
         for (int s = 0; s < SUB; ++s) {
           if constexpr (PAGE16) {
-            const int t = min((tb + 4 * (trip + lane)) * TILE + 16 * s, (R.n - 1) & ~15);
+            const int t = min((tb + 4 * (i + lane)) * TILE + 16 * s, (R.n - 1) & ~15);
             const int at = page_of(t), page = ldg(tab + at);
             const int64_t off = ((int64_t)page * A.page_stride + (int64_t)(t - at * A.page_size) * A.token_stride) * G::ES + head;
             const bool ok = page >= 0 && page < A.n_pages;
             place_lo[s] = ok ? (int32_t)(uint32_t)off : -1;
             place_hi[s] = ok ? (int32_t)(off >> 32) : -1;
           } else {
-            const int t = min((tb + 4 * trip) * TILE + 16 * s + m16, R.n - 1);
+            const int t = min((tb + 4 * i) * TILE + 16 * s + m16, R.n - 1);
             page_next[s] = ldg(tab + page_of(t));
           }
         }
       };
       int64_t off[SUB];       // PAGE16: of the block; else of this lane's position m16
       uint32_t bad[SUB];      // bits of the positions whose page is outside the cache
-      const auto locate = [&](int trip) {
+      const auto locate = [&](int i) {
 #pragma unroll
         for (int s = 0; s < SUB; ++s) {
           if constexpr (PAGE16) {
-            const int src = trip & 63;
+            const int src = i & 63;
             const int64_t o = (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane(place_hi[s], src) << 32) |
                                         (uint32_t)__builtin_amdgcn_readlane(place_lo[s], src));
             bad[s] = o < 0 ? 0xFFFFu : 0u;
             off[s] = o < 0 ? head : o;
           } else {
-            const int t = min((tb + 4 * trip) * TILE + 16 * s + m16, R.n - 1), page = page_next[s];
+            const int t = min((tb + 4 * i) * TILE + 16 * s + m16, R.n - 1), page = page_next[s];
             const bool ok = page >= 0 && page < A.n_pages;
             off[s] = (ok ? ((int64_t)page * A.page_stride + (int64_t)(t - page_of(t) * A.page_size) * A.token_stride) * G::ES
                          : 0) + head;
@@ -328,16 +349,16 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
           }
         }
       };
-      const auto load_k_as = [&](auto once) {
+      const auto load_k = [&]() {
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
 #pragma unroll
           for (int c = 0; c < G::NC; ++c) {
             const uint32_t at = EXACT ? 64 * c + 16 * gq : min(64 * c + 16 * gq, row_bytes - 16);
-            tile.k[s][c] = ldg_b16(kb + off[s], PAGE16 ? m16 * tok + at : at, once);
+            tile.k[s][c] = ldg_b16<ONCE>(kb + off[s], PAGE16 ? m16 * tok + at : at);
           }
       };
-      const auto load_v_as = [&](auto once) {
+      const auto load_v = [&]() {
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
 #pragma unroll
@@ -353,13 +374,10 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
 #pragma unroll
             for (int ng = 0; ng < G::NG; ++ng) {
               const int at = (16 * ng + m16) * G::VB;
-              tile.load_v(p, o + (EXACT ? at : min(at, row_bytes - G::VB)), s, j, ng, once);
+              tile.template load_v<ONCE>(p, o + (EXACT ? at : min(at, row_bytes - G::VB)), s, j, ng);
             }
           }
       };
-
-      const auto load_k = [&]() { A.once ? load_k_as(std::true_type()) : load_k_as(std::false_type()); };
-      const auto load_v = [&]() { A.once ? load_v_as(std::true_type()) : load_v_as(std::false_type()); };
 
       look_up(0);
       uint4 q[G::NC];
@@ -368,7 +386,7 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
 #pragma unroll
         for (int c = 0; c < G::NC; ++c) {
           const bool in = m16 < nq && (EXACT || 64 * c + 16 * gq < row_bytes);
-          q[c] = ldg_b16(qp, EXACT ? 64 * c + 16 * gq : min(64 * c + 16 * gq, row_bytes - 16));
+          q[c] = ldg_b16<false>(qp, EXACT ? 64 * c + 16 * gq : min(64 * c + 16 * gq, row_bytes - 16));
           if (!in) q[c] = make_uint4(0, 0, 0, 0);
         }
       }
@@ -376,7 +394,9 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
       load_k();
       load_v();
       if constexpr (!PAGE16) look_up(min(1, trips - 1));
-      for (int i = 0; i < trips; ++i) {
+      // (the loads of trip i + 1 run under the products of trip i; the last trip
+      // stands apart, so that the waits count what is in flight)
+      const auto trip = [&](int i, auto more) {
         const int t = (tb + 4 * i) * TILE;
         uint32_t gone[SUB];
         bool cut = t < R.lo || t + TILE > R.n;
@@ -387,8 +407,7 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
         }
         f32x4 sc[SUB];
         tile.scores(q, sc, gq, row_bytes);
-        const bool more = i + 1 < trips;
-        if (more) {
+        if constexpr (more) {
           if constexpr (PAGE16) {
             if (((i + 1) & 63) == 0) look_up(i + 1);
           }
@@ -435,11 +454,17 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
             l += sc[s][j];
           }
         tile.weigh(sc, acc);
-        if (more) load_v();
-      }
+        if constexpr (more) load_v();
+      };
+      for (int i = 0; i + 1 < trips; ++i) trip(i, std::true_type());
+      trip(trips - 1, std::false_type());
     }
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
+    // the next slice, asked for while the results are joined
+    const bool last_piece = u + units == u_end;
+    uint32_t next = slices;
+    if (last_piece && tail && tid == 0) next = workers + (uint32_t)arrive(A.count + ATT_QUEUE);
 
     // ---- the four waves' results joined in LDS ----
     const int waves = max(0, min(cnt, 4));  // those with tiles
@@ -468,7 +493,7 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
                                                        pack_bf2(__float_as_uint(x.z), __float_as_uint(x.w))};
       }
     };
-    const uint32_t slot = 2 * wg + (u == u_begin ? 0 : 1);
+    const uint32_t slot = 2 * slice + (u == u_begin ? 0 : 1);
     for (int e = tid; e < E; e += 256) {
       const int g = e / (D / 4), d = 4 * (e - g * (D / 4));
       float gm = -INFINITY, L = 0.f;
@@ -488,18 +513,28 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
       }
     }
     if (!whole) {
-      // pieces of this (row, head): one in each of the work-groups w0 .. w1
-      const uint32_t a = u - v0, b = a + R.units - 1, w0 = range_of(a), w1 = range_of(b);
-      wait_vm_all();
-      __syncthreads();
-      if (tid == 0) s_last = arrive(A.count + w0) == (int)(w1 - w0);
-      __syncthreads();
-      if (s_last) {
-        if (tid == 0) reset_counter(A.count + w0);
-        // a's piece is its work-group's first one only where its range begins there
-        const uint32_t first = 2 * w0 + (w0 * quot + min(w0, rem) == a ? 0 : 1);
-        const int np = (int)(w1 - w0) + 1, sets = E < 256 ? 256 / E : 1;
-        float* jo = &s_o[0][0][0];
+      // pieces of this (row, head): one in each of the slices w0 .. w1, the
+      // first piece of a slice but perhaps in w0
+      const uint32_t a = u - v0, b = a + R.units - 1, w0 = slice_of(a), w1 = slice_of(b);
+      const uint32_t slot0 = 2 * w0 + (slice_begin(w0) == a ? 0 : 1);
+      const int all = (int)(w1 - w0) + 1, fan = all > ATT_FAN ? (int)(slice - w0) / ATT_FAN * ATT_FAN : 0;
+      const int sets = E < 256 ? 256 / E : 1;
+      float* jo = &s_o[0][0][0];
+      // level 0: the pieces fan .. of one group (only where they are many);
+      // level 1: the groups' results, or the pieces
+      for (int level = all > ATT_FAN ? 0 : 1; level < 2; ++level) {
+        const int from = level == 0 ? fan : 0, stride = level == 1 && all > ATT_FAN ? ATT_FAN : 1;
+        const int np = level == 0 ? min(ATT_FAN, all - fan) : (all + stride - 1) / stride;
+        const uint32_t first = from == 0 ? slot0 : 2 * (w0 + from);
+        int32_t* count = A.count + ATT_ARRIVALS + (level ? ATT_PLACES * gridDim.x : 0) + first;
+        wait_vm_all();
+        __syncthreads();
+        if (tid == 0) {
+          s_last = arrive(count) == np - 1;
+          if (s_last) reset_counter(count);
+        }
+        __syncthreads();
+        if (!s_last) break;
         for (int e0 = 0; e0 < E; e0 += 256) {
           const int set = sets > 1 ? tid / E : 0, e = sets > 1 ? tid - set * E : e0 + tid;
           const bool on = set < sets && e < E;
@@ -507,22 +542,23 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
           float gm = -INFINITY, L = 0.f;
           f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
           if (on) {
-            for (int x = set; x < np; x += 4 * sets) {  // (four pieces' loads in flight)
-              f32x4 ml[4], po[4];
+            for (int x = set; x < np; x += 8 * sets) {  // (eight pieces' loads in flight)
+              f32x4 ml[8], po[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
+              for (int i = 0; i < 8; ++i) {
                 const int y = min(x + i * sets, np - 1);
-                const uint32_t at = (y == 0 ? first : 2 * (w0 + y)) * SLOT + g * (DP + 4) * 4;
+                const uint32_t at = (y == 0 ? first : 2 * (w0 + from + y * stride)) * SLOT + g * (DP + 4) * 4;
                 ml[i] = ld_sys4(part, at + DP * 4);
                 po[i] = ld_sys4(part, at + d * 4);
               }
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
+              for (int i = 0; i < 8; ++i) {
                 if (x + i * sets >= np) break;
-                const float mn = fmaxf(gm, ml[i].x), ref = mn == -INFINITY ? 0.f : mn;
-                const float fa = __builtin_amdgcn_exp2f(gm - ref), fb = __builtin_amdgcn_exp2f(ml[i].x - ref);
+                const float xm = stride > 1 ? ml[i].z : ml[i].x, xl = stride > 1 ? ml[i].w : ml[i].y;
+                const float mn = fmaxf(gm, xm), ref = mn == -INFINITY ? 0.f : mn;
+                const float fa = __builtin_amdgcn_exp2f(gm - ref), fb = __builtin_amdgcn_exp2f(xm - ref);
                 o = o * fa + po[i] * fb;
-                L = L * fa + ml[i].y * fb;
+                L = L * fa + xl * fb;
                 gm = mn;
               }
             }
@@ -543,24 +579,41 @@ __global__ __launch_bounds__(256, (att_groups<T, DP>())) void k_paged_attention(
               }
             }
           }
-          if (on && set == 0) put(g, d, o, L);
+          if (on && set == 0) {
+            if (level) {
+              put(g, d, o, L);
+            } else {  // (in the group's first place, whose elements only this thread reads, m and l beside its own)
+              const uint32_t at = first * SLOT + g * (DP + 4) * 4;
+              st_sys4(part, at + d * 4, o);
+              if (d == 0) st_sys2(part, at + DP * 4 + 8, __float_as_uint(gm), __float_as_uint(L));
+            }
+          }
         }
       }
     }
+    if (last_piece && tid == 0) s_next = next;
     __syncthreads();  // (the next piece reuses the LDS)
     u += units;
     if (u == base + (uint32_t)(R.units * H)) base = u, ++row;
+    if (last_piece) {
+      slice = (uint32_t)uni((int)s_next);
+      if (slice >= slices) break;
+    }
+  }
+  if (tail && tid == 0 && arrive(A.count + ATT_DONE) == (int)workers - 1) {
+    reset_counter(A.count + ATT_QUEUE);
+    reset_counter(A.count + ATT_DONE);
   }
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool ONCE>
 void att_launch(const AttArgs& A, int blocks, hipStream_t s) {
   if (A.page_size % 16)
-    hipLaunchKernelGGL((k_paged_attention<T, DP, false, false>), dim3(blocks), dim3(256), 0, s, A);
+    hipLaunchKernelGGL((k_paged_attention<T, DP, false, false, ONCE>), dim3(blocks), dim3(256), 0, s, A);
   else if (A.head_dim == DP)
-    hipLaunchKernelGGL((k_paged_attention<T, DP, true, true>), dim3(blocks), dim3(256), 0, s, A);
+    hipLaunchKernelGGL((k_paged_attention<T, DP, true, true, ONCE>), dim3(blocks), dim3(256), 0, s, A);
   else
-    hipLaunchKernelGGL((k_paged_attention<T, DP, true, false>), dim3(blocks), dim3(256), 0, s, A);
+    hipLaunchKernelGGL((k_paged_attention<T, DP, true, false, ONCE>), dim3(blocks), dim3(256), 0, s, A);
 }
 
 // compute units of `device`, asked once a device (a negative answer is an error)
@@ -575,9 +628,9 @@ int device_units(int device) {
   return n;
 }
 
-constexpr int ATT_GROUPS_MOST = 3;
 int att_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
-int64_t att_counter_bytes(int units) { return ((int64_t)units * ATT_GROUPS_MOST * 4 + 255) / 256 * 256; }
+int64_t att_places(int units) { return (int64_t)units * ATT_PLACES; }
+int64_t att_counter_bytes(int units) { return (4 * (ATT_ARRIVALS + 2 * att_places(units)) + 255) / 256 * 256; }
 
 }  // namespace scute
 
@@ -590,7 +643,7 @@ extern "C" scute_status scute_paged_attention_workspace(int32_t device, int32_t 
     return fail(SCUTE_E_SHAPE, "scute_paged_attention_workspace: head_dim must be a multiple of 8 in [8, 256]");
   const int units = device_units(device);
   if (units < 0) return fail(SCUTE_E_INVALID, "scute_paged_attention_workspace: no such HIP device");
-  *bytes = att_counter_bytes(units) + (int64_t)units * ATT_GROUPS_MOST * 2 * 16 * (att_dim(head_dim) + 4) * 4;
+  *bytes = att_counter_bytes(units) + att_places(units) * 16 * (att_dim(head_dim) + 4) * 4;
   return SCUTE_OK;
 }
 
@@ -636,18 +689,20 @@ extern "C" scute_status scute_paged_attention(const scute_kv_cache* C, const voi
   while ((1 << shift) < C->page_size) ++shift;
   const uint64_t mul = (((uint64_t)1 << (31 + shift)) + C->page_size - 1) / C->page_size;
   const int group = n_heads / C->n_kv_heads;
+  const int64_t reach = std::min<int64_t>((int64_t)table_width * C->page_size, (int64_t)1 << 29);
   AttArgs A{q, C->k, C->v, out, table, len, req, (float*)((char*)workspace + counters), (int32_t*)workspace, q_stride,
-            out_stride, C->page_stride, C->token_stride, C->head_stride, table_stride, C->n_pages,
-            !req && group <= 16, 0,
+            out_stride, C->page_stride, C->token_stride, C->head_stride, table_stride, C->n_pages, 0,
             (uint32_t)(need - counters), (uint32_t)mul, n_rows, C->n_kv_heads, (group + 15) / 16, group, C->head_dim,
-            C->page_size, shift, table_width, n_requests, window, scale * 1.4426950408889634f};
+            C->page_size, shift, (int32_t)reach, n_requests, window, scale * 1.4426950408889634f};
   // rows of one launch: their units, at the table's whole width, stay below 2^31
   const int64_t es = C->dtype == SCUTE_F32 ? 4 : 2, unit = es == 4 ? 64 : 128;
-  const int64_t reach = std::min<int64_t>((int64_t)table_width * C->page_size, (int64_t)1 << 29);
   const int64_t most = (((int64_t)1 << 31) - 1) / ((int64_t)A.n_kv * A.q_tiles * (reach / unit + 2));
   if (most < 1) return fail(SCUTE_E_SHAPE, "scute_paged_attention: too many heads for a table this wide");
   const hipStream_t s = (hipStream_t)stream;
-#define ATT(T, DP) att_launch<T, DP>(A, units * att_groups<T, DP>(), s)
+  const bool once = !req && A.q_tiles == 1;
+#define ATT(T, DP)                                              \
+  (once ? att_launch<T, DP, true>(A, units, s) \
+        : att_launch<T, DP, false>(A, units, s))
   for (int64_t r = 0; r < n_rows; r += most) {
     A.row0 = (int32_t)r;
     A.n_rows = (int32_t)std::min<int64_t>(most, n_rows - r);
