@@ -365,8 +365,8 @@ typedef struct scute_kv_cache {
  * request and every row past the last token up to max_tokens get slot -1,
  * request -1, pos 0 and len 0, which the operators below skip, so a captured
  * step may hold fewer tokens than rows.
- * Lengths, token and page totals may be at most 2^30; negative old lengths
- * count as 0. Errors: SCUTE_E_INVALID for null or misaligned pointers or an
+ * Lengths, token and page totals may be at most 2^30, new lengths 2^29;
+ * negative old lengths count as 0. Errors: SCUTE_E_INVALID for null or misaligned pointers or an
  * output that is also an input, SCUTE_E_SHAPE for sizes out of range. */
 typedef struct scute_cache_assign_args {
   int32_t device;
@@ -443,9 +443,10 @@ scute_status scute_paged_attention_workspace(int32_t device, int32_t head_dim, i
  * q and out [n_rows][n_heads][head_dim] in the cache's type, rows q_stride and
  * out_stride elements apart (multiples of 8, 16-byte aligned pointers).
  * Several rows of one request (its new tokens, each with its own length) are
- * several rows of one call. Scores, the softmax and the sums are fp32; the
- * weights are rounded once to bf16 for a bf16 cache. The result depends on
- * n_rows and the lengths only, never on the order in which work-groups end.
+ * several rows of one call; those that follow each other share the reads of
+ * its cache. Scores, the softmax and the sums are fp32; the weights are
+ * rounded once to bf16 for a bf16 cache. The result depends on the rows'
+ * requests and lengths only, never on the order in which work-groups end.
  * workspace: `workspace_bytes` (at least what scute_paged_attention_workspace
  * says), 256-byte aligned, zeroed once by the caller before its first use;
  * every call leaves its counters zero. Calls that may overlap in time need

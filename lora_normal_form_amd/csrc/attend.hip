@@ -20,13 +20,14 @@ struct AttArgs {
   int64_t q_stride, out_stride, page_stride, token_stride, head_stride, table_stride, n_pages;
   int32_t row0;  // the launch's first row (a request's own number where req is null)
   uint32_t part_bytes, ps_mul;  // t / page_size = t ps_mul >> 31 + ps_shift
-  int32_t n_rows, n_kv, q_tiles, group, head_dim, page_size, ps_shift, reach, n_requests, window;
+  int32_t n_rows, n_kv, q_tiles, group, together, head_dim, page_size, ps_shift, reach, n_requests, window;
   float scale_log2;  // scale log2(e): the softmax runs on powers of two
 };
 
 // How the work is cut. A unit is four tiles of positions, one for each wave (a
 // tile: 32 of bf16, 16 of fp32), of one row, key head and tile of 16 query
-// heads; units are numbered row by row, key head by key head, and cut into
+// heads (or up to four rows of one request); units are numbered row by row,
+// key head by key head, and cut into
 // slices of consecutive units, whatever rows and heads they cross: one slice a
 // work-group, all alike, and where each has 64 units or more a tail of short
 // slices (1/16 of the units, 1/8 from 128 on) that the work-groups take from a
@@ -46,19 +47,63 @@ constexpr int ATT_PLACES = 2 * 4;
 // ATT_ARRIVALS on the arrivals at each partial result's place, for groups of
 // pieces and for all of them
 constexpr int ATT_QUEUE = 0, ATT_DONE = 32, ATT_ARRIVALS = 64;
+// Rows of one request that follow each other share its K and V: up to four of
+// them (`together`, as many as fit the 16 columns of a query tile with all
+// heads of a key head) are one row of the numbering, their first; the others
+// have no units.
 struct AttRow {
-  int n, lo, first, units, req;  // positions seen: lo .. n - 1, in `units` units from tile `first`
+  int n, lo, first, units, req;     // positions some row sees: lo .. n - 1, in `units` units from tile `first`
+  int rows, every_lo, every_n;      // rows, and the positions that each of them sees
 };
 
-template <int TILE>
+// positions a row sees, from its length
+__device__ __forceinline__ int att_len(const AttArgs& A, int len, int req) {
+  return (uint32_t)req < (uint32_t)A.n_requests ? min(max(len, 0), A.reach) : 0;
+}
+__device__ __forceinline__ int att_first(const AttArgs& A, int n) {
+  return A.window > 0 && n > A.window ? n - A.window : 0;
+}
+
+template <int TILE, bool SHARED>
 __device__ __forceinline__ AttRow att_row(const AttArgs& A, int row) {
   AttRow r;
-  const int len = ldg(A.len + row);  // (asked for before req is known: one trip to memory, not two)
-  r.req = A.req ? ldg(A.req + row) : A.row0 + row;
-  r.n = (uint32_t)r.req < (uint32_t)A.n_requests ? min(max(len, 0), A.reach) : 0;
-  r.lo = A.window > 0 && r.n > A.window ? r.n - A.window : 0;
+  bool leads = true;
+  if (!SHARED || A.together == 1) {
+    const int len = ldg(A.len + row);  // (asked for before req is known: one trip to memory, not two)
+    r.req = A.req ? ldg(A.req + row) : A.row0 + row;
+    r.n = att_len(A, len, r.req);
+    r.lo = att_first(A, r.n);
+    r.rows = 1, r.every_lo = r.lo, r.every_n = r.n;
+  } else {
+    const int base = row / A.together * A.together, me = row - base;
+    int q[4], l[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int at = min(base + j, A.n_rows - 1);
+      q[j] = ldg(A.req + at);
+      l[j] = ldg(A.len + at);
+    }
+    const int own = me == 0 ? q[0] : me == 1 ? q[1] : me == 2 ? q[2] : q[3];
+    leads = me == 0 || own != (me == 1 ? q[0] : me == 2 ? q[1] : q[2]);
+    r.req = own, r.n = 0, r.lo = 0x7FFFFFFF, r.rows = 0, r.every_lo = 0, r.every_n = 0x7FFFFFFF;
+    bool on = true;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      on = on && (j < me || (j < A.together && base + j < A.n_rows && q[j] == own));
+      const int n = att_len(A, l[j], own), lo = att_first(A, n);
+      if (on && j >= me) {
+        r.n = max(r.n, n);
+        if (n > 0) r.lo = min(r.lo, lo);
+        r.every_lo = max(r.every_lo, lo);
+        r.every_n = min(r.every_n, n);
+        ++r.rows;
+      }
+    }
+    r.lo = min(r.lo, r.n);
+  }
   r.first = r.lo / TILE;
   r.units = max(1, ((r.n + TILE - 1) / TILE - r.first + 3) >> 2);  // (an empty row writes its zeros)
+  if (!leads) r.units = 0;
   return r;
 }
 
@@ -213,16 +258,16 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
   // Units (all below 2^31: the host cuts the rows into launches for that) and
   // where the rows' begin. Up to 64 rows: a row a lane, every wave for itself.
   const bool few = A.n_rows <= 64;
-  AttRow mine = {0, 0, 0, 0, 0};
+  AttRow mine = {};
   const int per = (A.n_rows + 255) / 256, r0 = min(A.n_rows, tid * per), r1 = min(A.n_rows, r0 + per);
   uint32_t own = 0, upto;  // units of one head: of this lane's rows, and up to them
   uint32_t U;
   if (few) {
-    if (lane < A.n_rows) mine = att_row<TILE>(A, lane);
+    if (lane < A.n_rows) mine = att_row<TILE, !ONCE>(A, lane);
     upto = wave_scan((uint32_t)mine.units);
     U = (uint32_t)lane_of((int)upto, 63) * H;
   } else {
-    for (int r = r0; r < r1; ++r) own += (uint32_t)att_row<TILE>(A, r).units;
+    for (int r = r0; r < r1; ++r) own += (uint32_t)att_row<TILE, !ONCE>(A, r).units;
     upto = wave_scan(own);
     if (lane == 63) s_wsum[w] = upto;
     __syncthreads();
@@ -265,7 +310,7 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
         uint32_t pre = upto - own;
         if (pre * H <= u && u < upto * H) {
           int r = r0;
-          for (uint32_t t = att_row<TILE>(A, r).units; (pre + t) * H <= u; t = att_row<TILE>(A, r).units) {
+          for (uint32_t t = att_row<TILE, !ONCE>(A, r).units; (pre + t) * H <= u; t = att_row<TILE, !ONCE>(A, r).units) {
             pre += t;
             ++r;
           }
@@ -278,19 +323,33 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
       }
     }
     AttRow R;
-    if (few) {
-      R = {lane_of(mine.n, row), lane_of(mine.lo, row), lane_of(mine.first, row), lane_of(mine.units, row),
-           lane_of(mine.req, row)};
-    } else {
-      R = att_row<TILE>(A, row);
-      R.n = uni(R.n), R.lo = uni(R.lo), R.first = uni(R.first), R.units = uni(R.units), R.req = uni(R.req);
+    for (;; ++row) {  // (rows without units are passed)
+      if (few) {
+        R = {lane_of(mine.n, row), lane_of(mine.lo, row), lane_of(mine.first, row), lane_of(mine.units, row),
+             lane_of(mine.req, row), 1, 0, 0};
+        if constexpr (!ONCE)
+          R.rows = lane_of(mine.rows, row), R.every_lo = lane_of(mine.every_lo, row), R.every_n = lane_of(mine.every_n, row);
+      } else {
+        R = att_row<TILE, !ONCE>(A, row);
+        R = {uni(R.n), uni(R.lo), uni(R.first), uni(R.units), uni(R.req), uni(R.rows), uni(R.every_lo), uni(R.every_n)};
+      }
+      if (ONCE || R.units) break;
     }
+    if constexpr (ONCE) R.every_lo = R.lo, R.every_n = R.n;
     const uint32_t hh = (u - base) / (uint32_t)R.units, v0 = u - base - hh * R.units;
     const uint32_t units = min(R.units - v0, u_end - u);
     // the piece's tiles of the row: t0 .. t0 + cnt - 1 from the row's first
     const int t0 = 4 * (int)v0, cnt = min(4 * (int)units, (R.n + TILE - 1) / TILE - R.first - t0);
     const int kvh = A.q_tiles == 1 ? hh : hh / A.q_tiles, h0 = kvh * A.group + (hh - kvh * A.q_tiles) * 16;
-    const int nq = min(16, (kvh + 1) * A.group - h0);
+    // columns of the query tile: column c is head h0 + c % wide of row c / wide
+    const bool shared = !ONCE && A.together > 1;
+    const int wide = shared ? A.group : 16, nq = shared ? R.rows * A.group : min(16, (kvh + 1) * A.group - h0);
+    const int my_row = ONCE ? 0 : min(m16, nq - 1) / wide;
+    int my_n = R.n, my_lo = R.lo;  // what this lane's column sees
+    if (shared && R.rows > 1) {
+      my_n = att_len(A, ldg(A.len + row + my_row), R.req);
+      my_lo = att_first(A, my_n);
+    }
 
     // ---- the wave's tiles t0 + w, t0 + w + 4, ... ----
     float mx = -INFINITY, l = 0.f;
@@ -358,7 +417,7 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
             tile.k[s][c] = ldg_b16<ONCE>(kb + off[s], PAGE16 ? m16 * tok + at : at);
           }
       };
-      const auto load_v = [&]() {
+      const auto load_v = [&](const int64_t (&off)[SUB]) {
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
 #pragma unroll
@@ -382,7 +441,7 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
       look_up(0);
       uint4 q[G::NC];
       {
-        const char* qp = (const char*)A.q + ((int64_t)row * A.q_stride + (int64_t)(h0 + min(m16, nq - 1)) * D) * G::ES;
+        const char* qp = (const char*)A.q + ((int64_t)(row + my_row) * A.q_stride + (int64_t)(h0 + min(m16, nq - 1) - my_row * wide) * D) * G::ES;
 #pragma unroll
         for (int c = 0; c < G::NC; ++c) {
           const bool in = m16 < nq && (EXACT || 64 * c + 16 * gq < row_bytes);
@@ -392,17 +451,19 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
       }
       locate(0);
       load_k();
-      load_v();
+      load_v(off);
       if constexpr (!PAGE16) look_up(min(1, trips - 1));
       // (the loads of trip i + 1 run under the products of trip i; the last trip
       // stands apart, so that the waits count what is in flight)
       const auto trip = [&](int i, auto more) {
         const int t = (tb + 4 * i) * TILE;
         uint32_t gone[SUB];
-        bool cut = t < R.lo || t + TILE > R.n;
+        int64_t here[SUB];
+        bool cut = t < R.every_lo || t + TILE > R.every_n;
 #pragma unroll
         for (int s = 0; s < SUB; ++s) {
           gone[s] = bad[s];
+          here[s] = off[s];
           cut = cut || bad[s] != 0;
         }
         f32x4 sc[SUB];
@@ -417,18 +478,26 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
         }
 #pragma unroll
         for (int s = 0; s < SUB; ++s) sc[s] *= A.scale_log2;
+        // a position that is not seen has no weight, and its value, which may be
+        // anything, is cleared
+        const auto clear = [&](int lo, int n) {
+#pragma unroll
+          for (int s = 0; s < SUB; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int at = t + 16 * s + 4 * gq + j;
+              if (at < lo || at >= n || ((gone[s] >> (4 * gq + j)) & 1)) tile.clear_v(s, j);
+            }
+        };
         if (cut) {
 #pragma unroll
           for (int s = 0; s < SUB; ++s)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int at = t + 16 * s + 4 * gq + j;
-              // (a position that is not seen: no weight, and its value, which may be anything, is cleared)
-              if (at < R.lo || at >= R.n || ((gone[s] >> (4 * gq + j)) & 1)) {
-                sc[s][j] = -INFINITY;
-                tile.clear_v(s, j);
-              }
+              if (at < my_lo || at >= my_n || ((gone[s] >> (4 * gq + j)) & 1)) sc[s][j] = -INFINITY;
             }
+          if (ONCE || R.rows == 1) clear(R.lo, R.n);
         }
         float tm = sc[0][0];
 #pragma unroll
@@ -453,8 +522,28 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
             sc[s][j] = __builtin_amdgcn_exp2f(sc[s][j] - ref);
             l += sc[s][j];
           }
-        tile.weigh(sc, acc);
-        if constexpr (more) load_v();
+        if (ONCE || !cut || R.rows == 1) {
+          tile.weigh(sc, acc);
+        } else {
+          // rows that see different parts of the tile: each on its own, with V
+          // cleared for it (what others see of it, times their weight of 0, may
+          // be NaN: only the row's own columns are kept)
+          for (int i = 0; i < R.rows; ++i) {
+            if (i) load_v(here);
+            clear(lane_of(my_lo, i * wide), lane_of(my_n, i * wide));
+            f32x4 with[G::NG][G::VD];
+#pragma unroll
+            for (int ng = 0; ng < G::NG; ++ng)
+#pragma unroll
+              for (int e = 0; e < G::VD; ++e) with[ng][e] = acc[ng][e];
+            tile.weigh(sc, with);
+#pragma unroll
+            for (int ng = 0; ng < G::NG; ++ng)
+#pragma unroll
+              for (int e = 0; e < G::VD; ++e) acc[ng][e] = my_row == i ? with[ng][e] : acc[ng][e];
+          }
+        }
+        if constexpr (more) load_v(off);
       };
       for (int i = 0; i + 1 < trips; ++i) trip(i, std::true_type());
       trip(trips - 1, std::false_type());
@@ -484,7 +573,8 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
     const int E = nq * D / 4;  // groups of four elements of the piece's output
     const auto put = [&](int g, int d, f32x4 o, float L) {
       const f32x4 x = L == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : o / L;
-      const int64_t at = (int64_t)row * A.out_stride + (int64_t)(h0 + g) * D + d;
+      const int i = ONCE ? 0 : g / wide;
+      const int64_t at = (int64_t)(row + i) * A.out_stride + (int64_t)(h0 + g - i * wide) * D + d;
       if constexpr (G::ES == 4) {
         stg4((float*)A.out + at, x);
       } else {
@@ -690,9 +780,10 @@ extern "C" scute_status scute_paged_attention(const scute_kv_cache* C, const voi
   const uint64_t mul = (((uint64_t)1 << (31 + shift)) + C->page_size - 1) / C->page_size;
   const int group = n_heads / C->n_kv_heads;
   const int64_t reach = std::min<int64_t>((int64_t)table_width * C->page_size, (int64_t)1 << 29);
+  const int together = req && group <= 8 ? std::min(4, 16 / group) : 1;
   AttArgs A{q, C->k, C->v, out, table, len, req, (float*)((char*)workspace + counters), (int32_t*)workspace, q_stride,
             out_stride, C->page_stride, C->token_stride, C->head_stride, table_stride, C->n_pages, 0,
-            (uint32_t)(need - counters), (uint32_t)mul, n_rows, C->n_kv_heads, (group + 15) / 16, group, C->head_dim,
+            (uint32_t)(need - counters), (uint32_t)mul, n_rows, C->n_kv_heads, (group + 15) / 16, group, together, C->head_dim,
             C->page_size, shift, (int32_t)reach, n_requests, window, scale * 1.4426950408889634f};
   // rows of one launch: their units, at the table's whole width, stay below 2^31
   const int64_t es = C->dtype == SCUTE_F32 ? 4 : 2, unit = es == 4 ? 64 : 128;

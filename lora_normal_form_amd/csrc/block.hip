@@ -23,10 +23,17 @@ namespace scute {
 // then found by a binary search over the borders and a walk over at most
 // `per` requests, so the whole step is one launch with no exchange between
 // work-groups: redoing the sums (8 bytes a request from L2) costs less than a
-// second launch. Sums saturate at 2^30 (saturating addition of non-negative
-// numbers is associative, so a scan may use it).
+// second launch. Bound by that chain of latencies, not by bytes. Sums saturate
+// at 2^30 (saturating addition of non-negative numbers is associative, so a
+// scan may use it).
 constexpr int ASG_THREADS = 1024;
 constexpr uint32_t ASG_MAX = 1u << 30;
+
+// the call's arguments, and x / page_size = x mul >> 31 + shift for x < 2^31
+struct AsgArgs {
+  scute_cache_assign_args a;
+  uint32_t mul, shift;
+};
 
 __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) {
   const uint32_t s = a + b;  // both at most 2^30
@@ -39,19 +46,35 @@ struct AsgReq {
   bool fits, ends;
 };
 
-__device__ __forceinline__ AsgReq asg_req(const scute_cache_assign_args& A, int r) {
+__device__ __forceinline__ uint32_t asg_page(const AsgArgs& A, uint32_t x) {
+  return (uint32_t)(((uint64_t)x * A.mul) >> (31 + A.shift));
+}
+
+__device__ __forceinline__ AsgReq asg_req(const AsgArgs& A, int32_t o, int32_t n) {
   AsgReq q;
-  const int32_t o = A.old_len[r], n = A.new_len[r];
   q.old = o > 0 ? min((uint32_t)o, ASG_MAX) : 0u;
   q.ends = n < 0;
-  q.add = n > 0 ? min((uint32_t)n, ASG_MAX) : 0u;
-  const uint32_t ps = (uint32_t)A.page_size;
-  q.held = (q.old + ps - 1) / ps;
-  const uint32_t upto = (q.old + q.add + ps - 1) / ps;
-  q.fits = !q.ends && upto <= (uint32_t)A.table_width;
+  q.add = n > 0 ? min((uint32_t)n, ASG_MAX / 2) : 0u;
+  const uint32_t ps = (uint32_t)A.a.page_size;
+  q.held = asg_page(A, q.old + ps - 1);
+  const uint32_t upto = asg_page(A, q.old + q.add + ps - 1);
+  q.fits = !q.ends && upto <= (uint32_t)A.a.table_width;
   q.want = q.fits ? upto - q.held : 0u;
-  q.gone = q.ends ? min(q.held, (uint32_t)A.table_width) : 0u;
+  q.gone = q.ends ? min(q.held, (uint32_t)A.a.table_width) : 0u;
   return q;
+}
+
+// inclusive saturating sum over the wave's lanes (row shifts and broadcasts)
+__device__ __forceinline__ uint32_t sat_scan(uint32_t v) {
+#define STEP(ctrl, rows) v = sat_add(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xF, false))
+  STEP(0x111, 0xF);
+  STEP(0x112, 0xF);
+  STEP(0x114, 0xF);
+  STEP(0x118, 0xF);
+  STEP(0x142, 0xA);
+  STEP(0x143, 0xC);
+#undef STEP
+  return v;
 }
 
 // index of the last border that is <= x (borders ascending, b[0] = 0)
@@ -63,59 +86,63 @@ __device__ __forceinline__ int asg_find(const uint32_t* b, uint32_t x) {
   return lo;
 }
 
-__global__ __launch_bounds__(ASG_THREADS) void k_cache_assign(scute_cache_assign_args A) {
+__global__ __launch_bounds__(ASG_THREADS) void k_cache_assign(AsgArgs G) {
+  const scute_cache_assign_args& A = G.a;
   __shared__ uint32_t ctok[ASG_THREADS], cpage[ASG_THREADS], cgone[ASG_THREADS];
+  __shared__ int32_t s_old[ASG_THREADS], s_new[ASG_THREADS];  // lengths, up to a request a thread
   __shared__ uint32_t wsum[3][ASG_THREADS / 64], wout[3][ASG_THREADS / 64];
-  __shared__ uint32_t s_tot[3];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int R = A.n_requests, per = (R + ASG_THREADS - 1) / ASG_THREADS;
   const int r0 = min(R, tid * per), r1 = min(R, r0 + per);
+  const int64_t head = A.cursor[0], tail = A.cursor[1];
 
   uint32_t own[3] = {0, 0, 0};
   for (int r = r0; r < r1; ++r) {
-    const AsgReq q = asg_req(A, r);
+    const int32_t o = A.old_len[r], n = A.new_len[r];
+    const AsgReq q = asg_req(G, o, n);
     own[0] = sat_add(own[0], q.add);
     own[1] = sat_add(own[1], q.want);
     own[2] = sat_add(own[2], q.gone);
+    if (per == 1) s_old[tid] = o, s_new[tid] = n;
   }
   uint32_t inc[3];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
-    inc[k] = own[k];
-    for (int o = 1; o < 64; o <<= 1) {
-      const uint32_t v = __shfl_up(inc[k], o, 64);
-      if (lane >= o) inc[k] = sat_add(inc[k], v);
-    }
+    inc[k] = sat_scan(own[k]);
     if (lane == 63) wsum[k][wv] = inc[k];
   }
   __syncthreads();
-  uint32_t pre[3];
+  uint32_t pre[3], tot[3];
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     uint32_t before = 0, all = 0;
+#pragma unroll
     for (int w = 0; w < ASG_THREADS / 64; ++w) {
-      if (w == wv) before = all;
+      before = w == wv ? all : before;
       all = sat_add(all, wsum[k][w]);
     }
-    const uint32_t left = __shfl_up(inc[k], 1, 64);
+    const uint32_t left = (uint32_t)__shfl_up((int)inc[k], 1, 64);
     pre[k] = sat_add(before, lane ? left : 0u);
-    if (tid == 0) s_tot[k] = all;
+    tot[k] = all;
   }
   ctok[tid] = pre[0];
   cpage[tid] = pre[1];
   cgone[tid] = pre[2];
+  const auto request = [&](int r) {
+    return per == 1 ? asg_req(G, s_old[r], s_new[r]) : asg_req(G, A.old_len[r], A.new_len[r]);
+  };
 
   const uint32_t cap = (uint32_t)A.ring_size;
-  const int64_t head = A.cursor[0], tail = A.cursor[1];
   const int64_t free64 = tail - head;
   const uint32_t avail = free64 <= 0 ? 0u : free64 < (int64_t)cap ? (uint32_t)free64 : cap;
   const uint32_t h0 = (uint32_t)((uint64_t)head % cap), t0 = (uint32_t)((uint64_t)tail % cap);
   // pages taken: requests that want pages are placed up to the first that the
   // free pages do not cover
+  uint32_t taken = 0;
   {
-    uint32_t tok = pre[0], page = pre[1], taken = 0, placed = 0, refused = 0;
+    uint32_t tok = pre[0], page = pre[1], placed = 0, refused = 0;
     for (int r = r0; r < r1; ++r) {
-      const AsgReq q = asg_req(A, r);
+      const AsgReq q = request(r);
       const uint32_t need = sat_add(page, q.want);
       const bool ok = q.fits && (q.want == 0 || need <= avail);
       if (ok && q.want) taken = need;
@@ -128,17 +155,22 @@ __global__ __launch_bounds__(ASG_THREADS) void k_cache_assign(scute_cache_assign
       tok = sat_add(tok, q.add);
       page = need;
     }
-    for (int o = 32; o > 0; o >>= 1) {
-      taken = max(taken, (uint32_t)__shfl_xor((int)taken, o, 64));
-      placed = sat_add(placed, (uint32_t)__shfl_xor((int)placed, o, 64));
-      refused += (uint32_t)__shfl_xor((int)refused, o, 64);
+    // (within a wave the last lane with pages taken has the most)
+    const uint64_t some = __ballot(taken != 0);
+    taken = some ? (uint32_t)__shfl((int)taken, 63 - __clzll((long long)some), 64) : 0u;
+    if (blockIdx.x == 0) {
+      for (int o = 32; o > 0; o >>= 1) {
+        placed = sat_add(placed, (uint32_t)__shfl_xor((int)placed, o, 64));
+        refused += (uint32_t)__shfl_xor((int)refused, o, 64);
+      }
     }
     if (lane == 0) wout[0][wv] = taken, wout[1][wv] = placed, wout[2][wv] = refused;
   }
   __syncthreads();
-  uint32_t taken = 0;
+  taken = 0;
+#pragma unroll
   for (int w = 0; w < ASG_THREADS / 64; ++w) taken = max(taken, wout[0][w]);
-  const uint32_t tokens = s_tot[0], gone = s_tot[2];
+  const uint32_t tokens = tot[0], gone = tot[2];
   if (blockIdx.x == 0 && tid == 0) {
     uint32_t placed = 0, refused = 0;
     for (int w = 0; w < ASG_THREADS / 64; ++w) placed = sat_add(placed, wout[1][w]), refused += wout[2][w];
@@ -160,19 +192,19 @@ __global__ __launch_bounds__(ASG_THREADS) void k_cache_assign(scute_cache_assign
       const int i = asg_find(ctok, t);
       uint32_t tok = ctok[i], page = cpage[i];
       int r = i * per;
-      AsgReq q = asg_req(A, r);
+      AsgReq q = request(r);
       while (t - tok >= q.add) {  // (the border of thread i + 1 is past t)
         tok = sat_add(tok, q.add);
         page = sat_add(page, q.want);
-        q = asg_req(A, ++r);
+        q = request(++r);
       }
       if (q.fits && (q.want == 0 || sat_add(page, q.want) <= avail)) {
-        const uint32_t p = q.old + (t - tok), at = p / ps;
+        const uint32_t p = q.old + (t - tok), at = asg_page(G, p);
         int32_t id;
         if (at < q.held) {
           id = A.table[(int64_t)r * A.table_stride + at];
         } else {
-          uint32_t c = h0 + page + (at - q.held);
+          const uint32_t c = h0 + page + (at - q.held);
           id = A.ring[c < cap ? c : c - cap];
         }
         slot = id < 0 ? -1 : (int64_t)id * ps + (p - at * ps);
@@ -190,10 +222,10 @@ __global__ __launch_bounds__(ASG_THREADS) void k_cache_assign(scute_cache_assign
     const int i = asg_find(cpage, k);
     uint32_t page = cpage[i];
     int r = i * per;
-    AsgReq q = asg_req(A, r);
+    AsgReq q = request(r);
     while (k - page >= q.want) {
       page = sat_add(page, q.want);
-      q = asg_req(A, ++r);
+      q = request(++r);
     }
     const uint32_t c = h0 + k;
     A.table[(int64_t)r * A.table_stride + q.held + (k - page)] = A.ring[c < cap ? c : c - cap];
@@ -203,10 +235,10 @@ __global__ __launch_bounds__(ASG_THREADS) void k_cache_assign(scute_cache_assign
     const int i = asg_find(cgone, k);
     uint32_t page = cgone[i];
     int r = i * per;
-    AsgReq q = asg_req(A, r);
+    AsgReq q = request(r);
     while (k - page >= q.gone) {
       page = sat_add(page, q.gone);
-      q = asg_req(A, ++r);
+      q = request(++r);
     }
     const uint32_t c = t0 + k;
     A.ring[c < cap ? c : c - cap] = A.table[(int64_t)r * A.table_stride + (k - page)];
@@ -229,10 +261,16 @@ struct RotArgs {
   int32_t head_dim, n_pairs, n_axes, interleaved, n_heads, n_kv_heads, page_size;
 };
 
-template <typename T, int V>
+// ONCE: read once in the launch (a non-temporal load)
+template <typename T, int V, bool ONCE = false>
 __device__ __forceinline__ void ld_vec(const void* p, int64_t i, float (&o)[V]) {
   if constexpr (V == 4 && sizeof(T) == 4) {
-    const f32x4 v = ldg4((const float*)p + i);
+    const GLOBAL f32x4* a = (const GLOBAL f32x4*)((const float*)p + i);
+    f32x4 v;
+    if constexpr (ONCE)
+      v = __builtin_nontemporal_load(a);
+    else
+      v = *a;
     o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
   } else if constexpr (V == 4) {
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -317,11 +355,11 @@ __global__ __launch_bounds__(256) void k_rotary_store(RotArgs A) {
     float a[V], b[V];
     if (u >= nk || at >= ur) {
       const int e = rd + (at - ur) * V;
-      ld_vec<S, V>(src, si + e, a);
+      ld_vec<S, V, true>(src, si + e, a);
       st_vec<D, V>(dst, di + e, a);
     } else if (A.interleaved) {
       if constexpr (V == 4) {
-        ld_vec<S, V>(src, si + 4 * at, a);
+        ld_vec<S, V, true>(src, si + 4 * at, a);
         const float c0 = cs[2 * at], s0 = sn[2 * at], c1 = cs[2 * at + 1], s1 = sn[2 * at + 1];
         b[0] = a[0] * c0 - a[1] * s0, b[1] = a[0] * s0 + a[1] * c0;
         b[2] = a[2] * c1 - a[3] * s1, b[3] = a[2] * s1 + a[3] * c1;
@@ -335,8 +373,8 @@ __global__ __launch_bounds__(256) void k_rotary_store(RotArgs A) {
         st_vec<D, 1>(dst, di + 2 * at + 1, o1);
       }
     } else {
-      ld_vec<S, V>(src, si + V * at, a);
-      ld_vec<S, V>(src, si + n + V * at, b);
+      ld_vec<S, V, true>(src, si + V * at, a);
+      ld_vec<S, V, true>(src, si + n + V * at, b);
       float x[V], y[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -364,14 +402,26 @@ struct NormArgs {
   float eps, h_scale, y_scale, inv_d;
 };
 
-// sum over the work-group; `red` is a buffer of its own for each call
+// Sum over the work-group's up to 16 waves; `red` is a buffer of its own for
+// each call. Row shifts and broadcasts inside the wave, then the waves' sums
+// in every 16 lanes.
 __device__ __forceinline__ float group_sum(float v, float* red) {
-  v = wave_sum(v);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+#define STEP(ctrl, rows) v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xF, false))
+  STEP(0x111, 0xF);
+  STEP(0x112, 0xF);
+  STEP(0x114, 0xF);
+  STEP(0x118, 0xF);
+  STEP(0x142, 0xA);
+  STEP(0x143, 0xC);
+  if ((threadIdx.x & 63) == 63) red[threadIdx.x >> 6] = v;
   __syncthreads();
-  float s = 0.f;
-  for (int w = 0; w < (int)(blockDim.x >> 6); ++w) s += red[w];
-  return s;
+  v = (threadIdx.x & 15) < (blockDim.x >> 6) ? red[threadIdx.x & 15] : 0.f;
+  STEP(0x111, 0xF);
+  STEP(0x112, 0xF);
+  STEP(0x114, 0xF);
+  STEP(0x118, 0xF);
+#undef STEP
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 15));
 }
 
 template <int V>
@@ -389,9 +439,36 @@ __device__ __forceinline__ void st_any(void* p, int bf, int64_t i, const float (
     st_vec<float, V>(p, i, o);
 }
 
-template <int V, int N>
-__device__ __forceinline__ void norm_row(float (&v)[N][V], const NormArgs& A, const float* w, const float* b,
-                                         float (*red)[16]) {
+// A vector's units of this thread, `fill` where it is null. EARLY: asked for
+// with the row, not after its sums.
+template <bool EARLY, int V, int N>
+struct NormVec {
+  const float* p;
+  float fill;
+  float r[EARLY ? N : 1][V];
+
+  __device__ __forceinline__ NormVec(const float* q, float f, bool used, int units) : p(q), fill(f) {
+    if constexpr (EARLY) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[k][i] = fill;
+        const int u = threadIdx.x + k * blockDim.x;
+        if (p && used && u < units) ld_vec<float, V>(p, (int64_t)u * V, r[k]);
+      }
+    }
+  }
+  __device__ __forceinline__ void get(int k, int u, float (&o)[V]) const {
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = EARLY ? r[EARLY ? k : 0][i] : fill;
+    if constexpr (!EARLY)
+      if (p) ld_vec<float, V>(p, (int64_t)u * V, o);
+  }
+};
+
+template <bool EARLY, int V, int N>
+__device__ __forceinline__ void norm_row(float (&v)[N][V], const NormArgs& A, const NormVec<EARLY, V, N>& w,
+                                         const NormVec<EARLY, V, N>& b, float (*red)[16]) {
   const int tid = threadIdx.x, th = blockDim.x, units = A.d / V;
   if (A.kind == SCUTE_NORM_LAYER) {
     float s = 0.f;
@@ -402,9 +479,8 @@ __device__ __forceinline__ void norm_row(float (&v)[N][V], const NormArgs& A, co
     const float mu = group_sum(s, red[0]) * A.inv_d;
 #pragma unroll
     for (int k = 0; k < N; ++k)
-      if (tid + k * th < units)
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[k][i] -= mu;
+      for (int i = 0; i < V; ++i) v[k][i] = tid + k * th < units ? v[k][i] - mu : 0.f;
   }
   float s = 0.f;
 #pragma unroll
@@ -417,10 +493,8 @@ __device__ __forceinline__ void norm_row(float (&v)[N][V], const NormArgs& A, co
     const int u = tid + k * th;
     if (u < units) {
       float g[V], c[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) g[i] = 1.f, c[i] = 0.f;
-      if (w) ld_vec<float, V>(w, (int64_t)u * V, g);
-      if (b) ld_vec<float, V>(b, (int64_t)u * V, c);
+      w.get(k, u, g);
+      b.get(k, u, c);
 #pragma unroll
       for (int i = 0; i < V; ++i) v[k][i] = v[k][i] * r * g[i] + c[i];
     }
@@ -429,12 +503,15 @@ __device__ __forceinline__ void norm_row(float (&v)[N][V], const NormArgs& A, co
 
 // One work-group per row, the row in registers (N units of V elements a
 // thread, zeros past its end): y and h are read once, h' and x written once.
+// Short rows' vectors are asked for with the row.
 template <int V, int N>
 __global__ __launch_bounds__(1024) void k_residual_norm(NormArgs A) {
+  constexpr bool EARLY = V * N <= 8;
   __shared__ float red[4][16];
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, th = blockDim.x, units = A.d / V;
   float v[N][V], h[N][V];
+  const bool post = A.y && A.post;
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int u = tid + k * th;
@@ -445,28 +522,82 @@ __global__ __launch_bounds__(1024) void k_residual_norm(NormArgs A) {
       ld_any<V>(A.h, A.h_bf, row * A.h_stride + (int64_t)u * V, h[k]);
     }
   }
-  if (A.y && A.post) norm_row<V, N>(v, A, A.post_w, A.post_b, red);
+  using Vec = NormVec<EARLY, V, N>;
+  const Vec pw(A.post_w, 1.f, post, units), pb(A.post_b, 0.f, post, units);
+  const Vec gate(A.gate ? A.gate + row * A.gate_stride : nullptr, 1.f, true, units);
+  const Vec ew(A.pre_w, 1.f, A.x != nullptr, units), eb(A.pre_b, 0.f, A.x != nullptr, units);
+  if (post) norm_row<EARLY, V, N>(v, A, pw, pb, red);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int u = tid + k * th;
     if (u < units) {
       float g[V];
+      gate.get(k, u, g);
 #pragma unroll
-      for (int i = 0; i < V; ++i) g[i] = 1.f;
-      if (A.gate) ld_vec<float, V>(A.gate, row * A.gate_stride + (int64_t)u * V, g);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        v[k][i] = A.h_scale * h[k][i] + (A.y ? A.y_scale * (v[k][i] * g[i]) : 0.f);
-      }
+      for (int i = 0; i < V; ++i) v[k][i] = A.h_scale * h[k][i] + (A.y ? A.y_scale * (v[k][i] * g[i]) : 0.f);
       if (A.h_out) st_any<V>(A.h_out, A.h_bf, row * A.h_out_stride + (int64_t)u * V, v[k]);
     }
   }
   if (!A.x) return;
-  norm_row<V, N>(v, A, A.pre_w, A.pre_b, red + 2);
+  norm_row<EARLY, V, N>(v, A, ew, eb, red + 2);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int u = tid + k * th;
     if (u < units) st_any<V>(A.x, A.x_bf, row * A.x_stride + (int64_t)u * V, v[k]);
+  }
+}
+
+// Rows too long for registers an element at a time (over 8192 of a length or
+// alignment that does not allow four): every pass computes the elements anew
+// from y and h, which stay in the L2.
+__global__ __launch_bounds__(1024) void k_residual_norm_long(NormArgs A) {
+  __shared__ float red[4][16];
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, th = blockDim.x;
+  const bool post = A.y && A.post, layer = A.kind == SCUTE_NORM_LAYER;
+  const auto at = [](const void* p, int bf, int64_t i) {
+    float o[1];
+    ld_any<1>(p, bf, i, o);
+    return o[0];
+  };
+  const auto y = [&](int u) { return at(A.y, A.y_bf, row * A.y_stride + u); };
+  float mu = 0.f, r = 1.f, s = 0.f;
+  if (post) {
+    if (layer) {
+      for (int u = tid; u < A.d; u += th) s += y(u);
+      mu = group_sum(s, red[0]) * A.inv_d;
+    }
+    s = 0.f;
+    for (int u = tid; u < A.d; u += th) s += (y(u) - mu) * (y(u) - mu);
+    r = rsqrtf(group_sum(s, red[1]) * A.inv_d + A.eps);
+  }
+  const auto h1 = [&](int u) {  // h'
+    float z = 0.f;
+    if (A.y) {
+      z = (y(u) - mu) * r;
+      if (post) z = z * (A.post_w ? ldg(A.post_w + u) : 1.f) + (A.post_b ? ldg(A.post_b + u) : 0.f);
+      z *= A.y_scale * (A.gate ? ldg(A.gate + row * A.gate_stride + u) : 1.f);
+    }
+    return A.h_scale * at(A.h, A.h_bf, row * A.h_stride + u) + z;
+  };
+  float m1 = 0.f, r1 = 1.f;
+  if (A.x) {
+    if (layer) {
+      s = 0.f;
+      for (int u = tid; u < A.d; u += th) s += h1(u);
+      m1 = group_sum(s, red[2]) * A.inv_d;
+    }
+    s = 0.f;
+    for (int u = tid; u < A.d; u += th) s += (h1(u) - m1) * (h1(u) - m1);
+    r1 = rsqrtf(group_sum(s, red[3]) * A.inv_d + A.eps);
+  }
+  for (int u = tid; u < A.d; u += th) {  // (h_out may be h: an element is read before it is written)
+    const float v[1] = {h1(u)};
+    if (A.h_out) st_any<1>(A.h_out, A.h_bf, row * A.h_out_stride + u, v);
+    if (A.x) {
+      const float o[1] = {(v[0] - m1) * r1 * (A.pre_w ? ldg(A.pre_w + u) : 1.f) + (A.pre_b ? ldg(A.pre_b + u) : 0.f)};
+      st_any<1>(A.x, A.x_bf, row * A.x_stride + u, o);
+    }
   }
 }
 
@@ -520,11 +651,14 @@ extern "C" scute_status scute_cache_assign(const scute_cache_assign_args* A, voi
     return fail(SCUTE_E_INVALID, "scute_cache_assign: an output is also an input");
   DeviceGuard g(A->device);
   if (!g.ok()) return hip_fail(g.err, fn);
+  AsgArgs G{*A, 0, 0};
+  while ((1 << G.shift) < A->page_size) ++G.shift;
+  G.mul = (uint32_t)((((uint64_t)1 << (31 + G.shift)) + A->page_size - 1) / A->page_size);
   // one round of the tokens over up to 512 work-groups; at least one work-group
   // for every 256 requests, whose pages may have to be copied
   const int64_t work = std::max<int64_t>(A->max_tokens, 4 * (int64_t)A->n_requests);
   const int64_t blocks = std::min<int64_t>(std::max<int64_t>(1, (work + ASG_THREADS - 1) / ASG_THREADS), 512);
-  hipLaunchKernelGGL(k_cache_assign, dim3((unsigned)blocks), dim3(ASG_THREADS), 0, (hipStream_t)stream, *A);
+  hipLaunchKernelGGL(k_cache_assign, dim3((unsigned)blocks), dim3(ASG_THREADS), 0, (hipStream_t)stream, G);
   return launched(fn);
 }
 
@@ -666,8 +800,12 @@ extern "C" scute_status scute_residual_norm(const scute_norm* N, const void* y, 
                    h_out_stride, x_stride, y_dtype == SCUTE_BF16, h_dtype == SCUTE_BF16, x_dtype == SCUTE_BF16,
                    N->kind, N->post, N->d, N->eps, N->h_scale, N->y_scale, 1.f / (float)N->d};
   const int V = vec ? 4 : 1, units = N->d / V;
+  // a unit a thread for few rows (128 rows of 4096: 4.4 us with 1024 threads,
+  // 4.9 with 512), more of them for many (8191 rows of 4096: 138 us with 1024,
+  // 114 with 512, 122 with 256), where other rows hide a row's latencies
+  const int most = n_rows <= 512 || units > 512 * 8 ? 1024 : 512;
   int threads = 64;
-  while (threads < 1024 && units > threads) threads *= 2;
+  while (threads < most && units > threads) threads *= 2;
   const int per = (units + threads - 1) / threads;  // at most 8 of 4 elements, 32 of one
   const hipStream_t s = (hipStream_t)stream;
 #define NORM(VV, NN) hipLaunchKernelGGL((k_residual_norm<VV, NN>), dim3((unsigned)n_rows), dim3(threads), 0, s, A)
@@ -680,7 +818,7 @@ extern "C" scute_status scute_residual_norm(const scute_norm* N, const void* y, 
     if (per <= 1) NORM(1, 1);
     else if (per <= 4) NORM(1, 4);
     else if (per <= 8) NORM(1, 8);
-    else NORM(1, 32);
+    else hipLaunchKernelGGL(k_residual_norm_long, dim3((unsigned)n_rows), dim3(threads), 0, s, A);
   }
 #undef NORM
   return launched(fn);

@@ -374,6 +374,35 @@ def test_attention_masked_places_hold_anything(dt, ps):
         _close(out, ref, tol, f"masked {bad}")
 
 
+@pytest.mark.parametrize("dt, Hq, Hk, D, ps, window", [
+    (BF16, 4, 4, 128, 16, 0), (BF16, 4, 2, 64, 16, 0), (BF16, 8, 2, 128, 32, 0), (BF16, 6, 2, 80, 5, 0),
+    (BF16, 10, 2, 128, 16, 20), (BF16, 16, 2, 64, 16, 7), (BF16, 9, 1, 64, 16, 0), (F32, 6, 2, 80, 5, 30),
+    (F32, 4, 1, 256, 16, 0), (BF16, 8, 2, 256, 48, 33)])
+def test_attention_rows_of_one_request(dt, Hq, Hk, D, ps, window):
+    """Rows of one request share the reads of its cache: runs of one to seven
+    rows, with lengths that rise, fall, repeat and vanish, rows of no request
+    between them; a NaN that only the longest row of a run sees stays with it."""
+    req = [0, 0, 0, 0, 0, 1, 1, 2, 3, 3, 3, -1, -1, 4, 4, 9, 4, 4, 5, 5, 5, 5, 5, 5, 5]
+    lens = [100, 101, 102, 103, 104, 33, 32, 64, 0, 1, 2, 50, 0, 130, 7, 9, 70, 70, 60, 61, 62, 63, 64, 65, 66]
+    kc, vc, table, _ = _attend_case(D + ps, [0] * 6, -(-140 // ps), ps, Hq, Hk, D, dt)
+    q = torch.randn((len(req), Hq, D), generator=torch.Generator().manual_seed(1)).to(DEV, dt)
+    _run_attend(kc, vc, table, q, lens, req=req, window=window)
+    for r, n in ((0, 104), (5, 66), (4, 130)):
+        page, at = int(table[r, (n - 1) // ps]), (n - 1) % ps
+        vc[page, at, :, 3:5] = torch.tensor([float("nan"), float("inf")], device=DEV)
+        kc[page, at, 0, 1] = float("nan")
+    cache = block.KVCache(kc, vc)
+    out = block.PagedAttention(cache, Hq, window=window).forward(q, table, _int(lens), torch.empty_like(q),
+                                                                 row_req=_int(req))
+    torch.cuda.synchronize()
+    ref, tol = _attend_ref(q, kc, vc, table, lens, req, window, 1 / math.sqrt(D))
+    clean = [i for i in range(len(req)) if i not in (4, 13, 24)]
+    assert bool(torch.isfinite(ref[clean]).all()) and bool(torch.isfinite(out[clean]).all())
+    _close(out[clean], ref[clean], tol[clean], "rows that do not see the NaN")
+    for i in (4, 13, 24):
+        assert bool(torch.isnan(out[i, :Hq // Hk]).all()) and bool(torch.isnan(out[i, :, 3]).all())
+
+
 def test_attention_extreme_scores():
     """Scores far apart (no overflow, the far ones vanish), equal scores, and
     values of the type's lowest in a seen place (the score is then -inf or
