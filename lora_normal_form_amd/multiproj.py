@@ -29,6 +29,9 @@ QKV, split   three layers and three forwards; any method.
 FFN          a gate layer (base weight only) and the up layer with the
              tenants' adapters ((IA)^3's l on its s slot), then
              scute_silu_gate: h = silu(g) (.) u.
+Attention    one step of a block's attention half around the fused QKV layer:
+             norm, q / k / v, rotary positions and the paged cache, attention,
+             the output projection (any method), residual and next norm.
 
     python -m lora_normal_form_amd.multiproj [--out PATH]   (timing on one GPU)
 """
@@ -263,6 +266,86 @@ class GatedUp:
             ld.layer.close()
 
 
+# ---- attention ---------------------------------------------------------------------------------
+
+class AttentionStep:
+    """One step of a decoder block's attention half for a batch of n rows:
+
+        x = N_in(h);  q, k, v = the fused layer;  q and k rotated, k and v into
+        the paged cache;  a = attention;  o = out(a)
+        h' = h_scale h + y_scale (gate (.) N_post(o));  x' = N_out(h')
+
+    qkv: a QKVFused over projections of n_heads, n_kv_heads and n_kv_heads
+    heads of head_dim columns. wl_out: the output projection's workload (d_in
+    n_heads head_dim, its own tenants), whose rows' inputs the attention
+    writes. The rows are the requests' new tokens in the requests' order (the
+    plans' tenants follow that order); rows past the last token, and those of
+    a request that found no pages, go through the layers and are skipped by the
+    cache and the attention.
+
+    The step keeps the requests' lengths, pages and free pages on the GPU:
+    table [n_requests][pages_per_request], ring (n_pages free pages at first).
+    one_each: every request brings one token in every step (n is n_requests);
+    the attention then streams the cache. freq (float64 [pairs]), axis, n_axes
+    and interleaved as in block.Rotary; norm_in, norm_post, norm_out: float32
+    weights [d] (norm_post None: no norm on o)."""
+
+    def __init__(self, qkv, wl_out, n_heads, n_kv_heads, head_dim, n_requests, pages_per_request, page_size,
+                 n_pages, freq, axis=None, n_axes=1, interleaved=False, norm_in=None, norm_post=None, norm_out=None,
+                 kind="rms", eps=1e-5, h_scale=1.0, y_scale=1.0, window=0, one_each=False, device=0):
+        import torch
+        from . import block
+        from . import workload as glue
+        if list(qkv.d_outs) != [n_heads * head_dim, n_kv_heads * head_dim, n_kv_heads * head_dim]:
+            raise ValueError("the q / k / v projections must be n_heads, n_kv_heads and n_kv_heads heads wide")
+        n, d = qkv.x.shape
+        if wl_out.n != n or wl_out.d_in != n_heads * head_dim or wl_out.d_out != d:
+            raise ValueError("the output projection must take the heads of every row back to the layer's width")
+        if one_each and n != n_requests:
+            raise ValueError("one_each needs a row for each request")
+        dev = qkv.x.device
+        self.qkv, self.out = qkv, glue.load(wl_out, device=device)
+        self.one_each, dt = one_each, qkv.x.dtype
+        q, k, v = (qkv.y[:, a:b] for a, b in zip((0, *np.cumsum(qkv.d_outs)), np.cumsum(qkv.d_outs)))
+        self.q, self.k, self.v = (t.unflatten(1, (-1, head_dim)) for t in (q, k, v))
+        shape = (n_pages, page_size, n_kv_heads, head_dim)
+        self.cache = block.KVCache(torch.zeros(shape, dtype=dt, device=dev), torch.zeros(shape, dtype=dt, device=dev))
+        self.table = torch.zeros((n_requests, pages_per_request), dtype=torch.int32, device=dev)
+        self.ring = torch.arange(n_pages, dtype=torch.int32, device=dev)
+        self.rows, self._other = block.Rows(n_requests, n, dev), block.Rows(n_requests, n, dev)
+        self.rows.cursor.copy_(torch.tensor([0, n_pages]))
+        self.rotary = block.Rotary(freq, head_dim, axis=axis, n_axes=n_axes, interleaved=interleaved)
+        self.attention = block.PagedAttention(self.cache, n_heads, window=window)
+        self.norm_in = block.ResidualNorm(d, kind, pre_weight=norm_in, eps=eps, device=dev)
+        self.norm_out = block.ResidualNorm(d, kind, post=norm_post is not None, post_weight=norm_post,
+                                           pre_weight=norm_out, h_scale=h_scale, y_scale=y_scale, eps=eps, device=dev)
+        self.q_rot = torch.empty((n, n_heads, head_dim), dtype=dt, device=dev)
+        self.a = self.out.x.view(n, n_heads, head_dim)
+
+    def forward(self, h, new_len, h_out, x_out, pos=None, gate=None):
+        """h [n][d] the residual stream; new_len int32 [n_requests] on the GPU
+        (negative: the request ends); pos int32 [n_axes][n] (None: every axis
+        at the token's position). Writes and returns (h_out, x_out); self.rows
+        holds the step's rows (block.Rows)."""
+        from . import block
+        prev, rows = self.rows, self._other
+        block.assign_pages(prev.seq_len, new_len, self.table, self.ring, prev.cursor, self.cache.page_size, rows)
+        self.rows, self._other = rows, prev
+        qkv, out = self.qkv, self.out
+        self.norm_in.forward(None, h, None, qkv.x)
+        qkv.layer.forward(qkv.batch, qkv.x, qkv.W, qkv.y)
+        if pos is None:
+            pos = rows.pos if self.rotary.n_axes == 1 else rows.pos.expand(self.rotary.n_axes, -1)
+        self.rotary.store(self.q, self.k, self.v, pos, rows.slot, self.cache, self.q_rot)
+        self.attention.forward(self.q_rot, self.table, rows.len, self.a, row_req=None if self.one_each else rows.req)
+        out.layer.forward(out.batch, out.x, out.W, out.y)
+        return self.norm_out.forward(out.y, h, h_out, x_out, gate=gate)
+
+    def close(self):
+        self.out.batch.close()
+        self.out.layer.close()
+
+
 # ---- timing ------------------------------------------------------------------------------------
 
 def _time(torch, fn, iters=200, reps=7):
@@ -333,7 +416,52 @@ def run():
     gu.close()
     rows.append({"layer": "ffn_up_gated", "tenants": up.name, "route": "gate + up + silu_gate", "us": t_gated})
     rows.append({"layer": "ffn_up_gated", "tenants": up.name, "route": "up only", "us": t_up})
+    for context in (512, 4096):
+        rows += attention_rows(torch, context)
+        print(f"multiproj: {rows[-1]}", file=sys.stderr, flush=True)
     return rows
+
+
+def attention_rows(torch, context, n=128, heads=32, kv_heads=8, head_dim=128, page_size=16):
+    """The attention step of n requests with `context` positions each (one
+    token a step), and its operators one by one."""
+    from synth import AdapterSpec, WorkloadSpec, make_workload
+    d = heads * head_dim
+    ten = qkv_tenants(False)
+    wls, tt = projection_workloads(ten, n, d, (d, kv_heads * head_dim, kv_heads * head_dim), seed=13)
+    wl_out = make_workload(WorkloadSpec("out", "bf16", d, d, n, [AdapterSpec("lora", rank=16)] * 4, assign="explicit",
+                                        token_adapter=np.asarray(tt) % 4, seed=14))
+    fu = QKVFused(wls, tt, len(ten))
+    dev = fu.x.device
+    freq = 500000.0 ** (-torch.arange(head_dim // 2, dtype=torch.float64, device=dev) / (head_dim // 2))
+    pages = -(-(context + 1) // page_size)
+    ones = torch.ones(d, device=dev)
+    st = AttentionStep(fu, wl_out, heads, kv_heads, head_dim, n, pages, page_size, n * pages, freq, norm_in=ones,
+                       norm_out=ones, one_each=True)
+    h, new = torch.randn((n, d), device=dev), torch.ones(n, dtype=torch.int32, device=dev)
+    h_out, x_out = torch.empty_like(h), torch.empty((n, d), dtype=fu.x.dtype, device=dev)
+    # every request holds `context` positions; the timed steps bring the same next token again
+    from . import block
+    grown = block.Rows(n, n * context, dev)
+    block.assign_pages(st.rows.seq_len, new * context, st.table, st.ring, st.rows.cursor, page_size, grown)
+    keep = (grown.seq_len.clone(), grown.cursor.clone())
+
+    def step():
+        st.rows.seq_len, st.rows.cursor = keep
+        return st.forward(h, new, h_out, x_out)
+
+    parts = [("attention step", step),
+             ("norm + pages + rotary", lambda: (
+                 st.norm_in.forward(None, h, None, fu.x),
+                 block.assign_pages(*keep[:1], new, st.table, st.ring, keep[1], page_size, st._other),
+                 st.rotary.store(st.q, st.k, st.v, st.rows.pos, st.rows.slot, st.cache, st.q_rot))),
+             ("attention over the cache", lambda: st.attention.forward(st.q_rot, st.table, st.rows.len, st.a)),
+             ("residual + norm", lambda: st.norm_out.forward(st.out.y, h, h_out, x_out))]
+    got = [{"layer": "attention", "tenants": f"{n} requests, {context} positions", "route": name,
+            "us": _time(torch, fn, iters=50)} for name, fn in parts]
+    st.close()
+    fu.close()
+    return got
 
 
 def main():
