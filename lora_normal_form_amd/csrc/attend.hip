@@ -40,6 +40,7 @@ struct AttArgs {
 // work-group finds the slices from the lengths by itself (4 bytes a row), so
 // nothing is planned on the host and a captured launch follows the lengths.
 constexpr int ATT_FAN = 32;
+constexpr uint32_t ATT_EXTRA = 1;  // (128 ragged rows of up to 4096 positions: 190 us with 0, 181 with 1, 182 with 2)
 // places of partial results a work-group: two a slice, at most 1 + 143 / 64
 // slices a work-group and one more
 constexpr int ATT_PLACES = 2 * 4;
@@ -108,6 +109,12 @@ __device__ __forceinline__ AttRow att_row(const AttArgs& A, int row) {
 }
 
 __device__ __forceinline__ int lane_of(int v, int src) { return __builtin_amdgcn_readlane(v, src); }
+// a uniform value that is computed with where it stands (a divisor whose
+// reciprocal is not wanted ahead of the loop, on the way to the first loads)
+__device__ __forceinline__ uint32_t in_place(uint32_t v) {
+  asm volatile("" : "+s"(v));
+  return v;
+}
 // inclusive sum over the wave's lanes, on row shifts and row broadcasts
 __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
   v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false);
@@ -257,6 +264,10 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
 
   // Units (all below 2^31: the host cuts the rows into launches for that) and
   // where the rows' begin. Up to 64 rows: a row a lane, every wave for itself.
+  // Where (row, head)s are more than work-groups, each counts `extra` units
+  // more than it has, in front of its own, for what a piece costs beside them.
+  const uint32_t extra = (uint32_t)A.n_rows * H > gridDim.x * A.together ? ATT_EXTRA : 0;
+  const auto cost = [&](const AttRow& r) { return r.units ? (uint32_t)r.units + extra : 0u; };
   const bool few = A.n_rows <= 64;
   AttRow mine = {};
   const int per = (A.n_rows + 255) / 256, r0 = min(A.n_rows, tid * per), r1 = min(A.n_rows, r0 + per);
@@ -264,10 +275,10 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
   uint32_t U;
   if (few) {
     if (lane < A.n_rows) mine = att_row<TILE, !ONCE>(A, lane);
-    upto = wave_scan((uint32_t)mine.units);
+    upto = wave_scan(cost(mine));
     U = (uint32_t)lane_of((int)upto, 63) * H;
   } else {
-    for (int r = r0; r < r1; ++r) own += (uint32_t)att_row<TILE, !ONCE>(A, r).units;
+    for (int r = r0; r < r1; ++r) own += cost(att_row<TILE, !ONCE>(A, r));
     upto = wave_scan(own);
     if (lane == 63) s_wsum[w] = upto;
     __syncthreads();
@@ -286,9 +297,10 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
   const uint32_t fixed = U - tail, quot = tail ? fixed / workers : each, longer = fixed - quot * workers;
   const uint32_t slices = workers + (tail ? (tail + step - 1) / step : 0);
   const auto slice_of = [&](uint32_t unit) {  // the slice that holds a unit
+    if (each == 1 && longer == 0) return unit;
     const uint32_t edge = longer * (quot + 1);
-    if (unit >= fixed) return workers + (unit - fixed) / step;
-    return unit < edge ? unit / (quot + 1) : longer + (unit - edge) / quot;
+    if (unit >= fixed) return workers + (unit - fixed) / in_place(step);
+    return unit < edge ? unit / in_place(quot + 1) : longer + (unit - edge) / in_place(quot);
   };
   const auto slice_begin = [&](uint32_t i) {
     return i < workers ? i * quot + min(i, longer) : min(U, fixed + (i - workers) * step);
@@ -299,8 +311,17 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
   uint32_t slice = blockIdx.x, u_begin = 0, u = 0, u_end = 0, base = 0;
   int row = 0;
   if (slice >= slices) return;
+  bool asked = true;  // `slice` is new
   for (;;) {
     if (u == u_end) {  // the slice's units, the row they begin in and that row's first unit
+      if (!asked) {
+        if (tail && tid == 0) s_next = workers + (uint32_t)arrive(A.count + ATT_QUEUE);
+        __syncthreads();
+        slice = tail ? (uint32_t)uni((int)s_next) : slices;
+        __syncthreads();
+      }
+      asked = false;
+      if (slice >= slices) break;
       u = u_begin = slice_begin(slice);
       u_end = slice_begin(slice + 1);
       if (few) {
@@ -310,7 +331,7 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
         uint32_t pre = upto - own;
         if (pre * H <= u && u < upto * H) {
           int r = r0;
-          for (uint32_t t = att_row<TILE, !ONCE>(A, r).units; (pre + t) * H <= u; t = att_row<TILE, !ONCE>(A, r).units) {
+          for (uint32_t t = cost(att_row<TILE, !ONCE>(A, r)); (pre + t) * H <= u; t = cost(att_row<TILE, !ONCE>(A, r))) {
             pre += t;
             ++r;
           }
@@ -336,15 +357,20 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
       if (ONCE || R.units) break;
     }
     if constexpr (ONCE) R.every_lo = R.lo, R.every_n = R.n;
-    const uint32_t hh = (u - base) / (uint32_t)R.units, v0 = u - base - hh * R.units;
-    const uint32_t units = min(R.units - v0, u_end - u);
+    const uint32_t whole_cost = R.units + extra, hh = (u - base) / in_place(whole_cost), x0 = u - base - hh * whole_cost;
+    const uint32_t taken = min(whole_cost - x0, u_end - u);
+    const uint32_t v0 = max(x0, extra) - extra, units = max(x0 + taken, extra) - extra - v0;
+    if (units == 0) {  // (only what the piece counts beside its own)
+      u += taken;
+      continue;
+    }
     // the piece's tiles of the row: t0 .. t0 + cnt - 1 from the row's first
     const int t0 = 4 * (int)v0, cnt = min(4 * (int)units, (R.n + TILE - 1) / TILE - R.first - t0);
-    const int kvh = A.q_tiles == 1 ? hh : hh / A.q_tiles, h0 = kvh * A.group + (hh - kvh * A.q_tiles) * 16;
+    const int kvh = A.q_tiles == 1 ? hh : hh / in_place(A.q_tiles), h0 = kvh * A.group + (hh - kvh * A.q_tiles) * 16;
     // columns of the query tile: column c is head h0 + c % wide of row c / wide
     const bool shared = !ONCE && A.together > 1;
     const int wide = shared ? A.group : 16, nq = shared ? R.rows * A.group : min(16, (kvh + 1) * A.group - h0);
-    const int my_row = ONCE ? 0 : min(m16, nq - 1) / wide;
+    const int my_row = ONCE ? 0 : min(m16, nq - 1) / in_place(wide);
     int my_n = R.n, my_lo = R.lo;  // what this lane's column sees
     if (shared && R.rows > 1) {
       my_n = att_len(A, ldg(A.len + row + my_row), R.req);
@@ -551,7 +577,7 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
     // the next slice, asked for while the results are joined
-    const bool last_piece = u + units == u_end;
+    const bool last_piece = u + taken == u_end;
     uint32_t next = slices;
     if (last_piece && tail && tid == 0) next = workers + (uint32_t)arrive(A.count + ATT_QUEUE);
 
@@ -586,13 +612,22 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
     const uint32_t slot = 2 * slice + (u == u_begin ? 0 : 1);
     for (int e = tid; e < E; e += 256) {
       const int g = e / (D / 4), d = 4 * (e - g * (D / 4));
-      float gm = -INFINITY, L = 0.f;
-      f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
-      for (int x = 0; x < waves; ++x) gm = fmaxf(gm, s_ml[x][g][0]);
-      for (int x = 0; x < waves; ++x) {
-        const float f = gm == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(s_ml[x][g][0] - gm);
-        L += s_ml[x][g][1] * f;
-        o += *(const f32x4*)&s_o[x][g][d] * f;
+      float gm = -INFINITY, L = 0.f, wm[4], wl[4];
+      f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f}, wo[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {  // (all four waves' at once; what a wave without tiles left there is not used)
+        wm[x] = s_ml[x][g][0], wl[x] = s_ml[x][g][1];
+        wo[x] = *(const f32x4*)&s_o[x][g][d];
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        wm[x] = x < waves ? wm[x] : -INFINITY;
+        gm = fmaxf(gm, wm[x]);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float f = gm == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(wm[x] - gm);
+        if (x < waves) L += wl[x] * f, o += wo[x] * f;
       }
       if (whole) {
         put(g, d, o, L);
@@ -605,8 +640,8 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
     if (!whole) {
       // pieces of this (row, head): one in each of the slices w0 .. w1, the
       // first piece of a slice but perhaps in w0
-      const uint32_t a = u - v0, b = a + R.units - 1, w0 = slice_of(a), w1 = slice_of(b);
-      const uint32_t slot0 = 2 * w0 + (slice_begin(w0) == a ? 0 : 1);
+      const uint32_t a = u - x0, w0 = slice_of(a + extra), w1 = slice_of(a + whole_cost - 1);
+      const uint32_t slot0 = 2 * w0 + (slice_begin(w0) >= a ? 0 : 1);
       const int all = (int)(w1 - w0) + 1, fan = all > ATT_FAN ? (int)(slice - w0) / ATT_FAN * ATT_FAN : 0;
       const int sets = E < 256 ? 256 / E : 1;
       float* jo = &s_o[0][0][0];
@@ -683,12 +718,9 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
     }
     if (last_piece && tid == 0) s_next = next;
     __syncthreads();  // (the next piece reuses the LDS)
-    u += units;
-    if (u == base + (uint32_t)(R.units * H)) base = u, ++row;
-    if (last_piece) {
-      slice = (uint32_t)uni((int)s_next);
-      if (slice >= slices) break;
-    }
+    u += taken;
+    if (u == base + whole_cost * H) base = u, ++row;
+    if (last_piece) slice = (uint32_t)uni((int)s_next), asked = true;
   }
   if (tail && tid == 0 && arrive(A.count + ATT_DONE) == (int)workers - 1) {
     reset_counter(A.count + ATT_QUEUE);
@@ -787,7 +819,7 @@ extern "C" scute_status scute_paged_attention(const scute_kv_cache* C, const voi
             C->page_size, shift, (int32_t)reach, n_requests, window, scale * 1.4426950408889634f};
   // rows of one launch: their units, at the table's whole width, stay below 2^31
   const int64_t es = C->dtype == SCUTE_F32 ? 4 : 2, unit = es == 4 ? 64 : 128;
-  const int64_t most = (((int64_t)1 << 31) - 1) / ((int64_t)A.n_kv * A.q_tiles * (reach / unit + 2));
+  const int64_t most = (((int64_t)1 << 31) - 1) / ((int64_t)A.n_kv * A.q_tiles * (reach / unit + 2 + ATT_EXTRA));
   if (most < 1) return fail(SCUTE_E_SHAPE, "scute_paged_attention: too many heads for a table this wide");
   const hipStream_t s = (hipStream_t)stream;
   const bool once = !req && A.q_tiles == 1;
