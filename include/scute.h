@@ -444,9 +444,9 @@ scute_status scute_paged_attention_workspace(int32_t device, int32_t head_dim, i
  * out_stride elements apart (multiples of 8, 16-byte aligned pointers).
  * Several rows of one request (its new tokens, each with its own length) are
  * several rows of one call; those that follow each other share the reads of
- * its cache. Scores, the softmax and the sums are fp32; the weights are
- * rounded once to bf16 for a bf16 cache. The result depends on the rows'
- * requests and lengths only, never on the order in which work-groups end.
+ * its cache. Scores, the softmax and the sums are fp32; the weights enter a
+ * bf16 cache's products as sums of two bf16 values. The result depends on the
+ * rows' requests and lengths only, never on the order in which work-groups end.
  * workspace: `workspace_bytes` (at least what scute_paged_attention_workspace
  * says), 256-byte aligned, zeroed once by the caller before its first use;
  * every call leaves its counters zero. Calls that may overlap in time need

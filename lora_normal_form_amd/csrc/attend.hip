@@ -211,11 +211,20 @@ struct AttTile {
   }
   __device__ __forceinline__ void weigh(const f32x4 (&p)[G::SUB], f32x4 (&acc)[G::NG][G::VD]) {
     if constexpr (G::ES == 2) {
-      uint4 b;  // the weights, rounded once to bf16 (relative 2^-8, as the values they multiply)
+      // the weights as sums of two bf16 (one alone would add an error of the
+      // output's own rounding, 2^-8; the second products cost no time)
+      uint4 b, b2;
       b.x = pack_bf2(__float_as_uint(p[0][0]), __float_as_uint(p[0][1]));
       b.y = pack_bf2(__float_as_uint(p[0][2]), __float_as_uint(p[0][3]));
       b.z = pack_bf2(__float_as_uint(p[1][0]), __float_as_uint(p[1][1]));
       b.w = pack_bf2(__float_as_uint(p[1][2]), __float_as_uint(p[1][3]));
+      const auto rest = [](uint32_t hi, float x, float y) {
+        return pack_bf2(__float_as_uint(x - __uint_as_float(hi << 16)), __float_as_uint(y - __uint_as_float(hi & 0xFFFF0000u)));
+      };
+      b2.x = rest(b.x, p[0][0], p[0][1]);
+      b2.y = rest(b.y, p[0][2], p[0][3]);
+      b2.z = rest(b.z, p[1][0], p[1][1]);
+      b2.w = rest(b.w, p[1][2], p[1][3]);
 #pragma unroll
       for (int ng = 0; ng < G::NG; ++ng)
 #pragma unroll
@@ -226,7 +235,7 @@ struct AttTile {
           a.y = __builtin_amdgcn_perm(v[0][3][ng][i / 2], v[0][2][ng][i / 2], sel);
           a.z = __builtin_amdgcn_perm(v[1][1][ng][i / 2], v[1][0][ng][i / 2], sel);
           a.w = __builtin_amdgcn_perm(v[1][3][ng][i / 2], v[1][2][ng][i / 2], sel);
-          acc[ng][i] = mfma16(a, b, acc[ng][i]);
+          acc[ng][i] = mfma16(a, b2, mfma16(a, b, acc[ng][i]));
         }
     } else {
 #pragma unroll

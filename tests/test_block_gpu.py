@@ -270,12 +270,12 @@ def _attend_ref(q, kc, vc, table, lens, req, window, scale):
             p = torch.softmax(s, 0)
             out[i, h] = p @ V[:, g]
             # a score is off by D + 3 fp32 roundings of its terms' magnitudes (and the exponent's argument by as
-            # much as the running maximum's again), exp2 by 2 ulp, the sums by n roundings; a weight is rounded
-            # once to the cache's type, and so is the output
+            # much as the running maximum's again), exp2 by 2 ulp, the sums by n roundings; a weight is the sum of
+            # two bf16 (off by 2^-8 2^-8) for a bf16 cache, and the output is rounded once
             off = float((K[:, g].abs() @ q[i, h].abs()).max()) * abs(scale) * (D + 3) * U[F32]
             rel = 2 * 2 * off + (2 * len(t) + 16) * U[F32]
             mag = p @ V[:, g].abs()
-            tol[i, h] = (rel + (U[dt] if dt == BF16 else 0.0)) * mag + U[dt] * (out[i, h].abs() + 2 * rel * mag)
+            tol[i, h] = (rel + (U[dt] ** 2 if dt == BF16 else 0.0)) * mag + U[dt] * (out[i, h].abs() + 2 * rel * mag)
     return out, tol
 
 
