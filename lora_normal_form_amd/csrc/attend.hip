@@ -191,6 +191,7 @@ struct AttTile {
       sc[s] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < G::NC; ++c) {
+        if (!EXACT && DP > 64 && 64 * c >= row_bytes) continue;  // (uniform)
         uint4 kk = k[s][c];
         if constexpr (!EXACT)  // past the head's end: other elements, which may hold anything
           if (64 * c + 16 * gq >= row_bytes) kk = make_uint4(0, 0, 0, 0);
@@ -448,11 +449,12 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
         for (int s = 0; s < SUB; ++s)
 #pragma unroll
           for (int c = 0; c < G::NC; ++c) {
+            if (!EXACT && DP > 64 && 64 * c >= row_bytes) continue;  // (uniform)
             const uint32_t at = EXACT ? 64 * c + 16 * gq : min(64 * c + 16 * gq, row_bytes - 16);
             tile.k[s][c] = ldg_b16<ONCE>(kb + off[s], PAGE16 ? m16 * tok + at : at);
           }
       };
-      const auto load_v = [&](const int64_t (&off)[SUB]) {
+      const auto load_v = [&]() {
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
 #pragma unroll
@@ -486,19 +488,17 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
       }
       locate(0);
       load_k();
-      load_v(off);
+      load_v();
       if constexpr (!PAGE16) look_up(min(1, trips - 1));
       // (the loads of trip i + 1 run under the products of trip i; the last trip
       // stands apart, so that the waits count what is in flight)
       const auto trip = [&](int i, auto more) {
         const int t = (tb + 4 * i) * TILE;
         uint32_t gone[SUB];
-        int64_t here[SUB];
         bool cut = t < R.every_lo || t + TILE > R.every_n;
 #pragma unroll
         for (int s = 0; s < SUB; ++s) {
           gone[s] = bad[s];
-          here[s] = off[s];
           cut = cut || bad[s] != 0;
         }
         f32x4 sc[SUB];
@@ -515,13 +515,13 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
         for (int s = 0; s < SUB; ++s) sc[s] *= A.scale_log2;
         // a position that is not seen has no weight, and its value, which may be
         // anything, is cleared
-        const auto clear = [&](int lo, int n) {
+        const auto clear = [&](AttTile<T, DP, EXACT>& of, int lo, int n) {
 #pragma unroll
           for (int s = 0; s < SUB; ++s)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int at = t + 16 * s + 4 * gq + j;
-              if (at < lo || at >= n || ((gone[s] >> (4 * gq + j)) & 1)) tile.clear_v(s, j);
+              if (at < lo || at >= n || ((gone[s] >> (4 * gq + j)) & 1)) of.clear_v(s, j);
             }
         };
         if (cut) {
@@ -532,7 +532,7 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
               const int at = t + 16 * s + 4 * gq + j;
               if (at < my_lo || at >= my_n || ((gone[s] >> (4 * gq + j)) & 1)) sc[s][j] = -INFINITY;
             }
-          if (ONCE || R.rows == 1) clear(R.lo, R.n);
+          if (ONCE || R.rows == 1) clear(tile, R.lo, R.n);
         }
         float tm = sc[0][0];
 #pragma unroll
@@ -564,21 +564,21 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
           // cleared for it (what others see of it, times their weight of 0, may
           // be NaN: only the row's own columns are kept)
           for (int i = 0; i < R.rows; ++i) {
-            if (i) load_v(here);
-            clear(lane_of(my_lo, i * wide), lane_of(my_n, i * wide));
+            AttTile<T, DP, EXACT> seen = tile;
+            clear(seen, lane_of(my_lo, i * wide), lane_of(my_n, i * wide));
             f32x4 with[G::NG][G::VD];
 #pragma unroll
             for (int ng = 0; ng < G::NG; ++ng)
 #pragma unroll
               for (int e = 0; e < G::VD; ++e) with[ng][e] = acc[ng][e];
-            tile.weigh(sc, with);
+            seen.weigh(sc, with);
 #pragma unroll
             for (int ng = 0; ng < G::NG; ++ng)
 #pragma unroll
               for (int e = 0; e < G::VD; ++e) acc[ng][e] = my_row == i ? with[ng][e] : acc[ng][e];
           }
         }
-        if constexpr (more) load_v(off);
+        if constexpr (more) load_v();
       };
       for (int i = 0; i + 1 < trips; ++i) trip(i, std::true_type());
       trip(trips - 1, std::false_type());
