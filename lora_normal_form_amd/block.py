@@ -15,7 +15,8 @@ The functions check shapes, types, strides and devices (ValueError) and hand
 pointers to the library, whose own checks raise ScuteError. Every launch goes
 to ``stream``, by default torch's current stream of the tensors' device, which
 need not be the current device. Nothing is allocated or synchronised after a
-handle is made, so the calls may be captured into a graph. A decode step
+handle is made, so the calls may be captured into a graph; the caller keeps the
+tensors until the stream has run them. A decode step
 (``multiproj.AttentionStep`` is one)::
 
     rows = assign_pages(seq_len, new_len, table, ring, cursor, 16, rows)

@@ -24,15 +24,21 @@ struct AttArgs {
   float scale_log2;  // scale log2(e): the softmax runs on powers of two
 };
 
+// out[h] = sum_t softmax_t(scale q[h] . K[t]) V[t] with a running maximum and
+// sum: one pass over K and V, bound by their bytes (64 rows of 16384 positions,
+// 32 query and 8 key heads of 128 elements: 652 us, 6.6 TB/s; a plain streaming
+// read of as much reaches 6.4 TB/s, with non-temporal loads 7.1).
+//
 // How the work is cut. A unit is four tiles of positions, one for each wave (a
 // tile: 32 of bf16, 16 of fp32), of one row, key head and tile of 16 query
-// heads (or up to four rows of one request); units are numbered row by row,
-// key head by key head, and cut into
-// slices of consecutive units, whatever rows and heads they cross: one slice a
-// work-group, all alike, and where each has 64 units or more a tail of short
-// slices (1/16 of the units, 1/8 from 128 on) that the work-groups take from a
-// counter as they get done: work-groups with equal work differ by a quarter in
-// time, by their die and its distance to the memory.
+// heads (or up to four rows of one request). Units are numbered row by row, key
+// head by key head, and cut into slices of consecutive units, whatever rows and
+// heads they cross: one slice a work-group, all alike, and where each has 64
+// units or more a tail of short slices (1/16 of the units, 1/8 from 128 on) that
+// the work-groups take from a counter as they get done: work-groups with equal
+// work differ by a quarter in time, by their die and its distance to the memory
+// (8 rows of 131072 positions: 758 us without the tail, 701 with; 2 of 100003,
+// which have none: 145 with it, 135 without).
 // A slice's part of one (row, head) is a piece. A piece that holds all of its
 // (row, head) writes the output; the others write partial results, and the
 // last of them to arrive adds them in the pieces' order (32 at a time where
@@ -48,6 +54,7 @@ constexpr int ATT_PLACES = 2 * 4;
 // ATT_ARRIVALS on the arrivals at each partial result's place, for groups of
 // pieces and for all of them
 constexpr int ATT_QUEUE = 0, ATT_DONE = 32, ATT_ARRIVALS = 64;
+
 // Rows of one request that follow each other share its K and V: up to four of
 // them (`together`, as many as fit the 16 columns of a query tile with all
 // heads of a key head) are one row of the numbering, their first; the others
@@ -253,9 +260,9 @@ struct AttTile {
 // PAGE16: pages hold multiples of 16 positions, so the 16 of a block lie in
 // one page and their place is one scalar; else every position is looked up.
 // EXACT: the head dimension is DP. ONCE: no two rows or query tiles read the
-// same positions, so K and V are loaded past the caches (64 rows of 16384
-// positions: 5.9 TB/s without, 6.4 with; rows that share positions lose: four
-// drafted tokens a request 48 us with it, 39 without).
+// same positions, so K and V are loaded past the caches (2 rows of 100003
+// positions: 157 us without, 141 with; rows that share positions lose: four
+// drafted tokens a request 39 us without, 48 with).
 // One work-group a compute unit: four waves with a tile of K and V each in
 // flight (64 KB at 128 elements) already fill the memory's queues, and fewer
 // streams at once run faster than more (64 rows of 16384 positions: 674 us
@@ -801,14 +808,15 @@ extern "C" scute_status scute_paged_attention(const scute_kv_cache* C, const voi
     return fail(SCUTE_E_SHAPE, "scute_paged_attention: q_stride and out_stride must be multiples of 8 in [0, 2^40]");
   if (n_rows > 1 && out_stride < wide) return fail(SCUTE_E_SHAPE, "scute_paged_attention: rows of out overlap");
   if (n_rows == 0) return SCUTE_OK;
-  if (!q || !table || !len || !out || !workspace) return fail(SCUTE_E_INVALID, "scute_paged_attention: null pointer");
+  if (!q || (!table && n_requests) || !len || !out || !workspace)
+    return fail(SCUTE_E_INVALID, "scute_paged_attention: null pointer");
   if (((uintptr_t)q | (uintptr_t)out) & 15)
     return fail(SCUTE_E_INVALID, "scute_paged_attention: q and out must be 16-byte aligned");
   if (((uintptr_t)table | (uintptr_t)len | (uintptr_t)req) & 3)
     return fail(SCUTE_E_INVALID, "scute_paged_attention: misaligned pointer");
   if ((uintptr_t)workspace & 255) return fail(SCUTE_E_INVALID, "scute_paged_attention: workspace must be 256-byte aligned");
   if (q == out) return fail(SCUTE_E_INVALID, "scute_paged_attention: out is also q");
-  DeviceGuard g(C->device);
+  OnDevice g(C->device);
   if (!g.ok()) return hip_fail(g.err, fn);
   int64_t need = 0;
   if ((st = scute_paged_attention_workspace(C->device, C->head_dim, &need)) != SCUTE_OK) return st;
@@ -832,9 +840,7 @@ extern "C" scute_status scute_paged_attention(const scute_kv_cache* C, const voi
   if (most < 1) return fail(SCUTE_E_SHAPE, "scute_paged_attention: too many heads for a table this wide");
   const hipStream_t s = (hipStream_t)stream;
   const bool once = !req && A.q_tiles == 1;
-#define ATT(T, DP)                                              \
-  (once ? att_launch<T, DP, true>(A, units, s) \
-        : att_launch<T, DP, false>(A, units, s))
+#define ATT(T, DP) (once ? att_launch<T, DP, true>(A, units, s) : att_launch<T, DP, false>(A, units, s))
   for (int64_t r = 0; r < n_rows; r += most) {
     A.row0 = (int32_t)r;
     A.n_rows = (int32_t)std::min<int64_t>(most, n_rows - r);

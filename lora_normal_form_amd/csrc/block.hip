@@ -623,6 +623,7 @@ scute_status launched(const char* fn) {
 extern "C" scute_status scute_cache_assign(const scute_cache_assign_args* A, void* stream) {
   const char* fn = "scute_cache_assign";
   if (!A) return fail(SCUTE_E_INVALID, "scute_cache_assign: args is null");
+  if (A->device < 0) return fail(SCUTE_E_INVALID, "scute_cache_assign: device must be >= 0");
   if (A->n_requests < 0 || A->n_requests > 65536)
     return fail(SCUTE_E_SHAPE, "scute_cache_assign: n_requests must be in [0, 65536]");
   if (A->page_size < 1 || A->page_size > 65536)
@@ -649,7 +650,7 @@ extern "C" scute_status scute_cache_assign(const scute_cache_assign_args* A, voi
   if (A->cursor == A->cursor_out || (some && (A->seq_len == A->old_len || A->seq_len == A->new_len ||
                                               A->cu_len == A->old_len || A->cu_len == A->new_len)))
     return fail(SCUTE_E_INVALID, "scute_cache_assign: an output is also an input");
-  DeviceGuard g(A->device);
+  OnDevice g(A->device);
   if (!g.ok()) return hip_fail(g.err, fn);
   AsgArgs G{*A, 0, 0};
   while ((1 << G.shift) < A->page_size) ++G.shift;
@@ -719,7 +720,7 @@ extern "C" scute_status scute_rotary_store(const scute_rotary* Ro, const scute_k
   if (misaligned(q, es) || misaligned(k, es) || misaligned(v, es) || misaligned(q_out, ed) || misaligned(pos, 4) ||
       misaligned(slot, 8) || misaligned(Ro->freq, 8) || misaligned(Ro->axis, 4))
     return fail(SCUTE_E_INVALID, "scute_rotary_store: misaligned pointer");
-  DeviceGuard g(C->device);
+  OnDevice g(C->device);
   if (!g.ok()) return hip_fail(g.err, fn);
 
   const int n = Ro->rot_dim / 2;
@@ -793,7 +794,7 @@ extern "C" scute_status scute_residual_norm(const scute_norm* N, const void* y, 
     if (misaligned(p, 4)) return fail(SCUTE_E_INVALID, "scute_residual_norm: misaligned pointer");
     vec = vec && !misaligned(p, 16);
   }
-  DeviceGuard g(N->device);
+  OnDevice g(N->device);
   if (!g.ok()) return hip_fail(g.err, fn);
 
   const NormArgs A{y, h, gate, h_out, x, N->post_w, N->post_b, N->pre_w, N->pre_b, y_stride, h_stride, gate_stride,

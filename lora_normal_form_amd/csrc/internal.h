@@ -390,25 +390,6 @@ scute_status hip_fail(hipError_t e, const char* what);
 
 size_t dtype_size(int32_t dt);
 
-// Runs with `dev` current and restores the caller's device afterwards. A
-// negative device leaves the current one; ok() is false if `dev` cannot be
-// made current.
-struct DeviceGuard {
-  int prev = -1;
-  bool active = false;
-  hipError_t err = hipSuccess;
-  explicit DeviceGuard(int dev) {
-    if (dev < 0 || (err = hipGetDevice(&prev)) != hipSuccess) return;
-    if (prev == dev) return;
-    err = hipSetDevice(dev);
-    active = err == hipSuccess;
-  }
-  ~DeviceGuard() {
-    if (active) (void)hipSetDevice(prev);
-  }
-  bool ok() const { return err == hipSuccess; }
-};
-
 // no-allocation forward (forward.hip): takes the device address of its
 // static scratch on `device` (current), once per device
 scute_status noalloc_setup(int32_t device);

@@ -173,6 +173,24 @@ static void dora_scale(const void* W, int32_t dt, int64_t d_in, int64_t d_out, i
   });
 }
 
+// ---------------------------------------------------------------------------
+// device guard: run with the layer's device current, restore afterwards
+// ---------------------------------------------------------------------------
+
+struct DeviceGuard {
+  int prev = -1;
+  bool active = false;
+  explicit DeviceGuard(int dev) {
+    if (dev >= 0 && hipGetDevice(&prev) == hipSuccess) {
+      active = true;
+      if (prev != dev) (void)hipSetDevice(dev);
+    }
+  }
+  ~DeviceGuard() {
+    if (active) (void)hipSetDevice(prev);
+  }
+};
+
 }  // namespace scute
 
 using namespace scute;

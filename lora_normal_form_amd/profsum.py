@@ -28,12 +28,15 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 
 
 def kernel_sources():
-    """Every source under csrc/ (kernels and the planners that set their
-    tile order, split factors and launch shapes), sorted."""
+    """Every source of the layer under csrc/ (kernels and the planners that set
+    their tile order, split factors and launch shapes), sorted."""
     d = os.path.join(PKG, "csrc")
     return sorted("csrc/" + f for f in os.listdir(d)
-                  if f.endswith((".hip", ".h", ".cpp")))
+                  if f.endswith((".hip", ".h", ".cpp")) and f not in NOT_THE_LAYER)
 
+
+# the operators between the layers, which the layer's kernels do not use
+NOT_THE_LAYER = ("block.hip", "block.h", "attend.hip")
 
 COPY_KERNEL = "__amd_rocclr_copyBuffer"
 

@@ -50,6 +50,7 @@ def _assign(**kw):
 
 
 @pytest.mark.parametrize("kw, code", [
+    (dict(device=-1), scute.E_INVALID),
     (dict(n_requests=-1), scute.E_SHAPE), (dict(n_requests=65537), scute.E_SHAPE),
     (dict(page_size=0), scute.E_SHAPE), (dict(page_size=65537), scute.E_SHAPE),
     (dict(table_width=0), scute.E_SHAPE), (dict(table_stride=7), scute.E_SHAPE),
