@@ -39,6 +39,7 @@ struct AttArgs {
 // work differ by a quarter in time, by their die and its distance to the memory
 // (8 rows of 131072 positions: 758 us without the tail, 701 with; 2 of 100003,
 // which have none: 145 with it, 135 without).
+// Few rows whose heads come out even are cut along them instead (below).
 // A slice's part of one (row, head) is a piece. A piece that holds all of its
 // (row, head) writes the output; the others write partial results, and the
 // last of them to arrive adds them in the pieces' order (32 at a time where
@@ -307,14 +308,30 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
     }
     U = (uint32_t)uni((int)U) * H;
   }
+  const uint32_t workers = min(U, gridDim.x), each = U / workers;
+  // Even pieces: no slice crosses from one (row, head) to the next, each of them
+  // cut into parts of at most `most` units, one a work-group. Taken where that
+  // costs at most one unit more than equal ranges: it saves the second piece of
+  // the ranges that cross (16 requests of four drafted rows, up to 3000
+  // positions: 36 us with ranges, 26 with parts; 2 rows of 100003: 133, 130;
+  // with up to four units more 8 ragged rows of up to 16000 lose: 64, 67).
+  bool even = false;
+  uint32_t parts = 0, parts_upto = 0, even_slices = 0;  // parts of this lane's row, and up to it
+  if (few && extra == 0 && each < 64) {
+    uint32_t most = (U + gridDim.x - 1) / gridDim.x;
+    for (int i = 0; i < 2 && !even; ++i, ++most) {
+      parts = ((uint32_t)mine.units + most - 1) / in_place(most);
+      parts_upto = wave_scan(parts);
+      even_slices = (uint32_t)lane_of((int)parts_upto, 63) * H;
+      even = even_slices <= gridDim.x;
+    }
+  }
   // slices: `workers` of quot or quot + 1 units (the first `longer`), then from
   // unit `fixed` on of `step` units each
-  const uint32_t workers = min(U, gridDim.x), each = U / workers;
   const uint32_t tail = each >= 128 ? U / 8 : each >= 64 ? U / 16 : 0, step = max(4u, each / 16);
   const uint32_t fixed = U - tail, quot = tail ? fixed / workers : each, longer = fixed - quot * workers;
-  const uint32_t slices = workers + (tail ? (tail + step - 1) / step : 0);
+  const uint32_t slices = even ? even_slices : workers + (tail ? (tail + step - 1) / step : 0);
   const auto slice_of = [&](uint32_t unit) {  // the slice that holds a unit
-    if (each == 1 && longer == 0) return unit;
     const uint32_t edge = longer * (quot + 1);
     if (unit >= fixed) return workers + (unit - fixed) / in_place(step);
     return unit < edge ? unit / in_place(quot + 1) : longer + (unit - edge) / in_place(quot);
@@ -330,7 +347,9 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
   if (slice >= slices) return;
   bool asked = true;  // `slice` is new
   for (;;) {
-    if (u == u_end) {  // the slice's units, the row they begin in and that row's first unit
+    if (even) {
+      row = (int)__popcll(__ballot(parts_upto * H <= slice));
+    } else if (u == u_end) {  // the slice's units, the row they begin in and that row's first unit
       if (!asked) {
         if (tail && tid == 0) s_next = workers + (uint32_t)arrive(A.count + ATT_QUEUE);
         __syncthreads();
@@ -374,12 +393,31 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
       if (ONCE || R.units) break;
     }
     if constexpr (ONCE) R.every_lo = R.lo, R.every_n = R.n;
-    const uint32_t whole_cost = R.units + extra, hh = (u - base) / in_place(whole_cost), x0 = u - base - hh * whole_cost;
-    const uint32_t taken = min(whole_cost - x0, u_end - u);
-    const uint32_t v0 = max(x0, extra) - extra, units = max(x0 + taken, extra) - extra - v0;
-    if (units == 0) {  // (only what the piece counts beside its own)
-      u += taken;
-      continue;
+    // head and units of the piece, and (all) the pieces of its (row, head): one in
+    // each of the slices w0 on, in the slice's first place but perhaps in w0
+    uint32_t hh, v0, units, taken = 0, w0 = 0, all = 0, slot0 = 0;
+    const uint32_t whole_cost = R.units + extra;
+    if (even) {
+      const uint32_t n = (uint32_t)lane_of((int)parts, row);
+      const uint32_t x = slice - (row ? (uint32_t)lane_of((int)parts_upto, row - 1) * H : 0);
+      hh = x / in_place(n);
+      const uint32_t j = x - hh * n;
+      v0 = j * R.units / in_place(n), units = (j + 1) * R.units / in_place(n) - v0;
+      w0 = slice - j, all = n, slot0 = 2 * w0;
+    } else {
+      hh = (u - base) / in_place(whole_cost);
+      const uint32_t x0 = u - base - hh * whole_cost;
+      taken = min(whole_cost - x0, u_end - u);
+      v0 = max(x0, extra) - extra, units = max(x0 + taken, extra) - extra - v0;
+      if (units == 0) {  // (only what the piece counts beside its own)
+        u += taken;
+        continue;
+      }
+      if (units != (uint32_t)R.units) {
+        const uint32_t a = u - x0;
+        w0 = slice_of(a + extra), all = slice_of(a + whole_cost - 1) - w0 + 1;
+        slot0 = 2 * w0 + (slice_begin(w0) >= a ? 0 : 1);
+      }
     }
     // the piece's tiles of the row: t0 .. t0 + cnt - 1 from the row's first
     const int t0 = 4 * (int)v0, cnt = min(4 * (int)units, (R.n + TILE - 1) / TILE - R.first - t0);
@@ -593,7 +631,7 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
     // the next slice, asked for while the results are joined
-    const bool last_piece = u + taken == u_end;
+    const bool last_piece = !even && u + taken == u_end;
     uint32_t next = slices;
     if (last_piece && tail && tid == 0) next = workers + (uint32_t)arrive(A.count + ATT_QUEUE);
 
@@ -625,7 +663,7 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
                                                        pack_bf2(__float_as_uint(x.z), __float_as_uint(x.w))};
       }
     };
-    const uint32_t slot = 2 * slice + (u == u_begin ? 0 : 1);
+    const uint32_t slot = 2 * slice + (even || u == u_begin ? 0 : 1);
     for (int e = tid; e < E; e += 256) {
       const int g = e / (D / 4), d = 4 * (e - g * (D / 4));
       float gm = -INFINITY, L = 0.f, wm[4], wl[4];
@@ -654,18 +692,14 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
       }
     }
     if (!whole) {
-      // pieces of this (row, head): one in each of the slices w0 .. w1, the
-      // first piece of a slice but perhaps in w0
-      const uint32_t a = u - x0, w0 = slice_of(a + extra), w1 = slice_of(a + whole_cost - 1);
-      const uint32_t slot0 = 2 * w0 + (slice_begin(w0) >= a ? 0 : 1);
-      const int all = (int)(w1 - w0) + 1, fan = all > ATT_FAN ? (int)(slice - w0) / ATT_FAN * ATT_FAN : 0;
+      const int n_pieces = (int)all, fan = n_pieces > ATT_FAN ? (int)(slice - w0) / ATT_FAN * ATT_FAN : 0;
       const int sets = E < 256 ? 256 / E : 1;
       float* jo = &s_o[0][0][0];
       // level 0: the pieces fan .. of one group (only where they are many);
       // level 1: the groups' results, or the pieces
-      for (int level = all > ATT_FAN ? 0 : 1; level < 2; ++level) {
-        const int from = level == 0 ? fan : 0, stride = level == 1 && all > ATT_FAN ? ATT_FAN : 1;
-        const int np = level == 0 ? min(ATT_FAN, all - fan) : (all + stride - 1) / stride;
+      for (int level = n_pieces > ATT_FAN ? 0 : 1; level < 2; ++level) {
+        const int from = level == 0 ? fan : 0, stride = level == 1 && n_pieces > ATT_FAN ? ATT_FAN : 1;
+        const int np = level == 0 ? min(ATT_FAN, n_pieces - fan) : (n_pieces + stride - 1) / stride;
         const uint32_t first = from == 0 ? slot0 : 2 * (w0 + from);
         int32_t* count = A.count + ATT_ARRIVALS + (level ? ATT_PLACES * gridDim.x : 0) + first;
         wait_vm_all();
@@ -732,6 +766,7 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
         }
       }
     }
+    if (even) break;
     if (last_piece && tid == 0) s_next = next;
     __syncthreads();  // (the next piece reuses the LDS)
     u += taken;
