@@ -321,6 +321,8 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
     uint32_t most = (U + gridDim.x - 1) / gridDim.x;
     for (int i = 0; i < 2 && !even; ++i, ++most) {
       parts = ((uint32_t)mine.units + most - 1) / in_place(most);
+      // (two units stay whole: joining parts costs 1.4 us, a second trip 1 us)
+      if (mine.units == 2) parts = 1;
       parts_upto = wave_scan(parts);
       even_slices = (uint32_t)lane_of((int)parts_upto, 63) * H;
       even = even_slices <= gridDim.x;
