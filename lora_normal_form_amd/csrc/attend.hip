@@ -31,9 +31,9 @@ struct AttArgs {
 //
 // How the work is cut. A unit is four tiles of positions, one for each wave (a
 // tile: 32 of bf16, 16 of fp32), of one row, key head and tile of 16 query
-// heads (or up to four rows of one request). Units are numbered row by row, key
-// head by key head, and cut into slices of consecutive units, whatever rows and
-// heads they cross: one slice a work-group, all alike, and where each has 64
+// heads (32 where a key head has more than 16; or up to four rows of one
+// request). Units are numbered row by row, key head by key head, and cut into
+// slices of consecutive units, whatever rows and heads they cross: one slice a work-group, all alike, and where each has 64
 // units or more a tail of short slices (1/16 of the units, 1/8 from 128 on) that
 // the work-groups take from a counter as they get done: work-groups with equal
 // work differ by a quarter in time, by their die and its distance to the memory
@@ -42,15 +42,15 @@ struct AttArgs {
 // Few rows whose heads come out even are cut along them instead (below).
 // A slice's part of one (row, head) is a piece. A piece that holds all of its
 // (row, head) writes the output; the others write partial results, and the
-// last of them to arrive adds them in the pieces' order (32 at a time where
-// they are more), so the result does not depend on who took which slice. Every
+// last of them to arrive adds them in the pieces' order (where they are many the
+// last of a group of 8 or more the group's first, then the last of all the
+// groups'), so the result does not depend on who took which slice. Every
 // work-group finds the slices from the lengths by itself (4 bytes a row), so
 // nothing is planned on the host and a captured launch follows the lengths.
-constexpr int ATT_FAN = 32;
 constexpr uint32_t ATT_EXTRA = 1;  // (128 ragged rows of up to 4096 positions: 190 us with 0, 181 with 1, 182 with 2)
 // places of partial results a work-group: two a slice, at most 1 + 143 / 64
 // slices a work-group and one more
-constexpr int ATT_PLACES = 2 * 4;
+constexpr int ATT_PLACES = 2 * 4, ATT_COLS = 32;  // (each of up to 32 columns)
 // counters of the workspace: slices taken, work-groups done, and from
 // ATT_ARRIVALS on the arrivals at each partial result's place, for groups of
 // pieces and for all of them
@@ -193,21 +193,26 @@ struct AttTile {
 #pragma unroll
     for (int e = 0; e < G::VB / 4; ++e) v[s][j][ng][e] = x[e];
   }
-  __device__ __forceinline__ void scores(const uint4 (&q)[G::NC], f32x4 (&sc)[G::SUB], int gq, int row_bytes) {
+  template <int QT>
+  __device__ __forceinline__ void scores(const uint4 (&q)[QT][G::NC], f32x4 (&sc)[QT][G::SUB], int gq, int row_bytes) {
 #pragma unroll
     for (int s = 0; s < G::SUB; ++s) {
-      sc[s] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int y = 0; y < QT; ++y) sc[y][s] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < G::NC; ++c) {
         if (!EXACT && DP > 64 && 64 * c >= row_bytes) continue;  // (uniform)
         uint4 kk = k[s][c];
         if constexpr (!EXACT)  // past the head's end: other elements, which may hold anything
           if (64 * c + 16 * gq >= row_bytes) kk = make_uint4(0, 0, 0, 0);
-        if constexpr (G::ES == 2) {
-          sc[s] = mfma16(kk, q[c], sc[s]);
-        } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[s] = mfma4(dword(kk, e), dword(q[c], e), sc[s]);
+        for (int y = 0; y < QT; ++y) {
+          if constexpr (G::ES == 2) {
+            sc[y][s] = mfma16(kk, q[y][c], sc[y][s]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[y][s] = mfma4(dword(kk, e), dword(q[y][c], e), sc[y][s]);
+          }
         }
       }
     }
@@ -218,22 +223,26 @@ struct AttTile {
 #pragma unroll
       for (int e = 0; e < G::VB / 4; ++e) v[s][j][ng][e] = 0;
   }
-  __device__ __forceinline__ void weigh(const f32x4 (&p)[G::SUB], f32x4 (&acc)[G::NG][G::VD]) {
+  template <int QT>
+  __device__ __forceinline__ void weigh(const f32x4 (&p)[QT][G::SUB], f32x4 (&acc)[QT][G::NG][G::VD]) {
     if constexpr (G::ES == 2) {
       // the weights as sums of two bf16 (one alone would add an error of the
       // output's own rounding, 2^-8; the second products cost no time)
-      uint4 b, b2;
-      b.x = pack_bf2(__float_as_uint(p[0][0]), __float_as_uint(p[0][1]));
-      b.y = pack_bf2(__float_as_uint(p[0][2]), __float_as_uint(p[0][3]));
-      b.z = pack_bf2(__float_as_uint(p[1][0]), __float_as_uint(p[1][1]));
-      b.w = pack_bf2(__float_as_uint(p[1][2]), __float_as_uint(p[1][3]));
+      uint4 b[QT], b2[QT];
       const auto rest = [](uint32_t hi, float x, float y) {
         return pack_bf2(__float_as_uint(x - __uint_as_float(hi << 16)), __float_as_uint(y - __uint_as_float(hi & 0xFFFF0000u)));
       };
-      b2.x = rest(b.x, p[0][0], p[0][1]);
-      b2.y = rest(b.y, p[0][2], p[0][3]);
-      b2.z = rest(b.z, p[1][0], p[1][1]);
-      b2.w = rest(b.w, p[1][2], p[1][3]);
+#pragma unroll
+      for (int y = 0; y < QT; ++y) {
+        b[y].x = pack_bf2(__float_as_uint(p[y][0][0]), __float_as_uint(p[y][0][1]));
+        b[y].y = pack_bf2(__float_as_uint(p[y][0][2]), __float_as_uint(p[y][0][3]));
+        b[y].z = pack_bf2(__float_as_uint(p[y][1][0]), __float_as_uint(p[y][1][1]));
+        b[y].w = pack_bf2(__float_as_uint(p[y][1][2]), __float_as_uint(p[y][1][3]));
+        b2[y].x = rest(b[y].x, p[y][0][0], p[y][0][1]);
+        b2[y].y = rest(b[y].y, p[y][0][2], p[y][0][3]);
+        b2[y].z = rest(b[y].z, p[y][1][0], p[y][1][1]);
+        b2[y].w = rest(b[y].w, p[y][1][2], p[y][1][3]);
+      }
 #pragma unroll
       for (int ng = 0; ng < G::NG; ++ng)
 #pragma unroll
@@ -244,7 +253,8 @@ struct AttTile {
           a.y = __builtin_amdgcn_perm(v[0][3][ng][i / 2], v[0][2][ng][i / 2], sel);
           a.z = __builtin_amdgcn_perm(v[1][1][ng][i / 2], v[1][0][ng][i / 2], sel);
           a.w = __builtin_amdgcn_perm(v[1][3][ng][i / 2], v[1][2][ng][i / 2], sel);
-          acc[ng][i] = mfma16(a, b2, mfma16(a, b, acc[ng][i]));
+#pragma unroll
+          for (int y = 0; y < QT; ++y) acc[y][ng][i] = mfma16(a, b2[y], mfma16(a, b[y], acc[y][ng][i]));
         }
     } else {
 #pragma unroll
@@ -253,27 +263,34 @@ struct AttTile {
         for (int i = 0; i < G::VD; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            acc[ng][i] = mfma4(v[0][j][ng][i], __float_as_uint(p[0][j]), acc[ng][i]);
+#pragma unroll
+            for (int y = 0; y < QT; ++y)
+              acc[y][ng][i] = mfma4(v[0][j][ng][i], __float_as_uint(p[y][0][j]), acc[y][ng][i]);
     }
   }
 };
 
 // PAGE16: pages hold multiples of 16 positions, so the 16 of a block lie in
 // one page and their place is one scalar; else every position is looked up.
-// EXACT: the head dimension is DP. ONCE: no two rows or query tiles read the
-// same positions, so K and V are loaded past the caches (2 rows of 100003
-// positions: 157 us without, 141 with; rows that share positions lose: four
-// drafted tokens a request 39 us without, 48 with).
+// EXACT: the head dimension is DP. MODE:
+//   ATT_ONCE    no two rows or query tiles read the same positions, so K and V
+//               are loaded past the caches (2 rows of 100003 positions: 157 us
+//               without, 141 with; rows that share positions lose: four drafted
+//               tokens a request 39 us without, 48 with)
+//   ATT_SHARED  rows of one request that follow each other are one query tile
+//   ATT_WIDE    two query tiles at once, for more than 16 query heads a key head
+enum : int { ATT_ONCE = 0, ATT_SHARED = 1, ATT_WIDE = 2 };
 // One work-group a compute unit: four waves with a tile of K and V each in
 // flight (64 KB at 128 elements) already fill the memory's queues, and fewer
 // streams at once run faster than more (64 rows of 16384 positions: 674 us
 // with one, 712 with two).
-template <typename T, int DP, bool PAGE16, bool EXACT, bool ONCE>
+template <typename T, int DP, bool PAGE16, bool EXACT, int MODE>
 __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
   using G = AttGeo<T, DP>;
-  constexpr int TILE = G::TILE, SUB = G::SUB, OS = DP + 4;
-  __shared__ float s_ml[4][16][2];
-  __shared__ __align__(16) float s_o[4][16][OS];
+  constexpr int TILE = G::TILE, SUB = G::SUB, OS = DP + 4, QT = MODE == ATT_WIDE ? 2 : 1, COLS = 16 * QT;
+  constexpr bool ONCE = MODE == ATT_ONCE, SHARED = MODE == ATT_SHARED;
+  __shared__ float s_ml[4][COLS][2];
+  __shared__ __align__(16) float s_o[4][COLS][OS];
   __shared__ uint32_t s_wsum[4], s_before;
   __shared__ uint32_t s_next;
   __shared__ int s_row, s_last;
@@ -292,11 +309,11 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
   uint32_t own = 0, upto;  // units of one head: of this lane's rows, and up to them
   uint32_t U;
   if (few) {
-    if (lane < A.n_rows) mine = att_row<TILE, !ONCE>(A, lane);
+    if (lane < A.n_rows) mine = att_row<TILE, SHARED>(A, lane);
     upto = wave_scan(cost(mine));
     U = (uint32_t)lane_of((int)upto, 63) * H;
   } else {
-    for (int r = r0; r < r1; ++r) own += cost(att_row<TILE, !ONCE>(A, r));
+    for (int r = r0; r < r1; ++r) own += cost(att_row<TILE, SHARED>(A, r));
     upto = wave_scan(own);
     if (lane == 63) s_wsum[w] = upto;
     __syncthreads();
@@ -342,7 +359,7 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
     return i < workers ? i * quot + min(i, longer) : min(U, fixed + (i - workers) * step);
   };
   const rsrc_t part = make_rsrc(A.part, A.part_bytes);
-  constexpr uint32_t SLOT = 16 * (DP + 4) * 4;  // bytes of a partial result: 16 x (DP values, m, l, a group's m, l)
+  constexpr uint32_t SLOT = COLS * (DP + 4) * 4;  // bytes of a partial result: COLS x (DP values, m, l, a group's m, l)
 
   uint32_t slice = blockIdx.x, u_begin = 0, u = 0, u_end = 0, base = 0;
   int row = 0;
@@ -369,7 +386,7 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
         uint32_t pre = upto - own;
         if (pre * H <= u && u < upto * H) {
           int r = r0;
-          for (uint32_t t = cost(att_row<TILE, !ONCE>(A, r)); (pre + t) * H <= u; t = cost(att_row<TILE, !ONCE>(A, r))) {
+          for (uint32_t t = cost(att_row<TILE, SHARED>(A, r)); (pre + t) * H <= u; t = cost(att_row<TILE, SHARED>(A, r))) {
             pre += t;
             ++r;
           }
@@ -386,15 +403,15 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
       if (few) {
         R = {lane_of(mine.n, row), lane_of(mine.lo, row), lane_of(mine.first, row), lane_of(mine.units, row),
              lane_of(mine.req, row), 1, 0, 0};
-        if constexpr (!ONCE)
+        if constexpr (SHARED)
           R.rows = lane_of(mine.rows, row), R.every_lo = lane_of(mine.every_lo, row), R.every_n = lane_of(mine.every_n, row);
       } else {
-        R = att_row<TILE, !ONCE>(A, row);
+        R = att_row<TILE, SHARED>(A, row);
         R = {uni(R.n), uni(R.lo), uni(R.first), uni(R.units), uni(R.req), uni(R.rows), uni(R.every_lo), uni(R.every_n)};
       }
-      if (ONCE || R.units) break;
+      if (!SHARED || R.units) break;
     }
-    if constexpr (ONCE) R.every_lo = R.lo, R.every_n = R.n;
+    if constexpr (!SHARED) R.every_lo = R.lo, R.every_n = R.n;
     // head and units of the piece, and (all) the pieces of its (row, head): one in
     // each of the slices w0 on, in the slice's first place but perhaps in w0
     uint32_t hh, v0, units, taken = 0, w0 = 0, all = 0, slot0 = 0;
@@ -423,11 +440,11 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
     }
     // the piece's tiles of the row: t0 .. t0 + cnt - 1 from the row's first
     const int t0 = 4 * (int)v0, cnt = min(4 * (int)units, (R.n + TILE - 1) / TILE - R.first - t0);
-    const int kvh = A.q_tiles == 1 ? hh : hh / in_place(A.q_tiles), h0 = kvh * A.group + (hh - kvh * A.q_tiles) * 16;
+    const int kvh = A.q_tiles == 1 ? hh : hh / in_place(A.q_tiles), h0 = kvh * A.group + (hh - kvh * A.q_tiles) * COLS;
     // columns of the query tile: column c is head h0 + c % wide of row c / wide
-    const bool shared = !ONCE && A.together > 1;
-    const int wide = shared ? A.group : 16, nq = shared ? R.rows * A.group : min(16, (kvh + 1) * A.group - h0);
-    const int my_row = ONCE ? 0 : min(m16, nq - 1) / in_place(wide);
+    const bool shared = SHARED && A.together > 1;
+    const int wide = shared ? A.group : COLS, nq = shared ? R.rows * A.group : min(COLS, (kvh + 1) * A.group - h0);
+    const int my_row = !SHARED ? 0 : min(m16, nq - 1) / in_place(wide);
     int my_n = R.n, my_lo = R.lo;  // what this lane's column sees
     if (shared && R.rows > 1) {
       my_n = att_len(A, ldg(A.len + row + my_row), R.req);
@@ -435,12 +452,16 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
     }
 
     // ---- the wave's tiles t0 + w, t0 + w + 4, ... ----
-    float mx = -INFINITY, l = 0.f;
-    f32x4 acc[G::NG][G::VD];
+    float mx[QT], l[QT];
+    f32x4 acc[QT][G::NG][G::VD];
 #pragma unroll
-    for (int ng = 0; ng < G::NG; ++ng)
+    for (int y = 0; y < QT; ++y) {
+      mx[y] = -INFINITY, l[y] = 0.f;
 #pragma unroll
-      for (int i = 0; i < G::VD; ++i) acc[ng][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int ng = 0; ng < G::NG; ++ng)
+#pragma unroll
+        for (int i = 0; i < G::VD; ++i) acc[y][ng][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
     if (w < cnt) {  // (an empty row has none)
       const char *kb = (const char*)A.k, *vb = (const char*)A.v;
       const int32_t* tab = A.table + (int64_t)R.req * A.table_stride;
@@ -523,14 +544,16 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
       };
 
       look_up(0);
-      uint4 q[G::NC];
-      {
-        const char* qp = (const char*)A.q + ((int64_t)(row + my_row) * A.q_stride + (int64_t)(h0 + min(m16, nq - 1) - my_row * wide) * D) * G::ES;
+      uint4 q[QT][G::NC];
+#pragma unroll
+      for (int y = 0; y < QT; ++y) {
+        const int col = 16 * y + m16;
+        const char* qp = (const char*)A.q + ((int64_t)(row + my_row) * A.q_stride + (int64_t)(h0 + min(col, nq - 1) - my_row * wide) * D) * G::ES;
 #pragma unroll
         for (int c = 0; c < G::NC; ++c) {
-          const bool in = m16 < nq && (EXACT || 64 * c + 16 * gq < row_bytes);
-          q[c] = ldg_b16<false>(qp, EXACT ? 64 * c + 16 * gq : min(64 * c + 16 * gq, row_bytes - 16));
-          if (!in) q[c] = make_uint4(0, 0, 0, 0);
+          const bool in = col < nq && (EXACT || 64 * c + 16 * gq < row_bytes);
+          q[y][c] = ldg_b16<false>(qp, EXACT ? 64 * c + 16 * gq : min(64 * c + 16 * gq, row_bytes - 16));
+          if (!in) q[y][c] = make_uint4(0, 0, 0, 0);
         }
       }
       locate(0);
@@ -548,8 +571,8 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
           gone[s] = bad[s];
           cut = cut || bad[s] != 0;
         }
-        f32x4 sc[SUB];
-        tile.scores(q, sc, gq, row_bytes);
+        f32x4 sc[QT][SUB];
+        tile.template scores<QT>(q, sc, gq, row_bytes);
         if constexpr (more) {
           if constexpr (PAGE16) {
             if (((i + 1) & 63) == 0) look_up(i + 1);
@@ -559,7 +582,9 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
           if constexpr (!PAGE16) look_up(min(i + 2, trips - 1));
         }
 #pragma unroll
-        for (int s = 0; s < SUB; ++s) sc[s] *= A.scale_log2;
+        for (int y = 0; y < QT; ++y)
+#pragma unroll
+          for (int s = 0; s < SUB; ++s) sc[y][s] *= A.scale_log2;
         // a position that is not seen has no weight, and its value, which may be
         // anything, is cleared
         const auto clear = [&](AttTile<T, DP, EXACT>& of, int lo, int n) {
@@ -577,35 +602,41 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int at = t + 16 * s + 4 * gq + j;
-              if (at < my_lo || at >= my_n || ((gone[s] >> (4 * gq + j)) & 1)) sc[s][j] = -INFINITY;
+              if (at < my_lo || at >= my_n || ((gone[s] >> (4 * gq + j)) & 1)) {
+#pragma unroll
+                for (int y = 0; y < QT; ++y) sc[y][s][j] = -INFINITY;
+              }
             }
-          if (ONCE || R.rows == 1) clear(tile, R.lo, R.n);
+          if (!SHARED || R.rows == 1) clear(tile, R.lo, R.n);
         }
-        float tm = sc[0][0];
 #pragma unroll
-        for (int s = 0; s < SUB; ++s)
+        for (int y = 0; y < QT; ++y) {
+          float tm = sc[y][0][0];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) tm = fmaxf(tm, sc[s][j]);
-        const float mn = fmaxf(mx, max_over_quarters(tm));
-        if (__any(mn > mx)) {
-          const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mx - mn);
-          l *= f;
+          for (int s = 0; s < SUB; ++s)
 #pragma unroll
-          for (int ng = 0; ng < G::NG; ++ng)
+            for (int j = 0; j < 4; ++j) tm = fmaxf(tm, sc[y][s][j]);
+          const float mn = fmaxf(mx[y], max_over_quarters(tm));
+          if (__any(mn > mx[y])) {
+            const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mx[y] - mn);
+            l[y] *= f;
 #pragma unroll
-            for (int e = 0; e < G::VD; ++e) acc[ng][e] *= f;
-          mx = mn;
-        }
-        const float ref = mx == -INFINITY ? 0.f : mx;
+            for (int ng = 0; ng < G::NG; ++ng)
 #pragma unroll
-        for (int s = 0; s < SUB; ++s)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            sc[s][j] = __builtin_amdgcn_exp2f(sc[s][j] - ref);
-            l += sc[s][j];
+              for (int e = 0; e < G::VD; ++e) acc[y][ng][e] *= f;
+            mx[y] = mn;
           }
-        if (ONCE || !cut || R.rows == 1) {
-          tile.weigh(sc, acc);
+          const float ref = mx[y] == -INFINITY ? 0.f : mx[y];
+#pragma unroll
+          for (int s = 0; s < SUB; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              sc[y][s][j] = __builtin_amdgcn_exp2f(sc[y][s][j] - ref);
+              l[y] += sc[y][s][j];
+            }
+        }
+        if (!SHARED || !cut || R.rows == 1) {
+          tile.template weigh<QT>(sc, acc);
         } else {
           // rows that see different parts of the tile: each on its own, with V
           // cleared for it (what others see of it, times their weight of 0, may
@@ -613,16 +644,16 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
           for (int i = 0; i < R.rows; ++i) {
             AttTile<T, DP, EXACT> seen = tile;
             clear(seen, lane_of(my_lo, i * wide), lane_of(my_n, i * wide));
-            f32x4 with[G::NG][G::VD];
+            f32x4 with[QT][G::NG][G::VD];
 #pragma unroll
             for (int ng = 0; ng < G::NG; ++ng)
 #pragma unroll
-              for (int e = 0; e < G::VD; ++e) with[ng][e] = acc[ng][e];
-            seen.weigh(sc, with);
+              for (int e = 0; e < G::VD; ++e) with[0][ng][e] = acc[0][ng][e];
+            seen.template weigh<QT>(sc, with);
 #pragma unroll
             for (int ng = 0; ng < G::NG; ++ng)
 #pragma unroll
-              for (int e = 0; e < G::VD; ++e) acc[ng][e] = my_row == i ? with[ng][e] : acc[ng][e];
+              for (int e = 0; e < G::VD; ++e) acc[0][ng][e] = my_row == i ? with[0][ng][e] : acc[0][ng][e];
           }
         }
         if constexpr (more) load_v();
@@ -630,8 +661,11 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
       for (int i = 0; i + 1 < trips; ++i) trip(i, std::true_type());
       trip(trips - 1, std::false_type());
     }
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
+#pragma unroll
+    for (int y = 0; y < QT; ++y) {
+      l[y] += __shfl_xor(l[y], 16, 64);
+      l[y] += __shfl_xor(l[y], 32, 64);
+    }
     // the next slice, asked for while the results are joined
     const bool last_piece = !even && u + taken == u_end;
     uint32_t next = slices;
@@ -639,23 +673,27 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
 
     // ---- the four waves' results joined in LDS ----
     const int waves = max(0, min(cnt, 4));  // those with tiles
-    if (w < waves && m16 < nq) {
-      if (gq == 0) s_ml[w][m16][0] = mx, s_ml[w][m16][1] = l;
 #pragma unroll
-      for (int ng = 0; ng < G::NG; ++ng)
+    for (int y = 0; y < QT; ++y) {
+      const int col = 16 * y + m16;
+      if (w < waves && col < nq) {
+        if (gq == 0) s_ml[w][col][0] = mx[y], s_ml[w][col][1] = l[y];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int ng = 0; ng < G::NG; ++ng)
 #pragma unroll
-          for (int i = 0; i < G::VD; i += 4)
-            *(f32x4*)&s_o[w][m16][16 * G::VD * ng + G::VD * (4 * gq + r) + i] =
-                f32x4{acc[ng][i][r], acc[ng][i + 1][r], acc[ng][i + 2][r], acc[ng][i + 3][r]};
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < G::VD; i += 4)
+              *(f32x4*)&s_o[w][col][16 * G::VD * ng + G::VD * (4 * gq + r) + i] =
+                  f32x4{acc[y][ng][i][r], acc[y][ng][i + 1][r], acc[y][ng][i + 2][r], acc[y][ng][i + 3][r]};
+      }
     }
     __syncthreads();
     const bool whole = units == (uint32_t)R.units;
     const int E = nq * D / 4;  // groups of four elements of the piece's output
     const auto put = [&](int g, int d, f32x4 o, float L) {
       const f32x4 x = L == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : o / L;
-      const int i = ONCE ? 0 : g / wide;
+      const int i = !SHARED ? 0 : g / wide;
       const int64_t at = (int64_t)(row + i) * A.out_stride + (int64_t)(h0 + g - i * wide) * D + d;
       if constexpr (G::ES == 4) {
         stg4((float*)A.out + at, x);
@@ -694,14 +732,20 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
       }
     }
     if (!whole) {
-      const int n_pieces = (int)all, fan = n_pieces > ATT_FAN ? (int)(slice - w0) / ATT_FAN * ATT_FAN : 0;
-      const int sets = E < 256 ? 256 / E : 1;
+      // Groups as large as the loads of one trip to memory, which costs about
+      // 1.5 us: 1 row of 8192 positions, 16 query heads over one, 64 pieces of
+      // 512 x 4 elements: 37 us by groups of 32, 25 by groups of 8, 21 with two
+      // elements a thread at once.
+      const int n_pieces = (int)all, sets = E < 256 ? 256 / E : 1, trip = 8 * sets;  // (pieces whose loads are in flight)
+      const bool two = n_pieces > (E > 256 ? trip : 2 * trip);
+      const int fan = n_pieces <= trip * trip ? trip : n_pieces <= 4 * trip * trip ? 2 * trip : 4 * trip;
+      const int group0 = two ? (int)(slice - w0) / fan * fan : 0;
       float* jo = &s_o[0][0][0];
       // level 0: the pieces fan .. of one group (only where they are many);
       // level 1: the groups' results, or the pieces
-      for (int level = n_pieces > ATT_FAN ? 0 : 1; level < 2; ++level) {
-        const int from = level == 0 ? fan : 0, stride = level == 1 && n_pieces > ATT_FAN ? ATT_FAN : 1;
-        const int np = level == 0 ? min(ATT_FAN, n_pieces - fan) : (n_pieces + stride - 1) / stride;
+      for (int level = two ? 0 : 1; level < 2; ++level) {
+        const int from = level == 0 ? group0 : 0, stride = level == 1 && two ? fan : 1;
+        const int np = level == 0 ? min(fan, n_pieces - group0) : (n_pieces + stride - 1) / stride;
         const uint32_t first = from == 0 ? slot0 : 2 * (w0 + from);
         int32_t* count = A.count + ATT_ARRIVALS + (level ? ATT_PLACES * gridDim.x : 0) + first;
         wait_vm_all();
@@ -712,60 +756,84 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
         }
         __syncthreads();
         if (!s_last) break;
-        for (int e0 = 0; e0 < E; e0 += 256) {
-          const int set = sets > 1 ? tid / E : 0, e = sets > 1 ? tid - set * E : e0 + tid;
-          const bool on = set < sets && e < E;
-          const int g = on ? e / (D / 4) : 0, d = on ? 4 * (e - g * (D / 4)) : 0;
-          float gm = -INFINITY, L = 0.f;
-          f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
-          if (on) {
-            for (int x = set; x < np; x += 8 * sets) {  // (eight pieces' loads in flight)
-              f32x4 ml[8], po[8];
+        // Y elements a thread at once, so that their loads share one trip to memory
+        const auto join = [&](auto at_once) {
+          constexpr int Y = at_once;
+          for (int e0 = 0; e0 < E; e0 += 256 * Y) {
+            const int set = sets > 1 ? tid / E : 0;
+            int g[Y], d[Y];
+            bool on[Y];
+            float gm[Y], L[Y];
+            f32x4 o[Y];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int y = min(x + i * sets, np - 1);
-                const uint32_t at = (y == 0 ? first : 2 * (w0 + from + y * stride)) * SLOT + g * (DP + 4) * 4;
-                ml[i] = ld_sys4(part, at + DP * 4);
-                po[i] = ld_sys4(part, at + d * 4);
-              }
+            for (int y = 0; y < Y; ++y) {
+              const int e = sets > 1 ? tid - set * E : e0 + 256 * y + tid;
+              on[y] = set < sets && e < E;
+              g[y] = on[y] ? e / (D / 4) : 0, d[y] = on[y] ? 4 * (e - g[y] * (D / 4)) : 0;
+              gm[y] = -INFINITY, L[y] = 0.f, o[y] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+            if (on[0]) {
+              for (int x = set; x < np; x += 8 * sets) {  // (eight pieces' loads in flight)
+                f32x4 ml[Y][8], po[Y][8];
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                if (x + i * sets >= np) break;
-                const float xm = stride > 1 ? ml[i].z : ml[i].x, xl = stride > 1 ? ml[i].w : ml[i].y;
-                const float mn = fmaxf(gm, xm), ref = mn == -INFINITY ? 0.f : mn;
-                const float fa = __builtin_amdgcn_exp2f(gm - ref), fb = __builtin_amdgcn_exp2f(xm - ref);
-                o = o * fa + po[i] * fb;
-                L = L * fa + xl * fb;
-                gm = mn;
+                for (int i = 0; i < 8; ++i) {
+                  const int p = min(x + i * sets, np - 1);
+                  const uint32_t from_p = (p == 0 ? first : 2 * (w0 + from + p * stride)) * SLOT;
+#pragma unroll
+                  for (int y = 0; y < Y; ++y) {
+                    const uint32_t at = from_p + g[y] * (DP + 4) * 4;
+                    ml[y][i] = ld_sys4(part, at + DP * 4);
+                    po[y][i] = ld_sys4(part, at + d[y] * 4);
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  if (x + i * sets >= np) break;
+#pragma unroll
+                  for (int y = 0; y < Y; ++y) {
+                    const float xm = stride > 1 ? ml[y][i].z : ml[y][i].x, xl = stride > 1 ? ml[y][i].w : ml[y][i].y;
+                    const float mn = fmaxf(gm[y], xm), ref = mn == -INFINITY ? 0.f : mn;
+                    const float fa = __builtin_amdgcn_exp2f(gm[y] - ref), fb = __builtin_amdgcn_exp2f(xm - ref);
+                    o[y] = o[y] * fa + po[y][i] * fb;
+                    L[y] = L[y] * fa + xl * fb;
+                    gm[y] = mn;
+                  }
+                }
               }
             }
-          }
-          if (sets > 1) {  // the sets' sums in the sets' order
-            if (on) {
-              *(f32x4*)&jo[4 * tid] = o;
-              jo[1024 + 2 * tid] = gm, jo[1024 + 2 * tid + 1] = L;
-            }
-            __syncthreads();
-            if (on && set == 0) {
-              for (int x = 1; x < sets; ++x) {
-                const float xm = jo[1024 + 2 * (tid + x * E)], mn = fmaxf(gm, xm), ref = mn == -INFINITY ? 0.f : mn;
-                const float fa = __builtin_amdgcn_exp2f(gm - ref), fb = __builtin_amdgcn_exp2f(xm - ref);
-                o = o * fa + *(const f32x4*)&jo[4 * (tid + x * E)] * fb;
-                L = L * fa + jo[1024 + 2 * (tid + x * E) + 1] * fb;
-                gm = mn;
+            if (Y == 1 && sets > 1) {  // the sets' sums in the sets' order
+              if (on[0]) {
+                *(f32x4*)&jo[4 * tid] = o[0];
+                jo[1024 + 2 * tid] = gm[0], jo[1024 + 2 * tid + 1] = L[0];
+              }
+              __syncthreads();
+              if (on[0] && set == 0) {
+                for (int x = 1; x < sets; ++x) {
+                  const float xm = jo[1024 + 2 * (tid + x * E)], mn = fmaxf(gm[0], xm), ref = mn == -INFINITY ? 0.f : mn;
+                  const float fa = __builtin_amdgcn_exp2f(gm[0] - ref), fb = __builtin_amdgcn_exp2f(xm - ref);
+                  o[0] = o[0] * fa + *(const f32x4*)&jo[4 * (tid + x * E)] * fb;
+                  L[0] = L[0] * fa + jo[1024 + 2 * (tid + x * E) + 1] * fb;
+                  gm[0] = mn;
+                }
               }
             }
+#pragma unroll
+            for (int y = 0; y < Y; ++y)
+              if (on[y] && set == 0) {
+                if (level) {
+                  put(g[y], d[y], o[y], L[y]);
+                } else {  // (in the group's first place, whose elements only this thread reads, m and l beside its own)
+                  const uint32_t at = first * SLOT + g[y] * (DP + 4) * 4;
+                  st_sys4(part, at + d[y] * 4, o[y]);
+                  if (d[y] == 0) st_sys2(part, at + DP * 4 + 8, __float_as_uint(gm[y]), __float_as_uint(L[y]));
+                }
+              }
           }
-          if (on && set == 0) {
-            if (level) {
-              put(g, d, o, L);
-            } else {  // (in the group's first place, whose elements only this thread reads, m and l beside its own)
-              const uint32_t at = first * SLOT + g * (DP + 4) * 4;
-              st_sys4(part, at + d * 4, o);
-              if (d == 0) st_sys2(part, at + DP * 4 + 8, __float_as_uint(gm), __float_as_uint(L));
-            }
-          }
-        }
+        };
+        if (__builtin_expect(E <= 256, 1))
+          join(std::integral_constant<int, 1>{});
+        else
+          join(std::integral_constant<int, 2>{});
       }
     }
     if (even) break;
@@ -781,14 +849,32 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
   }
 }
 
-template <typename T, int DP, bool ONCE>
+// Two query tiles at once for more than 16 query heads a key head: K and V are
+// read and turned once for both (64 rows of up to 4096 positions, 64 heads over
+// one: 84 us without, 54 with; 1 row of 700: 18 and 20, the wider pieces' join).
+// fp32 rows of more than 128 elements would not fit the registers (12 rows of
+// up to 2282 positions, 76 heads of 224 over 4: 220 us without, 256 with).
+constexpr bool att_widens(int es, int dp) { return es == 2 || dp <= 128; }
+
+template <typename T, int DP, int MODE>
 void att_launch(const AttArgs& A, int blocks, hipStream_t s) {
   if (A.page_size % 16)
-    hipLaunchKernelGGL((k_paged_attention<T, DP, false, false, ONCE>), dim3(blocks), dim3(256), 0, s, A);
+    hipLaunchKernelGGL((k_paged_attention<T, DP, false, false, MODE>), dim3(blocks), dim3(256), 0, s, A);
   else if (A.head_dim == DP)
-    hipLaunchKernelGGL((k_paged_attention<T, DP, true, true, ONCE>), dim3(blocks), dim3(256), 0, s, A);
+    hipLaunchKernelGGL((k_paged_attention<T, DP, true, true, MODE>), dim3(blocks), dim3(256), 0, s, A);
   else
-    hipLaunchKernelGGL((k_paged_attention<T, DP, true, false, ONCE>), dim3(blocks), dim3(256), 0, s, A);
+    hipLaunchKernelGGL((k_paged_attention<T, DP, true, false, MODE>), dim3(blocks), dim3(256), 0, s, A);
+}
+
+template <typename T, int DP>
+void att_mode(const AttArgs& A, int blocks, hipStream_t s) {
+  if constexpr (att_widens(sizeof(T), DP)) {
+    if (A.group > 16) return att_launch<T, DP, ATT_WIDE>(A, blocks, s);
+  }
+  if (A.req || A.group > 16)
+    att_launch<T, DP, ATT_SHARED>(A, blocks, s);
+  else
+    att_launch<T, DP, ATT_ONCE>(A, blocks, s);
 }
 
 // compute units of `device`, asked once a device (a negative answer is an error)
@@ -818,7 +904,7 @@ extern "C" scute_status scute_paged_attention_workspace(int32_t device, int32_t 
     return fail(SCUTE_E_SHAPE, "scute_paged_attention_workspace: head_dim must be a multiple of 8 in [8, 256]");
   const int units = device_units(device);
   if (units < 0) return fail(SCUTE_E_INVALID, "scute_paged_attention_workspace: no such HIP device");
-  *bytes = att_counter_bytes(units) + att_places(units) * 16 * (att_dim(head_dim) + 4) * 4;
+  *bytes = att_counter_bytes(units) + att_places(units) * ATT_COLS * (att_dim(head_dim) + 4) * 4;
   return SCUTE_OK;
 }
 
@@ -866,18 +952,18 @@ extern "C" scute_status scute_paged_attention(const scute_kv_cache* C, const voi
   const uint64_t mul = (((uint64_t)1 << (31 + shift)) + C->page_size - 1) / C->page_size;
   const int group = n_heads / C->n_kv_heads;
   const int64_t reach = std::min<int64_t>((int64_t)table_width * C->page_size, (int64_t)1 << 29);
+  const int64_t es = C->dtype == SCUTE_F32 ? 4 : 2, unit = es == 4 ? 64 : 128;
+  const int columns = group > 16 && att_widens((int)es, dp) ? 32 : 16;  // (of a query tile: att_mode)
   const int together = req && group <= 8 ? std::min(4, 16 / group) : 1;
   AttArgs A{q, C->k, C->v, out, table, len, req, (float*)((char*)workspace + counters), (int32_t*)workspace, q_stride,
             out_stride, C->page_stride, C->token_stride, C->head_stride, table_stride, C->n_pages, 0,
-            (uint32_t)(need - counters), (uint32_t)mul, n_rows, C->n_kv_heads, (group + 15) / 16, group, together, C->head_dim,
-            C->page_size, shift, (int32_t)reach, n_requests, window, scale * 1.4426950408889634f};
+            (uint32_t)(need - counters), (uint32_t)mul, n_rows, C->n_kv_heads,
+            (group + columns - 1) / columns, group, together, C->head_dim, C->page_size, shift, (int32_t)reach,
+            n_requests, window, scale * 1.4426950408889634f};
   // rows of one launch: their units, at the table's whole width, stay below 2^31
-  const int64_t es = C->dtype == SCUTE_F32 ? 4 : 2, unit = es == 4 ? 64 : 128;
   const int64_t most = (((int64_t)1 << 31) - 1) / ((int64_t)A.n_kv * A.q_tiles * (reach / unit + 2 + ATT_EXTRA));
   if (most < 1) return fail(SCUTE_E_SHAPE, "scute_paged_attention: too many heads for a table this wide");
   const hipStream_t s = (hipStream_t)stream;
-  const bool once = !req && A.q_tiles == 1;
-#define ATT(T, DP) (once ? att_launch<T, DP, true>(A, units, s) : att_launch<T, DP, false>(A, units, s))
   for (int64_t r = 0; r < n_rows; r += most) {
     A.row0 = (int32_t)r;
     A.n_rows = (int32_t)std::min<int64_t>(most, n_rows - r);
@@ -886,16 +972,15 @@ extern "C" scute_status scute_paged_attention(const scute_kv_cache* C, const voi
     A.len = len + r;
     A.req = req ? req + r : nullptr;
     if (es == 4) {
-      if (dp == 64) ATT(float, 64);
-      else if (dp == 128) ATT(float, 128);
-      else ATT(float, 256);
+      if (dp == 64) att_mode<float, 64>(A, units, s);
+      else if (dp == 128) att_mode<float, 128>(A, units, s);
+      else att_mode<float, 256>(A, units, s);
     } else {
-      if (dp == 64) ATT(uint16_t, 64);
-      else if (dp == 128) ATT(uint16_t, 128);
-      else ATT(uint16_t, 256);
+      if (dp == 64) att_mode<uint16_t, 64>(A, units, s);
+      else if (dp == 128) att_mode<uint16_t, 128>(A, units, s);
+      else att_mode<uint16_t, 256>(A, units, s);
     }
   }
-#undef ATT
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SCUTE_OK : hip_fail(e, fn);
 }

@@ -305,7 +305,8 @@ def _run_attend(kc, vc, table, q, lens, req=None, window=0, scale=None):
 @pytest.mark.parametrize("D, Hq, Hk, ps, by_head", [
     (128, 32, 8, 16, False), (128, 32, 8, 16, True), (64, 8, 8, 32, False), (256, 4, 2, 16, False),
     (8, 5, 1, 16, False), (80, 12, 4, 5, False), (72, 6, 2, 1, True), (96, 17, 1, 48, False), (136, 40, 2, 7, False),
-    (192, 3, 1, 64, True), (248, 2, 2, 100, False)])
+    (192, 3, 1, 64, True), (248, 2, 2, 100, False),
+    (128, 32, 1, 16, False), (64, 33, 1, 16, True), (256, 100, 2, 6, False), (40, 64, 1, 1, False)])
 def test_attention_shapes(dt, D, Hq, Hk, ps, by_head):
     lens = [1, 0, 2, 15, 16, 17, 31, 32, 33, 64, 65, 130]
     kc, vc, table, q = _attend_case(D + Hq, lens, -(-130 // ps), ps, Hq, Hk, D, dt, by_head)
@@ -322,7 +323,8 @@ def test_attention_window(dt, window):
 
 @pytest.mark.parametrize("dt, Hq, Hk, D, lens", [
     (BF16, 8, 2, 128, [5000]), (BF16, 1, 1, 64, [9000, 1]), (F32, 4, 1, 128, [3000, 0, 2999]),
-    (BF16, 16, 1, 256, [4097]), (BF16, 20, 1, 64, [2048] * 3)])
+    (BF16, 16, 1, 256, [4097]), (BF16, 20, 1, 64, [2048] * 3),
+    (BF16, 80, 2, 128, [6000, 17, 4001]), (F32, 71, 1, 256, [2500, 600])])
 def test_attention_long(dt, Hq, Hk, D, lens):
     """A few rows over long contexts: the work is split over the length."""
     kc, vc, table, q = _attend_case(len(lens), lens, -(-max(lens) // 16), 16, Hq, Hk, D, dt)
