@@ -63,6 +63,14 @@ def _gpu(device, *tensors):
             _bad(f"tensors on {t.device} and {device} in one call")
 
 
+def _settle(device):
+    """Waits for a new handle's zeros, so that its first call may be on any stream."""
+    if device.type == "cuda":
+        with torch.cuda.device(device):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream(device).synchronize()
+
+
 def _vector(t, n, dtype, name):
     """A contiguous one-dimensional tensor of n elements; its address."""
     if t.dtype != dtype or t.shape != (n,) or not t.is_contiguous():
@@ -132,6 +140,7 @@ class Rows:
         for name in ("seq_len", "cu_len", "slot", "req", "pos", "len", "counts"):
             setattr(a, name, getattr(self, name).data_ptr())
         a.cursor_out = self.cursor.data_ptr()
+        _settle(dev)
 
 
 def assign_pages(old_len, new_len, table, ring, cursor, page_size, rows, stream=None):
@@ -216,6 +225,7 @@ class PagedAttention:
     """Attention of new tokens over a KVCache with n_heads query heads
     (n_heads / n_kv_heads of them share a key head). scale: 1 / sqrt(head_dim)
     by default; window: a row sees its last `window` positions (0: all).
+    max_rows: calls of more rows are refused (None: up to 2^20).
 
     The handle owns the workspace of one call at a time: calls that may
     overlap (other streams, graphs replayed side by side) need handles of their
@@ -230,6 +240,8 @@ class PagedAttention:
         self.scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale)
         nbytes = scute.scute_paged_attention_workspace(cache.device.index, cache.head_dim)
         self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=cache.device)
+        self.max_rows = None if max_rows is None else int(max_rows)
+        _settle(cache.device)
 
     def forward(self, q, table, row_len, out, row_req=None, stream=None):
         """q, out [rows][n_heads][head_dim] (the cache's type); table int32
@@ -239,6 +251,8 @@ class PagedAttention:
         c = self.cache
         N, D, H = q.shape[0], c.head_dim, self.n_heads
         qs, os = _heads(q, N, H, D, "q"), _heads(out, N, H, D, "out")
+        if self.max_rows is not None and N > self.max_rows:
+            _bad(f"{N} rows: the handle takes up to {self.max_rows}")
         if q.dtype != c.dtype or out.dtype != c.dtype:
             _bad("q and out must have the cache's type")
         if table.dtype != _I32 or table.dim() != 2:

@@ -540,6 +540,34 @@ def test_attention_refusals_with_tensors():
     assert none.shape[0] == 0
 
 
+def test_attention_row_limit():
+    kc, vc, table, q = _attend_case(1, [5, 5], 2, 16, 4, 2, 64, BF16)
+    att = block.PagedAttention(block.KVCache(kc, vc), 4, max_rows=1)
+    att.forward(q[:1], table, _int([5]), torch.empty_like(q[:1]))
+    with pytest.raises(ValueError):
+        att.forward(q, table, _int([5, 5]), torch.empty_like(q))
+    torch.cuda.synchronize()
+
+
+def test_handles_are_ready_on_every_stream():
+    """A handle made behind a stream's work is zeroed by the time it is there."""
+    kc, vc, table, q = _attend_case(1, [5, 5], 2, 16, 4, 2, 64, BF16)
+    busy = torch.randn((4096, 4096), device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            busy = torch.mm(busy, busy).clamp_(-1, 1)
+        rows = block.Rows(64, 1000, DEV)
+        for _ in range(20):
+            busy = torch.mm(busy, busy).clamp_(-1, 1)
+        att = block.PagedAttention(block.KVCache(kc, vc), 4)
+    rows.slot.fill_(7)
+    att.workspace[:64].fill_(7)
+    torch.cuda.synchronize()
+    assert bool((rows.slot == 7).all()) and bool((att.workspace[:64] == 7).all())
+
+
 # ---- the norms around the residual ----------------------------------------------------------------------
 
 def _norm_ref(z, e, kind, w, b, eps):
