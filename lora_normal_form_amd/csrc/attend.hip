@@ -223,8 +223,16 @@ struct AttTile {
 #pragma unroll
       for (int e = 0; e < G::VB / 4; ++e) v[s][j][ng][e] = 0;
   }
-  template <int QT>
-  __device__ __forceinline__ void weigh(const f32x4 (&p)[QT][G::SUB], f32x4 (&acc)[QT][G::NG][G::VD]) {
+  // SOME: of the positions that `mask` (ones or zeros for each) leaves, for the
+  // columns of the lanes that `keep`
+  template <int QT, bool SOME = false>
+  __device__ __forceinline__ void weigh(const f32x4 (&p)[QT][G::SUB], f32x4 (&acc)[QT][G::NG][G::VD],
+                                        const uint32_t (*mask)[4] = nullptr, bool keep = true) {
+    const auto val = [&](int s, int j, int ng, int i) { return SOME ? v[s][j][ng][i] & mask[s][j] : v[s][j][ng][i]; };
+    const auto put = [&](f32x4& to, f32x4 x) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) to[r] = !SOME || keep ? x[r] : to[r];
+    };
     if constexpr (G::ES == 2) {
       // the weights as sums of two bf16 (one alone would add an error of the
       // output's own rounding, 2^-8; the second products cost no time)
@@ -249,12 +257,12 @@ struct AttTile {
         for (int i = 0; i < G::VD; ++i) {
           const uint32_t sel = i & 1 ? 0x07060302u : 0x05040100u;
           uint4 a;
-          a.x = __builtin_amdgcn_perm(v[0][1][ng][i / 2], v[0][0][ng][i / 2], sel);
-          a.y = __builtin_amdgcn_perm(v[0][3][ng][i / 2], v[0][2][ng][i / 2], sel);
-          a.z = __builtin_amdgcn_perm(v[1][1][ng][i / 2], v[1][0][ng][i / 2], sel);
-          a.w = __builtin_amdgcn_perm(v[1][3][ng][i / 2], v[1][2][ng][i / 2], sel);
+          a.x = __builtin_amdgcn_perm(val(0, 1, ng, i / 2), val(0, 0, ng, i / 2), sel);
+          a.y = __builtin_amdgcn_perm(val(0, 3, ng, i / 2), val(0, 2, ng, i / 2), sel);
+          a.z = __builtin_amdgcn_perm(val(1, 1, ng, i / 2), val(1, 0, ng, i / 2), sel);
+          a.w = __builtin_amdgcn_perm(val(1, 3, ng, i / 2), val(1, 2, ng, i / 2), sel);
 #pragma unroll
-          for (int y = 0; y < QT; ++y) acc[y][ng][i] = mfma16(a, b2[y], mfma16(a, b[y], acc[y][ng][i]));
+          for (int y = 0; y < QT; ++y) put(acc[y][ng][i], mfma16(a, b2[y], mfma16(a, b[y], acc[y][ng][i])));
         }
     } else {
 #pragma unroll
@@ -262,10 +270,12 @@ struct AttTile {
 #pragma unroll
         for (int i = 0; i < G::VD; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int y = 0; y < QT; ++y) {
+            f32x4 x = acc[y][ng][i];
 #pragma unroll
-            for (int y = 0; y < QT; ++y)
-              acc[y][ng][i] = mfma4(v[0][j][ng][i], __float_as_uint(p[y][0][j]), acc[y][ng][i]);
+            for (int j = 0; j < 4; ++j) x = mfma4(val(0, j, ng, i), __float_as_uint(p[y][0][j]), x);
+            put(acc[y][ng][i], x);
+          }
     }
   }
 };
@@ -585,29 +595,25 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
         for (int y = 0; y < QT; ++y)
 #pragma unroll
           for (int s = 0; s < SUB; ++s) sc[y][s] *= A.scale_log2;
+        const auto each_place = [&](auto f) {  // f(block, position of it, position, whether its page is not there)
+#pragma unroll
+          for (int s = 0; s < SUB; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f(s, j, t + 16 * s + 4 * gq + j, (gone[s] >> (4 * gq + j)) & 1);
+        };
         // a position that is not seen has no weight, and its value, which may be
         // anything, is cleared
-        const auto clear = [&](AttTile<T, DP, EXACT>& of, int lo, int n) {
-#pragma unroll
-          for (int s = 0; s < SUB; ++s)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int at = t + 16 * s + 4 * gq + j;
-              if (at < lo || at >= n || ((gone[s] >> (4 * gq + j)) & 1)) of.clear_v(s, j);
-            }
-        };
         if (cut) {
+          each_place([&](int s, int j, int at, bool away) {
+            if (at < my_lo || at >= my_n || away) {
 #pragma unroll
-          for (int s = 0; s < SUB; ++s)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int at = t + 16 * s + 4 * gq + j;
-              if (at < my_lo || at >= my_n || ((gone[s] >> (4 * gq + j)) & 1)) {
-#pragma unroll
-                for (int y = 0; y < QT; ++y) sc[y][s][j] = -INFINITY;
-              }
+              for (int y = 0; y < QT; ++y) sc[y][s][j] = -INFINITY;
             }
-          if (!SHARED || R.rows == 1) clear(tile, R.lo, R.n);
+          });
+          if (!SHARED || R.rows == 1)
+            each_place([&](int s, int j, int at, bool away) {
+              if (at < R.lo || at >= R.n || away) tile.clear_v(s, j);
+            });
         }
 #pragma unroll
         for (int y = 0; y < QT; ++y) {
@@ -640,20 +646,15 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
         } else {
           // rows that see different parts of the tile: each on its own, with V
           // cleared for it (what others see of it, times their weight of 0, may
-          // be NaN: only the row's own columns are kept)
+          // be NaN: only the row's own columns are kept). V is masked as it is
+          // used: with copies of V and of the sums heads of more than 128 elements
+          // left the registers (136 requests of five rows over 1895 positions, 11
+          // heads of 240 over one: 472 us with copies, 200 without).
           for (int i = 0; i < R.rows; ++i) {
-            AttTile<T, DP, EXACT> seen = tile;
-            clear(seen, lane_of(my_lo, i * wide), lane_of(my_n, i * wide));
-            f32x4 with[QT][G::NG][G::VD];
-#pragma unroll
-            for (int ng = 0; ng < G::NG; ++ng)
-#pragma unroll
-              for (int e = 0; e < G::VD; ++e) with[0][ng][e] = acc[0][ng][e];
-            seen.template weigh<QT>(sc, with);
-#pragma unroll
-            for (int ng = 0; ng < G::NG; ++ng)
-#pragma unroll
-              for (int e = 0; e < G::VD; ++e) acc[0][ng][e] = my_row == i ? with[0][ng][e] : acc[0][ng][e];
+            const int lo = lane_of(my_lo, i * wide), n = lane_of(my_n, i * wide);
+            uint32_t mask[SUB][4];
+            each_place([&](int s, int j, int at, bool away) { mask[s][j] = at < lo || at >= n || away ? 0u : ~0u; });
+            tile.template weigh<QT, true>(sc, acc, mask, my_row == i);
           }
         }
         if constexpr (more) load_v();

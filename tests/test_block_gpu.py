@@ -379,7 +379,9 @@ def test_attention_masked_places_hold_anything(dt, ps):
 @pytest.mark.parametrize("dt, Hq, Hk, D, ps, window", [
     (BF16, 4, 4, 128, 16, 0), (BF16, 4, 2, 64, 16, 0), (BF16, 8, 2, 128, 32, 0), (BF16, 6, 2, 80, 5, 0),
     (BF16, 10, 2, 128, 16, 20), (BF16, 16, 2, 64, 16, 7), (BF16, 9, 1, 64, 16, 0), (F32, 6, 2, 80, 5, 30),
-    (F32, 4, 1, 256, 16, 0), (BF16, 8, 2, 256, 48, 33)])
+    (F32, 4, 1, 256, 16, 0), (BF16, 8, 2, 256, 48, 33), (BF16, 16, 2, 128, 16, 0), (BF16, 5, 1, 96, 16, 40),
+    (F32, 7, 1, 128, 6, 0), (BF16, 33, 3, 64, 16, 0), (F32, 16, 1, 72, 16, 25), (BF16, 24, 1, 128, 16, 0),
+    (BF16, 20, 1, 256, 16, 0), (BF16, 6, 1, 256, 16, 0)])
 def test_attention_rows_of_one_request(dt, Hq, Hk, D, ps, window):
     """Rows of one request share the reads of its cache: runs of one to seven
     rows, with lengths that rise, fall, repeat and vanish, rows of no request
