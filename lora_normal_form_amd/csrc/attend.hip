@@ -193,8 +193,9 @@ struct AttTile {
 #pragma unroll
     for (int e = 0; e < G::VB / 4; ++e) v[s][j][ng][e] = x[e];
   }
-  template <int QT>
-  __device__ __forceinline__ void scores(const uint4 (&q)[QT][G::NC], f32x4 (&sc)[QT][G::SUB], int gq, int row_bytes) {
+  // q(y, c): chunk c of query tile y
+  template <int QT, typename Q>
+  __device__ __forceinline__ void scores(const Q& q, f32x4 (&sc)[QT][G::SUB], int gq, int row_bytes) {
 #pragma unroll
     for (int s = 0; s < G::SUB; ++s) {
 #pragma unroll
@@ -208,10 +209,10 @@ struct AttTile {
 #pragma unroll
         for (int y = 0; y < QT; ++y) {
           if constexpr (G::ES == 2) {
-            sc[y][s] = mfma16(kk, q[y][c], sc[y][s]);
+            sc[y][s] = mfma16(kk, q(y, c), sc[y][s]);
           } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[y][s] = mfma4(dword(kk, e), dword(q[y][c], e), sc[y][s]);
+            for (int e = 0; e < 4; ++e) sc[y][s] = mfma4(dword(kk, e), dword(q(y, c), e), sc[y][s]);
           }
         }
       }
@@ -301,6 +302,13 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
   constexpr bool ONCE = MODE == ATT_ONCE, SHARED = MODE == ATT_SHARED;
   __shared__ float s_ml[4][COLS][2];
   __shared__ __align__(16) float s_o[4][COLS][OS];
+  // The queries stay in LDS where the registers would not hold them too (23 rows
+  // of 33324 positions, 18 heads of 176 over one: 301 us without, 130 with; where
+  // they fit they are faster there: 64 rows of up to 2000, fp32, 48 heads of 128
+  // over two: 64 us, 70 from LDS).
+  constexpr bool Q_LDS = DP == 256 && QT * G::ES > 2;
+  constexpr int QROW = DP * G::ES + 16;
+  __shared__ __align__(16) char s_q[Q_LDS ? COLS * QROW : 16];
   __shared__ uint32_t s_wsum[4], s_before;
   __shared__ uint32_t s_next;
   __shared__ int s_row, s_last;
@@ -472,6 +480,19 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
 #pragma unroll
         for (int i = 0; i < G::VD; ++i) acc[y][ng][i] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
+    // 16 bytes of a column of the query tile, zeros past its end
+    const auto query = [&](int col, int of_row, int at) {
+      const char* qp = (const char*)A.q + ((int64_t)(row + of_row) * A.q_stride + (int64_t)(h0 + min(col, nq - 1) - of_row * wide) * D) * G::ES;
+      const uint4 x = ldg_b16<false>(qp, EXACT ? at : min(at, row_bytes - 16));
+      return col < nq && (EXACT || at < row_bytes) ? x : make_uint4(0, 0, 0, 0);
+    };
+    if constexpr (Q_LDS) {
+      for (int i = tid; i < COLS * G::NC * 4; i += 256) {
+        const int col = i / (G::NC * 4), at = 16 * (i % (G::NC * 4));
+        *(uint4*)&s_q[col * QROW + at] = query(col, SHARED ? min(col, nq - 1) / in_place(wide) : 0, at);
+      }
+      __syncthreads();
+    }
     if (w < cnt) {  // (an empty row has none)
       const char *kb = (const char*)A.k, *vb = (const char*)A.v;
       const int32_t* tab = A.table + (int64_t)R.req * A.table_stride;
@@ -554,17 +575,12 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
       };
 
       look_up(0);
-      uint4 q[QT][G::NC];
+      uint4 q[Q_LDS ? 1 : QT][G::NC];
+      if constexpr (!Q_LDS) {
 #pragma unroll
-      for (int y = 0; y < QT; ++y) {
-        const int col = 16 * y + m16;
-        const char* qp = (const char*)A.q + ((int64_t)(row + my_row) * A.q_stride + (int64_t)(h0 + min(col, nq - 1) - my_row * wide) * D) * G::ES;
+        for (int y = 0; y < QT; ++y)
 #pragma unroll
-        for (int c = 0; c < G::NC; ++c) {
-          const bool in = col < nq && (EXACT || 64 * c + 16 * gq < row_bytes);
-          q[y][c] = ldg_b16<false>(qp, EXACT ? 64 * c + 16 * gq : min(64 * c + 16 * gq, row_bytes - 16));
-          if (!in) q[y][c] = make_uint4(0, 0, 0, 0);
-        }
+          for (int c = 0; c < G::NC; ++c) q[y][c] = query(16 * y + m16, my_row, 64 * c + 16 * gq);
       }
       locate(0);
       load_k();
@@ -582,7 +598,12 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
           cut = cut || bad[s] != 0;
         }
         f32x4 sc[QT][SUB];
-        tile.template scores<QT>(q, sc, gq, row_bytes);
+        if constexpr (Q_LDS) {
+          const char* qp = &s_q[m16 * QROW + 16 * gq + (int)in_place(0)];  // (read in every trip, not kept)
+          tile.template scores<QT>([&](int y, int c) { return *(const uint4*)(qp + 16 * y * QROW + 64 * c); }, sc, gq, row_bytes);
+        } else {
+          tile.template scores<QT>([&](int y, int c) { return q[y][c]; }, sc, gq, row_bytes);
+        }
         if constexpr (more) {
           if constexpr (PAGE16) {
             if (((i + 1) & 63) == 0) look_up(i + 1);
