@@ -874,8 +874,8 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
 // Two query tiles at once for more than 16 query heads a key head: K and V are
 // read and turned once for both (64 rows of up to 4096 positions, 64 heads over
 // one: 84 us without, 54 with; 1 row of 700: 18 and 20, the wider pieces' join).
-// fp32 rows of more than 128 elements would not fit the registers (12 rows of
-// up to 2282 positions, 76 heads of 224 over 4: 220 us without, 256 with).
+// fp32 heads of more than 128 elements stay at one: the four waves' sums and
+// the queries of two would take 166 KB of LDS.
 constexpr bool att_widens(int es, int dp) { return es == 2 || dp <= 128; }
 
 template <typename T, int DP, int MODE>
