@@ -186,6 +186,7 @@ class Rotary:
             _bad("n_axes must be in [1, 8]")
         _gpu(freq.device, axis)
         self.freq, self.axis, self.n_axes, self.device = freq, axis, int(n_axes), freq.device
+        self.head_dim = int(head_dim)
         self.desc = scute.RotaryDesc(head_dim, 2 * n, n_axes, 1 if interleaved else 0, freq.data_ptr(),
                                      None if axis is None else axis.data_ptr())
 
@@ -198,6 +199,9 @@ class Rotary:
         if q.dim() != 3:
             _bad("q must be [tokens][n_heads][head_dim]")
         T, H, D = q.shape
+        if D != cache.head_dim or D != self.head_dim:
+            _bad(f"q's heads, the cache's and the rotary's must have one head_dim, got {D}, {cache.head_dim} and "
+                 f"{self.head_dim}")
         dt = q.dtype
         if dt not in _DTYPES or k.dtype != dt or v.dtype != dt:
             _bad("q, k and v must all be float32 or all bfloat16")

@@ -1,0 +1,37 @@
+"""What the operators between a block's adapter layers refuse at their edges,
+without a GPU: handles are stood in for, so every call below has to be turned
+away by its argument checks."""
+
+from types import SimpleNamespace
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from lora_normal_form_amd import block  # noqa: E402
+
+F32, BF16, I32, I64 = torch.float32, torch.bfloat16, torch.int32, torch.int64
+
+
+def _handle(cls, **attrs):
+    """A handle of `cls` that no constructor has seen."""
+    h = cls.__new__(cls)
+    h.__dict__.update(attrs)
+    return h
+
+
+# ---- rotary positions ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("q_dim, k_dim, cache_dim, rot_dim", [
+    (64, 64, 128, 128), (128, 128, 64, 64), (64, 64, 64, 128), (64, 128, 128, 128)])
+def test_rotary_refuses_heads_of_another_size(q_dim, k_dim, cache_dim, rot_dim):
+    """The kernel strides by the cache's head size: q, k, v, q_out and the
+    rotary's heads have to be of that size."""
+    cache = SimpleNamespace(device=torch.device("cpu"), index=0, dtype=BF16, n_kv_heads=2, head_dim=cache_dim,
+                            page_size=16, desc=None)
+    ro = _handle(block.Rotary, freq=torch.ones(4, dtype=torch.float64), axis=None, n_axes=1, head_dim=rot_dim,
+                 device=torch.device("cpu"), desc=None)
+    q, k, v = torch.zeros(3, 4, q_dim), torch.zeros(3, 2, k_dim), torch.zeros(3, 2, k_dim)
+    with pytest.raises(ValueError, match="head_dim"):
+        ro.store(q, k, v, torch.zeros(3, dtype=I32), torch.zeros(3, dtype=I64), cache,
+                 torch.zeros(3, 4, q_dim, dtype=BF16))
