@@ -445,7 +445,9 @@ scute_status scute_paged_attention_workspace(int32_t device, int32_t head_dim, i
  * Several rows of one request (its new tokens, each with its own length) are
  * several rows of one call; those that follow each other share the reads of
  * its cache. Scores, the softmax and the sums are fp32; the weights enter a
- * bf16 cache's products as sums of two bf16 values. The result depends on the
+ * bf16 cache's products as sums of two bf16 values. A V that is not finite makes
+ * those elements of the output not finite that see it, as the sum says: an
+ * infinity stays one. The result depends on the
  * rows' requests and lengths only, never on the order in which work-groups end.
  * workspace: `workspace_bytes` (at least what scute_paged_attention_workspace
  * says), 256-byte aligned, zeroed once by the caller before its first use;

@@ -236,7 +236,9 @@ struct AttTile {
     };
     if constexpr (G::ES == 2) {
       // the weights as sums of two bf16 (one alone would add an error of the
-      // output's own rounding, 2^-8; the second products cost no time)
+      // output's own rounding, 2^-8; the second products cost no time). The
+      // second is 0 or of either sign, so an infinite V gives a sum of any kind,
+      // which is put right where the waves' results are joined.
       uint4 b[QT], b2[QT];
       const auto rest = [](uint32_t hi, float x, float y) {
         return pack_bf2(__float_as_uint(x - __uint_as_float(hi << 16)), __float_as_uint(y - __uint_as_float(hi & 0xFFFF0000u)));
@@ -744,6 +746,43 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
       for (int x = 0; x < 4; ++x) {
         const float f = gm == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(wm[x] - gm);
         if (x < waves) L += wl[x] * f, o += wo[x] * f;
+      }
+      if constexpr (G::ES == 2) {
+        // Not finite, beside weights whose sum is: some V that the column sees is
+        // not finite. These elements are the sum of what is not finite there,
+        // whatever the (positive) weights: the piece's positions are gone through
+        // once more for it (four loads in flight: with eight the 32 columns of 256
+        // elements spilled in their main loop, 64 rows of 3000 positions, 24 heads
+        // over one: 61 us with four, 69 with eight).
+        if (__builtin_expect(fmaf(o.x, 0.f, fmaf(o.y, 0.f, fmaf(o.z, 0.f, o.w * 0.f))) != 0.f && isfinite(L), 0)) {
+          typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+          const int n = shared ? att_len(A, ldg(A.len + row + g / wide), R.req) : R.n, lo = att_first(A, n);
+          const int32_t* tab = A.table + (int64_t)R.req * A.table_stride;
+          const char* vp = (const char*)A.v + ((int64_t)kvh * A.head_stride + d) * G::ES;
+          const int from = max(lo, (R.first + t0) * TILE), to = min(n, (R.first + t0 + cnt) * TILE);
+          f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+          for (int t = from; t < to; t += 4) {
+            u32x2 v[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int at = min(t + x, to - 1), p = (int)(((uint64_t)(uint32_t)at * A.ps_mul) >> (31 + A.ps_shift));
+              const int page = ldg(tab + p);
+              const bool seen = t + x < to && page >= 0 && page < A.n_pages;
+              const int64_t off = seen ? (int64_t)page * A.page_stride + (int64_t)(at - p * A.page_size) * A.token_stride : 0;
+              v[x] = *(const GLOBAL u32x2*)(vp + off * G::ES);
+              if (!seen) v[x] = u32x2{0, 0};
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const f32x4 e = f32x4{__uint_as_float(v[x].x << 16), __uint_as_float(v[x].x & 0xFFFF0000u),
+                                    __uint_as_float(v[x].y << 16), __uint_as_float(v[x].y & 0xFFFF0000u)};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) sum[k] += isfinite(e[k]) ? 0.f : e[k];
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[k] = sum[k] != 0.f ? sum[k] : o[k];
+        }
       }
       if (whole) {
         put(g, d, o, L);
