@@ -756,21 +756,22 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
         // over one: 61 us with four, 69 with eight).
         if (__builtin_expect(fmaf(o.x, 0.f, fmaf(o.y, 0.f, fmaf(o.z, 0.f, o.w * 0.f))) != 0.f && isfinite(L), 0)) {
           typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-          const int n = shared ? att_len(A, ldg(A.len + row + g / wide), R.req) : R.n, lo = att_first(A, n);
+          const int i = SHARED ? g / wide : 0;
+          const int n = shared ? att_len(A, ldg(A.len + row + i), R.req) : R.n, lo = att_first(A, n);
           const int32_t* tab = A.table + (int64_t)R.req * A.table_stride;
           const char* vp = (const char*)A.v + ((int64_t)kvh * A.head_stride + d) * G::ES;
           const int from = max(lo, (R.first + t0) * TILE), to = min(n, (R.first + t0 + cnt) * TILE);
           f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
           for (int t = from; t < to; t += 4) {
-            u32x2 v[4];
+            uint2 v[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               const int at = min(t + x, to - 1), p = (int)(((uint64_t)(uint32_t)at * A.ps_mul) >> (31 + A.ps_shift));
               const int page = ldg(tab + p);
               const bool seen = t + x < to && page >= 0 && page < A.n_pages;
-              const int64_t off = seen ? (int64_t)page * A.page_stride + (int64_t)(at - p * A.page_size) * A.token_stride : 0;
-              v[x] = *(const GLOBAL u32x2*)(vp + off * G::ES);
-              if (!seen) v[x] = u32x2{0, 0};
+              const u32x2 e = *(const GLOBAL u32x2*)(vp + (seen ? (int64_t)page * A.page_stride +
+                                                                 (int64_t)(at - p * A.page_size) * A.token_stride : 0) * G::ES);
+              v[x] = seen ? make_uint2(e.x, e.y) : make_uint2(0, 0);
             }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
