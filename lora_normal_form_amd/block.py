@@ -123,24 +123,29 @@ class Rows:
     and max_tokens tokens: seq_len [n_requests], cu_len [n_requests + 1], and
     for each token slot (int64), req, pos, len [max_tokens] (rows past the last
     token: -1, -1, 0, 0); cursor [2] (int64) and counts [4] (tokens placed,
-    pages taken, requests refused, pages returned)."""
+    pages taken, requests refused, pages returned). The tensors stay the
+    handle's, whose descriptor holds their addresses: their elements may be
+    written, the attributes not set."""
 
     def __init__(self, n_requests, max_tokens, device=None):
         dev = torch.device("cuda" if device is None else device)
         if dev.type == "cuda" and dev.index is None:
             dev = torch.device("cuda", torch.cuda.current_device())
-        new = lambda n, dt=_I32: torch.zeros(n, dtype=dt, device=dev)  # noqa: E731
         self.n_requests, self.max_tokens, self.device = int(n_requests), int(max_tokens), dev
-        self.seq_len, self.cu_len = new(n_requests), new(n_requests + 1)
-        self.slot, self.req, self.pos, self.len = new(max_tokens, _I64), new(max_tokens), new(max_tokens), new(max_tokens)
-        self.cursor, self.counts = new(2, _I64), new(4)
         a = self.args = scute.CacheAssignArgs()
         a.device = dev.index if dev.type == "cuda" else -1
         a.n_requests, a.max_tokens = n_requests, max_tokens
-        for name in ("seq_len", "cu_len", "slot", "req", "pos", "len", "counts"):
-            setattr(a, name, getattr(self, name).data_ptr())
-        a.cursor_out = self.cursor.data_ptr()
+        sizes = {"seq_len": n_requests, "cu_len": n_requests + 1, "slot": max_tokens, "req": max_tokens,
+                 "pos": max_tokens, "len": max_tokens, "cursor": 2, "counts": 4}
+        self._filled = {name: torch.zeros(n, dtype=_I64 if name in ("slot", "cursor") else _I32, device=dev)
+                        for name, n in sizes.items()}
+        for name, t in self._filled.items():
+            setattr(a, "cursor_out" if name == "cursor" else name, t.data_ptr())
         _settle(dev)
+
+    seq_len, cu_len, slot, req, pos, len, cursor, counts = (
+        property(lambda self, name=name: self._filled[name])
+        for name in ("seq_len", "cu_len", "slot", "req", "pos", "len", "cursor", "counts"))
 
 
 def assign_pages(old_len, new_len, table, ring, cursor, page_size, rows, stream=None):

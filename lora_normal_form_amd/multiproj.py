@@ -442,20 +442,19 @@ def attention_rows(torch, context, n=128, heads=32, kv_heads=8, head_dim=128, pa
     h_out, x_out = torch.empty_like(h), torch.empty((n, d), dtype=fu.x.dtype, device=dev)
     # every request holds `context` positions; the timed steps bring the same next token again
     from . import block
-    grown = block.Rows(n, n * context, dev)
+    grown, rows = block.Rows(n, n * context, dev), block.Rows(n, n, dev)
     block.assign_pages(st.rows.seq_len, new * context, st.table, st.ring, st.rows.cursor, page_size, grown)
-    keep = (grown.seq_len.clone(), grown.cursor.clone())
 
     def step():
-        st.rows.seq_len, st.rows.cursor = keep
+        st.rows, st._other = grown, rows
         return st.forward(h, new, h_out, x_out)
 
     parts = [("attention step", step),
              ("norm + pages + rotary", lambda: (
                  st.norm_in.forward(None, h, None, fu.x),
-                 block.assign_pages(*keep[:1], new, st.table, st.ring, keep[1], page_size, st._other),
-                 st.rotary.store(st.q, st.k, st.v, st.rows.pos, st.rows.slot, st.cache, st.q_rot))),
-             ("attention over the cache", lambda: st.attention.forward(st.q_rot, st.table, st.rows.len, st.a)),
+                 block.assign_pages(grown.seq_len, new, st.table, st.ring, grown.cursor, page_size, rows),
+                 st.rotary.store(st.q, st.k, st.v, rows.pos, rows.slot, st.cache, st.q_rot))),
+             ("attention over the cache", lambda: st.attention.forward(st.q_rot, st.table, rows.len, st.a)),
              ("residual + norm", lambda: st.norm_out.forward(st.out.y, h, h_out, x_out))]
     got = [{"layer": "attention", "tenants": f"{n} requests, {context} positions", "route": name,
             "us": _time(torch, fn, iters=50)} for name, fn in parts]

@@ -67,3 +67,14 @@ def test_attention_infinite_v(dt, D, Hq, Hk, ps, lens, req, window):
                            torch.nan_to_num(odd[hit], nan=7.0, posinf=8.0, neginf=9.0))
         zero = torch.zeros_like(got)
         _close(torch.where(hit, zero, got), torch.where(hit, zero, ref), tol, "elsewhere")
+
+
+# ---- the attention step -----------------------------------------------------------------------------------
+
+def test_timed_step_rows():
+    """The timing of the attention step runs its steps on tensors that stay."""
+    from lora_normal_form_amd import multiproj
+    got = multiproj.attention_rows(torch, 40, n=8, heads=4, kv_heads=2, head_dim=64, page_size=16)
+    assert [r["route"] for r in got] == ["attention step", "norm + pages + rotary", "attention over the cache",
+                                         "residual + norm"]
+    assert all(r["us"] > 0 for r in got)

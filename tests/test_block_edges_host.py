@@ -35,3 +35,19 @@ def test_rotary_refuses_heads_of_another_size(q_dim, k_dim, cache_dim, rot_dim):
     with pytest.raises(ValueError, match="head_dim"):
         ro.store(q, k, v, torch.zeros(3, dtype=I32), torch.zeros(3, dtype=I64), cache,
                  torch.zeros(3, 4, q_dim, dtype=BF16))
+
+
+# ---- pages and slots -------------------------------------------------------------------------------
+
+def test_rows_keep_what_their_descriptor_points_to():
+    """assign_pages writes to the addresses in `args`, so the tensors behind
+    them cannot be replaced (the first would be freed, and then written)."""
+    rows = block.Rows(3, 5, device="cpu")
+    shapes = {"seq_len": 3, "cu_len": 4, "slot": 5, "req": 5, "pos": 5, "len": 5, "cursor": 2, "counts": 4}
+    for name, n in shapes.items():
+        t = getattr(rows, name)
+        assert t.shape == (n,) and t.dtype == (I64 if name in ("slot", "cursor") else I32)
+        assert t.data_ptr() == getattr(rows.args, "cursor_out" if name == "cursor" else name)
+        with pytest.raises(AttributeError):
+            setattr(rows, name, t.clone())
+        assert getattr(rows, name) is t
