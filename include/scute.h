@@ -366,8 +366,19 @@ typedef struct scute_kv_cache {
  * request -1, pos 0 and len 0, which the operators below skip, so a captured
  * step may hold fewer tokens than rows.
  * Lengths, token and page totals may be at most 2^30, new lengths 2^29;
- * negative old lengths count as 0. Errors: SCUTE_E_INVALID for null or misaligned pointers or an
- * output that is also an input, SCUTE_E_SHAPE for sizes out of range. */
+ * negative old lengths count as 0; the cursors count from 0 up. Errors:
+ * SCUTE_E_INVALID for null or misaligned pointers, an output that is also an
+ * input or an unknown flag, SCUTE_E_SHAPE for sizes out of range. */
+typedef enum scute_assign_flag {
+  /* a request is refused, and keeps old_len, when one of its tokens has no row
+   * (its tokens and those of the requests before it are more than max_tokens);
+   * those after it that bring tokens are then refused too. Without the flag
+   * such a request is placed: tokens past the last row have pages and count in
+   * seq_len, and nothing of them can be stored, so it is the caller who sees to
+   * cu_len[n_requests] <= max_tokens */
+  SCUTE_ASSIGN_FIT_ROWS = 1
+} scute_assign_flag;
+
 typedef struct scute_cache_assign_args {
   int32_t device;
   int32_t n_requests;   /* 0 .. 65536                                        */
@@ -392,6 +403,8 @@ typedef struct scute_cache_assign_args {
   int32_t* len;           /* [max_tokens]                                    */
   int32_t* counts;        /* [4] tokens placed, pages taken, requests refused,
                              pages returned                                  */
+  uint32_t flags;         /* a bitwise or of scute_assign_flag               */
+  uint32_t reserved;      /* 0                                               */
 } scute_cache_assign_args;
 
 scute_status scute_cache_assign(const scute_cache_assign_args* args, void* stream);

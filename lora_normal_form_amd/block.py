@@ -148,13 +148,15 @@ class Rows:
         for name in ("seq_len", "cu_len", "slot", "req", "pos", "len", "cursor", "counts"))
 
 
-def assign_pages(old_len, new_len, table, ring, cursor, page_size, rows, stream=None):
+def assign_pages(old_len, new_len, table, ring, cursor, page_size, rows, stream=None, fit_rows=False):
     """One step's pages and slots (scute_cache_assign): requests hold old_len
     [R] positions and bring new_len [R] tokens (negative: the request ends and
     its pages go back). table [R][P] and ring are updated; everything else goes
     into rows, which is returned. The next step takes rows.seq_len and
     rows.cursor as old_len and cursor and another Rows (inputs and outputs may
-    not be the same tensors)."""
+    not be the same tensors). fit_rows: requests with tokens past rows.max_tokens
+    are refused; without it they are placed, although those tokens have no row
+    (rows.cu_len[R] says how many tokens there are)."""
     R = rows.n_requests
     a = rows.args
     a.old_len, a.new_len = _vector(old_len, R, _I32, "old_len"), _vector(new_len, R, _I32, "new_len")
@@ -166,6 +168,7 @@ def assign_pages(old_len, new_len, table, ring, cursor, page_size, rows, stream=
     a.ring_size = size = ring.shape[0]
     a.ring, a.cursor = _vector(ring, size, _I32, "ring"), _vector(cursor, 2, _I64, "cursor")
     _gpu(rows.device, old_len, new_len, table, ring, cursor)
+    a.flags = scute.ASSIGN_FIT_ROWS if fit_rows else 0
     a.table_width, a.page_size, a.table_stride, a.table = P, page_size, ts if R > 1 else P, table.data_ptr()
     scute._check(scute.lib.scute_cache_assign(a, _stream(stream, rows.device.index)))
     return rows

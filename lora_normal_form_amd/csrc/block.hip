@@ -129,6 +129,12 @@ __global__ __launch_bounds__(ASG_THREADS) void k_cache_assign(AsgArgs G) {
   ctok[tid] = pre[0];
   cpage[tid] = pre[1];
   cgone[tid] = pre[2];
+  // whether the request's tokens, the first of them token `tok`, all have rows
+  // (where one's have not, neither have those of any that follow: pages are
+  // taken up to it, and the sums before it hold as they are)
+  const auto has_rows = [&](const AsgReq& q, uint32_t tok) {
+    return !(A.flags & SCUTE_ASSIGN_FIT_ROWS) || q.add == 0 || tok + q.add <= (uint32_t)A.max_tokens;
+  };
   const auto request = [&](int r) {
     return per == 1 ? asg_req(G, s_old[r], s_new[r]) : asg_req(G, A.old_len[r], A.new_len[r]);
   };
@@ -145,7 +151,7 @@ __global__ __launch_bounds__(ASG_THREADS) void k_cache_assign(AsgArgs G) {
     for (int r = r0; r < r1; ++r) {
       const AsgReq q = request(r);
       const uint32_t need = sat_add(page, q.want);
-      const bool ok = q.fits && (q.want == 0 || need <= avail);
+      const bool ok = q.fits && (q.want == 0 || need <= avail) && has_rows(q, tok);
       if (ok && q.want) taken = need;
       if (ok) placed = sat_add(placed, q.add);
       refused += !q.ends && !ok;
@@ -199,7 +205,7 @@ __global__ __launch_bounds__(ASG_THREADS) void k_cache_assign(AsgArgs G) {
         page = sat_add(page, q.want);
         q = request(++r);
       }
-      if (q.fits && (q.want == 0 || sat_add(page, q.want) <= avail)) {
+      if (q.fits && (q.want == 0 || sat_add(page, q.want) <= avail) && has_rows(q, tok)) {
         const uint32_t p = q.old + (t - tok), at = asg_page(G, p);
         int32_t id;
         if (at < q.held) {
@@ -652,6 +658,8 @@ extern "C" scute_status scute_cache_assign(const scute_cache_assign_args* A, voi
     if (misaligned(p, 4)) return fail(SCUTE_E_INVALID, "scute_cache_assign: misaligned pointer");
   for (const void* p : {(const void*)A->cursor, (const void*)A->cursor_out, (const void*)A->slot})
     if (misaligned(p, 8)) return fail(SCUTE_E_INVALID, "scute_cache_assign: misaligned pointer");
+  if (A->flags & ~(uint32_t)SCUTE_ASSIGN_FIT_ROWS)
+    return fail(SCUTE_E_INVALID, "scute_cache_assign: unknown flag");
   // work-groups read the inputs while others write the outputs
   if (A->cursor == A->cursor_out || (some && (A->seq_len == A->old_len || A->seq_len == A->new_len ||
                                               A->cu_len == A->old_len || A->cu_len == A->new_len)))

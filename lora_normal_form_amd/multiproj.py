@@ -281,7 +281,8 @@ class AttentionStep:
     writes. The rows are the requests' new tokens in the requests' order (the
     plans' tenants follow that order); rows past the last token, and those of
     a request that found no pages, go through the layers and are skipped by the
-    cache and the attention.
+    cache and the attention. So is a request with tokens past the last row:
+    it keeps its length and may bring them again.
 
     The step keeps the requests' lengths, pages and free pages on the GPU:
     table [n_requests][pages_per_request], ring (n_pages free pages at first).
@@ -329,7 +330,8 @@ class AttentionStep:
         holds the step's rows (block.Rows)."""
         from . import block
         prev, rows = self.rows, self._other
-        block.assign_pages(prev.seq_len, new_len, self.table, self.ring, prev.cursor, self.cache.page_size, rows)
+        block.assign_pages(prev.seq_len, new_len, self.table, self.ring, prev.cursor, self.cache.page_size, rows,
+                           fit_rows=True)
         self.rows, self._other = rows, prev
         qkv, out = self.qkv, self.out
         self.norm_in.forward(None, h, None, qkv.x)

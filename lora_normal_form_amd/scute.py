@@ -85,7 +85,10 @@ class CacheAssignArgs(C.Structure):
                 ("table", C.c_void_p), ("ring", C.c_void_p), ("cursor", C.c_void_p),
                 ("cursor_out", C.c_void_p), ("seq_len", C.c_void_p), ("cu_len", C.c_void_p),
                 ("slot", C.c_void_p), ("req", C.c_void_p), ("pos", C.c_void_p), ("len", C.c_void_p),
-                ("counts", C.c_void_p)]
+                ("counts", C.c_void_p), ("flags", C.c_uint32), ("reserved", C.c_uint32)]
+
+
+ASSIGN_FIT_ROWS = 1
 
 
 class RotaryDesc(C.Structure):

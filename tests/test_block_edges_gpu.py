@@ -10,7 +10,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from lora_normal_form_amd import block  # noqa: E402
-from test_block_gpu import BF16, DEV, F32, _attend_case, _attend_ref, _close, _int  # noqa: E402
+from test_block_step_gpu import D, H, N, _step  # noqa: E402
+from test_block_gpu import BF16, DEV, F32, _assign_case, _attend_case, _attend_ref, _close, _int  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -69,6 +70,70 @@ def test_attention_infinite_v(dt, D, Hq, Hk, ps, lens, req, window):
         _close(torch.where(hit, zero, got), torch.where(hit, zero, ref), tol, "elsewhere")
 
 
+# ---- pages and slots ----------------------------------------------------------------------------------------
+
+def _assign_flags_ref(old, new, table, ring, head, tail, ps, max_tokens, fit):
+    """The step in plain loops, request by request."""
+    table, ring = table.copy(), ring.copy()
+    (R, P), cap = table.shape, len(ring)
+    rows = {"seq_len": np.zeros(R, np.int64), "cu_len": np.zeros(R + 1, np.int64), "slot": np.full(max_tokens, -1),
+            "req": np.full(max_tokens, -1), "pos": np.zeros(max_tokens, np.int64), "len": np.zeros(max_tokens, np.int64)}
+    free = [int(ring[c % cap]) for c in range(head, tail)]
+    wanted = taken = placed = refused = t = 0
+    back = []
+    for r in range(R):
+        o, n = max(0, int(old[r])), int(new[r])
+        held = -(-o // ps)
+        rows["cu_len"][r] = t
+        if n < 0:
+            back += [int(p) for p in table[r, :min(held, P)]]
+            continue
+        first, t = t, t + n
+        want = -(-(o + n) // ps) - held
+        ok = held + want <= P and not (fit and n and first + n > max_tokens)
+        if ok and want:
+            wanted += want
+            ok = wanted <= len(free)
+            if ok:
+                table[r, held:held + want] = free[wanted - want:wanted]
+                taken = wanted
+        refused += not ok
+        rows["seq_len"][r] = o + n if ok else o
+        placed += n if ok else 0
+        for i in range(min(n, max_tokens - first) if ok else 0):
+            rows["slot"][first + i] = int(table[r, (o + i) // ps]) * ps + (o + i) % ps
+            rows["req"][first + i], rows["pos"][first + i], rows["len"][first + i] = r, o + i, o + i + 1
+    rows["cu_len"][R] = t
+    for j, p in enumerate(back):
+        ring[(tail + j) % cap] = p
+    rows["cursor"] = np.array([head + taken, tail + len(back)])
+    rows["counts"] = np.array([placed, taken, refused, len(back)])
+    return table, ring, rows
+
+
+@pytest.mark.parametrize("R, P, ps, max_new, rows, free_share, fit", [
+    (300, 12, 5, 40, 2000, 1.0, True), (300, 12, 5, 40, 2000, 1.0, False), (300, 12, 5, 40, 0, 1.0, True),
+    (64, 9, 16, 3, 40, 0.05, True), (2500, 3, 8, 6, 3000, 0.6, True), (40000, 2, 4, 2, 20000, 0.5, True),
+    (65536, 1, 16, 1, 65536, 1.0, True), (5, 4, 16, 7, 1, 1.0, True)])
+def test_assign_fits_rows(R, P, ps, max_new, rows, free_share, fit):
+    """A request whose tokens pass the last row is refused (with fit_rows):
+    what seq_len counts has a row, so it can be stored."""
+    old, new, table, ring, head, tail = _assign_case(R + rows, R, P, ps, max_new, free_share)
+    want = _assign_flags_ref(old, new, table, ring, head, tail, ps, rows, fit)
+    got = block.Rows(R, rows, DEV)
+    tab, ring_d = _int(table), _int(ring)
+    old_d = _int(old)
+    block.assign_pages(old_d, _int(new), tab, ring_d, torch.tensor([head, tail], device=DEV), ps, got, fit_rows=fit)
+    torch.cuda.synchronize()
+    assert np.array_equal(tab.cpu().numpy(), want[0]) and np.array_equal(ring_d.cpu().numpy(), want[1])
+    for name, v in want[2].items():
+        assert np.array_equal(getattr(got, name).cpu().numpy(), v), name
+    if fit:
+        grown = (got.seq_len - old_d.clamp(min=0)).clamp(min=0)
+        here = got.req[got.req >= 0].long()
+        assert torch.equal(torch.bincount(here, minlength=R), grown.long())
+
+
 # ---- the attention step -----------------------------------------------------------------------------------
 
 def test_timed_step_rows():
@@ -78,3 +143,17 @@ def test_timed_step_rows():
     assert [r["route"] for r in got] == ["attention step", "norm + pages + rotary", "attention over the cache",
                                          "residual + norm"]
     assert all(r["us"] > 0 for r in got)
+
+
+def test_step_refuses_tokens_past_its_rows():
+    """A request whose tokens do not all have rows keeps its length; when it
+    comes again it is placed."""
+    st, *_ = _step(91)
+    h = torch.zeros((N, H * D), device=DEV)
+    h_out, x_out = torch.empty_like(h), torch.empty((N, H * D), dtype=BF16, device=DEV)
+    for new, lens in (([9, 7, 4, 8, 0], [9, 7, 4, 0, 0]), ([1, 1, 0, 8, 20], [10, 8, 4, 8, 0]),
+                      ([0, 0, 1, 0, 20], [10, 8, 5, 8, 20])):
+        st.forward(h, _int(new), h_out, x_out)
+        assert st.rows.seq_len.tolist() == lens, new
+    st.close()
+    st.qkv.close()

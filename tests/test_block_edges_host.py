@@ -8,7 +8,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from lora_normal_form_amd import block  # noqa: E402
+from lora_normal_form_amd import block, scute  # noqa: E402
 
 F32, BF16, I32, I64 = torch.float32, torch.bfloat16, torch.int32, torch.int64
 
@@ -51,3 +51,15 @@ def test_rows_keep_what_their_descriptor_points_to():
         with pytest.raises(AttributeError):
             setattr(rows, name, t.clone())
         assert getattr(rows, name) is t
+
+
+def test_assign_refuses_unknown_flags():
+    a = scute.CacheAssignArgs()
+    a.n_requests, a.table_width, a.page_size, a.ring_size, a.max_tokens, a.table_stride = 4, 8, 16, 100, 32, 8
+    for i, name in enumerate(("old_len", "new_len", "table", "ring", "cursor", "cursor_out", "seq_len", "cu_len", "slot",
+                              "req", "pos", "len", "counts")):
+        setattr(a, name, (1 << 20) + 4096 * i)  # addresses that no check may follow
+    a.flags = 1 << 16
+    with pytest.raises(scute.ScuteError, match="flag") as e:
+        scute.scute_cache_assign(a, 0)
+    assert e.value.code == scute.E_INVALID
