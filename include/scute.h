@@ -376,7 +376,12 @@ typedef enum scute_assign_flag {
    * such a request is placed: tokens past the last row have pages and count in
    * seq_len, and nothing of them can be stored, so it is the caller who sees to
    * cu_len[n_requests] <= max_tokens */
-  SCUTE_ASSIGN_FIT_ROWS = 1
+  SCUTE_ASSIGN_FIT_ROWS = 1,
+  /* row r is request r's: its one token, or nothing (slot -1) where it brings
+   * none, ends or is refused, so that a row keeps its request from step to step
+   * (cu_len[r] is r). A request that brings more than one token is refused.
+   * max_tokens is n_requests or more (SCUTE_E_SHAPE otherwise) */
+  SCUTE_ASSIGN_ONE_EACH = 2
 } scute_assign_flag;
 
 typedef struct scute_cache_assign_args {

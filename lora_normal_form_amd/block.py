@@ -148,7 +148,8 @@ class Rows:
         for name in ("seq_len", "cu_len", "slot", "req", "pos", "len", "cursor", "counts"))
 
 
-def assign_pages(old_len, new_len, table, ring, cursor, page_size, rows, stream=None, fit_rows=False):
+def assign_pages(old_len, new_len, table, ring, cursor, page_size, rows, stream=None, fit_rows=False,
+                 one_each=False):
     """One step's pages and slots (scute_cache_assign): requests hold old_len
     [R] positions and bring new_len [R] tokens (negative: the request ends and
     its pages go back). table [R][P] and ring are updated; everything else goes
@@ -156,7 +157,9 @@ def assign_pages(old_len, new_len, table, ring, cursor, page_size, rows, stream=
     rows.cursor as old_len and cursor and another Rows (inputs and outputs may
     not be the same tensors). fit_rows: requests with tokens past rows.max_tokens
     are refused; without it they are placed, although those tokens have no row
-    (rows.cu_len[R] says how many tokens there are)."""
+    (rows.cu_len[R] says how many tokens there are). one_each: row r is request
+    r's one token, or empty where it brings none, ends or is refused (as with
+    more than one token); rows then need no request to say whose they are."""
     R = rows.n_requests
     a = rows.args
     a.old_len, a.new_len = _vector(old_len, R, _I32, "old_len"), _vector(new_len, R, _I32, "new_len")
@@ -168,7 +171,7 @@ def assign_pages(old_len, new_len, table, ring, cursor, page_size, rows, stream=
     a.ring_size = size = ring.shape[0]
     a.ring, a.cursor = _vector(ring, size, _I32, "ring"), _vector(cursor, 2, _I64, "cursor")
     _gpu(rows.device, old_len, new_len, table, ring, cursor)
-    a.flags = scute.ASSIGN_FIT_ROWS if fit_rows else 0
+    a.flags = (scute.ASSIGN_FIT_ROWS if fit_rows else 0) | (scute.ASSIGN_ONE_EACH if one_each else 0)
     a.table_width, a.page_size, a.table_stride, a.table = P, page_size, ts if R > 1 else P, table.data_ptr()
     scute._check(scute.lib.scute_cache_assign(a, _stream(stream, rows.device.index)))
     return rows

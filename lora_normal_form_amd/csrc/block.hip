@@ -42,7 +42,7 @@ __device__ __forceinline__ uint32_t sat_add(uint32_t a, uint32_t b) {
 }
 
 struct AsgReq {
-  uint32_t old, add;          // positions held, tokens brought
+  uint32_t old, add, rows;    // positions held, tokens brought, rows of them
   uint32_t held, want, gone;  // pages held, wanted, returned
   bool fits, ends;
 };
@@ -56,10 +56,12 @@ __device__ __forceinline__ AsgReq asg_req(const AsgArgs& A, int32_t o, int32_t n
   q.old = o > 0 ? min((uint32_t)o, ASG_MAX) : 0u;
   q.ends = n < 0;
   q.add = n > 0 ? min((uint32_t)n, ASG_MAX / 2) : 0u;
+  const bool one_each = A.a.flags & SCUTE_ASSIGN_ONE_EACH;
+  q.rows = one_each ? 1u : q.add;
   const uint32_t ps = (uint32_t)A.a.page_size;
   q.held = asg_page(A, q.old + ps - 1);
   const uint32_t upto = asg_page(A, q.old + q.add + ps - 1);
-  q.fits = !q.ends && upto <= (uint32_t)A.a.table_width;
+  q.fits = !q.ends && upto <= (uint32_t)A.a.table_width && !(one_each && q.add > 1);
   q.want = q.fits ? upto - q.held : 0u;
   q.gone = q.ends ? min(q.held, (uint32_t)A.a.table_width) : 0u;
   return q;
@@ -101,7 +103,7 @@ __global__ __launch_bounds__(ASG_THREADS) void k_cache_assign(AsgArgs G) {
   for (int r = r0; r < r1; ++r) {
     const int32_t o = A.old_len[r], n = A.new_len[r];
     const AsgReq q = asg_req(G, o, n);
-    own[0] = sat_add(own[0], q.add);
+    own[0] = sat_add(own[0], q.rows);
     own[1] = sat_add(own[1], q.want);
     own[2] = sat_add(own[2], q.gone);
     if (per == 1) s_old[tid] = o, s_new[tid] = n;
@@ -159,7 +161,7 @@ __global__ __launch_bounds__(ASG_THREADS) void k_cache_assign(AsgArgs G) {
         A.cu_len[r] = (int32_t)tok;
         A.seq_len[r] = q.ends ? 0 : (int32_t)(ok ? q.old + q.add : q.old);
       }
-      tok = sat_add(tok, q.add);
+      tok = sat_add(tok, q.rows);
       page = need;
     }
     // (within a wave the last lane with pages taken has the most)
@@ -200,12 +202,12 @@ __global__ __launch_bounds__(ASG_THREADS) void k_cache_assign(AsgArgs G) {
       uint32_t tok = ctok[i], page = cpage[i];
       int r = i * per;
       AsgReq q = request(r);
-      while (t - tok >= q.add) {  // (the border of thread i + 1 is past t)
-        tok = sat_add(tok, q.add);
+      while (t - tok >= q.rows) {  // (the border of thread i + 1 is past t)
+        tok = sat_add(tok, q.rows);
         page = sat_add(page, q.want);
         q = request(++r);
       }
-      if (q.fits && (q.want == 0 || sat_add(page, q.want) <= avail) && has_rows(q, tok)) {
+      if (q.fits && t - tok < q.add && (q.want == 0 || sat_add(page, q.want) <= avail) && has_rows(q, tok)) {
         const uint32_t p = q.old + (t - tok), at = asg_page(G, p);
         int32_t id;
         if (at < q.held) {
@@ -658,8 +660,10 @@ extern "C" scute_status scute_cache_assign(const scute_cache_assign_args* A, voi
     if (misaligned(p, 4)) return fail(SCUTE_E_INVALID, "scute_cache_assign: misaligned pointer");
   for (const void* p : {(const void*)A->cursor, (const void*)A->cursor_out, (const void*)A->slot})
     if (misaligned(p, 8)) return fail(SCUTE_E_INVALID, "scute_cache_assign: misaligned pointer");
-  if (A->flags & ~(uint32_t)SCUTE_ASSIGN_FIT_ROWS)
+  if (A->flags & ~(uint32_t)(SCUTE_ASSIGN_FIT_ROWS | SCUTE_ASSIGN_ONE_EACH))
     return fail(SCUTE_E_INVALID, "scute_cache_assign: unknown flag");
+  if ((A->flags & SCUTE_ASSIGN_ONE_EACH) && A->max_tokens < A->n_requests)
+    return fail(SCUTE_E_SHAPE, "scute_cache_assign: a row for each request needs max_tokens >= n_requests");
   // work-groups read the inputs while others write the outputs
   if (A->cursor == A->cursor_out || (some && (A->seq_len == A->old_len || A->seq_len == A->new_len ||
                                               A->cu_len == A->old_len || A->cu_len == A->new_len)))

@@ -286,8 +286,9 @@ class AttentionStep:
 
     The step keeps the requests' lengths, pages and free pages on the GPU:
     table [n_requests][pages_per_request], ring (n_pages free pages at first).
-    one_each: every request brings one token in every step (n is n_requests);
-    the attention then streams the cache. freq (float64 [pairs]), axis, n_axes
+    one_each: row i is request i's, with one token or, where the request brings
+    none, ends or finds no page, empty (n is n_requests; more tokens are
+    refused); the attention then streams the cache. freq (float64 [pairs]), axis, n_axes
     and interleaved as in block.Rotary; norm_in, norm_post, norm_out: float32
     weights [d] (norm_post None: no norm on o)."""
 
@@ -331,7 +332,8 @@ class AttentionStep:
         from . import block
         prev, rows = self.rows, self._other
         block.assign_pages(prev.seq_len, new_len, self.table, self.ring, prev.cursor, self.cache.page_size, rows,
-                           fit_rows=True)
+                           fit_rows=True,
+                           one_each=self.one_each)
         self.rows, self._other = rows, prev
         qkv, out = self.qkv, self.out
         self.norm_in.forward(None, h, None, qkv.x)

@@ -88,7 +88,7 @@ class CacheAssignArgs(C.Structure):
                 ("counts", C.c_void_p), ("flags", C.c_uint32), ("reserved", C.c_uint32)]
 
 
-ASSIGN_FIT_ROWS = 1
+ASSIGN_FIT_ROWS, ASSIGN_ONE_EACH = 1, 2
 
 
 class RotaryDesc(C.Structure):

@@ -72,7 +72,7 @@ def test_attention_infinite_v(dt, D, Hq, Hk, ps, lens, req, window):
 
 # ---- pages and slots ----------------------------------------------------------------------------------------
 
-def _assign_flags_ref(old, new, table, ring, head, tail, ps, max_tokens, fit):
+def _assign_flags_ref(old, new, table, ring, head, tail, ps, max_tokens, fit, one_each=False):
     """The step in plain loops, request by request."""
     table, ring = table.copy(), ring.copy()
     (R, P), cap = table.shape, len(ring)
@@ -84,13 +84,13 @@ def _assign_flags_ref(old, new, table, ring, head, tail, ps, max_tokens, fit):
     for r in range(R):
         o, n = max(0, int(old[r])), int(new[r])
         held = -(-o // ps)
-        rows["cu_len"][r] = t
+        rows["cu_len"][r] = first = t
+        t += 1 if one_each else max(0, n)
         if n < 0:
             back += [int(p) for p in table[r, :min(held, P)]]
             continue
-        first, t = t, t + n
         want = -(-(o + n) // ps) - held
-        ok = held + want <= P and not (fit and n and first + n > max_tokens)
+        ok = held + want <= P and not (fit and n and first + n > max_tokens) and not (one_each and n > 1)
         if ok and want:
             wanted += want
             ok = wanted <= len(free)
@@ -134,6 +134,23 @@ def test_assign_fits_rows(R, P, ps, max_new, rows, free_share, fit):
         assert torch.equal(torch.bincount(here, minlength=R), grown.long())
 
 
+@pytest.mark.parametrize("R, P, ps, max_new, spare, free_share", [
+    (1, 3, 4, 1, 0, 1.0), (7, 3, 1, 3, 2, 1.0), (128, 30, 16, 1, 0, 1.0), (1025, 4, 4, 2, 5, 0.1), (3000, 3, 4, 1, 0, 0.5)])
+def test_assign_a_row_each(R, P, ps, max_new, spare, free_share):
+    """Row r stays request r's, whoever ended, brought nothing or was refused."""
+    old, new, table, ring, head, tail = _assign_case(R, R, P, ps, max_new, free_share, ended=0.2)
+    want = _assign_flags_ref(old, new, table, ring, head, tail, ps, R + spare, True, one_each=True)
+    got = block.Rows(R, R + spare, DEV)
+    tab, ring_d = _int(table), _int(ring)
+    block.assign_pages(_int(old), _int(new), tab, ring_d, torch.tensor([head, tail], device=DEV), ps, got, fit_rows=True,
+                       one_each=True)
+    torch.cuda.synchronize()
+    assert np.array_equal(tab.cpu().numpy(), want[0]) and np.array_equal(ring_d.cpu().numpy(), want[1])
+    for name, v in want[2].items():
+        assert np.array_equal(getattr(got, name).cpu().numpy(), v), name
+    assert bool(((got.req[:R] == -1) | (got.req[:R] == torch.arange(R, device=DEV))).all())
+
+
 # ---- the attention step -----------------------------------------------------------------------------------
 
 def test_timed_step_rows():
@@ -155,5 +172,67 @@ def test_step_refuses_tokens_past_its_rows():
                       ([0, 0, 1, 0, 20], [10, 8, 5, 8, 20])):
         st.forward(h, _int(new), h_out, x_out)
         assert st.rows.seq_len.tolist() == lens, new
+    st.close()
+    st.qkv.close()
+
+
+def _request_step(seed, n_requests, n_pages, n=N, **kw):
+    """An attention step of n rows for n_requests requests of up to 9 pages of 4."""
+    from lora_normal_form_amd import multiproj
+    from synth import AdapterSpec, WorkloadSpec, make_workload
+    d, lora, dora, ia3 = H * D, AdapterSpec("lora", rank=16, bias=True), AdapterSpec("dora", rank=16), AdapterSpec("ia3")
+    ten = [(lora, lora, lora), (None, ia3, ia3), (dora, None, lora)]
+    wls, tt = multiproj.projection_workloads(ten, n, d, (d, 2 * D, 2 * D), seed=seed)
+    wl_out = make_workload(WorkloadSpec("out", "bf16", d, d, n, [lora, dora], assign="explicit",
+                                        token_adapter=np.asarray(tt) % 3 - 1, seed=seed + 9))
+    qkv = multiproj.QKVFused(wls, tt, len(ten))
+    freq = 10000.0 ** (-torch.arange(D // 2, dtype=torch.float64, device=DEV) / (D // 2))
+    st = multiproj.AttentionStep(qkv, wl_out, H, 2, D, n_requests, 9, 4, n_pages, freq, **kw)
+    return st, wls, wl_out
+
+
+def _oracle_attention(st, q, k, v, seen):
+    """Attention of each row over what its request has stored (lists of k and
+    v rows, in the cache's type), in 64 bits: (out, bound) by _attend_ref."""
+    kc = torch.zeros((N, 64, st.cache.n_kv_heads, D), dtype=BF16)
+    vc = torch.zeros_like(kc)
+    lens = []
+    for i, r in enumerate(seen):
+        lens.append(len(k[r]) if r >= 0 else 0)
+        for t in range(lens[-1]):
+            kc[i, t], vc[i, t] = k[r][t], v[r][t]
+    table = torch.arange(N, dtype=torch.int32)[:, None]
+    return _attend_ref(q, kc, vc, table, lens, range(N), 0, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("one_each", [False, True])
+def test_step_reads_its_own_request(one_each):
+    """Every row's attention is over what its own request stored, whatever
+    requests before it ended, rested or found no page (a record of each
+    request's keys and values is kept here, by request and not by row)."""
+    st, *_ = _request_step(93, N, 40, one_each=one_each)
+    g = torch.Generator().manual_seed(3)
+    k, v, held = [[] for _ in range(N)], [[] for _ in range(N)], 0
+    rng = np.random.default_rng(4)
+    for step in range(7):
+        new = np.where(rng.random(N) < 0.25, np.where(rng.random(N) < 0.5, -1, 0), 1) if step else np.ones(N, int)
+        h = torch.randn((N, H * D), generator=g).to(DEV)
+        st.forward(h, _int(new), torch.empty_like(h), torch.empty((N, H * D), dtype=BF16, device=DEV))
+        torch.cuda.synchronize()
+        seen, slot = st.rows.req.tolist(), st.rows.slot.tolist()
+        for r in range(N):
+            if new[r] < 0:
+                k[r], v[r] = [], []
+        for i, r in enumerate(seen):
+            if r < 0:
+                continue
+            assert new[r] == 1 and (not one_each or i == r)
+            at = divmod(slot[i], st.cache.page_size)
+            k[r].append(st.cache.k[at].cpu())
+            v[r].append(st.cache.v[at].cpu())
+        assert [len(x) for x in k] == st.rows.seq_len.tolist()
+        assert [len(x) for x in k] != [step + 1] * N or step == 0
+        ref, tol = _oracle_attention(st, st.q_rot, k, v, seen)
+        _close(st.a, ref, tol, f"attention, step {step}")
     st.close()
     st.qkv.close()

@@ -53,13 +53,24 @@ def test_rows_keep_what_their_descriptor_points_to():
         assert getattr(rows, name) is t
 
 
-def test_assign_refuses_unknown_flags():
+def _assign_args(**kw):
     a = scute.CacheAssignArgs()
     a.n_requests, a.table_width, a.page_size, a.ring_size, a.max_tokens, a.table_stride = 4, 8, 16, 100, 32, 8
     for i, name in enumerate(("old_len", "new_len", "table", "ring", "cursor", "cursor_out", "seq_len", "cu_len", "slot",
                               "req", "pos", "len", "counts")):
         setattr(a, name, (1 << 20) + 4096 * i)  # addresses that no check may follow
-    a.flags = 1 << 16
+    for name, v in kw.items():
+        setattr(a, name, v)
+    return a
+
+
+def test_assign_refuses_unknown_flags():
     with pytest.raises(scute.ScuteError, match="flag") as e:
-        scute.scute_cache_assign(a, 0)
+        scute.scute_cache_assign(_assign_args(flags=1 << 16), 0)
     assert e.value.code == scute.E_INVALID
+
+
+def test_assign_refuses_fewer_rows_than_requests():
+    with pytest.raises(scute.ScuteError, match="a row for each") as e:
+        scute.scute_cache_assign(_assign_args(flags=scute.ASSIGN_ONE_EACH, max_tokens=3), 0)
+    assert e.value.code == scute.E_SHAPE
