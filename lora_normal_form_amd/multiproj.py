@@ -334,7 +334,6 @@ class AttentionStep:
         block.assign_pages(prev.seq_len, new_len, self.table, self.ring, prev.cursor, self.cache.page_size, rows,
                            fit_rows=True,
                            one_each=self.one_each)
-        self.rows, self._other = rows, prev
         qkv, out = self.qkv, self.out
         self.norm_in.forward(None, h, None, qkv.x)
         qkv.layer.forward(qkv.batch, qkv.x, qkv.W, qkv.y)
@@ -343,7 +342,10 @@ class AttentionStep:
         self.rotary.store(self.q, self.k, self.v, pos, rows.slot, self.cache, self.q_rot)
         self.attention.forward(self.q_rot, self.table, rows.len, self.a, row_req=None if self.one_each else rows.req)
         out.layer.forward(out.batch, out.x, out.W, out.y)
-        return self.norm_out.forward(out.y, h, h_out, x_out, gate=gate)
+        self.norm_out.forward(out.y, h, h_out, x_out, gate=gate)
+        # (last, so that a call that was refused on its way may be made again)
+        self.rows, self._other = rows, prev
+        return h_out, x_out
 
     def close(self):
         self.out.batch.close()

@@ -236,3 +236,22 @@ def test_step_reads_its_own_request(one_each):
         _close(st.a, ref, tol, f"attention, step {step}")
     st.close()
     st.qkv.close()
+
+
+def test_step_refused_on_its_way_may_come_again():
+    """A call that is turned away by a later operator's checks has not moved
+    the requests on."""
+    st, *_ = _request_step(95, 5, 30)
+    h = torch.randn((N, H * D), generator=torch.Generator().manual_seed(1)).to(DEV)
+    good, x_out = torch.empty_like(h), torch.empty((N, H * D), dtype=BF16, device=DEV)
+    st.forward(h, _int([3, 4, 0, 5, 1]), good, x_out)
+    for args, kw in (((good.to(BF16), x_out), {}), ((good, x_out[:5]), {}), ((good, None), {}),
+                     ((good, x_out), dict(gate=h.to(BF16))), ((good, x_out), dict(pos=torch.zeros(3, N, device=DEV)))):
+        with pytest.raises(ValueError):
+            st.forward(h, _int([2, -1, 6, 1, 0]), *args, **kw)
+    st.forward(h, _int([2, -1, 6, 1, 0]), good, x_out)
+    assert st.rows.seq_len.tolist() == [5, 0, 6, 6, 1]
+    # 5 pages were taken, then 3 and one given back
+    assert st.rows.cursor.tolist() == [5 + 3, 30 + 1], st.rows.cursor.tolist()
+    st.close()
+    st.qkv.close()
