@@ -118,6 +118,11 @@ class KVCache:
 
 # ---- pages and slots ----------------------------------------------------------------------------
 
+def split_state(state, n_requests):
+    """(cursor, seq_len) of a Rows' state buffer, or of another laid out like it."""
+    return state[:2], state[2:].view(_I32)[:n_requests]
+
+
 class Rows:
     """What assign_pages fills in for a step of at most n_requests requests
     and max_tokens tokens: seq_len [n_requests], cu_len [n_requests + 1], and
@@ -125,7 +130,8 @@ class Rows:
     token: -1, -1, 0, 0); cursor [2] (int64) and counts [4] (tokens placed,
     pages taken, requests refused, pages returned). The tensors stay the
     handle's, whose descriptor holds their addresses: their elements may be
-    written, the attributes not set."""
+    written, the attributes not set. cursor and seq_len, which the next step
+    begins with, are parts of one buffer, `state` (int64)."""
 
     def __init__(self, n_requests, max_tokens, device=None):
         dev = torch.device("cuda" if device is None else device)
@@ -135,10 +141,11 @@ class Rows:
         a = self.args = scute.CacheAssignArgs()
         a.device = dev.index if dev.type == "cuda" else -1
         a.n_requests, a.max_tokens = n_requests, max_tokens
-        sizes = {"seq_len": n_requests, "cu_len": n_requests + 1, "slot": max_tokens, "req": max_tokens,
-                 "pos": max_tokens, "len": max_tokens, "cursor": 2, "counts": 4}
-        self._filled = {name: torch.zeros(n, dtype=_I64 if name in ("slot", "cursor") else _I32, device=dev)
-                        for name, n in sizes.items()}
+        self._state = torch.zeros(2 + (n_requests + 1) // 2, dtype=_I64, device=dev)
+        self._filled = dict(zip(("cursor", "seq_len"), split_state(self._state, n_requests)))
+        for name, n, dt in (("cu_len", n_requests + 1, _I32), ("slot", max_tokens, _I64), ("req", max_tokens, _I32),
+                            ("pos", max_tokens, _I32), ("len", max_tokens, _I32), ("counts", 4, _I32)):
+            self._filled[name] = torch.zeros(n, dtype=dt, device=dev)
         for name, t in self._filled.items():
             setattr(a, "cursor_out" if name == "cursor" else name, t.data_ptr())
         _settle(dev)
@@ -146,6 +153,7 @@ class Rows:
     seq_len, cu_len, slot, req, pos, len, cursor, counts = (
         property(lambda self, name=name: self._filled[name])
         for name in ("seq_len", "cu_len", "slot", "req", "pos", "len", "cursor", "counts"))
+    state = property(lambda self: self._state)
 
 
 def assign_pages(old_len, new_len, table, ring, cursor, page_size, rows, stream=None, fit_rows=False,

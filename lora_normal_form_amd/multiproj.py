@@ -285,7 +285,9 @@ class AttentionStep:
     it keeps its length and may bring them again.
 
     The step keeps the requests' lengths, pages and free pages on the GPU:
-    table [n_requests][pages_per_request], ring (n_pages free pages at first).
+    table [n_requests][pages_per_request], ring (n_pages free pages at first),
+    state (cursor and lengths, as in block.Rows). A forward moves them on by its
+    last launch, so a captured forward is a new step whenever it is replayed.
     one_each: row i is request i's, with one token or, where the request brings
     none, ends or finds no page, empty (n is n_requests; more tokens are
     refused); the attention then streams the cache. freq (float64 [pairs]), axis, n_axes
@@ -314,8 +316,9 @@ class AttentionStep:
         self.cache = block.KVCache(torch.zeros(shape, dtype=dt, device=dev), torch.zeros(shape, dtype=dt, device=dev))
         self.table = torch.zeros((n_requests, pages_per_request), dtype=torch.int32, device=dev)
         self.ring = torch.arange(n_pages, dtype=torch.int32, device=dev)
-        self.rows, self._other = block.Rows(n_requests, n, dev), block.Rows(n_requests, n, dev)
+        self.rows = block.Rows(n_requests, n, dev)
         self.rows.cursor.copy_(torch.tensor([0, n_pages]))
+        self.state = self.rows.state.clone()
         self.rotary = block.Rotary(freq, head_dim, axis=axis, n_axes=n_axes, interleaved=interleaved)
         self.attention = block.PagedAttention(self.cache, n_heads, window=window)
         self.norm_in = block.ResidualNorm(d, kind, pre_weight=norm_in, eps=eps, device=dev)
@@ -329,10 +332,11 @@ class AttentionStep:
         (negative: the request ends); pos int32 [n_axes][n] (None: every axis
         at the token's position). Writes and returns (h_out, x_out); self.rows
         holds the step's rows (block.Rows)."""
+        import torch
         from . import block
-        prev, rows = self.rows, self._other
-        block.assign_pages(prev.seq_len, new_len, self.table, self.ring, prev.cursor, self.cache.page_size, rows,
-                           fit_rows=True,
+        rows = self.rows
+        cursor, seq_len = block.split_state(self.state, rows.n_requests)
+        block.assign_pages(seq_len, new_len, self.table, self.ring, cursor, self.cache.page_size, rows, fit_rows=True,
                            one_each=self.one_each)
         qkv, out = self.qkv, self.out
         self.norm_in.forward(None, h, None, qkv.x)
@@ -344,7 +348,7 @@ class AttentionStep:
         out.layer.forward(out.batch, out.x, out.W, out.y)
         self.norm_out.forward(out.y, h, h_out, x_out, gate=gate)
         # (last, so that a call that was refused on its way may be made again)
-        self.rows, self._other = rows, prev
+        torch.add(rows.state, 0, out=self.state)
         return h_out, x_out
 
     def close(self):
@@ -448,11 +452,11 @@ def attention_rows(torch, context, n=128, heads=32, kv_heads=8, head_dim=128, pa
     h_out, x_out = torch.empty_like(h), torch.empty((n, d), dtype=fu.x.dtype, device=dev)
     # every request holds `context` positions; the timed steps bring the same next token again
     from . import block
-    grown, rows = block.Rows(n, n * context, dev), block.Rows(n, n, dev)
+    grown, rows = block.Rows(n, n * context, dev), st.rows
     block.assign_pages(st.rows.seq_len, new * context, st.table, st.ring, st.rows.cursor, page_size, grown)
 
     def step():
-        st.rows, st._other = grown, rows
+        st.state.copy_(grown.state)
         return st.forward(h, new, h_out, x_out)
 
     parts = [("attention step", step),

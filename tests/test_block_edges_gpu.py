@@ -205,8 +205,8 @@ def _oracle_attention(st, q, k, v, seen):
     return _attend_ref(q, kc, vc, table, lens, range(N), 0, 1 / math.sqrt(D))
 
 
-@pytest.mark.parametrize("one_each", [False, True])
-def test_step_reads_its_own_request(one_each):
+@pytest.mark.parametrize("one_each, captured", [(False, False), (True, False), (False, True), (True, True)])
+def test_step_reads_its_own_request(one_each, captured):
     """Every row's attention is over what its own request stored, whatever
     requests before it ended, rested or found no page (a record of each
     request's keys and values is kept here, by request and not by row)."""
@@ -214,10 +214,21 @@ def test_step_reads_its_own_request(one_each):
     g = torch.Generator().manual_seed(3)
     k, v, held = [[] for _ in range(N)], [[] for _ in range(N)], 0
     rng = np.random.default_rng(4)
-    for step in range(7):
+    h, new_d = torch.zeros((N, H * D), device=DEV), _int(np.zeros(N))
+    h_out, x_out = torch.empty_like(h), torch.empty((N, H * D), dtype=BF16, device=DEV)
+    if captured:
+        st.forward(h, new_d, h_out, x_out)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            st.forward(h, new_d, h_out, x_out)
+    for step in range(9):
         new = np.where(rng.random(N) < 0.25, np.where(rng.random(N) < 0.5, -1, 0), 1) if step else np.ones(N, int)
-        h = torch.randn((N, H * D), generator=g).to(DEV)
-        st.forward(h, _int(new), torch.empty_like(h), torch.empty((N, H * D), dtype=BF16, device=DEV))
+        h.copy_(torch.randn((N, H * D), generator=g))
+        new_d.copy_(_int(new))
+        if captured and step % 4 != 2:
+            graph.replay()
+        else:
+            st.forward(h, new_d, h_out, x_out)
         torch.cuda.synchronize()
         seen, slot = st.rows.req.tolist(), st.rows.slot.tolist()
         for r in range(N):
