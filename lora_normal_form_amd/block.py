@@ -43,13 +43,13 @@ def _bad(what):
 
 # torch's current stream of a device as an address (its accessor without the
 # Stream object, which costs more than a launch's other checks together)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _stream(stream, index):
     if stream is None:
-        return _raw_stream(index)
+        return current_stream(index)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 

@@ -331,22 +331,24 @@ class AttentionStep:
         """h [n][d] the residual stream; new_len int32 [n_requests] on the GPU
         (negative: the request ends); pos int32 [n_axes][n] (None: every axis
         at the token's position). Writes and returns (h_out, x_out); self.rows
-        holds the step's rows (block.Rows)."""
+        holds the step's rows (block.Rows). Runs on torch's current stream of
+        the tensors' device, the layers too."""
         import torch
         from . import block
-        rows = self.rows
+        rows, s = self.rows, block.current_stream(self.cache.index)
         cursor, seq_len = block.split_state(self.state, rows.n_requests)
-        block.assign_pages(seq_len, new_len, self.table, self.ring, cursor, self.cache.page_size, rows, fit_rows=True,
-                           one_each=self.one_each)
+        block.assign_pages(seq_len, new_len, self.table, self.ring, cursor, self.cache.page_size, rows, stream=s,
+                           fit_rows=True, one_each=self.one_each)
         qkv, out = self.qkv, self.out
-        self.norm_in.forward(None, h, None, qkv.x)
-        qkv.layer.forward(qkv.batch, qkv.x, qkv.W, qkv.y)
+        self.norm_in.forward(None, h, None, qkv.x, stream=s)
+        qkv.layer.forward(qkv.batch, qkv.x, qkv.W, qkv.y, stream=s)
         if pos is None:
             pos = rows.pos if self.rotary.n_axes == 1 else rows.pos.expand(self.rotary.n_axes, -1)
-        self.rotary.store(self.q, self.k, self.v, pos, rows.slot, self.cache, self.q_rot)
-        self.attention.forward(self.q_rot, self.table, rows.len, self.a, row_req=None if self.one_each else rows.req)
-        out.layer.forward(out.batch, out.x, out.W, out.y)
-        self.norm_out.forward(out.y, h, h_out, x_out, gate=gate)
+        self.rotary.store(self.q, self.k, self.v, pos, rows.slot, self.cache, self.q_rot, stream=s)
+        self.attention.forward(self.q_rot, self.table, rows.len, self.a, row_req=None if self.one_each else rows.req,
+                               stream=s)
+        out.layer.forward(out.batch, out.x, out.W, out.y, stream=s)
+        self.norm_out.forward(out.y, h, h_out, x_out, gate=gate, stream=s)
         # (last, so that a call that was refused on its way may be made again)
         torch.add(rows.state, 0, out=self.state)
         return h_out, x_out

@@ -74,3 +74,27 @@ def test_assign_refuses_fewer_rows_than_requests():
     with pytest.raises(scute.ScuteError, match="a row for each") as e:
         scute.scute_cache_assign(_assign_args(flags=scute.ASSIGN_ONE_EACH, max_tokens=3), 0)
     assert e.value.code == scute.E_SHAPE
+
+
+# ---- the attention step ----------------------------------------------------------------------------
+
+def test_step_runs_on_the_stream_of_its_tensors_device(monkeypatch):
+    """The layers and the operators between them run on one stream, that of the
+    device of the step's tensors, whichever device is current."""
+    from lora_normal_form_amd import multiproj
+    streams = []
+
+    class Part:
+        def __getattr__(self, name):
+            return lambda *a, stream=None, **kw: streams.append((name, stream))
+
+    layer = lambda: SimpleNamespace(layer=Part(), batch=0, x=0, W=0, y=0)  # noqa: E731
+    rows = block.Rows(2, 3, device="cpu")
+    st = _handle(multiproj.AttentionStep, qkv=layer(), out=layer(), one_each=False, rows=rows, state=rows.state.clone(),
+                 table=0, ring=0, cache=SimpleNamespace(index=1, page_size=4), rotary=SimpleNamespace(n_axes=1, store=Part().store),
+                 attention=Part(), norm_in=Part(), norm_out=Part(), q=0, k=0, v=0, q_rot=0, a=0)
+    monkeypatch.setattr(block, "current_stream", lambda index: 1000 + index)
+    monkeypatch.setattr(block, "assign_pages", Part().assign_pages)
+    st.forward(0, 0, 0, 0)
+    assert streams == [(name, 1001) for name in ("assign_pages", "forward", "forward", "store", "forward", "forward",
+                                                 "forward")]
