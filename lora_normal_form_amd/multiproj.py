@@ -278,11 +278,19 @@ class AttentionStep:
     qkv: a QKVFused over projections of n_heads, n_kv_heads and n_kv_heads
     heads of head_dim columns. wl_out: the output projection's workload (d_in
     n_heads head_dim, its own tenants), whose rows' inputs the attention
-    writes. The rows are the requests' new tokens in the requests' order (the
-    plans' tenants follow that order); rows past the last token, and those of
+    writes. The rows are the requests' new tokens in the requests' order; rows past the last token, and those of
     a request that found no pages, go through the layers and are skipped by the
     cache and the attention. So is a request with tokens past the last row:
     it keeps its length and may bring them again.
+
+    Whose adapters a row runs under: without `tenants` those that the two plans
+    give row i in every step, which fits steps whose rows stay their requests'
+    (one_each, or the same new lengths every time). tenants: int32 [2][n_requests]
+    on the GPU, each request's adapter in the q / k / v layer and in the output
+    projection (-1: none); every row then runs under its request's, whichever
+    row it is, in layers that take the rows' adapters from the GPU
+    (scute_layer_forward_noalloc: its sizes, its speed). `tenants` stays the
+    step's, to be written where a request changes hands.
 
     The step keeps the requests' lengths, pages and free pages on the GPU:
     table [n_requests][pages_per_request], ring (n_pages free pages at first),
@@ -296,7 +304,8 @@ class AttentionStep:
 
     def __init__(self, qkv, wl_out, n_heads, n_kv_heads, head_dim, n_requests, pages_per_request, page_size,
                  n_pages, freq, axis=None, n_axes=1, interleaved=False, norm_in=None, norm_post=None, norm_out=None,
-                 kind="rms", eps=1e-5, h_scale=1.0, y_scale=1.0, window=0, one_each=False, device=0):
+                 kind="rms", eps=1e-5, h_scale=1.0, y_scale=1.0, window=0, one_each=False, device=0,
+                 tenants=None):
         import torch
         from . import block
         from . import workload as glue
@@ -308,6 +317,8 @@ class AttentionStep:
         if one_each and n != n_requests:
             raise ValueError("one_each needs a row for each request")
         dev = qkv.x.device
+        if tenants is not None and (tenants.dtype != torch.int32 or tenants.shape != (2, n_requests)):
+            raise ValueError("tenants must be int32 [2][n_requests]")
         self.qkv, self.out = qkv, glue.load(wl_out, device=device)
         self.one_each, dt = one_each, qkv.x.dtype
         q, k, v = (qkv.y[:, a:b] for a, b in zip((0, *np.cumsum(qkv.d_outs)), np.cumsum(qkv.d_outs)))
@@ -324,6 +335,10 @@ class AttentionStep:
         self.norm_in = block.ResidualNorm(d, kind, pre_weight=norm_in, eps=eps, device=dev)
         self.norm_out = block.ResidualNorm(d, kind, post=norm_post is not None, post_weight=norm_post,
                                            pre_weight=norm_out, h_scale=h_scale, y_scale=y_scale, eps=eps, device=dev)
+        # (column 0: rows of no request)
+        self._ids = torch.full((2, n_requests + 1), -1, dtype=torch.int32, device=dev)
+        self.tenants = None if tenants is None else self._ids[:, 1:].copy_(tenants)
+        self._column, self._row_ids = (torch.empty(s, dtype=torch.int32, device=dev) for s in ((n,), (2, n)))
         self.q_rot = torch.empty((n, n_heads, head_dim), dtype=dt, device=dev)
         self.a = self.out.x.view(n, n_heads, head_dim)
 
@@ -341,17 +356,26 @@ class AttentionStep:
                            fit_rows=True, one_each=self.one_each)
         qkv, out = self.qkv, self.out
         self.norm_in.forward(None, h, None, qkv.x, stream=s)
-        qkv.layer.forward(qkv.batch, qkv.x, qkv.W, qkv.y, stream=s)
+        if self.tenants is not None:
+            torch.add(rows.req, 1, out=self._column)
+            torch.index_select(self._ids, 1, self._column, out=self._row_ids)
+        self._layer(qkv, 0, s)
         if pos is None:
             pos = rows.pos if self.rotary.n_axes == 1 else rows.pos.expand(self.rotary.n_axes, -1)
         self.rotary.store(self.q, self.k, self.v, pos, rows.slot, self.cache, self.q_rot, stream=s)
         self.attention.forward(self.q_rot, self.table, rows.len, self.a, row_req=None if self.one_each else rows.req,
                                stream=s)
-        out.layer.forward(out.batch, out.x, out.W, out.y, stream=s)
+        self._layer(out, 1, s)
         self.norm_out.forward(out.y, h, h_out, x_out, gate=gate, stream=s)
         # (last, so that a call that was refused on its way may be made again)
         torch.add(rows.state, 0, out=self.state)
         return h_out, x_out
+
+    def _layer(self, ld, which, stream):
+        if self.tenants is None:
+            ld.layer.forward(ld.batch, ld.x, ld.W, ld.y, stream=stream)
+        else:
+            ld.layer.forward_noalloc(self._row_ids[which], ld.x, ld.W, ld.y, stream=stream)
 
     def close(self):
         self.out.batch.close()

@@ -2,6 +2,7 @@
 sizes and orders of calls that the documentation allows, against plain
 implementations in 64 bits (tests/test_block_gpu.py, whose bounds hold here)."""
 
+import dataclasses
 import math
 
 import numpy as np
@@ -10,7 +11,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from lora_normal_form_amd import block  # noqa: E402
-from test_block_step_gpu import D, H, N, _step  # noqa: E402
+from test_block_step_gpu import D, H, N, _bar, _step  # noqa: E402
 from test_block_gpu import BF16, DEV, F32, _assign_case, _attend_case, _attend_ref, _close, _int  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -264,5 +265,43 @@ def test_step_refused_on_its_way_may_come_again():
     assert st.rows.seq_len.tolist() == [5, 0, 6, 6, 1]
     # 5 pages were taken, then 3 and one given back
     assert st.rows.cursor.tolist() == [5 + 3, 30 + 1], st.rows.cursor.tolist()
+    st.close()
+    st.qkv.close()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_step_runs_rows_under_their_requests_adapters(captured):
+    """With `tenants` a row's adapters are its request's, whichever row it is:
+    requests that rest, end, bring prompts, and one that changes hands."""
+    ids = np.array([[0, 1, 2, 4, -1], [0, 2, -1, 1, 1]])
+    st, wls, wl_out, *_ = _step(97, tenants=_int(ids))
+    g = torch.Generator().manual_seed(9)
+    h, new_d = torch.zeros((N, H * D), device=DEV), _int(np.zeros(5))
+    h_out, x_out = torch.empty_like(h), torch.empty((N, H * D), dtype=BF16, device=DEV)
+    st.forward(h, new_d, h_out, x_out)
+    graph = torch.cuda.CUDAGraph() if captured else None
+    if captured:
+        with torch.cuda.graph(graph):
+            st.forward(h, new_d, h_out, x_out)
+    for step, new in enumerate(([9, 0, 1, 2, 5], [0, 6, 1, 0, 1], [1, -1, 0, 1, 1], [-1, 3, 1, 12, 2], [4, 1, 1, 1, 1])):
+        if step == 3:
+            ids[:, 1] = (3, 0)
+            st.tenants[:, 1] = _int(ids[:, 1])
+        h.copy_(torch.randn((N, H * D), generator=g))
+        new_d.copy_(_int(new))
+        graph.replay() if captured and step != 2 else st.forward(h, new_d, h_out, x_out)
+        torch.cuda.synchronize()
+        req = st.rows.req.cpu().numpy()
+        assert np.array_equal(req[req >= 0], np.repeat(np.arange(5), np.maximum(0, new)))
+        ten = np.where(req >= 0, ids[:, req], -1)
+        c0 = 0
+        for wl, of in wls:
+            wl = dataclasses.replace(wl, token_adapter=np.array([of.get(t, -1) for t in ten[0].tolist()]))
+            _bar(wl, st.qkv.x.cpu().double().numpy(), st.qkv.y[:, c0:c0 + wl.d_out].cpu().double().numpy())
+            c0 += wl.d_out
+        _bar(dataclasses.replace(wl_out, token_adapter=ten[1]), st.out.x.cpu().double().numpy(),
+             st.out.y.cpu().double().numpy())
+    with pytest.raises(ValueError, match="tenants"):
+        _step(97, tenants=_int(ids[:, :4]))
     st.close()
     st.qkv.close()

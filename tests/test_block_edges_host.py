@@ -90,7 +90,7 @@ def test_step_runs_on_the_stream_of_its_tensors_device(monkeypatch):
 
     layer = lambda: SimpleNamespace(layer=Part(), batch=0, x=0, W=0, y=0)  # noqa: E731
     rows = block.Rows(2, 3, device="cpu")
-    st = _handle(multiproj.AttentionStep, qkv=layer(), out=layer(), one_each=False, rows=rows, state=rows.state.clone(),
+    st = _handle(multiproj.AttentionStep, qkv=layer(), out=layer(), one_each=False, tenants=None, rows=rows, state=rows.state.clone(),
                  table=0, ring=0, cache=SimpleNamespace(index=1, page_size=4), rotary=SimpleNamespace(n_axes=1, store=Part().store),
                  attention=Part(), norm_in=Part(), norm_out=Part(), q=0, k=0, v=0, q_rot=0, a=0)
     monkeypatch.setattr(block, "current_stream", lambda index: 1000 + index)
