@@ -627,6 +627,9 @@ namespace {
 
 bool misaligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) != 0; }
 
+// work-groups of `threads` that one launch may have in x (2^32 - 1 threads)
+int64_t most_groups(int threads) { return 0xFFFFFFFFll / threads; }
+
 scute_status launched(const char* fn) {
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SCUTE_OK : hip_fail(e, fn);
@@ -742,7 +745,7 @@ extern "C" scute_status scute_rotary_store(const scute_rotary* Ro, const scute_k
   if (!g.ok()) return hip_fail(g.err, fn);
 
   const int n = Ro->rot_dim / 2;
-  const RotArgs A{Ro->freq, Ro->axis, q, k, v, pos, slot, q_out, C->k, C->v, q_stride, k_stride, v_stride, pos_stride,
+  RotArgs A{Ro->freq, Ro->axis, q, k, v, pos, slot, q_out, C->k, C->v, q_stride, k_stride, v_stride, pos_stride,
                   q_out_stride, C->page_stride, C->token_stride, C->head_stride, C->n_pages * C->page_size,
                   C->head_dim, n, Ro->n_axes, Ro->interleaved, n_heads, C->n_kv_heads, C->page_size};
   // four elements an access where every row's accesses are aligned to them and
@@ -756,8 +759,15 @@ extern "C" scute_status scute_rotary_store(const scute_rotary* Ro, const scute_k
   // few tokens: their units spread over more work-groups, one unit a thread
   const int64_t parts = std::min<int64_t>(std::min<int64_t>((units + 255) / 256, 4096),
                                           std::max<int64_t>(1, 1024 / n_tokens));
-  const dim3 grid((unsigned)n_tokens, (unsigned)parts);
   const hipStream_t s = (hipStream_t)stream;
+  for (int64_t t = 0; t < n_tokens; t += most_groups(256)) {
+    const dim3 grid((unsigned)std::min(most_groups(256), n_tokens - t), (unsigned)parts);
+    A.q = (const char*)q + t * q_stride * (int64_t)es;
+    A.k = (const char*)k + t * k_stride * (int64_t)es;
+    A.v = (const char*)v + t * v_stride * (int64_t)es;
+    A.q_out = (char*)q_out + t * q_out_stride * (int64_t)ed;
+    A.pos = pos ? pos + t : nullptr;
+    A.slot = slot + t;
 #define ROT(S, D)                                                                    \
   do {                                                                               \
     if (vec)                                                                         \
@@ -765,16 +775,19 @@ extern "C" scute_status scute_rotary_store(const scute_rotary* Ro, const scute_k
     else                                                                             \
       hipLaunchKernelGGL((k_rotary_store<S, D, 1>), grid, dim3(256), 0, s, A);       \
   } while (0)
-  if (es == 4 && ed == 4)
-    ROT(float, float);
-  else if (es == 4)
-    ROT(float, uint16_t);
-  else if (ed == 4)
-    ROT(uint16_t, float);
-  else
-    ROT(uint16_t, uint16_t);
+    if (es == 4 && ed == 4)
+      ROT(float, float);
+    else if (es == 4)
+      ROT(float, uint16_t);
+    else if (ed == 4)
+      ROT(uint16_t, float);
+    else
+      ROT(uint16_t, uint16_t);
 #undef ROT
-  return launched(fn);
+    const scute_status ls = launched(fn);
+    if (ls != SCUTE_OK) return ls;
+  }
+  return SCUTE_OK;
 }
 
 extern "C" scute_status scute_residual_norm(const scute_norm* N, const void* y, int32_t y_dtype, int64_t y_stride,
@@ -815,7 +828,7 @@ extern "C" scute_status scute_residual_norm(const scute_norm* N, const void* y, 
   OnDevice g(N->device);
   if (!g.ok()) return hip_fail(g.err, fn);
 
-  const NormArgs A{y, h, gate, h_out, x, N->post_w, N->post_b, N->pre_w, N->pre_b, y_stride, h_stride, gate_stride,
+  NormArgs A{y, h, gate, h_out, x, N->post_w, N->post_b, N->pre_w, N->pre_b, y_stride, h_stride, gate_stride,
                    h_out_stride, x_stride, y_dtype == SCUTE_BF16, h_dtype == SCUTE_BF16, x_dtype == SCUTE_BF16,
                    N->kind, N->post, N->d, N->eps, N->h_scale, N->y_scale, 1.f / (float)N->d};
   const int V = vec ? 4 : 1, units = N->d / V;
@@ -827,18 +840,28 @@ extern "C" scute_status scute_residual_norm(const scute_norm* N, const void* y, 
   while (threads < most && units > threads) threads *= 2;
   const int per = (units + threads - 1) / threads;  // at most 8 of 4 elements, 32 of one
   const hipStream_t s = (hipStream_t)stream;
-#define NORM(VV, NN) hipLaunchKernelGGL((k_residual_norm<VV, NN>), dim3((unsigned)n_rows), dim3(threads), 0, s, A)
-  if (vec) {
-    if (per <= 1) NORM(4, 1);
-    else if (per <= 2) NORM(4, 2);
-    else if (per <= 4) NORM(4, 4);
-    else NORM(4, 8);
-  } else {
-    if (per <= 1) NORM(1, 1);
-    else if (per <= 4) NORM(1, 4);
-    else if (per <= 8) NORM(1, 8);
-    else hipLaunchKernelGGL(k_residual_norm_long, dim3((unsigned)n_rows), dim3(threads), 0, s, A);
-  }
+  for (int64_t r = 0; r < n_rows; r += most_groups(threads)) {
+    const dim3 grid((unsigned)std::min(most_groups(threads), n_rows - r));
+    A.y = y ? (const char*)y + r * y_stride * (int64_t)ey : nullptr;
+    A.h = (const char*)h + r * h_stride * (int64_t)eh;
+    A.gate = gate ? gate + r * gate_stride : nullptr;
+    A.h_out = h_out ? (char*)h_out + r * h_out_stride * (int64_t)eh : nullptr;
+    A.x = x ? (char*)x + r * x_stride * (int64_t)ex : nullptr;
+#define NORM(VV, NN) hipLaunchKernelGGL((k_residual_norm<VV, NN>), grid, dim3(threads), 0, s, A)
+    if (vec) {
+      if (per <= 1) NORM(4, 1);
+      else if (per <= 2) NORM(4, 2);
+      else if (per <= 4) NORM(4, 4);
+      else NORM(4, 8);
+    } else {
+      if (per <= 1) NORM(1, 1);
+      else if (per <= 4) NORM(1, 4);
+      else if (per <= 8) NORM(1, 8);
+      else hipLaunchKernelGGL(k_residual_norm_long, grid, dim3(threads), 0, s, A);
+    }
 #undef NORM
-  return launched(fn);
+    const scute_status ls = launched(fn);
+    if (ls != SCUTE_OK) return ls;
+  }
+  return SCUTE_OK;
 }

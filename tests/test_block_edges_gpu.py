@@ -12,7 +12,7 @@ torch = pytest.importorskip("torch")
 
 from lora_normal_form_amd import block  # noqa: E402
 from test_block_step_gpu import D, H, N, _bar, _step  # noqa: E402
-from test_block_gpu import BF16, DEV, F32, _assign_case, _attend_case, _attend_ref, _close, _int  # noqa: E402
+from test_block_gpu import BF16, DEV, F32, U, _assign_case, _attend_case, _attend_ref, _close, _int  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -150,6 +150,58 @@ def test_assign_a_row_each(R, P, ps, max_new, spare, free_share):
     for name, v in want[2].items():
         assert np.array_equal(getattr(got, name).cpu().numpy(), v), name
     assert bool(((got.req[:R] == -1) | (got.req[:R] == torch.arange(R, device=DEV))).all())
+
+
+# ---- more rows than one launch has threads for ------------------------------------------------------------
+
+def test_rotary_more_tokens_than_a_launch():
+    """2^24 + 5 tokens (a launch has fewer than 2^32 threads): every token of
+    every launch is turned, and stored where its slot says."""
+    T, D = (1 << 24) + 5, 8
+    g = torch.Generator(device=DEV).manual_seed(1)
+    y = torch.randn((T, 3 * D), generator=g, device=DEV, dtype=F32).to(BF16)
+    q, k, v = (t.unflatten(1, (1, D)) for t in y.split(D, dim=1))
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    slot = torch.full((T,), -1, dtype=torch.int64, device=DEV)
+    kept = [0, 3, (1 << 24) - 2, (1 << 24) - 1, 1 << 24, T - 1]
+    slot[torch.tensor(kept, device=DEV)] = torch.arange(len(kept), device=DEV)
+    kc, vc = torch.zeros((2, 4, 1, D), dtype=BF16, device=DEV), torch.zeros((2, 4, 1, D), dtype=BF16, device=DEV)
+    out = torch.zeros((T + 1, 1, D), dtype=BF16, device=DEV)
+    freq = torch.tensor([1.0, 0.1, 0.01, 0.001], dtype=torch.float64, device=DEV)
+    block.Rotary(freq, D).store(q, k, v, pos, slot, block.KVCache(kc, vc), out[:T])
+    torch.cuda.synchronize()
+    ang = pos.double()[:, None] * freq
+    c, s = torch.cos(ang).float(), torch.sin(ang).float()
+
+    def worst(z, got, rows=slice(None)):
+        a, b = z[rows, 0, :4].float(), z[rows, 0, 4:].float()
+        want = torch.cat([a * c[rows] - b * s[rows], a * s[rows] + b * c[rows]], 1)
+        # one rounding to bf16; angle, sine and products in fp32 (the bound of the smaller sizes: under 1e-5)
+        tol = U[BF16] * want.abs() + 1e-5 * (a.abs() + b.abs()).repeat(1, 2)
+        return float(((got[:, 0].float() - want).abs() - tol).max())
+
+    assert worst(q, out[:T]) <= 0 and bool((out[T] == 0).all())
+    at = torch.tensor(kept, device=DEV)
+    assert worst(k, kc.view(8, 1, D)[:6], at) <= 0 and torch.equal(vc.view(8, 1, D)[:6], v[at])
+    assert bool((kc.view(8, D)[6:] == 0).all())
+
+
+def test_norm_more_rows_than_a_launch():
+    """2^26 + 7 rows of one element: 64 threads a row pass 2^32."""
+    T = (1 << 26) + 7
+    g = torch.Generator(device=DEV).manual_seed(1)
+    h, y = torch.randn((T, 1), generator=g, device=DEV), torch.randn((T, 1), generator=g, device=DEV)
+    gate = torch.rand((T, 1), generator=g, device=DEV) + 0.5
+    h_out, x = torch.full((T + 1, 1), 5.0, device=DEV), torch.full((T + 1, 1), 5.0, device=DEV)
+    block.ResidualNorm(1, eps=0.25, device=DEV).forward(y, h, h_out[:T], x[:T], gate=gate)
+    torch.cuda.synchronize()
+    hp = h.double() + y.double() * gate
+    # h': a product and a sum, a rounding each; x: under 16 more roundings of its own size
+    assert bool(((h_out[:T] - hp).abs() <= 2 * U[F32] * (h.abs() + (y * gate).abs())).all())
+    hp = h_out[:T].double()
+    want = hp / torch.sqrt(hp * hp + 0.25)
+    assert bool(((x[:T] - want).abs() <= 16 * U[F32] * want.abs()).all())
+    assert float(h_out[T]) == 5.0 and float(x[T]) == 5.0
 
 
 # ---- the attention step -----------------------------------------------------------------------------------
