@@ -472,8 +472,8 @@ scute_status scute_paged_attention_workspace(int32_t device, int32_t head_dim, i
  * every call leaves its counters zero. Calls that may overlap in time need
  * workspaces of their own.
  * Errors: SCUTE_E_INVALID for null or misaligned pointers, a workspace that
- * is too small, or a scale that is not finite; SCUTE_E_SHAPE for sizes out of
- * range. */
+ * is too small, or a scale that is not finite (times log2(e) in fp32);
+ * SCUTE_E_SHAPE for sizes out of range. */
 scute_status scute_paged_attention(const scute_kv_cache* cache, const void* q, int64_t q_stride,
                                    int32_t n_heads, const int32_t* table, int64_t table_stride,
                                    int32_t n_requests, int32_t table_width, const int32_t* len,

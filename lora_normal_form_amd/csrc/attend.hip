@@ -987,7 +987,8 @@ extern "C" scute_status scute_paged_attention(const scute_kv_cache* C, const voi
     return fail(SCUTE_E_SHAPE,
                 "scute_paged_attention: table_width must be in [1, 2^24] and at most table_stride");
   if (window < 0) return fail(SCUTE_E_SHAPE, "scute_paged_attention: window must be >= 0");
-  if (!isfinite(scale)) return fail(SCUTE_E_INVALID, "scute_paged_attention: scale must be finite");
+  // (the softmax runs on powers of two)
+  if (!isfinite(scale * 1.4426950408889634f)) return fail(SCUTE_E_INVALID, "scute_paged_attention: scale, and scale log2(e) in fp32, must be finite");
   const int64_t wide = (int64_t)n_heads * C->head_dim, big = (int64_t)1 << 40;
   if (q_stride < 0 || q_stride > big || q_stride % 8 || out_stride < 0 || out_stride > big || out_stride % 8)
     return fail(SCUTE_E_SHAPE, "scute_paged_attention: q_stride and out_stride must be multiples of 8 in [0, 2^40]");

@@ -98,3 +98,16 @@ def test_step_runs_on_the_stream_of_its_tensors_device(monkeypatch):
     st.forward(0, 0, 0, 0)
     assert streams == [(name, 1001) for name in ("assign_pages", "forward", "forward", "store", "forward", "forward",
                                                  "forward")]
+
+
+# ---- attention -------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("scale, ok", [(2.4e38, False), (-3.0e38, False), (2.3e38, True)])
+def test_attention_refuses_a_scale_past_fp32(scale, ok):
+    """The scores are taken times scale log2(e): an infinite product would make
+    NaN of equal scores. (What passes the check is turned away for its q.)"""
+    addr = 1 << 20
+    cache = scute.KVCacheDesc(0, scute.BF16, 16, 2, 64, 0, 10, 16 * 128, 128, 64, addr, addr)
+    with pytest.raises(scute.ScuteError, match="null" if ok else "scale"):
+        scute.scute_paged_attention(cache, None, 512, 8, addr, 8, 5, 8, addr, None, 5, scale, 0, addr + 4096, 512, addr,
+                                    1 << 30, 0)
