@@ -451,13 +451,13 @@ scute_status scute_paged_attention_workspace(int32_t device, int32_t head_dim, i
 
 /* Attention of new tokens over the paged cache. Row i belongs to request
  * req[i] (null: request i) and sees that request's positions
- * max(0, n - window) .. n - 1, n = len[i] (window 0: all of them); position t
- * lies in page table[request][t / page_size].
+ * max(0, n - window) .. n - 1 (window 0: all of them), with n = len[i] or, where
+ * that is less, what a row of the table can hold (table_width page_size, and
+ * 2^29); position t lies in page table[request][t / page_size].
  *   out[i][h] = sum_t softmax_t(scale q[i][h] . K[t][g]) V[t][g]
  * with g = h / (n_heads / n_kv_heads). A row that sees nothing (len <= 0, or a
- * request outside 0 .. n_requests - 1) gives zeros; positions past the
- * table's width or from 2^29 on, or whose page lies outside the cache, are not
- * seen.
+ * request outside 0 .. n_requests - 1) gives zeros; positions whose page lies
+ * outside the cache are not seen.
  * q and out [n_rows][n_heads][head_dim] in the cache's type, rows q_stride and
  * out_stride elements apart (multiples of 8, 16-byte aligned pointers).
  * Several rows of one request (its new tokens, each with its own length) are
@@ -465,8 +465,9 @@ scute_status scute_paged_attention_workspace(int32_t device, int32_t head_dim, i
  * its cache. Scores, the softmax and the sums are fp32; the weights enter a
  * bf16 cache's products as sums of two bf16 values. A V that is not finite makes
  * those elements of the output not finite that see it, as the sum says: an
- * infinity stays one. The result depends on the
- * rows' requests and lengths only, never on the order in which work-groups end.
+ * infinity stays one (where its weight is not 0 in fp32). The result depends on
+ * the rows' requests and lengths only, never on the order in which work-groups
+ * end.
  * workspace: `workspace_bytes` (at least what scute_paged_attention_workspace
  * says), 256-byte aligned, zeroed once by the caller before its first use;
  * every call leaves its counters zero. Calls that may overlap in time need
@@ -505,8 +506,8 @@ typedef struct scute_norm {
  * null, [d] (gate_stride 0) or [n_rows][d] float32; h_out [n_rows][d] in h's
  * type (null: not written; may be h itself), x [n_rows][d] (null: no N_pre).
  * Types SCUTE_F32 or SCUTE_BF16, rows *_stride elements apart. x is computed
- * from h' before it is rounded to h's type. Sums are fp32; the variance is
- * summed about the mean.
+ * from h' before it is rounded to h's type. Sums are fp32 (squares whose sum
+ * passes fp32 give zeros); the variance is summed about the mean.
  * Errors: SCUTE_E_INVALID for null or misaligned pointers (each to its
  * element), a bad dtype, x that is also h, y or h_out, or neither output;
  * SCUTE_E_SHAPE for sizes out of range. */
