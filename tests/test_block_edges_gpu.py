@@ -12,7 +12,8 @@ torch = pytest.importorskip("torch")
 
 from lora_normal_form_amd import block  # noqa: E402
 from test_block_step_gpu import D, H, N, _bar, _step  # noqa: E402
-from test_block_gpu import BF16, DEV, F32, U, _assign_case, _attend_case, _attend_ref, _close, _int  # noqa: E402
+from test_block_gpu import (BF16, DEV, F32, U, _assign_case, _attend_case, _attend_ref, _close, _int,  # noqa: E402
+                            _run_attend, test_residual_norm as _check_norm)
 
 pytestmark = pytest.mark.gpu
 
@@ -69,6 +70,130 @@ def test_attention_infinite_v(dt, D, Hq, Hk, ps, lens, req, window):
                            torch.nan_to_num(odd[hit], nan=7.0, posinf=8.0, neginf=9.0))
         zero = torch.zeros_like(got)
         _close(torch.where(hit, zero, got), torch.where(hit, zero, ref), tol, "elsewhere")
+
+
+# ---- attention: every way the work is cut ------------------------------------------------------------------
+
+def _counters(att):
+    """The workspace's counters: the queue's two, and the arrivals at eight
+    places a compute unit, for groups and for all."""
+    units = torch.cuda.get_device_properties(0).multi_processor_count
+    return att.workspace[:4 * (64 + 2 * 8 * units)].view(torch.int32)
+
+
+def _long_ref(q, kc, vc, table, lens, req, window, chain):
+    """(out, bound) on the GPU in 64 bits, all heads of a key head at once. The
+    bound: scores as in _attend_ref; sums whose longest chain has `chain` roundings."""
+    N, H, D = q.shape
+    n_pages, ps, Hk, _ = kc.shape
+    G, out, tol, dt = H // Hk, torch.zeros(q.shape, dtype=torch.float64, device=DEV), [], kc.dtype
+    for i, n in enumerate(lens):
+        lo = max(0, n - window) if window else 0
+        tol.append(torch.zeros((H, D), dtype=torch.float64, device=DEV))
+        if n <= lo:
+            continue
+        pages = table[req[i], :-(-n // ps)].long()
+        for g in range(Hk):
+            K, V = (c[pages, :, g].flatten(0, 1)[lo:n].double() for c in (kc, vc))
+            qh = q[i, g * G:(g + 1) * G].double() / math.sqrt(D)
+            p = torch.softmax(torch.mm(qh, K.T.contiguous()), 1)
+            out[i, g * G:(g + 1) * G] = o = torch.mm(p, V)
+            off = float(torch.mm(qh.abs(), K.abs().T.contiguous()).max()) * (D + 3) * U[F32]
+            rel, mag = 4 * off + chain * U[F32], torch.mm(p, V.abs())
+            tol[-1][g * G:(g + 1) * G] = (rel + (U[dt] ** 2 if dt == BF16 else 0.0)) * mag + U[dt] * (o.abs() + 2 * rel * mag)
+    return out.cpu(), torch.stack(tol).cpu()
+
+
+@pytest.mark.parametrize("dt, each, rows, Hq, Hk, D, ps, run, window", [
+    (BF16, 70, 8, 4, 1, 64, 64, 0, 0),      # a tail of a 16th of the units
+    (BF16, 140, 5, 4, 1, 64, 64, 0, 0),     # of an 8th
+    (BF16, 70, 3, 40, 1, 64, 16, 0, 0),     # two query tiles at once
+    (BF16, 70, 20, 4, 1, 64, 32, 4, 0),     # rows of one request
+    (BF16, 75, 90, 2, 2, 64, 16, 0, 0),     # more than 64 rows
+    (BF16, 72, 300, 2, 1, 64, 16, 0, 0),    # more pieces than work-groups
+    (BF16, 68, 8, 6, 1, 64, 13, 0, 290000),  # pages of any size, a window
+    (F32, 70, 7, 2, 1, 64, 16, 0, 0), (F32, 130, 3, 24, 1, 40, 16, 0, 0)])
+def test_attention_long_work(dt, each, rows, Hq, Hk, D, ps, run, window):
+    """Work enough for the tail of short slices that work-groups take from a
+    counter: values that follow the position, so that no slice can be left out,
+    taken twice or mixed up; the counters are left zero, and the bits repeat."""
+    units = torch.cuda.get_device_properties(0).multi_processor_count
+    per = each * units * (128 if dt == BF16 else 64) // (Hk * max(1, rows // max(1, run)))  # positions a request
+    rng = np.random.default_rng(rows)
+    R = rows // run if run else rows
+    total = (per * (0.8 + 0.4 * rng.random(R))).astype(int)
+    total[-1] += R * per - total.sum()  # (the work asked for, whatever the shares)
+    P = -(-int(total.max()) // ps)
+    g = torch.Generator(device=DEV).manual_seed(each)
+    n_pages = int(sum(-(-int(n) // ps) for n in total)) + 3
+    free = torch.randperm(n_pages, generator=g, device=DEV)
+    kc = torch.randn((n_pages, ps, Hk, D), generator=g, device=DEV, dtype=dt)
+    vc = torch.empty_like(kc)
+    table = torch.full((R, P), -1, dtype=torch.int32, device=DEV)
+    at = 0
+    for r, n in enumerate(total.tolist()):
+        m = -(-n // ps)
+        mine = free[at:at + m]
+        table[r, :m] = mine.int()
+        at += m
+        t = torch.arange(m * ps, device=DEV, dtype=F32)
+        wave = torch.cos(t[:, None] * (2 * math.pi / n) * (1 + torch.arange(D, device=DEV) % 29) + r)
+        vc[mine] = wave.view(m, ps, 1, D).to(dt)
+    q = (0.2 * torch.randn((rows, Hq, D), generator=g, device=DEV)).to(dt)
+    req = np.repeat(np.arange(R), run) if run else np.arange(R)
+    lens = [int(total[r]) - (run - 1 - i % run if run else 0) for i, r in enumerate(req)]
+    att = block.PagedAttention(block.KVCache(kc, vc), Hq, window=window)
+    call = lambda: att.forward(q, table, _int(lens), torch.full_like(q, 9.0), row_req=_int(req) if run else None)  # noqa: E731
+    out = call()
+    torch.cuda.synchronize()
+    assert int(_counters(att).abs().sum()) == 0
+    # a slice has at most 144 units, a tile of each a wave: 40 roundings a tile (32 products and their sums, in two
+    # parts, the running maximum's factor), and as many again for the joins
+    ref, tol = _long_ref(q, kc, vc, table, lens, req, window, 2 * 40 * 144)
+    _close(out, ref, tol, "out")
+    assert torch.equal(call(), out)
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("rows", [65, 257, 600])
+@pytest.mark.parametrize("Hq, Hk, D, ps", [(4, 2, 64, 16), (18, 1, 72, 5), (2, 2, 136, 16)])
+def test_attention_row_a_request(dt, rows, Hq, Hk, D, ps):
+    """More rows than lanes, and than threads, each of a request of its own."""
+    lens = np.random.default_rng(rows).integers(0, 70, size=rows)
+    lens[:5] = [0, 1, 200, 64, 65]
+    kc, vc, table, q = _attend_case(rows + D, lens.tolist(), -(-200 // ps), ps, Hq, Hk, D, dt)
+    att, _ = _run_attend(kc, vc, table, q, lens.tolist())
+    assert int(_counters(att).abs().sum()) == 0
+
+
+@pytest.mark.parametrize("by_request", [False, True])
+def test_attention_in_several_launches(by_request):
+    """A table so wide that the rows go through several launches: later
+    launches read their own rows, requests and lengths."""
+    Hk, D, ps, P = 8, 16, 32, 1 << 24
+    rows = 150 if by_request else 70
+    R = 3 if by_request else rows
+    table = torch.empty((R, P), dtype=torch.int32, device=DEV)
+    table[:, :7] = torch.arange(R * 7, device=DEV).view(R, 7)
+    kc, vc = (torch.randn((R * 7, ps, Hk, D), generator=torch.Generator().manual_seed(s)).to(DEV, BF16) for s in (1, 2))
+    q = torch.randn((rows, 8, D), generator=torch.Generator().manual_seed(3)).to(DEV, BF16)
+    lens = np.random.default_rng(1).integers(0, 200, size=rows)
+    req = np.sort(np.random.default_rng(2).integers(0, R, size=rows)) if by_request else np.arange(rows)
+    out = block.PagedAttention(block.KVCache(kc, vc), 8).forward(
+        q, table, _int(lens), torch.full_like(q, 5.0), row_req=_int(req) if by_request else None)
+    torch.cuda.synchronize()
+    ref, tol = _attend_ref(q, kc, vc, table[:, :7], lens.tolist(), req.tolist(), 0, 1 / math.sqrt(D))
+    _close(out, ref, tol, "out")
+
+
+# ---- the norms: rows by the hundred, and one element an access ------------------------------------------------
+
+@pytest.mark.parametrize("T, d, kind, gate, off", [
+    (600, 4096, "rms", None, 0), (513, 8192, "layer", "token", 0), (520, 16384, "rms", "channel", 0),
+    (513, 1500, "layer", "token", 1), (520, 4001, "rms", "channel", 0), (3, 2500, "layer", None, 1),
+    (2, 6000, "rms", "token", 1), (513, 9000, "layer", None, 1), (700, 64, "rms", None, 0)])
+def test_norm_many_rows(T, d, kind, gate, off):
+    _check_norm(T, d, kind, True, True, gate, F32, BF16 if off else F32, BF16, True, off)
 
 
 # ---- pages and slots ----------------------------------------------------------------------------------------
