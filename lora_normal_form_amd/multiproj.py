@@ -296,6 +296,8 @@ class AttentionStep:
     table [n_requests][pages_per_request], ring (n_pages free pages at first),
     state (cursor and lengths, as in block.Rows). A forward moves them on by its
     last launch, so a captured forward is a new step whenever it is replayed.
+    like: another step of the same sizes, whose cache, table, ring and state this
+    one works on too: one with rows for prompts and a one_each step take turns.
     one_each: row i is request i's, with one token or, where the request brings
     none, ends or finds no page, empty (n is n_requests; more tokens are
     refused); the attention then streams the cache. freq (float64 [pairs]), axis, n_axes
@@ -305,7 +307,7 @@ class AttentionStep:
     def __init__(self, qkv, wl_out, n_heads, n_kv_heads, head_dim, n_requests, pages_per_request, page_size,
                  n_pages, freq, axis=None, n_axes=1, interleaved=False, norm_in=None, norm_post=None, norm_out=None,
                  kind="rms", eps=1e-5, h_scale=1.0, y_scale=1.0, window=0, one_each=False, device=0,
-                 tenants=None):
+                 tenants=None, like=None):
         import torch
         from . import block
         from . import workload as glue
@@ -316,20 +318,27 @@ class AttentionStep:
             raise ValueError("the output projection must take the heads of every row back to the layer's width")
         if one_each and n != n_requests:
             raise ValueError("one_each needs a row for each request")
-        dev = qkv.x.device
+        dev, dt = qkv.x.device, qkv.x.dtype
+        shape = (n_pages, page_size, n_kv_heads, head_dim)
+        if like is not None and (like.cache.k.shape, like.table.shape, like.cache.dtype, like.cache.device) != (
+                shape, (n_requests, pages_per_request), dt, dev):
+            raise ValueError("like: a step whose requests, pages, heads, type or device are others")
         if tenants is not None and (tenants.dtype != torch.int32 or tenants.shape != (2, n_requests)):
             raise ValueError("tenants must be int32 [2][n_requests]")
         self.qkv, self.out = qkv, glue.load(wl_out, device=device)
-        self.one_each, dt = one_each, qkv.x.dtype
+        self.one_each = one_each
         q, k, v = (qkv.y[:, a:b] for a, b in zip((0, *np.cumsum(qkv.d_outs)), np.cumsum(qkv.d_outs)))
         self.q, self.k, self.v = (t.unflatten(1, (-1, head_dim)) for t in (q, k, v))
-        shape = (n_pages, page_size, n_kv_heads, head_dim)
-        self.cache = block.KVCache(torch.zeros(shape, dtype=dt, device=dev), torch.zeros(shape, dtype=dt, device=dev))
-        self.table = torch.zeros((n_requests, pages_per_request), dtype=torch.int32, device=dev)
-        self.ring = torch.arange(n_pages, dtype=torch.int32, device=dev)
         self.rows = block.Rows(n_requests, n, dev)
-        self.rows.cursor.copy_(torch.tensor([0, n_pages]))
-        self.state = self.rows.state.clone()
+        if like is None:
+            self.cache = block.KVCache(torch.zeros(shape, dtype=dt, device=dev), torch.zeros(shape, dtype=dt, device=dev))
+            self.table = torch.zeros((n_requests, pages_per_request), dtype=torch.int32, device=dev)
+            self.ring = torch.arange(n_pages, dtype=torch.int32, device=dev)
+            self.rows.cursor.copy_(torch.tensor([0, n_pages]))
+            self.state = self.rows.state.clone()
+        else:
+            self.cache, self.table, self.ring, self.state = like.cache, like.table, like.ring, like.state
+            self.rows.state.copy_(self.state)
         self.rotary = block.Rotary(freq, head_dim, axis=axis, n_axes=n_axes, interleaved=interleaved)
         self.attention = block.PagedAttention(self.cache, n_heads, window=window)
         self.norm_in = block.ResidualNorm(d, kind, pre_weight=norm_in, eps=eps, device=dev)

@@ -544,3 +544,49 @@ def test_step_forms(dtype, kind, window, interleaved, gate, scales):
         _close(x_out, want, tol + U[dt] * (want.abs() + tol), "x'")
     st.close()
     st.qkv.close()
+
+
+def test_steps_take_turns_on_one_cache():
+    """A step with rows for prompts and a one_each step on the same requests:
+    each goes on from what the other stored."""
+    prompts, *_ = _request_step(101, 5, 40)
+    decode, *_ = _request_step(103, 5, 40, n=5, one_each=True, like=prompts)
+    g, lens = torch.Generator().manual_seed(2), np.zeros(5, int)
+    graph, h5, new5 = torch.cuda.CUDAGraph(), torch.zeros((5, H * D), device=DEV), _int(np.zeros(5))
+    outs = torch.empty_like(h5), torch.empty((5, H * D), dtype=BF16, device=DEV)
+    decode.forward(h5, new5, *outs)
+    with torch.cuda.graph(graph):
+        decode.forward(h5, new5, *outs)
+    for st, new in ((prompts, [9, 7, 0, 8, 0]), (decode, [1, 1, 0, 1, 0]), (decode, [1, -1, 0, 1, 0]),
+                    (prompts, [0, 12, 6, 1, 0]), (decode, [1, 1, 1, 1, 1]), (decode, [0, 1, -1, 1, 1]),
+                    (prompts, [1, 1, 20, 0, 1]), (decode, [1, 1, 1, 1, 1])):
+        n = st.q_rot.shape[0]
+        h = torch.randn((n, H * D), generator=g).to(DEV)
+        if st is decode:
+            h5.copy_(h)
+            new5.copy_(_int(new))
+            graph.replay()
+        else:
+            st.forward(h, _int(new), torch.empty_like(h), torch.empty((n, H * D), dtype=BF16, device=DEV))
+        torch.cuda.synchronize()
+        rows = [(r, lens[r] + i + 1) for r in range(5) for i in range(new[r])]
+        if st is decode:
+            rows = [(r, lens[r] + 1 if new[r] == 1 else 0) for r in range(5)]
+        lens = np.where(np.array(new) < 0, 0, lens + np.maximum(0, new))
+        assert st.rows.seq_len.tolist() == lens.tolist()
+        rows += [(-1, 0)] * (n - len(rows))
+        ref, tol = _attend_ref(st.q_rot, st.cache.k, st.cache.v, st.table, [x for _, x in rows], [r for r, _ in rows], 0,
+                               1 / math.sqrt(D))
+        _close(st.a, ref, tol, "attention")
+        # (the newest key of every row is the one that the step just turned: in its place, not another's)
+        for i, (r, x) in enumerate(rows):
+            if x:
+                at = divmod(x - 1, 4)
+                k = st.cache.k[int(st.table[r, at[0]]), at[1]]
+                v = st.cache.v[int(st.table[r, at[0]]), at[1]]
+                assert torch.equal(v, st.v[i].to(BF16)) and bool(torch.isfinite(k.float()).all())
+    with pytest.raises(ValueError, match="like"):
+        _request_step(103, 5, 41, n=5, one_each=True, like=prompts)
+    for st in (decode, prompts):
+        st.close()
+        st.qkv.close()
