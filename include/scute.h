@@ -324,8 +324,8 @@ scute_status scute_silu_gate(const float* g, const float* u, float* h, int64_t c
  * device's default stream) with that device current, allocates nothing, keeps
  * nothing between calls and may be captured into a graph. Pointers are DEVICE
  * pointers on that device, borrowed for the call, and outputs overlap no
- * input unless stated. Every call checks its arguments before it touches the
- * device. */
+ * input or other output unless stated (SCUTE_E_INVALID where the addresses show
+ * it). Every call checks its arguments before it touches the device. */
 
 /* A paged key-value cache: n_pages pages of page_size positions. Element
  * (page p, position i of the page, head g, dim j) of K and of V lies
@@ -436,7 +436,7 @@ typedef struct scute_rotary {
  * [n_tokens]: a token whose slot is negative or past the cache is not
  * stored; slots that repeat leave one of their tokens, whichever. q_out
  * [n_tokens][n_heads][head_dim] in the cache's type, its rows q_out_stride
- * apart. Products are fp32, rounded once to the cache's type.
+ * apart; it may be q itself where type and stride are the same. Products are fp32, rounded once to the cache's type.
  * Errors: SCUTE_E_INVALID for null or misaligned pointers (each to its
  * element) or a bad dtype, SCUTE_E_SHAPE for sizes out of range. */
 scute_status scute_rotary_store(const scute_rotary* rotary, const scute_kv_cache* cache, const void* q,

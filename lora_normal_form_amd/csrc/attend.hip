@@ -1001,7 +1001,9 @@ extern "C" scute_status scute_paged_attention(const scute_kv_cache* C, const voi
   if (((uintptr_t)table | (uintptr_t)len | (uintptr_t)req) & 3)
     return fail(SCUTE_E_INVALID, "scute_paged_attention: misaligned pointer");
   if ((uintptr_t)workspace & 255) return fail(SCUTE_E_INVALID, "scute_paged_attention: workspace must be 256-byte aligned");
-  if (q == out) return fail(SCUTE_E_INVALID, "scute_paged_attention: out is also q");
+  const int64_t es = C->dtype == SCUTE_F32 ? 4 : 2;
+  if (q == out || rows_meet(q, q_stride * es, wide * es, out, out_stride * es, wide * es, n_rows))
+    return fail(SCUTE_E_INVALID, "scute_paged_attention: out is also q");
   OnDevice g(C->device);
   if (!g.ok()) return hip_fail(g.err, fn);
   int64_t need = 0;
@@ -1015,7 +1017,7 @@ extern "C" scute_status scute_paged_attention(const scute_kv_cache* C, const voi
   const uint64_t mul = (((uint64_t)1 << (31 + shift)) + C->page_size - 1) / C->page_size;
   const int group = n_heads / C->n_kv_heads;
   const int64_t reach = std::min<int64_t>((int64_t)table_width * C->page_size, (int64_t)1 << 29);
-  const int64_t es = C->dtype == SCUTE_F32 ? 4 : 2, unit = es == 4 ? 64 : 128;
+  const int64_t unit = es == 4 ? 64 : 128;
   const int columns = group > 16 && att_widens((int)es, dp) ? 32 : 16;  // (of a query tile: att_mode)
   const int together = req && group <= 8 ? std::min(4, 16 / group) : 1;
   AttArgs A{q, C->k, C->v, out, table, len, req, (float*)((char*)workspace + counters), (int32_t*)workspace, q_stride,

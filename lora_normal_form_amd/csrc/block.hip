@@ -668,9 +668,23 @@ extern "C" scute_status scute_cache_assign(const scute_cache_assign_args* A, voi
   if ((A->flags & SCUTE_ASSIGN_ONE_EACH) && A->max_tokens < A->n_requests)
     return fail(SCUTE_E_SHAPE, "scute_cache_assign: a row for each request needs max_tokens >= n_requests");
   // work-groups read the inputs while others write the outputs
-  if (A->cursor == A->cursor_out || (some && (A->seq_len == A->old_len || A->seq_len == A->new_len ||
-                                              A->cu_len == A->old_len || A->cu_len == A->new_len)))
-    return fail(SCUTE_E_INVALID, "scute_cache_assign: an output is also an input");
+  struct Range {
+    const void* p;
+    int64_t bytes;
+  };
+  const int64_t R = A->n_requests, T = A->max_tokens;
+  const Range ins[] = {{A->cursor, 16}, {some ? A->old_len : nullptr, 4 * R}, {some ? A->new_len : nullptr, 4 * R}};
+  const Range outs[] = {{A->cursor_out, 16}, {some ? A->seq_len : nullptr, 4 * R}, {A->cu_len, 4 * (R + 1)}, {A->counts, 16},
+                        {T ? A->slot : nullptr, 8 * T}, {T ? A->req : nullptr, 4 * T}, {T ? A->pos : nullptr, 4 * T},
+                        {T ? A->len : nullptr, 4 * T}, {A->ring, 4 * (int64_t)A->ring_size}};
+  for (const Range& o : outs) {
+    for (const Range& i : ins)
+      if (rows_meet(o.p, 0, o.bytes, i.p, 0, i.bytes, 1))
+        return fail(SCUTE_E_INVALID, "scute_cache_assign: an output is also an input");
+    for (const Range* b = outs; b < &o; ++b)
+      if (rows_meet(o.p, 0, o.bytes, b->p, 0, b->bytes, 1))
+        return fail(SCUTE_E_INVALID, "scute_cache_assign: outputs overlap");
+  }
   OnDevice g(A->device);
   if (!g.ok()) return hip_fail(g.err, fn);
   AsgArgs G{*A, 0, 0};
@@ -741,6 +755,12 @@ extern "C" scute_status scute_rotary_store(const scute_rotary* Ro, const scute_k
   if (misaligned(q, es) || misaligned(k, es) || misaligned(v, es) || misaligned(q_out, ed) || misaligned(pos, 4) ||
       misaligned(slot, 8) || misaligned(Ro->freq, 8) || misaligned(Ro->axis, 4))
     return fail(SCUTE_E_INVALID, "scute_rotary_store: misaligned pointer");
+  const int64_t wq = n_heads * hd, wk = C->n_kv_heads * hd, si = (int64_t)es, so = (int64_t)ed, T = n_tokens;
+  const bool same = q == q_out && es == ed && (T == 1 || q_stride == q_out_stride);
+  if ((!same && rows_meet(q, q_stride * si, wq * si, q_out, q_out_stride * so, wq * so, T)) ||
+      rows_meet(k, k_stride * si, wk * si, q_out, q_out_stride * so, wq * so, T) ||
+      rows_meet(v, v_stride * si, wk * si, q_out, q_out_stride * so, wq * so, T) || (q == q_out && !same))
+    return fail(SCUTE_E_INVALID, "scute_rotary_store: q_out overlaps q (of another type or stride), k or v");
   OnDevice g(C->device);
   if (!g.ok()) return hip_fail(g.err, fn);
 
@@ -812,13 +832,23 @@ extern "C" scute_status scute_residual_norm(const scute_norm* N, const void* y, 
   if (n_rows == 0) return SCUTE_OK;
   if (!h_out && !x) return fail(SCUTE_E_INVALID, "scute_residual_norm: h_out and x are null");
   if (!h) return fail(SCUTE_E_INVALID, "scute_residual_norm: h is null");
-  if (x && (x == h || x == y || x == h_out))
-    return fail(SCUTE_E_INVALID, "scute_residual_norm: x is also h, y or h_out");
-  if (h_out && (h_out == y || (h_out == h && h_out_stride != h_stride)))
-    return fail(SCUTE_E_INVALID, "scute_residual_norm: h_out is also y, or h with another stride");
   const uintptr_t ey = y_dtype == SCUTE_F32 ? 4 : 2, eh = h_dtype == SCUTE_F32 ? 4 : 2, ex = x_dtype == SCUTE_F32 ? 4 : 2;
   if (misaligned(y, ey) || misaligned(h, eh) || misaligned(h_out, eh) || misaligned(x, ex))
     return fail(SCUTE_E_INVALID, "scute_residual_norm: misaligned pointer");
+  struct Rows {
+    const void* p;
+    int64_t stride, es;
+  };
+  const Rows ry{y, y_stride, (int64_t)ey}, rh{h, h_stride, (int64_t)eh}, rg{gate, gate_stride, 4};
+  const Rows rho{h_out, h_out_stride, (int64_t)eh}, rx{x, x_stride, (int64_t)ex};
+  const auto meet = [&](const Rows& a, const Rows& b) {
+    return a.p && (a.p == b.p || rows_meet(a.p, a.stride * a.es, N->d * a.es, b.p, b.stride * b.es, N->d * b.es, n_rows));
+  };
+  if (meet(rx, rh) || meet(rx, ry) || meet(rx, rho) || meet(rx, rg))
+    return fail(SCUTE_E_INVALID, "scute_residual_norm: x is also h, y, gate or h_out");
+  const bool in_place = h_out == h && (n_rows == 1 || h_out_stride == h_stride);
+  if (meet(rho, ry) || meet(rho, rg) || (!in_place && meet(rho, rh)))
+    return fail(SCUTE_E_INVALID, "scute_residual_norm: h_out is also y or gate, or h at another place or stride");
   bool vec = N->d % 4 == 0 && ((y_stride | h_stride | gate_stride | h_out_stride | x_stride) % 4 == 0) &&
              !misaligned(y, 4 * ey) && !misaligned(h, 4 * eh) && !misaligned(h_out, 4 * eh) && !misaligned(x, 4 * ex);
   for (const float* p : {gate, N->post_w, N->post_b, N->pre_w, N->pre_b}) {

@@ -196,6 +196,42 @@ def test_norm_many_rows(T, d, kind, gate, off):
     _check_norm(T, d, kind, True, True, gate, F32, BF16 if off else F32, BF16, True, off)
 
 
+# ---- inputs and outputs in one buffer ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows", [1, 6])
+def test_columns_of_one_buffer(rows):
+    """Column ranges of one buffer are no overlap, a row's outputs may follow
+    its inputs, and q may be turned where it lies: the same bits as apart."""
+    g = torch.Generator().manual_seed(rows)
+    kc, vc, table, _ = _attend_case(3, [20] * rows, 2, 16, 4, 2, 64, BF16)
+    cache, lens = block.KVCache(kc, vc), _int([20 - i for i in range(rows)])
+    att = block.PagedAttention(cache, 4)
+    wide = torch.randn((rows, 12, 64), generator=g).to(DEV, BF16)
+    apart = att.forward(wide[:, 4:8].contiguous(), table, lens, torch.empty((rows, 4, 64), dtype=BF16, device=DEV))
+    for at in (0, 8):
+        att.forward(wide[:, 4:8], table, lens, wide[:, at:at + 4])
+        torch.cuda.synchronize()
+        assert torch.equal(wide[:, at:at + 4], apart)
+    # rotary: q, k, v and q_out in one buffer, then in place
+    y = torch.randn((rows, 12, 64), generator=g).to(DEV, BF16)
+    q, k, v, out = y[:, :4], y[:, 4:6], y[:, 6:8], y[:, 8:12]
+    ro = block.Rotary(torch.tensor([0.7 ** i for i in range(32)], dtype=torch.float64, device=DEV), 64)
+    pos, slot = _int(range(5, 5 + rows)), torch.arange(rows, device=DEV)
+    apart = ro.store(q.contiguous(), k, v, pos, slot, cache, torch.empty((rows, 4, 64), dtype=BF16, device=DEV))
+    ro.store(q, k, v, pos, slot, cache, out)
+    ro.store(q, k, v, pos, slot, cache, q)
+    torch.cuda.synchronize()
+    assert torch.equal(out, apart) and torch.equal(q, apart)
+    # norms: h, h' and x as columns of one buffer
+    b = torch.randn((rows, 3 * 64), generator=g).to(DEV)
+    norm = block.ResidualNorm(64, device=DEV)
+    y = torch.randn((rows, 64), generator=g).to(DEV)
+    want = norm.forward(y, b[:, 64:128].contiguous(), torch.empty((rows, 64), device=DEV), torch.empty((rows, 64), device=DEV))
+    norm.forward(y, b[:, 64:128], b[:, :64], b[:, 128:])
+    torch.cuda.synchronize()
+    assert torch.equal(b[:, :64], want[0]) and torch.equal(b[:, 128:], want[1])
+
+
 # ---- pages and slots ----------------------------------------------------------------------------------------
 
 def _assign_flags_ref(old, new, table, ring, head, tail, ps, max_tokens, fit, one_each=False):

@@ -111,3 +111,62 @@ def test_attention_refuses_a_scale_past_fp32(scale, ok):
     with pytest.raises(scute.ScuteError, match="null" if ok else "scale"):
         scute.scute_paged_attention(cache, None, 512, 8, addr, 8, 5, 8, addr, None, 5, scale, 0, addr + 4096, 512, addr,
                                     1 << 30, 0)
+
+
+# ---- outputs that overlap inputs -------------------------------------------------------------------
+
+A0 = 1 << 20  # an address that no check may follow
+
+
+def _cache_desc(dtype=scute.BF16):
+    return scute.KVCacheDesc(0, dtype, 16, 2, 64, 0, 10, 16 * 128, 128, 64, 1 << 30, 1 << 31)
+
+
+@pytest.mark.parametrize("output, other, by", [
+    ("cu_len", "old_len", -16), ("seq_len", "old_len", 12), ("seq_len", "new_len", -12), ("pos", "new_len", 0),
+    ("cursor_out", "cursor", 8), ("cursor_out", "seq_len", -8), ("counts", "cursor", 8), ("slot", "cursor", -248),
+    ("req", "pos", -124), ("len", "cu_len", 16), ("ring", "counts", -396), ("ring", "old_len", 12)])
+def test_assign_refuses_overlaps(output, other, by):
+    """Four requests, 32 rows, a ring of 100: one output `by` bytes from another
+    array, of which they share the first or the last element."""
+    a = _assign_args()
+    setattr(a, output, getattr(a, other) + by)
+    with pytest.raises(scute.ScuteError, match="output") as e:
+        scute.scute_cache_assign(a, 0)
+    assert e.value.code == scute.E_INVALID
+
+
+@pytest.mark.parametrize("src, q, q_stride, k, v, out, out_stride, tokens", [
+    (scute.F32, 0, 768, 2048, 2560, 0, 768, 5),            # q_out over a wider q
+    (scute.BF16, 0, 768, 1024, 1280, 0, 1024, 5),          # the same place, another stride
+    (scute.BF16, 0, 768, 1024, 1280, 512, 768, 5),         # a column range that reaches into q's and k's
+    (scute.BF16, 0, 768, 1024, 1280, 768 * 2 * 4 + 16, 768, 5),  # the last row's
+    (scute.BF16, 1 << 14, 512, 0, 1 << 16, 128, 512, 1), (scute.BF16, 1 << 14, 512, 1 << 17, 0, -256, 512, 1)])
+def test_rotary_refuses_overlaps(src, q, q_stride, k, v, out, out_stride, tokens):
+    ro = scute.RotaryDesc(64, 64, 1, 0, 1 << 32, None)
+    with pytest.raises(scute.ScuteError, match="overlaps") as e:
+        scute.scute_rotary_store(ro, _cache_desc(), A0 + q, q_stride, A0 + k, q_stride, A0 + v, q_stride, src, 1 << 33, 0,
+                                 1 << 34, tokens, 8, A0 + out, out_stride, 0)
+    assert e.value.code == scute.E_INVALID
+
+
+@pytest.mark.parametrize("out, q_stride, out_stride, rows", [
+    (0, 512, 512, 5), (16, 512, 512, 1), (-1008, 512, 512, 1), (1024 * 4, 512, 512, 5), (-1024 * 4, 512, 512, 5),
+    (512, 1024, 1024, 5), (2048 * 4 - 16, 1024, 1024, 5)])
+def test_attention_refuses_overlaps(out, q_stride, out_stride, rows):
+    with pytest.raises(scute.ScuteError, match="also q") as e:
+        scute.scute_paged_attention(_cache_desc(), A0 + 8192, q_stride, 8, A0, 8, 5, 8, A0, None, rows, 0.1, 0, A0 + 8192 + out,
+                                    out_stride, 1 << 32, 1 << 30, 0)
+    assert e.value.code == scute.E_INVALID
+
+
+@pytest.mark.parametrize("h_out, x, gate, rows", [
+    (256, 1 << 16, None, 3), (-256, 1 << 16, None, 3), (1 << 16, 512, None, 3), (1 << 16, (1 << 16) + 4, None, 1),
+    (1 << 16, 1 << 17, 1 << 16, 3), (1 << 16, 1 << 17, (1 << 17) + 8, 1), (1 << 15, 1 << 16, None, 3)])
+def test_norm_refuses_overlaps(h_out, x, gate, rows):
+    """h (fp32, 64 elements a row) at 0, y at 2^15."""
+    n = scute.NormDesc(device=0, kind=0, d=64, post=1, eps=1e-5, h_scale=1.0, y_scale=1.0)
+    with pytest.raises(scute.ScuteError, match="is also") as e:
+        scute.scute_residual_norm(n, A0 + (1 << 15), scute.F32, 64, A0, scute.F32, 64, None if gate is None else A0 + gate, 64,
+                                  A0 + h_out, 64, A0 + x, scute.F32, 64, rows, 0)
+    assert e.value.code == scute.E_INVALID
