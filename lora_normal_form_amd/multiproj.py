@@ -290,7 +290,8 @@ class AttentionStep:
     projection (-1: none); every row then runs under its request's, whichever
     row it is, in layers that take the rows' adapters from the GPU
     (scute_layer_forward_noalloc: its sizes, its speed). `tenants` stays the
-    step's, to be written where a request changes hands.
+    step's, to be written where a request changes hands. A caller who knows the
+    new lengths may plan a step's rows instead and hand the plans to forward.
 
     The step keeps the requests' lengths, pages and free pages on the GPU:
     table [n_requests][pages_per_request], ring (n_pages free pages at first),
@@ -351,40 +352,47 @@ class AttentionStep:
         self.q_rot = torch.empty((n, n_heads, head_dim), dtype=dt, device=dev)
         self.a = self.out.x.view(n, n_heads, head_dim)
 
-    def forward(self, h, new_len, h_out, x_out, pos=None, gate=None):
+    def forward(self, h, new_len, h_out, x_out, pos=None, gate=None, plans=None):
         """h [n][d] the residual stream; new_len int32 [n_requests] on the GPU
         (negative: the request ends); pos int32 [n_axes][n] (None: every axis
-        at the token's position). Writes and returns (h_out, x_out); self.rows
-        holds the step's rows (block.Rows). Runs on torch's current stream of
-        the tensors' device, the layers too."""
+        at the token's position); plans: this step's (q / k / v plan, output
+        projection plan) in place of the step's own, each of n rows (of
+        self.qkv.layer and self.out.layer). Writes and returns (h_out, x_out);
+        self.rows holds the step's rows (block.Rows). Runs on torch's current
+        stream of the tensors' device, the layers too."""
         import torch
         from . import block
         rows, s = self.rows, block.current_stream(self.cache.index)
+        if plans is not None and [p.info()["n"] for p in plans] != 2 * [rows.max_tokens]:
+            raise ValueError(f"plans must be two plans of {rows.max_tokens} rows")
         cursor, seq_len = block.split_state(self.state, rows.n_requests)
         block.assign_pages(seq_len, new_len, self.table, self.ring, cursor, self.cache.page_size, rows, stream=s,
                            fit_rows=True, one_each=self.one_each)
         qkv, out = self.qkv, self.out
         self.norm_in.forward(None, h, None, qkv.x, stream=s)
-        if self.tenants is not None:
+        ids = self._row_ids if self.tenants is not None and plans is None else (None, None)
+        plans = plans or (qkv.batch, out.batch)
+        if ids[0] is not None:
             torch.add(rows.req, 1, out=self._column)
             torch.index_select(self._ids, 1, self._column, out=self._row_ids)
-        self._layer(qkv, 0, s)
+        self._layer(qkv, plans[0], ids[0], s)
         if pos is None:
             pos = rows.pos if self.rotary.n_axes == 1 else rows.pos.expand(self.rotary.n_axes, -1)
         self.rotary.store(self.q, self.k, self.v, pos, rows.slot, self.cache, self.q_rot, stream=s)
         self.attention.forward(self.q_rot, self.table, rows.len, self.a, row_req=None if self.one_each else rows.req,
                                stream=s)
-        self._layer(out, 1, s)
+        self._layer(out, plans[1], ids[1], s)
         self.norm_out.forward(out.y, h, h_out, x_out, gate=gate, stream=s)
         # (last, so that a call that was refused on its way may be made again)
         torch.add(rows.state, 0, out=self.state)
         return h_out, x_out
 
-    def _layer(self, ld, which, stream):
-        if self.tenants is None:
-            ld.layer.forward(ld.batch, ld.x, ld.W, ld.y, stream=stream)
+    @staticmethod
+    def _layer(ld, plan, ids, stream):
+        if ids is None:
+            ld.layer.forward(plan, ld.x, ld.W, ld.y, stream=stream)
         else:
-            ld.layer.forward_noalloc(self._row_ids[which], ld.x, ld.W, ld.y, stream=stream)
+            ld.layer.forward_noalloc(ids, ld.x, ld.W, ld.y, stream=stream)
 
     def close(self):
         self.out.batch.close()

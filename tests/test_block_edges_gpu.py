@@ -10,7 +10,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from lora_normal_form_amd import block  # noqa: E402
+from lora_normal_form_amd import block, scute  # noqa: E402
 from test_block_step_gpu import D, H, N, _bar, _step  # noqa: E402
 from test_block_gpu import (BF16, DEV, F32, U, _assign_case, _attend_case, _attend_ref, _close, _int,  # noqa: E402
                             _norm_ref, _run_attend, test_residual_norm as _check_norm)
@@ -482,31 +482,40 @@ def test_step_refused_on_its_way_may_come_again():
     st.qkv.close()
 
 
-@pytest.mark.parametrize("captured", [False, True])
-def test_step_runs_rows_under_their_requests_adapters(captured):
-    """With `tenants` a row's adapters are its request's, whichever row it is:
-    requests that rest, end, bring prompts, and one that changes hands."""
+@pytest.mark.parametrize("how", ["tenants", "captured", "plans"])
+def test_step_runs_rows_under_their_requests_adapters(how):
+    """With `tenants`, or plans made for the step, a row's adapters are its
+    request's, whichever row it is: requests that rest, end, bring prompts, and
+    one that changes hands."""
     ids = np.array([[0, 1, 2, 4, -1], [0, 2, -1, 1, 1]])
-    st, wls, wl_out, *_ = _step(97, tenants=_int(ids))
+    st, wls, wl_out, *_ = _step(97, **({} if how == "plans" else dict(tenants=_int(ids))))
     g = torch.Generator().manual_seed(9)
     h, new_d = torch.zeros((N, H * D), device=DEV), _int(np.zeros(5))
     h_out, x_out = torch.empty_like(h), torch.empty((N, H * D), dtype=BF16, device=DEV)
     st.forward(h, new_d, h_out, x_out)
-    graph = torch.cuda.CUDAGraph() if captured else None
-    if captured:
+    graph = torch.cuda.CUDAGraph()
+    if how == "captured":
         with torch.cuda.graph(graph):
             st.forward(h, new_d, h_out, x_out)
     for step, new in enumerate(([9, 0, 1, 2, 5], [0, 6, 1, 0, 1], [1, -1, 0, 1, 1], [-1, 3, 1, 12, 2], [4, 1, 1, 1, 1])):
         if step == 3:
             ids[:, 1] = (3, 0)
-            st.tenants[:, 1] = _int(ids[:, 1])
+            if how != "plans":
+                st.tenants[:, 1] = _int(ids[:, 1])
         h.copy_(torch.randn((N, H * D), generator=g))
         new_d.copy_(_int(new))
-        graph.replay() if captured and step != 2 else st.forward(h, new_d, h_out, x_out)
+        want = np.repeat(np.arange(5), np.maximum(0, new))
+        ten = np.concatenate([ids[:, want], np.full((2, N - len(want)), -1)], 1)
+        if how == "plans":
+            plans = st.qkv.layer.plan(ten[0]), st.out.layer.plan(ten[1])
+            st.forward(h, new_d, h_out, x_out, plans=plans)
+        elif how == "captured" and step != 2:
+            graph.replay()
+        else:
+            st.forward(h, new_d, h_out, x_out)
         torch.cuda.synchronize()
         req = st.rows.req.cpu().numpy()
-        assert np.array_equal(req[req >= 0], np.repeat(np.arange(5), np.maximum(0, new)))
-        ten = np.where(req >= 0, ids[:, req], -1)
+        assert np.array_equal(req[req >= 0], want)
         c0 = 0
         for wl, of in wls:
             wl = dataclasses.replace(wl, token_adapter=np.array([of.get(t, -1) for t in ten[0].tolist()]))
@@ -514,70 +523,16 @@ def test_step_runs_rows_under_their_requests_adapters(captured):
             c0 += wl.d_out
         _bar(dataclasses.replace(wl_out, token_adapter=ten[1]), st.out.x.cpu().double().numpy(),
              st.out.y.cpu().double().numpy())
+    short = st.qkv.layer.plan(ten[0][:5]), st.out.layer.plan(ten[1])
+    lens = st.rows.seq_len.tolist()
+    with pytest.raises(ValueError, match="plans"):
+        st.forward(h, new_d, h_out, x_out, plans=short)
+    with pytest.raises(scute.ScuteError):  # (each plan belongs to its layer)
+        st.forward(h, new_d, h_out, x_out, plans=(st.out.batch, st.qkv.batch))
+    st.forward(h, _int([0] * 5), h_out, x_out)
+    assert st.rows.seq_len.tolist() == lens
     with pytest.raises(ValueError, match="tenants"):
         _step(97, tenants=_int(ids[:, :4]))
-    st.close()
-    st.qkv.close()
-
-
-def _rotated(z, pos, freq, interleaved):
-    """(pairs turned in 64 bits, bound before the last rounding), z [N][heads][D]."""
-    n = D // 2
-    a, b = (2 * torch.arange(n), 2 * torch.arange(n) + 1) if interleaved else (torch.arange(n), torch.arange(n) + n)
-    c, s = (f(pos.double()[:, None] * freq)[:, None] for f in (torch.cos, torch.sin))
-    out, mag = torch.empty_like(z), torch.empty_like(z)
-    out[..., a], out[..., b] = z[..., a] * c - z[..., b] * s, z[..., a] * s + z[..., b] * c
-    mag[..., a] = mag[..., b] = 2e-6 * (z[..., a].abs() + z[..., b].abs())
-    return out, mag
-
-
-@pytest.mark.parametrize("dtype, kind, window, interleaved, gate, scales", [
-    ("bf16", "layer", 5, True, "channel", (0.5, 2.0)), ("bf16", "rms", 3, False, "token", (1.0, -1.0)),
-    ("f32", "rms", 0, True, None, (1.0, 1.0)), ("f32", "layer", 6, False, "token", (0.25, 1.5))])
-def test_step_forms(dtype, kind, window, interleaved, gate, scales):
-    """The step's forms: fp32 layers, layer norms, windows, adjacent pairs,
-    gates and scales; each operator on what the ones before it left."""
-    from lora_normal_form_amd import multiproj
-    from synth import AdapterSpec, WorkloadSpec, make_workload
-    d, lora, dt, R = H * D, AdapterSpec("lora", rank=16), BF16 if dtype == "bf16" else F32, 5
-    wls, tt = multiproj.projection_workloads([(lora, lora, lora)], N, d, (d, 2 * D, 2 * D), seed=5, dtype=dtype)
-    wl_out = make_workload(WorkloadSpec("out", dtype, d, d, N, [lora], assign="explicit",
-                                        token_adapter=np.zeros(N, int), seed=6))
-    qkv = multiproj.QKVFused(wls, tt, 1)
-    g = torch.Generator().manual_seed(7)
-    w = [(1.0 + 0.2 * torch.randn(d, generator=g)).to(DEV) for _ in range(2)]
-    freq = 100.0 ** (-torch.arange(D // 2, dtype=torch.float64) / (D // 2))
-    st = multiproj.AttentionStep(qkv, wl_out, H, 2, D, R, 9, 4, 40, freq.to(DEV), interleaved=interleaved, norm_in=w[0],
-                                 norm_out=w[1], kind=kind, window=window, h_scale=scales[0], y_scale=scales[1])
-    gt = {None: None, "channel": torch.randn(d, generator=g).to(DEV), "token": torch.randn((N, d), generator=g).to(DEV)}[gate]
-    zero = torch.zeros((N, d), dtype=torch.float64)
-    for new in ([9, 7, 0, 8, 0], [1, 1, 5, 1, 16], [1, -1, 1, 1, 1]):
-        h = torch.randn((N, d), generator=g).to(DEV)
-        x_out = torch.empty((N, d), dtype=dt, device=DEV)
-        h_out, got = st.forward(h, _int(new), torch.empty_like(h), x_out, gate=gt)
-        torch.cuda.synchronize()
-        assert got is x_out
-        want, tol = _norm_ref(h.cpu().double(), zero, kind, w[0], None, 1e-5)
-        _close(st.qkv.x, want, tol + U[dt] * (want.abs() + tol), "x")
-        y, pos = st.qkv.y.cpu().double(), st.rows.pos.cpu()
-        heads = lambda z: z.unflatten(1, (-1, D))  # noqa: E731
-        want, tol = _rotated(heads(y[:, :d]), pos, freq, interleaved)
-        _close(st.q_rot, want, tol + U[dt] * (want.abs() + tol), "q")
-        live = st.rows.slot.cpu() >= 0
-        at = st.rows.slot[live.to(DEV)]
-        want, tol = _rotated(heads(y[:, d:d + 2 * D]), pos, freq, interleaved)
-        _close(st.cache.k.flatten(0, 1)[at], want[live], (tol + U[dt] * (want.abs() + tol))[live], "k")
-        want = heads(y[:, d + 2 * D:])[live]
-        _close(st.cache.v.flatten(0, 1)[at], want, U[dt] * want.abs(), "v")
-        ref, tol = _attend_ref(st.q_rot, st.cache.k, st.cache.v, st.table, st.rows.len.tolist(), st.rows.req.tolist(),
-                               window, 1 / math.sqrt(D))
-        _close(st.a, ref, tol, "attention")
-        z = st.out.y.cpu().double() * (1.0 if gt is None else gt.cpu().double()) * scales[1]
-        hp = scales[0] * h.cpu().double() + z
-        e = 4 * U[F32] * ((scales[0] * h.cpu().double()).abs() + z.abs())
-        _close(h_out, hp, e + U[F32] * hp.abs(), "h'")
-        want, tol = _norm_ref(hp, e, kind, w[1], None, 1e-5)
-        _close(x_out, want, tol + U[dt] * (want.abs() + tol), "x'")
     st.close()
     st.qkv.close()
 
