@@ -462,7 +462,8 @@ scute_status scute_paged_attention_workspace(int32_t device, int32_t head_dim, i
  * out_stride elements apart (multiples of 8, 16-byte aligned pointers).
  * Several rows of one request (its new tokens, each with its own length) are
  * several rows of one call; those that follow each other share the reads of
- * its cache. Scores, the softmax and the sums are fp32; the weights enter a
+ * its cache. Scores, the softmax and the sums are fp32 (values whose sum over a
+ * row's positions passes fp32 give infinities); the weights enter a
  * bf16 cache's products as sums of two bf16 values. A V that is not finite makes
  * those elements of the output not finite that see it, as the sum says: an
  * infinity stays one (where its weight is not 0 in fp32). The result depends on

@@ -26,7 +26,7 @@ struct AttArgs {
 
 // out[h] = sum_t softmax_t(scale q[h] . K[t]) V[t] with a running maximum and
 // sum: one pass over K and V, bound by their bytes (64 rows of 16384 positions,
-// 32 query and 8 key heads of 128 elements: 652 us, 6.6 TB/s; a plain streaming
+// 32 query and 8 key heads of 128 elements: 655 us, 6.6 TB/s; a plain streaming
 // read of as much reaches 6.4 TB/s, with non-temporal loads 7.1).
 //
 // How the work is cut. A unit is four tiles of positions, one for each wave (a
@@ -915,7 +915,11 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
 // read and turned once for both (64 rows of up to 4096 positions, 64 heads over
 // one: 84 us without, 54 with; 1 row of 700: 18 and 20, the wider pieces' join).
 // fp32 heads of more than 128 elements stay at one: the four waves' sums and
-// the queries of two would take 166 KB of LDS.
+// the queries of two would take 166 KB of LDS. bf16 heads of more than 128
+// elements take two although the sums of 32 columns fill the registers: 41 are
+// spilled where the head has 256 elements and pages hold multiples of 16
+// positions, up to 9 otherwise (64 rows of 3000 positions, 24 heads of 256 over
+// one: 62 us, 41 are the bytes').
 constexpr bool att_widens(int es, int dp) { return es == 2 || dp <= 128; }
 
 template <typename T, int DP, int MODE>
