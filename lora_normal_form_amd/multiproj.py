@@ -357,7 +357,8 @@ class AttentionStep:
         (negative: the request ends); pos int32 [n_axes][n] (None: every axis
         at the token's position); plans: this step's (q / k / v plan, output
         projection plan) in place of the step's own, each of n rows (of
-        self.qkv.layer and self.out.layer). Writes and returns (h_out, x_out);
+        self.qkv.layer and self.out.layer; the caller keeps them until the
+        stream has run the step, a graph's as long as the graph). Writes and returns (h_out, x_out);
         self.rows holds the step's rows (block.Rows). Runs on torch's current
         stream of the tensors' device, the layers too."""
         import torch
