@@ -63,8 +63,9 @@ def _gpu(device, *tensors):
             _bad(f"tensors on {t.device} and {device} in one call")
 
 
-def _settle(device):
-    """Waits for a new handle's zeros, so that its first call may be on any stream."""
+def settle(device):
+    """Waits for what a new handle is filled with, so that its first call may be
+    on any stream."""
     if device.type == "cuda":
         with torch.cuda.device(device):
             if not torch.cuda.is_current_stream_capturing():
@@ -148,7 +149,7 @@ class Rows:
             self._filled[name] = torch.zeros(n, dtype=dt, device=dev)
         for name, t in self._filled.items():
             setattr(a, "cursor_out" if name == "cursor" else name, t.data_ptr())
-        _settle(dev)
+        settle(dev)
 
     seq_len, cu_len, slot, req, pos, len, cursor, counts = (
         property(lambda self, name=name: self._filled[name])
@@ -264,7 +265,7 @@ class PagedAttention:
         nbytes = scute.scute_paged_attention_workspace(cache.device.index, cache.head_dim)
         self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=cache.device)
         self.max_rows = None if max_rows is None else int(max_rows)
-        _settle(cache.device)
+        settle(cache.device)
 
     def forward(self, q, table, row_len, out, row_req=None, stream=None):
         """q, out [rows][n_heads][head_dim] (the cache's type); table int32

@@ -351,6 +351,7 @@ class AttentionStep:
         self._column, self._row_ids = (torch.empty(s, dtype=torch.int32, device=dev) for s in ((n,), (2, n)))
         self.q_rot = torch.empty((n, n_heads, head_dim), dtype=dt, device=dev)
         self.a = self.out.x.view(n, n_heads, head_dim)
+        block.settle(dev)
 
     def forward(self, h, new_len, h_out, x_out, pos=None, gate=None, plans=None):
         """h [n][d] the residual stream; new_len int32 [n_requests] on the GPU
@@ -358,9 +359,9 @@ class AttentionStep:
         at the token's position); plans: this step's (q / k / v plan, output
         projection plan) in place of the step's own, each of n rows (of
         self.qkv.layer and self.out.layer; the caller keeps them until the
-        stream has run the step, a graph's as long as the graph). Writes and returns (h_out, x_out);
-        self.rows holds the step's rows (block.Rows). Runs on torch's current
-        stream of the tensors' device, the layers too."""
+        stream has run the step, a graph's as long as the graph). Writes and
+        returns (h_out, x_out); self.rows holds the step's rows (block.Rows).
+        Runs on torch's current stream of the tensors' device, the layers too."""
         import torch
         from . import block
         rows, s = self.rows, block.current_stream(self.cache.index)

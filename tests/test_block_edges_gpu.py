@@ -581,3 +581,28 @@ def test_steps_take_turns_on_one_cache():
     for st in (decode, prompts):
         st.close()
         st.qkv.close()
+
+
+def test_step_is_ready_on_every_stream(monkeypatch):
+    """What a step made behind a stream's work keeps is there by the time the
+    step is: its requests' adapters, lengths and pages."""
+    ids = np.array([[0, 1, 2, 4, -1], [0, 2, -1, 1, 1]])
+    side, busy = torch.cuda.Stream(), torch.randn((4096, 4096), device=DEV)
+    side.wait_stream(torch.cuda.current_stream())
+    made = block.ResidualNorm
+
+    def behind_work(*a, **kw):
+        nonlocal busy
+        for _ in range(20):
+            busy = torch.mm(busy, busy).clamp_(-1, 1)
+        return made(*a, **kw)
+
+    monkeypatch.setattr(block, "ResidualNorm", behind_work)
+    with torch.cuda.stream(side):
+        st, *_ = _step(105, tenants=torch.tensor(ids, dtype=torch.int32))
+    got = st.tenants.cpu(), st._ids[:, 0].cpu(), st.state.cpu(), st.ring.cpu()
+    assert np.array_equal(got[0].numpy(), ids) and bool((got[1] == -1).all())
+    assert got[2].tolist() == [0, 30, 0, 0, 0] and got[3].tolist() == list(range(30))
+    torch.cuda.synchronize()
+    st.close()
+    st.qkv.close()
