@@ -414,6 +414,92 @@ typedef struct scute_cache_assign_args {
 
 scute_status scute_cache_assign(const scute_cache_assign_args* args, void* stream);
 
+/* Requests that go on from others, without the host. Request r holds, after
+ * the call, the first keep[r] positions of what request parent[r] held before
+ * it (itself: kept or cut back; another: samples of one prompt, beams; a parent
+ * outside 0 .. n_requests - 1: the request ends), n = min(len[parent], keep)
+ * of them, at most table_width page_size. len[r] positions were held, their
+ * pages in table[r]; entries outside 0 .. n_pages - 1 hold no page.
+ *   - Whole pages are shared: table_out[r] names the parent's.
+ *   - The last page, where n does not fill it, is written next, so it must be
+ *     its request's alone: of the requests that hold it partly the first keeps
+ *     it, when none holds it wholly; each of the others takes a page from the
+ *     head of the ring, in the requests' order, and src[r], dst[r], n[r] say
+ *     which page's first n positions to copy where (scute_cache_copy, for each
+ *     layer's cache; -1, -1, 0: nothing). Where the free pages run out a
+ *     request is refused: it keeps its whole pages, and seq_len[r] says so.
+ *   - window > 0: a page whose positions all lie in [sinks, n - window) is
+ *     dropped (table_out -1), as rows from n on do not see it
+ *     (scute_sink_attention with this window and these sinks).
+ *   - Pages that some request held and none holds any more go to the tail of
+ *     the ring in ascending order, and may be taken from the next step on.
+ * Entries of table_out past a request's pages are -1. The table that is handed
+ * in stays as it is, and table_out may not overlap it. Requests that share
+ * pages, or have dropped some, end here: scute_cache_assign gives back every
+ * entry of a request that ends there.
+ * Lengths and cursors as in scute_cache_assign. workspace: at least what
+ * scute_cache_fork_workspace says, 256-byte aligned, zeroed once before its
+ * first use; calls that may overlap in time need workspaces of their own.
+ * Errors: as scute_cache_assign's; SCUTE_E_INVALID for a workspace that is too
+ * small. */
+typedef struct scute_cache_fork_args {
+  int32_t device;
+  int32_t n_requests;   /* 0 .. 65536                                        */
+  int32_t table_width;  /* 1 .. 2^24                                         */
+  int32_t page_size;    /* 1 .. 65536                                        */
+  int32_t ring_size;    /* 1 .. 2^30                                         */
+  int32_t n_pages;      /* pages of the cache, 1 .. 2^24                     */
+  int32_t window;       /* 0: no page is dropped                             */
+  int32_t sinks;        /* >= 0                                              */
+  int64_t table_stride, table_out_stride; /* >= table_width                  */
+  const int32_t* len;     /* [n_requests]                                    */
+  const int32_t* parent;  /* [n_requests]                                    */
+  const int32_t* keep;    /* [n_requests], null: all                         */
+  const int32_t* table;   /* [n_requests][table_stride]                      */
+  int32_t* ring;          /* [ring_size], updated                            */
+  const int64_t* cursor;  /* [2] head, tail                                  */
+  int64_t* cursor_out;    /* [2]                                             */
+  int32_t* table_out;     /* [n_requests][table_out_stride]                  */
+  int32_t* seq_len;       /* [n_requests] positions held after the call      */
+  int32_t* src;           /* [n_requests] page to copy from                  */
+  int32_t* dst;           /* [n_requests] page to copy to                    */
+  int32_t* n;             /* [n_requests] positions to copy                  */
+  int32_t* counts;        /* [4] requests that hold positions, pages taken,
+                             requests refused, pages returned                */
+  void* workspace;
+  int64_t workspace_bytes;
+} scute_cache_fork_args;
+
+scute_status scute_cache_fork_workspace(int32_t n_requests, int32_t n_pages, int64_t* bytes);
+scute_status scute_cache_fork(const scute_cache_fork_args* args, void* stream);
+
+/* Copy the first n[i] positions (at most a page's) of page src[i] to page
+ * dst[i], K and V, for i in 0 .. n_copies - 1 (device arrays). An entry whose
+ * pages are the same or outside the cache, or whose n is not positive, copies
+ * nothing. No page may be written by two entries, or be read by one and written by another.
+ * Errors: SCUTE_E_INVALID for null or misaligned pointers, SCUTE_E_SHAPE for
+ * n_copies outside 0 .. 2^20. */
+scute_status scute_cache_copy(const scute_kv_cache* cache, const int32_t* src, const int32_t* dst,
+                              const int32_t* n, int32_t n_copies, void* stream);
+
+/* Positions that stay, moved together: of request r, place start[r] + j gets
+ * what position kept[r][j] held before the call, K and V, for j below n_kept[r]
+ * (at most kept_width), so the request then holds new_len[r] = start[r] +
+ * n_kept[r] positions (scute_cache_fork with keep = new_len gives the pages
+ * behind them back). A position only moves down: where kept[r][j] lies before
+ * its new place, or either lies past the table or on a page outside the cache,
+ * the place keeps what it held. Ascending positions always move down.
+ * The pages that are written may not be another request's too. Several layers'
+ * caches are compacted by a call each. start below 0 counts as 0.
+ * table [n_requests][table_stride], kept [n_requests][kept_stride], new_len
+ * null or [n_requests] (start + n_kept saturates at 2^30).
+ * Errors: SCUTE_E_INVALID for null or misaligned pointers or a new_len that is
+ * an input, SCUTE_E_SHAPE for sizes out of range. */
+scute_status scute_cache_compact(const scute_kv_cache* cache, const int32_t* table, int64_t table_stride,
+                                 int32_t n_requests, int32_t table_width, const int32_t* start,
+                                 const int32_t* kept, int64_t kept_stride, int32_t kept_width,
+                                 const int32_t* n_kept, int32_t* new_len, void* stream);
+
 /* Rotary positions: pair i of a head's first rot_dim elements is turned by
  * the angle pos[axis[i]][t] * freq[i] (one axis for text; time, height and
  * width for images and video). The angle is reduced in 64 bits, so far

@@ -4,6 +4,11 @@ and the norms around the residual.
 
   assign_pages    pages and slots of a step's tokens from the requests'
                   lengths, on the GPU (scute_cache_assign)
+  fork_pages      requests that go on from others, are cut back, end or lose
+                  the pages behind a window (scute_cache_fork); copy_pages
+                  copies what it says in each layer's cache (scute_cache_copy)
+  compact         positions of a request that stay, moved together
+                  (scute_cache_compact)
   Rotary.store    rotary positions with several axes; k and v into the paged
                   cache (scute_rotary_store)
   PagedAttention  attention of new tokens over the paged cache
@@ -184,6 +189,95 @@ def assign_pages(old_len, new_len, table, ring, cursor, page_size, rows, stream=
     a.table_width, a.page_size, a.table_stride, a.table = P, page_size, ts if R > 1 else P, table.data_ptr()
     scute._check(scute.lib.scute_cache_assign(a, _stream(stream, rows.device.index)))
     return rows
+
+
+# ---- requests that share pages --------------------------------------------------------------------
+
+class Fork:
+    """What fork_pages fills in for n_requests requests of up to `pages` pages
+    each over a cache of n_pages: table [n_requests][pages], seq_len, and for
+    each request the page to copy, where to, and its positions (src, dst, n
+    [n_requests]; -1, -1, 0: none); cursor [2] (int64) and counts [4] (requests
+    that hold positions, pages taken, requests refused, pages returned). The
+    tensors stay the handle's, as those of Rows; cursor and seq_len are parts of
+    `state`, laid out like a Rows'. The handle owns the workspace of one call at
+    a time: calls that may overlap need handles of their own."""
+
+    def __init__(self, n_requests, pages, n_pages, device=None):
+        dev = torch.device("cuda" if device is None else device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.n_requests, self.pages, self.n_pages, self.device = int(n_requests), int(pages), int(n_pages), dev
+        nbytes = scute.scute_cache_fork_workspace(n_requests, n_pages)
+        a = self.args = scute.CacheForkArgs()
+        a.device = dev.index if dev.type == "cuda" else -1
+        a.n_requests, a.table_width, a.n_pages, a.table_out_stride = n_requests, pages, n_pages, pages
+        self._state = torch.zeros(2 + (n_requests + 1) // 2, dtype=_I64, device=dev)
+        self._filled = dict(zip(("cursor", "seq_len"), split_state(self._state, n_requests)))
+        self._filled["table"] = torch.full((n_requests, pages), -1, dtype=_I32, device=dev)
+        for name, m in (("src", n_requests), ("dst", n_requests), ("n", n_requests), ("counts", 4)):
+            self._filled[name] = torch.zeros(m, dtype=_I32, device=dev)
+        for name, t in self._filled.items():
+            setattr(a, {"cursor": "cursor_out", "table": "table_out"}.get(name, name), t.data_ptr())
+        self._workspace = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        a.workspace, a.workspace_bytes = self._workspace.data_ptr(), nbytes
+        settle(dev)
+
+    table, seq_len, src, dst, n, cursor, counts = (
+        property(lambda self, name=name: self._filled[name])
+        for name in ("table", "seq_len", "src", "dst", "n", "cursor", "counts"))
+    state = property(lambda self: self._state)
+
+
+def fork_pages(seq_len, parent, table, ring, cursor, page_size, fork, keep=None, window=0, sinks=0, stream=None):
+    """Requests that go on from others (scute_cache_fork): request r then holds
+    the first keep[r] (None: all) positions of request parent[r] (itself,
+    another, or outside the requests: it ends). Whole pages are shared; a last
+    page that others hold too is to be copied (copy_pages, in each layer's
+    cache); pages that nobody holds any more go back to the ring; window > 0
+    drops the pages between sinks and the last `window` positions. seq_len,
+    parent, keep int32 [R]; table [R][P] is left as it is, the new one is
+    fork.table. Everything but the ring goes into fork, which is returned."""
+    R, P, a = fork.n_requests, fork.pages, fork.args
+    a.len, a.parent = _vector(seq_len, R, _I32, "seq_len"), _vector(parent, R, _I32, "parent")
+    a.keep = None if keep is None else _vector(keep, R, _I32, "keep")
+    if table.dtype != _I32 or table.shape != (R, P) or (table.stride(1) != 1 and P > 1):
+        _bad(f"table must be int32 [{R}][{P}] with contiguous rows")
+    a.ring_size = size = ring.shape[0]
+    a.ring, a.cursor = _vector(ring, size, _I32, "ring"), _vector(cursor, 2, _I64, "cursor")
+    _gpu(fork.device, seq_len, parent, keep, table, ring, cursor)
+    a.table, a.table_stride, a.page_size = table.data_ptr(), table.stride(0) if R > 1 else P, page_size
+    a.window, a.sinks = window, sinks
+    scute._check(scute.lib.scute_cache_fork(a, _stream(stream, fork.device.index)))
+    return fork
+
+
+def copy_pages(cache, src, dst, n, stream=None):
+    """The first n[i] positions of page src[i] to page dst[i] of a KVCache
+    (scute_cache_copy), int32 [m] each: a Fork's src, dst and n."""
+    m = src.shape[0]
+    sp, dp, np_ = _vector(src, m, _I32, "src"), _vector(dst, m, _I32, "dst"), _vector(n, m, _I32, "n")
+    _gpu(cache.device, src, dst, n)
+    scute._check(scute.lib.scute_cache_copy(cache.desc, sp, dp, np_, m, _stream(stream, cache.index)))
+
+
+def compact(cache, table, start, kept, n_kept, new_len=None, stream=None):
+    """Positions that stay, moved together (scute_cache_compact): place
+    start[r] + j of request r gets what position kept[r][j] held, for
+    j < n_kept[r]. kept int32 [R][places], ascending; new_len int32 [R] gets
+    start + n_kept (the keep of fork_pages, which gives back the pages behind)."""
+    if kept.dim() != 2 or kept.dtype != _I32 or (kept.stride(1) != 1 and kept.shape[1] > 1):
+        _bad("kept must be int32 [n_requests][places] with contiguous rows")
+    R, W = kept.shape
+    if table.dtype != _I32 or table.dim() != 2 or table.shape[0] != R or (table.stride(1) != 1 and table.shape[1] > 1):
+        _bad(f"table must be int32 [{R}][pages] with contiguous rows")
+    P = table.shape[1]
+    sp, kp = _vector(start, R, _I32, "start"), _vector(n_kept, R, _I32, "n_kept")
+    lp = None if new_len is None else _vector(new_len, R, _I32, "new_len")
+    _gpu(cache.device, table, start, kept, n_kept, new_len)
+    scute._check(scute.lib.scute_cache_compact(
+        cache.desc, table.data_ptr(), table.stride(0) if R > 1 else P, R, P, sp, kept.data_ptr(),
+        kept.stride(0) if R > 1 else W, W, kp, lp, _stream(stream, cache.index)))
 
 
 # ---- rotary positions ------------------------------------------------------------------------------

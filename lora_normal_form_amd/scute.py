@@ -91,6 +91,17 @@ class CacheAssignArgs(C.Structure):
 ASSIGN_FIT_ROWS, ASSIGN_ONE_EACH = 1, 2
 
 
+class CacheForkArgs(C.Structure):
+    _fields_ = [("device", C.c_int32), ("n_requests", C.c_int32), ("table_width", C.c_int32),
+                ("page_size", C.c_int32), ("ring_size", C.c_int32), ("n_pages", C.c_int32),
+                ("window", C.c_int32), ("sinks", C.c_int32), ("table_stride", C.c_int64),
+                ("table_out_stride", C.c_int64), ("len", C.c_void_p), ("parent", C.c_void_p),
+                ("keep", C.c_void_p), ("table", C.c_void_p), ("ring", C.c_void_p), ("cursor", C.c_void_p),
+                ("cursor_out", C.c_void_p), ("table_out", C.c_void_p), ("seq_len", C.c_void_p),
+                ("src", C.c_void_p), ("dst", C.c_void_p), ("n", C.c_void_p), ("counts", C.c_void_p),
+                ("workspace", C.c_void_p), ("workspace_bytes", C.c_int64)]
+
+
 class RotaryDesc(C.Structure):
     """scute_rotary"""
     _fields_ = [("head_dim", C.c_int32), ("rot_dim", C.c_int32), ("n_axes", C.c_int32),
@@ -136,6 +147,11 @@ SIGNATURES = {
     "scute_launch_empty": (C.c_int32, [C.c_int32, _P]),
     "scute_silu_gate": (C.c_int32, [_P, _P, _P, C.c_int64, _P]),
     "scute_cache_assign": (C.c_int32, [C.POINTER(CacheAssignArgs), _P]),
+    "scute_cache_fork_workspace": (C.c_int32, [C.c_int32, C.c_int32, C.POINTER(C.c_int64)]),
+    "scute_cache_fork": (C.c_int32, [C.POINTER(CacheForkArgs), _P]),
+    "scute_cache_copy": (C.c_int32, [C.POINTER(KVCacheDesc), _P, _P, _P, C.c_int32, _P]),
+    "scute_cache_compact": (C.c_int32, [C.POINTER(KVCacheDesc), _P, C.c_int64, C.c_int32, C.c_int32, _P, _P,
+                                        C.c_int64, C.c_int32, _P, _P, _P]),
     "scute_rotary_store": (C.c_int32, [C.POINTER(RotaryDesc), C.POINTER(KVCacheDesc), _P, C.c_int64,
                                        _P, C.c_int64, _P, C.c_int64, C.c_int32, _P, C.c_int64, _P,
                                        C.c_int32, C.c_int32, _P, C.c_int64, _P]),
@@ -275,6 +291,27 @@ def scute_silu_gate(g, u, h, count=None, stream=None) -> None:
 
 def scute_cache_assign(args: CacheAssignArgs, stream=None) -> None:
     _check(lib.scute_cache_assign(C.byref(args), _stream_ptr(stream)))
+
+
+def scute_cache_fork_workspace(n_requests: int, n_pages: int) -> int:
+    out = C.c_int64(0)
+    _check(lib.scute_cache_fork_workspace(n_requests, n_pages, C.byref(out)))
+    return out.value
+
+
+def scute_cache_fork(args: CacheForkArgs, stream=None) -> None:
+    _check(lib.scute_cache_fork(C.byref(args), _stream_ptr(stream)))
+
+
+def scute_cache_copy(cache: KVCacheDesc, src, dst, n, n_copies, stream=None) -> None:
+    _check(lib.scute_cache_copy(cache, _ptr(src), _ptr(dst), _ptr(n), n_copies, _stream_ptr(stream)))
+
+
+def scute_cache_compact(cache: KVCacheDesc, table, table_stride, n_requests, table_width, start, kept,
+                        kept_stride, kept_width, n_kept, new_len, stream=None) -> None:
+    _check(lib.scute_cache_compact(cache, _ptr(table), table_stride, n_requests, table_width, _ptr(start),
+                                   _ptr(kept), kept_stride, kept_width, _ptr(n_kept), _ptr(new_len),
+                                   _stream_ptr(stream)))
 
 
 def scute_rotary_store(rotary: RotaryDesc, cache: KVCacheDesc, q, q_stride, k, k_stride, v, v_stride,
