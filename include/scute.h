@@ -531,6 +531,33 @@ scute_status scute_rotary_store(const scute_rotary* rotary, const scute_kv_cache
                                 int64_t pos_stride, const int64_t* slot, int32_t n_tokens,
                                 int32_t n_heads, void* q_out, int64_t q_out_stride, void* stream);
 
+/* Norms of the heads of q and of k, each over a head's head_dim elements,
+ *   N(v) = v / sqrt(mean(v^2) + eps) (.) w + b (SCUTE_NORM_RMS)
+ * or the same of v - mean(v) (SCUTE_NORM_LAYER). */
+typedef struct scute_head_norm {
+  int32_t kind;       /* SCUTE_NORM_RMS (0) or SCUTE_NORM_LAYER (1)           */
+  float eps;
+  const float* q_w;   /* [head_dim], or of each head; null: ones (weights),   */
+  const float* q_b;   /* zeros (biases)                                       */
+  const float* k_w;
+  const float* k_b;
+  int32_t q_stride;   /* elements between the heads' vectors: 0 where all     */
+  int32_t k_stride;   /* heads have the same, head_dim or more otherwise      */
+} scute_head_norm;
+
+/* scute_rotary_store with norms of the heads of q and k before the rotation,
+ * in the same pass: N(q) and N(k) are rotated, v is stored as it is. All of it
+ * is fp32 and rounded once, to the cache's type (squares whose sum passes fp32
+ * give the biases alone; the variance is summed about the mean). Arguments and
+ * errors as there, and SCUTE_E_INVALID for a kind or a vector's address that is
+ * not one, SCUTE_E_SHAPE for a stride between 1 and head_dim - 1, below 0 or past 2^20. */
+scute_status scute_norm_rotary_store(const scute_rotary* rotary, const scute_head_norm* norm,
+                                     const scute_kv_cache* cache, const void* q, int64_t q_stride,
+                                     const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                     int32_t src_dtype, const int32_t* pos, int64_t pos_stride,
+                                     const int64_t* slot, int32_t n_tokens, int32_t n_heads, void* q_out,
+                                     int64_t q_out_stride, void* stream);
+
 /* Bytes of workspace that scute_paged_attention may use on `device` for
  * heads of head_dim elements. */
 scute_status scute_paged_attention_workspace(int32_t device, int32_t head_dim, int64_t* bytes);

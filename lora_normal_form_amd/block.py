@@ -10,7 +10,8 @@ and the norms around the residual.
   compact         positions of a request that stay, moved together
                   (scute_cache_compact)
   Rotary.store    rotary positions with several axes; k and v into the paged
-                  cache (scute_rotary_store)
+                  cache (scute_rotary_store), with norms of the heads (HeadNorm)
+                  in the same pass (scute_norm_rotary_store)
   PagedAttention  attention of new tokens over the paged cache
                   (scute_paged_attention)
   ResidualNorm    the norms after and before a block, with its gate and
@@ -282,6 +283,36 @@ def compact(cache, table, start, kept, n_kept, new_len=None, stream=None):
 
 # ---- rotary positions ------------------------------------------------------------------------------
 
+class HeadNorm:
+    """Norms of q's and k's heads, each over a head's head_dim elements, before
+    the rotation (Rotary.store). kind "rms" or "layer"; weights and biases
+    float32 [head_dim], or [n_heads][head_dim] ([n_kv_heads][head_dim] for k's)
+    for each head its own, on the GPU (None: ones, zeros)."""
+
+    def __init__(self, head_dim, kind="rms", q_weight=None, k_weight=None, q_bias=None, k_bias=None, eps=1e-6):
+        if kind not in ("rms", "layer"):
+            _bad("kind must be 'rms' or 'layer'")
+        self.head_dim, self._vecs, self.heads, ptrs = int(head_dim), (q_weight, q_bias, k_weight, k_bias), [], []
+        for pair, name in (((q_weight, q_bias), "q"), ((k_weight, k_bias), "k")):
+            heads = None
+            for t in pair:
+                if t is not None and (t.dtype != _F32 or t.dim() not in (1, 2) or t.shape[-1] != head_dim or
+                                      not t.is_contiguous()):
+                    _bad(f"{name}'s vectors must be contiguous float32 [{head_dim}] or [heads][{head_dim}]")
+                ptrs.append(None if t is None else t.data_ptr())
+                if t is not None:
+                    own = t.shape[0] if t.dim() == 2 else 0
+                    if heads not in (None, own):
+                        _bad(f"{name}'s weight and bias must be of the same heads")
+                    heads = own
+            self.heads.append(heads or 0)
+        self.device = next((t.device for t in self._vecs if t is not None), None)
+        if self.device is not None:
+            _gpu(self.device, *self._vecs)
+        self.desc = scute.HeadNormDesc(scute.NORM_RMS if kind == "rms" else scute.NORM_LAYER, eps, *ptrs,
+                                       *(head_dim if h else 0 for h in self.heads))
+
+
 class Rotary:
     """Rotary positions of heads of head_dim elements: pair i of the first
     2 len(freq) elements is turned by pos[axis[i]] * freq[i] radians. freq
@@ -304,12 +335,12 @@ class Rotary:
         self.desc = scute.RotaryDesc(head_dim, 2 * n, n_axes, 1 if interleaved else 0, freq.data_ptr(),
                                      None if axis is None else axis.data_ptr())
 
-    def store(self, q, k, v, pos, slot, cache, q_out, stream=None):
+    def store(self, q, k, v, pos, slot, cache, q_out, stream=None, norm=None):
         """q [T][n_heads][head_dim] rotated into q_out (the cache's type), k
         [T][n_kv_heads][head_dim] rotated and v as it is into the cache at slot
         [T] (int64; negative: not stored). q, k, v float32 or bfloat16, e.g.
         column ranges of one layer's output; pos int32 [n_axes][T] ([T] with
-        one axis)."""
+        one axis). norm: a HeadNorm that q's and k's heads go through first."""
         if q.dim() != 3:
             _bad("q must be [tokens][n_heads][head_dim]")
         T, H, D = q.shape
@@ -331,8 +362,15 @@ class Rotary:
         if not ok or pos.dtype != _I32 or (pc != 1 and T > 1):
             _bad(f"pos must be int32 [{self.n_axes}][{T}] with contiguous rows")
         _gpu(cache.device, self.freq, q, k, v, pos, slot, q_out)
-        scute._check(scute.lib.scute_rotary_store(
-            self.desc, cache.desc, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPES[dt],
+        call, desc = scute.lib.scute_rotary_store, (self.desc,)
+        if norm is not None:
+            if norm.head_dim != D or norm.heads[0] not in (0, H) or norm.heads[1] not in (0, cache.n_kv_heads):
+                _bad(f"the norm's vectors must be of {D} elements, and of all heads or of {H} and {cache.n_kv_heads}")
+            if norm.device is not None and norm.device != cache.device:
+                _bad(f"tensors on {norm.device} and {cache.device} in one call")
+            call, desc = scute.lib.scute_norm_rotary_store, (self.desc, norm.desc)
+        scute._check(call(
+            *desc, cache.desc, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPES[dt],
             pos.data_ptr(), ps, sp, T, H, q_out.data_ptr(), os, _stream(stream, cache.index)))
         return q_out
 

@@ -1,6 +1,7 @@
 // Operators between a decoder block's adapter layers: pages and slots of a
 // step's tokens (scute_cache_assign), rotary positions with the cache store
-// (scute_rotary_store) and the norms around the residual
+// (scute_rotary_store), with norms of the heads in the same pass
+// (scute_norm_rotary_store), and the norms around the residual
 // (scute_residual_norm). The attention over the cache is in attend.hip.
 
 #include <math.h>
@@ -407,6 +408,166 @@ __global__ __launch_bounds__(256) void k_rotary_store(RotArgs A) {
 }
 
 // ---------------------------------------------------------------------------
+// norms of the heads, rotary positions and the cache store
+// ---------------------------------------------------------------------------
+
+struct HeadNormArgs {
+  RotArgs r;
+  const float *q_w, *q_b, *k_w, *k_b;
+  int64_t q_stride, k_stride;  // of the weights' heads
+  int32_t layer;
+  float eps, inv_d;
+};
+
+// sum over groups of LP lanes, in each of them
+template <int LP>
+__device__ __forceinline__ float lanes_sum(float v) {
+#define STEP(ctrl) v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, 0xF, 0xF, false))
+  STEP(0xB1);  // (neighbours, pairs, the two quads of 8, the two halves of 16)
+  STEP(0x4E);
+  STEP(0x141);
+  if constexpr (LP >= 16) STEP(0x140);
+#undef STEP
+  if constexpr (LP >= 32) v += __shfl_xor(v, 16, 64);
+  if constexpr (LP >= 64) v += __shfl_xor(v, 32, 64);
+  return v;
+}
+
+// A head's rotation needs its norm, and its norm the whole head: LP lanes hold a
+// head (N units each, a unit as in k_rotary_store: V pairs of the halves, V / 2
+// adjacent pairs, or V elements that are not rotated), so q, k and v are read
+// once and written once and nothing but two sums crosses lanes. A work-group's
+// groups of lanes take a token's heads in turn, q's, k's, then v's.
+template <typename S, typename D, int V, int LP, int N>
+__global__ __launch_bounds__(256) void k_norm_rotary_store(HeadNormArgs G) {
+  const RotArgs& A = G.r;
+  __shared__ float cs[128], sn[128];
+  const int64_t t = blockIdx.x;
+  const int n = A.n_pairs, hd = A.head_dim, rd = 2 * n, tid = threadIdx.x, lane = tid % LP;
+  const int64_t slot = A.slot[t];
+  const bool store = slot >= 0 && slot < A.n_slots;
+  int64_t crow = 0;
+  if (store) {
+    const int64_t page = slot / A.page_size;
+    crow = page * A.page_stride + (slot - page * A.page_size) * A.token_stride;
+  }
+  const bool joined = V == 4 && A.interleaved;  // a unit's pairs lie side by side
+  const int ur = joined ? rd / V : n / V, per = ur + (hd - rd) / V;
+  const int nq = A.n_heads, nk = nq + A.n_kv_heads, all = nk + A.n_kv_heads;
+  // elements of unit u: V from e0 on and, where it is rotated in halves (or one
+  // pair), V from e1 on
+  const auto two = [&](int u) { return u < ur && !joined; };
+  const auto e0 = [&](int u) { return u >= ur ? rd + (u - ur) * V : A.interleaved && V == 1 ? 2 * u : V * u; };
+  const auto e1 = [&](int u) { return A.interleaved ? 2 * u + 1 : n + V * u; };
+  const auto load = [&](int h, float (&a)[N][V], float (&b)[N][V]) {
+    const void* src = h < nq ? A.q : A.k;
+    const int64_t at = h < nq ? t * A.q_stride + (int64_t)h * hd : t * A.k_stride + (int64_t)(h - nq) * hd;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int u = lane + k * LP;
+#pragma unroll
+      for (int i = 0; i < V; ++i) a[k][i] = b[k][i] = 0.f;
+      if (h < nk && u < per) {
+        ld_vec<S, V, true>(src, at + e0(u), a[k]);
+        if (two(u)) ld_vec<S, V, true>(src, at + e1(u), b[k]);
+      }
+    }
+  };
+  const int step = gridDim.y * (256 / LP);
+  int h = blockIdx.y * (256 / LP) + tid / LP;
+  float a[N][V], b[N][V];
+  load(h, a, b);
+  for (int i = tid; i < n; i += 256) {
+    const int ax = A.axis ? A.axis[i] : 0;
+    const int p = A.pos[(ax > 0 && ax < A.n_axes ? ax : 0) * A.pos_stride + t];
+    const double turns = (double)p * (A.freq[i] * 0.15915494309189533577);
+    float s, c;
+    sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+    cs[i] = c;
+    sn[i] = s;
+  }
+  __syncthreads();
+  for (; h < nk; h += step) {
+    // the next head's loads under this one's sums
+    float na[N][V], nb[N][V];
+    load(h + step, na, nb);
+    const bool of_q = h < nq;
+    if (of_q || store) {
+      float mu = 0.f, s = 0.f;
+      if (G.layer) {
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+          for (int i = 0; i < V; ++i) s += a[k][i] + b[k][i];
+        mu = lanes_sum<LP>(s) * G.inv_d;
+        s = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int u = lane + k * LP;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (u < per) a[k][i] -= mu, s += a[k][i] * a[k][i];
+          if (u < per && two(u)) b[k][i] -= mu, s += b[k][i] * b[k][i];
+        }
+      }
+      const float r = rsqrtf(lanes_sum<LP>(s) * G.inv_d + G.eps);
+      const float *w = of_q ? G.q_w : G.k_w, *c = of_q ? G.q_b : G.k_b;
+      const int64_t wat = of_q ? h * G.q_stride : (h - nq) * G.k_stride;
+      void* dst = of_q ? A.q_out : A.kc;
+      const int64_t di = of_q ? t * A.q_out_stride + (int64_t)h * hd : crow + (h - nq) * A.head_stride;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int u = lane + k * LP;
+        if (u >= per) continue;
+        const auto scaled = [&](float (&x)[V], int e) {
+          float g[V], o[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) g[i] = 1.f, o[i] = 0.f;
+          if (w) ld_vec<float, V>(w, wat + e, g);
+          if (c) ld_vec<float, V>(c, wat + e, o);
+#pragma unroll
+          for (int i = 0; i < V; ++i) x[i] = x[i] * r * g[i] + o[i];
+        };
+        scaled(a[k], e0(u));
+        if (u >= ur) {
+          st_vec<D, V>(dst, di + e0(u), a[k]);
+        } else if (joined) {
+          if constexpr (V == 4) {
+            const float c0 = cs[2 * u], s0 = sn[2 * u], c1 = cs[2 * u + 1], s1 = sn[2 * u + 1];
+            const float o[4] = {a[k][0] * c0 - a[k][1] * s0, a[k][0] * s0 + a[k][1] * c0,
+                                a[k][2] * c1 - a[k][3] * s1, a[k][2] * s1 + a[k][3] * c1};
+            st_vec<D, V>(dst, di + 4 * u, o);
+          }
+        } else {
+          scaled(b[k], e1(u));
+          float x[V], y[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float cc = cs[V * u + i], ss = sn[V * u + i];
+            x[i] = a[k][i] * cc - b[k][i] * ss;
+            y[i] = a[k][i] * ss + b[k][i] * cc;
+          }
+          st_vec<D, V>(dst, di + e0(u), x);
+          st_vec<D, V>(dst, di + e1(u), y);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) a[k][i] = na[k][i], b[k][i] = nb[k][i];
+  }
+  if (store)
+    for (; h < all; h += step)
+      for (int e = lane * V; e < hd; e += LP * V) {
+        float x[V];
+        ld_vec<S, V, true>(A.v, t * A.v_stride + (int64_t)(h - nk) * hd + e, x);
+        st_vec<D, V>(A.vc, crow + (h - nk) * A.head_stride + e, x);
+      }
+}
+
+// ---------------------------------------------------------------------------
 // the norms around the residual
 // ---------------------------------------------------------------------------
 
@@ -734,44 +895,53 @@ scute_status check_cache(const scute_kv_cache* C, const char* fn) {
 
 }  // namespace scute
 
-extern "C" scute_status scute_rotary_store(const scute_rotary* Ro, const scute_kv_cache* C, const void* q,
-                                           int64_t q_stride, const void* k, int64_t k_stride, const void* v,
-                                           int64_t v_stride, int32_t src_dtype, const int32_t* pos,
-                                           int64_t pos_stride, const int64_t* slot, int32_t n_tokens,
-                                           int32_t n_heads, void* q_out, int64_t q_out_stride, void* stream) {
-  const char* fn = "scute_rotary_store";
-  if (!Ro) return fail(SCUTE_E_INVALID, "scute_rotary_store: rotary is null");
+namespace {
+
+// Both entry points: norm null for the rotation alone.
+scute_status rotary_store(const char* fn, const scute_rotary* Ro, const scute_head_norm* norm, const scute_kv_cache* C,
+                          const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, int32_t src_dtype, const int32_t* pos, int64_t pos_stride,
+                          const int64_t* slot, int32_t n_tokens, int32_t n_heads, void* q_out, int64_t q_out_stride,
+                          void* stream) {
+  const auto bad = [&](scute_status code, const char* what) { return fail(code, std::string(fn) + ": " + what); };
+  if (!Ro) return bad(SCUTE_E_INVALID, "rotary is null");
   scute_status st = check_cache(C, fn);
   if (st != SCUTE_OK) return st;
-  if (Ro->head_dim != C->head_dim)
-    return fail(SCUTE_E_SHAPE, "scute_rotary_store: the rotary's and the cache's head_dim differ");
+  if (Ro->head_dim != C->head_dim) return bad(SCUTE_E_SHAPE, "the rotary's and the cache's head_dim differ");
   if (Ro->rot_dim < 0 || Ro->rot_dim > Ro->head_dim || Ro->rot_dim % 2)
-    return fail(SCUTE_E_SHAPE, "scute_rotary_store: rot_dim must be even and in [0, head_dim]");
-  if (Ro->n_axes < 1 || Ro->n_axes > 8) return fail(SCUTE_E_SHAPE, "scute_rotary_store: n_axes must be in [1, 8]");
-  if (Ro->interleaved != 0 && Ro->interleaved != 1)
-    return fail(SCUTE_E_INVALID, "scute_rotary_store: interleaved must be 0 or 1");
+    return bad(SCUTE_E_SHAPE, "rot_dim must be even and in [0, head_dim]");
+  if (Ro->n_axes < 1 || Ro->n_axes > 8) return bad(SCUTE_E_SHAPE, "n_axes must be in [1, 8]");
+  if (Ro->interleaved != 0 && Ro->interleaved != 1) return bad(SCUTE_E_INVALID, "interleaved must be 0 or 1");
   if (src_dtype != SCUTE_F32 && src_dtype != SCUTE_BF16)
-    return fail(SCUTE_E_INVALID, "scute_rotary_store: src_dtype must be SCUTE_F32 or SCUTE_BF16");
+    return bad(SCUTE_E_INVALID, "src_dtype must be SCUTE_F32 or SCUTE_BF16");
   if (n_tokens < 0 || n_heads < 1 || n_heads > 65536)
-    return fail(SCUTE_E_SHAPE, "scute_rotary_store: n_tokens must be >= 0 and n_heads in [1, 65536]");
+    return bad(SCUTE_E_SHAPE, "n_tokens must be >= 0 and n_heads in [1, 65536]");
   const int64_t hd = C->head_dim, big = (int64_t)1 << 40;
   for (int64_t s : {q_stride, k_stride, v_stride, q_out_stride, pos_stride})
-    if (s < 0 || s > big) return fail(SCUTE_E_SHAPE, "scute_rotary_store: strides must be in [0, 2^40]");
-  if (n_tokens > 1 && q_out_stride < n_heads * hd)
-    return fail(SCUTE_E_SHAPE, "scute_rotary_store: rows of q_out overlap");
+    if (s < 0 || s > big) return bad(SCUTE_E_SHAPE, "strides must be in [0, 2^40]");
+  if (n_tokens > 1 && q_out_stride < n_heads * hd) return bad(SCUTE_E_SHAPE, "rows of q_out overlap");
+  if (norm) {
+    if (norm->kind != SCUTE_NORM_RMS && norm->kind != SCUTE_NORM_LAYER)
+      return bad(SCUTE_E_INVALID, "kind must be SCUTE_NORM_RMS or SCUTE_NORM_LAYER");
+    for (int32_t s : {norm->q_stride, norm->k_stride})
+      if (s < 0 || s > (1 << 20) || (s > 0 && s < hd))
+        return bad(SCUTE_E_SHAPE, "the norm's strides must be 0 or in [head_dim, 2^20]");
+    for (const float* p : {norm->q_w, norm->q_b, norm->k_w, norm->k_b})
+      if (misaligned(p, 4)) return bad(SCUTE_E_INVALID, "misaligned pointer");
+  }
   if (n_tokens == 0) return SCUTE_OK;
   if (!q || !k || !v || !slot || !q_out || (Ro->rot_dim && (!pos || !Ro->freq)))
-    return fail(SCUTE_E_INVALID, "scute_rotary_store: null pointer");
+    return bad(SCUTE_E_INVALID, "null pointer");
   const uintptr_t es = src_dtype == SCUTE_F32 ? 4 : 2, ed = C->dtype == SCUTE_F32 ? 4 : 2;
   if (misaligned(q, es) || misaligned(k, es) || misaligned(v, es) || misaligned(q_out, ed) || misaligned(pos, 4) ||
       misaligned(slot, 8) || misaligned(Ro->freq, 8) || misaligned(Ro->axis, 4))
-    return fail(SCUTE_E_INVALID, "scute_rotary_store: misaligned pointer");
+    return bad(SCUTE_E_INVALID, "misaligned pointer");
   const int64_t wq = n_heads * hd, wk = C->n_kv_heads * hd, si = (int64_t)es, so = (int64_t)ed, T = n_tokens;
   const bool same = q == q_out && es == ed && (T == 1 || q_stride == q_out_stride);
   if ((!same && rows_meet(q, q_stride * si, wq * si, q_out, q_out_stride * so, wq * so, T)) ||
       rows_meet(k, k_stride * si, wk * si, q_out, q_out_stride * so, wq * so, T) ||
       rows_meet(v, v_stride * si, wk * si, q_out, q_out_stride * so, wq * so, T) || (q == q_out && !same))
-    return fail(SCUTE_E_INVALID, "scute_rotary_store: q_out overlaps q (of another type or stride), k or v");
+    return bad(SCUTE_E_INVALID, "q_out overlaps q (of another type or stride), k or v");
   OnDevice g(C->device);
   if (!g.ok()) return hip_fail(g.err, fn);
 
@@ -781,14 +951,21 @@ extern "C" scute_status scute_rotary_store(const scute_rotary* Ro, const scute_k
                   C->head_dim, n, Ro->n_axes, Ro->interleaved, n_heads, C->n_kv_heads, C->page_size};
   // four elements an access where every row's accesses are aligned to them and
   // no unit crosses the rotated part's halves or end
-  const bool vec = ((q_stride | k_stride | v_stride | q_out_stride) % 4 == 0) && !misaligned(q, 4 * es) &&
-                   !misaligned(k, 4 * es) && !misaligned(v, 4 * es) && !misaligned(q_out, 4 * ed) &&
-                   (Ro->interleaved ? n % 2 == 0 : n % 4 == 0);
+  bool vec = ((q_stride | k_stride | v_stride | q_out_stride) % 4 == 0) && !misaligned(q, 4 * es) &&
+             !misaligned(k, 4 * es) && !misaligned(v, 4 * es) && !misaligned(q_out, 4 * ed) &&
+             (Ro->interleaved ? n % 2 == 0 : n % 4 == 0);
+  if (norm) {
+    vec = vec && (norm->q_stride | norm->k_stride) % 4 == 0;
+    for (const float* p : {norm->q_w, norm->q_b, norm->k_w, norm->k_b}) vec = vec && !misaligned(p, 16);
+  }
   const int V = vec ? 4 : 1;
-  const int64_t rot = Ro->interleaved && V == 4 ? 2 * n / V : n / V;
-  const int64_t units = (n_heads + C->n_kv_heads) * (rot + (hd - 2 * n) / V) + C->n_kv_heads * (hd / V);
+  const int64_t rot = Ro->interleaved && V == 4 ? 2 * n / V : n / V, per = rot + (hd - 2 * n) / V;
+  const int64_t units = (n_heads + C->n_kv_heads) * per + C->n_kv_heads * (hd / V);
   // few tokens: their units spread over more work-groups, one unit a thread
-  const int64_t parts = std::min<int64_t>(std::min<int64_t>((units + 255) / 256, 4096),
+  // (norms: one head a group of lanes)
+  const int lanes = !vec || per > 32 ? 64 : per > 16 ? 32 : per > 8 ? 16 : 8;
+  const int64_t rounds = norm ? ((int64_t)n_heads + 2 * C->n_kv_heads) * lanes : units;
+  const int64_t parts = std::min<int64_t>(std::min<int64_t>((rounds + 255) / 256, 4096),
                                           std::max<int64_t>(1, 1024 / n_tokens));
   const hipStream_t s = (hipStream_t)stream;
   for (int64_t t = 0; t < n_tokens; t += most_groups(256)) {
@@ -799,12 +976,27 @@ extern "C" scute_status scute_rotary_store(const scute_rotary* Ro, const scute_k
     A.q_out = (char*)q_out + t * q_out_stride * (int64_t)ed;
     A.pos = pos ? pos + t : nullptr;
     A.slot = slot + t;
-#define ROT(S, D)                                                                    \
-  do {                                                                               \
-    if (vec)                                                                         \
-      hipLaunchKernelGGL((k_rotary_store<S, D, 4>), grid, dim3(256), 0, s, A);       \
-    else                                                                             \
-      hipLaunchKernelGGL((k_rotary_store<S, D, 1>), grid, dim3(256), 0, s, A);       \
+#define ROT(S, D)                                                                              \
+  do {                                                                                         \
+    if (norm) {                                                                                \
+      const HeadNormArgs H{A, norm->q_w, norm->q_b, norm->k_w, norm->k_b, norm->q_stride,      \
+                           norm->k_stride, norm->kind == SCUTE_NORM_LAYER, norm->eps,          \
+                           1.f / (float)hd};                                                   \
+      if (!vec)                                                                                \
+        hipLaunchKernelGGL((k_norm_rotary_store<S, D, 1, 64, 4>), grid, dim3(256), 0, s, H);   \
+      else if (lanes == 8)                                                                     \
+        hipLaunchKernelGGL((k_norm_rotary_store<S, D, 4, 8, 1>), grid, dim3(256), 0, s, H);    \
+      else if (lanes == 16)                                                                    \
+        hipLaunchKernelGGL((k_norm_rotary_store<S, D, 4, 16, 1>), grid, dim3(256), 0, s, H);   \
+      else if (lanes == 32)                                                                    \
+        hipLaunchKernelGGL((k_norm_rotary_store<S, D, 4, 32, 1>), grid, dim3(256), 0, s, H);   \
+      else                                                                                     \
+        hipLaunchKernelGGL((k_norm_rotary_store<S, D, 4, 64, 1>), grid, dim3(256), 0, s, H);   \
+    } else if (vec) {                                                                          \
+      hipLaunchKernelGGL((k_rotary_store<S, D, 4>), grid, dim3(256), 0, s, A);                 \
+    } else {                                                                                   \
+      hipLaunchKernelGGL((k_rotary_store<S, D, 1>), grid, dim3(256), 0, s, A);                 \
+    }                                                                                          \
   } while (0)
     if (es == 4 && ed == 4)
       ROT(float, float);
@@ -819,6 +1011,28 @@ extern "C" scute_status scute_rotary_store(const scute_rotary* Ro, const scute_k
     if (ls != SCUTE_OK) return ls;
   }
   return SCUTE_OK;
+}
+
+}  // namespace
+
+extern "C" scute_status scute_rotary_store(const scute_rotary* Ro, const scute_kv_cache* C, const void* q,
+                                           int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                           int64_t v_stride, int32_t src_dtype, const int32_t* pos,
+                                           int64_t pos_stride, const int64_t* slot, int32_t n_tokens,
+                                           int32_t n_heads, void* q_out, int64_t q_out_stride, void* stream) {
+  return rotary_store("scute_rotary_store", Ro, nullptr, C, q, q_stride, k, k_stride, v, v_stride, src_dtype, pos,
+                      pos_stride, slot, n_tokens, n_heads, q_out, q_out_stride, stream);
+}
+
+extern "C" scute_status scute_norm_rotary_store(const scute_rotary* Ro, const scute_head_norm* norm,
+                                                const scute_kv_cache* C, const void* q, int64_t q_stride, const void* k,
+                                                int64_t k_stride, const void* v, int64_t v_stride, int32_t src_dtype,
+                                                const int32_t* pos, int64_t pos_stride, const int64_t* slot,
+                                                int32_t n_tokens, int32_t n_heads, void* q_out, int64_t q_out_stride,
+                                                void* stream) {
+  if (!norm) return fail(SCUTE_E_INVALID, "scute_norm_rotary_store: norm is null");
+  return rotary_store("scute_norm_rotary_store", Ro, norm, C, q, q_stride, k, k_stride, v, v_stride, src_dtype, pos,
+                      pos_stride, slot, n_tokens, n_heads, q_out, q_out_stride, stream);
 }
 
 extern "C" scute_status scute_residual_norm(const scute_norm* N, const void* y, int32_t y_dtype, int64_t y_stride,

@@ -119,6 +119,12 @@ class NormDesc(C.Structure):
 NORM_RMS, NORM_LAYER = 0, 1
 
 
+class HeadNormDesc(C.Structure):
+    """scute_head_norm"""
+    _fields_ = [("kind", C.c_int32), ("eps", C.c_float), ("q_w", C.c_void_p), ("q_b", C.c_void_p),
+                ("k_w", C.c_void_p), ("k_b", C.c_void_p), ("q_stride", C.c_int32), ("k_stride", C.c_int32)]
+
+
 # exported symbols and their signatures (must match include/scute.h)
 _P = C.c_void_p
 SIGNATURES = {
@@ -155,6 +161,10 @@ SIGNATURES = {
     "scute_rotary_store": (C.c_int32, [C.POINTER(RotaryDesc), C.POINTER(KVCacheDesc), _P, C.c_int64,
                                        _P, C.c_int64, _P, C.c_int64, C.c_int32, _P, C.c_int64, _P,
                                        C.c_int32, C.c_int32, _P, C.c_int64, _P]),
+    "scute_norm_rotary_store": (C.c_int32, [C.POINTER(RotaryDesc), C.POINTER(HeadNormDesc),
+                                            C.POINTER(KVCacheDesc), _P, C.c_int64, _P, C.c_int64, _P,
+                                            C.c_int64, C.c_int32, _P, C.c_int64, _P, C.c_int32, C.c_int32,
+                                            _P, C.c_int64, _P]),
     "scute_paged_attention_workspace": (C.c_int32, [C.c_int32, C.c_int32, C.POINTER(C.c_int64)]),
     "scute_paged_attention": (C.c_int32, [C.POINTER(KVCacheDesc), _P, C.c_int64, C.c_int32, _P,
                                           C.c_int64, C.c_int32, C.c_int32, _P, _P, C.c_int32,
@@ -320,6 +330,14 @@ def scute_rotary_store(rotary: RotaryDesc, cache: KVCacheDesc, q, q_stride, k, k
     _check(lib.scute_rotary_store(rotary, cache, _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
                                   src_dtype, _ptr(pos), pos_stride, _ptr(slot), n_tokens, n_heads,
                                   _ptr(q_out), q_out_stride, _stream_ptr(stream)))
+
+
+def scute_norm_rotary_store(rotary: RotaryDesc, norm: HeadNormDesc, cache: KVCacheDesc, q, q_stride, k, k_stride,
+                            v, v_stride, src_dtype, pos, pos_stride, slot, n_tokens, n_heads, q_out,
+                            q_out_stride, stream=None) -> None:
+    _check(lib.scute_norm_rotary_store(rotary, norm, cache, _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v),
+                                       v_stride, src_dtype, _ptr(pos), pos_stride, _ptr(slot), n_tokens,
+                                       n_heads, _ptr(q_out), q_out_stride, _stream_ptr(stream)))
 
 
 def scute_paged_attention_workspace(device: int, head_dim: int) -> int:
