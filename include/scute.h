@@ -596,6 +596,18 @@ scute_status scute_paged_attention(const scute_kv_cache* cache, const void* q, i
                                    void* out, int64_t out_stride, void* workspace,
                                    int64_t workspace_bytes, void* stream);
 
+/* scute_paged_attention where the first `sinks` positions stay visible: row i
+ * sees t < n with t < sinks or t >= n - window (window 0 or sinks 0: as there).
+ * Positions between them are not read, and their pages need not be in the
+ * cache (scute_cache_fork drops them). Arguments, workspace and errors as
+ * there, and SCUTE_E_SHAPE for sinks below 0. */
+scute_status scute_sink_attention(const scute_kv_cache* cache, const void* q, int64_t q_stride,
+                                  int32_t n_heads, const int32_t* table, int64_t table_stride,
+                                  int32_t n_requests, int32_t table_width, const int32_t* len,
+                                  const int32_t* req, int32_t n_rows, float scale, int32_t window,
+                                  int32_t sinks, void* out, int64_t out_stride, void* workspace,
+                                  int64_t workspace_bytes, void* stream);
+
 /* The norms around a block's residual:
  *   h' = h_scale h + y_scale (gate (.) N_post(y))     x = N_pre(h')
  * N(v) = v / sqrt(mean(v^2) + eps) (.) w + b (SCUTE_NORM_RMS), or the same of

@@ -13,7 +13,8 @@ and the norms around the residual.
                   cache (scute_rotary_store), with norms of the heads (HeadNorm)
                   in the same pass (scute_norm_rotary_store)
   PagedAttention  attention of new tokens over the paged cache
-                  (scute_paged_attention)
+                  (scute_paged_attention; with a window and first positions
+                  that stay visible scute_sink_attention)
   ResidualNorm    the norms after and before a block, with its gate and
                   residual scale (scute_residual_norm)
 
@@ -380,19 +381,21 @@ class Rotary:
 class PagedAttention:
     """Attention of new tokens over a KVCache with n_heads query heads
     (n_heads / n_kv_heads of them share a key head). scale: 1 / sqrt(head_dim)
-    by default; window: a row sees its last `window` positions (0: all).
-    max_rows: calls of more rows are refused (None: up to 2^20).
+    by default; window: a row sees its last `window` positions (0: all);
+    sinks: and the first `sinks`, which stay visible. max_rows: calls of more rows are refused (None: up to 2^20).
 
     The handle owns the workspace of one call at a time: calls that may
     overlap (other streams, graphs replayed side by side) need handles of their
     own."""
 
-    def __init__(self, cache, n_heads, max_rows=None, scale=None, window=0):
+    def __init__(self, cache, n_heads, max_rows=None, scale=None, window=0, sinks=0):
         if n_heads < 1 or n_heads % cache.n_kv_heads:
             _bad("n_heads must be a multiple of the cache's n_kv_heads")
         if window < 0:
             _bad("window must be >= 0")
-        self.cache, self.n_heads, self.window = cache, int(n_heads), int(window)
+        if sinks < 0:
+            _bad("sinks must be >= 0")
+        self.cache, self.n_heads, self.window, self.sinks = cache, int(n_heads), int(window), int(sinks)
         self.scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale)
         nbytes = scute.scute_paged_attention_workspace(cache.device.index, cache.head_dim)
         self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=cache.device)
@@ -423,9 +426,12 @@ class PagedAttention:
             _bad("more rows than requests: row_req says whose they are")
         _gpu(c.device, q, table, row_len, out, row_req)
         ws = self.workspace
-        scute._check(scute.lib.scute_paged_attention(
+        call, seen = scute.lib.scute_paged_attention, (self.window,)
+        if self.sinks:
+            call, seen = scute.lib.scute_sink_attention, (self.window, self.sinks)
+        scute._check(call(
             c.desc, q.data_ptr(), qs if N > 1 else 0, H, table.data_ptr(), ts if R > 1 else P, R, P, lp, rp, N,
-            self.scale, self.window, out.data_ptr(), os if N > 1 else 0, ws.data_ptr(), ws.shape[0],
+            self.scale, *seen, out.data_ptr(), os if N > 1 else 0, ws.data_ptr(), ws.shape[0],
             _stream(stream, c.index)))
         return out
 

@@ -169,6 +169,9 @@ SIGNATURES = {
     "scute_paged_attention": (C.c_int32, [C.POINTER(KVCacheDesc), _P, C.c_int64, C.c_int32, _P,
                                           C.c_int64, C.c_int32, C.c_int32, _P, _P, C.c_int32,
                                           C.c_float, C.c_int32, _P, C.c_int64, _P, C.c_int64, _P]),
+    "scute_sink_attention": (C.c_int32, [C.POINTER(KVCacheDesc), _P, C.c_int64, C.c_int32, _P,
+                                         C.c_int64, C.c_int32, C.c_int32, _P, _P, C.c_int32,
+                                         C.c_float, C.c_int32, C.c_int32, _P, C.c_int64, _P, C.c_int64, _P]),
     "scute_residual_norm": (C.c_int32, [C.POINTER(NormDesc), _P, C.c_int32, C.c_int64, _P, C.c_int32,
                                         C.c_int64, _P, C.c_int64, _P, C.c_int64, _P, C.c_int32,
                                         C.c_int64, C.c_int32, _P]),
@@ -353,6 +356,14 @@ def scute_paged_attention(cache: KVCacheDesc, q, q_stride, n_heads, table, table
                                      n_requests, table_width, _ptr(len), _ptr(req), n_rows, scale, window,
                                      _ptr(out), out_stride, _ptr(workspace), workspace_bytes,
                                      _stream_ptr(stream)))
+
+
+def scute_sink_attention(cache: KVCacheDesc, q, q_stride, n_heads, table, table_stride, n_requests, table_width,
+                         len, req, n_rows, scale, window, sinks, out, out_stride, workspace, workspace_bytes,
+                         stream=None) -> None:
+    _check(lib.scute_sink_attention(cache, _ptr(q), q_stride, n_heads, _ptr(table), table_stride, n_requests,
+                                    table_width, _ptr(len), _ptr(req), n_rows, scale, window, sinks, _ptr(out),
+                                    out_stride, _ptr(workspace), workspace_bytes, _stream_ptr(stream)))
 
 
 def scute_residual_norm(norm: NormDesc, y, y_dtype, y_stride, h, h_dtype, h_stride, gate, gate_stride,
