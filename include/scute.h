@@ -608,6 +608,35 @@ scute_status scute_sink_attention(const scute_kv_cache* cache, const void* q, in
                                   int32_t sinks, void* out, int64_t out_stride, void* workspace,
                                   int64_t workspace_bytes, void* stream);
 
+/* Bytes of workspace that scute_shared_attention may use for calls of up to
+ * max_rows rows in up to max_groups groups. Errors as for the call's sizes. */
+scute_status scute_shared_attention_workspace(int32_t device, int32_t dtype, int32_t head_dim,
+                                              int32_t n_heads, int32_t n_kv_heads, int32_t max_rows,
+                                              int32_t max_groups, int64_t* bytes);
+
+/* scute_paged_attention, without a window, of rows whose contexts begin with
+ * the same positions: rows group[g] .. group[g + 1] - 1 (group [n_groups + 1],
+ * ascending) are of requests that hold their first shared_len[g] positions in
+ * the same pages (a prompt's samples, a system prompt's users), which are read
+ * once for all of them, through the table of a row of the group that sees most
+ * of them. A row sees its positions below len as there, shared or its own,
+ * rows of no request or of length 0 nothing; rows of no group share nothing,
+ * and shared_len may be 0. Results are those of scute_paged_attention but for
+ * the order of the sums (an infinite V that a bf16 row sees with a weight under 2^-100
+ * may give NaN).
+ * group and shared_len are device arrays; group is not checked: offsets that
+ * do not ascend give rows whose output is not defined, no access out of bounds.
+ * workspace as there, of at least what scute_shared_attention_workspace says
+ * for n_rows and n_groups. Errors as there, SCUTE_E_SHAPE for n_groups outside
+ * 0 .. 65536 or, at the table's whole width, 2^31 units of 16 positions and 64 columns. */
+scute_status scute_shared_attention(const scute_kv_cache* cache, const void* q, int64_t q_stride,
+                                    int32_t n_heads, const int32_t* table, int64_t table_stride,
+                                    int32_t n_requests, int32_t table_width, const int32_t* len,
+                                    const int32_t* req, int32_t n_rows, const int32_t* group,
+                                    const int32_t* shared_len, int32_t n_groups, float scale, void* out,
+                                    int64_t out_stride, void* workspace, int64_t workspace_bytes,
+                                    void* stream);
+
 /* The norms around a block's residual:
  *   h' = h_scale h + y_scale (gate (.) N_post(y))     x = N_pre(h')
  * N(v) = v / sqrt(mean(v^2) + eps) (.) w + b (SCUTE_NORM_RMS), or the same of

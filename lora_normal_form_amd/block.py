@@ -15,6 +15,8 @@ and the norms around the residual.
   PagedAttention  attention of new tokens over the paged cache
                   (scute_paged_attention; with a window and first positions
                   that stay visible scute_sink_attention)
+  SharedAttention the same for rows whose contexts begin with the same
+                  positions, read once (scute_shared_attention)
   ResidualNorm    the norms after and before a block, with its gate and
                   residual scale (scute_residual_norm)
 
@@ -432,6 +434,57 @@ class PagedAttention:
         scute._check(call(
             c.desc, q.data_ptr(), qs if N > 1 else 0, H, table.data_ptr(), ts if R > 1 else P, R, P, lp, rp, N,
             self.scale, *seen, out.data_ptr(), os if N > 1 else 0, ws.data_ptr(), ws.shape[0],
+            _stream(stream, c.index)))
+        return out
+
+
+class SharedAttention:
+    """Attention over a KVCache of rows whose contexts begin with the same
+    positions (samples of a prompt, users of a system prompt): those are read
+    once for all rows of a group. Up to max_rows rows in up to max_groups groups
+    a call; scale as in PagedAttention, and as there the handle owns the
+    workspace of one call at a time."""
+
+    def __init__(self, cache, n_heads, max_rows, max_groups, scale=None):
+        if n_heads < 1 or n_heads % cache.n_kv_heads:
+            _bad("n_heads must be a multiple of the cache's n_kv_heads")
+        self.cache, self.n_heads = cache, int(n_heads)
+        self.max_rows, self.max_groups = int(max_rows), int(max_groups)
+        self.scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale)
+        nbytes = scute.scute_shared_attention_workspace(cache.device.index, _DTYPES[cache.dtype], cache.head_dim,
+                                                        self.n_heads, cache.n_kv_heads, max_rows, max_groups)
+        self.workspace = torch.zeros(nbytes, dtype=torch.uint8, device=cache.device)
+        settle(cache.device)
+
+    def forward(self, q, table, row_len, group, shared_len, out, row_req=None, stream=None):
+        """q, table, row_len, out, row_req as in PagedAttention.forward. group
+        int32 [n_groups + 1]: rows group[g] .. group[g + 1] - 1 hold the first
+        shared_len[g] (int32 [n_groups]) positions of their requests in the
+        same pages."""
+        c = self.cache
+        N, D, H = q.shape[0], c.head_dim, self.n_heads
+        qs, os = _heads(q, N, H, D, "q"), _heads(out, N, H, D, "out")
+        n_groups = shared_len.shape[0]
+        if N > self.max_rows or n_groups > self.max_groups:
+            _bad(f"{N} rows in {n_groups} groups: the handle takes up to {self.max_rows} in {self.max_groups}")
+        if q.dtype != c.dtype or out.dtype != c.dtype:
+            _bad("q and out must have the cache's type")
+        if table.dtype != _I32 or table.dim() != 2:
+            _bad("table must be int32 [n_requests][pages] with contiguous rows")
+        (R, P), (ts, tc) = table.shape, table.stride()
+        if tc != 1 and P > 1:
+            _bad("table must be int32 [n_requests][pages] with contiguous rows")
+        lp, rp = _vector(row_len, N, _I32, "row_len"), None
+        if row_req is not None:
+            rp = _vector(row_req, N, _I32, "row_req")
+        elif N > R:
+            _bad("more rows than requests: row_req says whose they are")
+        gp, sp = _vector(group, n_groups + 1, _I32, "group"), _vector(shared_len, n_groups, _I32, "shared_len")
+        _gpu(c.device, q, table, row_len, group, shared_len, out, row_req)
+        ws = self.workspace
+        scute._check(scute.lib.scute_shared_attention(
+            c.desc, q.data_ptr(), qs if N > 1 else 0, H, table.data_ptr(), ts if R > 1 else P, R, P, lp, rp, N, gp, sp,
+            n_groups, self.scale, out.data_ptr(), os if N > 1 else 0, ws.data_ptr(), ws.shape[0],
             _stream(stream, c.index)))
         return out
 

@@ -18,13 +18,14 @@ namespace scute {
 //               been taken by k_shared_prefix and are added at the end
 enum : int { ATT_PLAIN = 0, ATT_SINKS = 1, ATT_SUFFIX = 2 };
 
-// A row's shared positions and where their partial results lie: column c of the
-// row's group (row of the group times heads of a key head, and head of it) has
-// `parts` slots from slot0 + (key head tiles + c / columns) parts on.
-struct AttRowFrom {
-  int32_t from, parts, tiles, col0;
-  int64_t slot0;
-  int64_t pad;
+// A row's shared positions and where their partial results lie: the row's group
+// has `tiles` tiles of columns (row of the group times heads of a key head, and
+// head of it; the row's first is col0) for each key head, the x0-th on, of `units`
+// units from the u0-th on; work-group u / each of k_shared_prefix took unit u, and
+// its part of the x-th tile is in slot u / each + x.
+struct alignas(16) AttRowFrom {
+  int32_t from, tiles, col0, units;
+  uint32_t u0, x0, each, pad;
 };
 
 struct AttArgs {
@@ -268,8 +269,10 @@ struct AttTile {
       for (int e = 0; e < G::VB / 4; ++e) v[s][j][ng][e] = 0;
   }
   // SOME: of the positions that `mask` (ones or zeros for each) leaves, for the
-  // columns of the lanes that `keep`
-  template <int QT, bool SOME = false>
+  // columns of the lanes that `keep`. POS: both parts of a weight are positive (the
+  // first cut off instead of rounded, the second 2^-20 of the weight more than the
+  // rest), so that an infinite V stays infinite; the weight is off by 2^-15 at most.
+  template <int QT, bool SOME = false, bool POS = false>
   __device__ __forceinline__ void weigh(const f32x4 (&p)[QT][G::SUB], f32x4 (&acc)[QT][G::NG][G::VD],
                                         const uint32_t (*mask)[4] = nullptr, bool keep = true) {
     const auto val = [&](int s, int j, int ng, int i) { return SOME ? v[s][j][ng][i] & mask[s][j] : v[s][j][ng][i]; };
@@ -283,15 +286,22 @@ struct AttTile {
       // second is 0 or of either sign, so an infinite V gives a sum of any kind,
       // which is put right where the waves' results are joined.
       uint4 b[QT], b2[QT];
+      const auto first = [](float x, float y) {
+        return POS ? __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u)
+                   : pack_bf2(__float_as_uint(x), __float_as_uint(y));
+      };
       const auto rest = [](uint32_t hi, float x, float y) {
+        if constexpr (POS)
+          return pack_bf2(__float_as_uint(fmaf(x, 1.f + 0x1p-20f, -__uint_as_float(hi << 16))),
+                          __float_as_uint(fmaf(y, 1.f + 0x1p-20f, -__uint_as_float(hi & 0xFFFF0000u))));
         return pack_bf2(__float_as_uint(x - __uint_as_float(hi << 16)), __float_as_uint(y - __uint_as_float(hi & 0xFFFF0000u)));
       };
 #pragma unroll
       for (int y = 0; y < QT; ++y) {
-        b[y].x = pack_bf2(__float_as_uint(p[y][0][0]), __float_as_uint(p[y][0][1]));
-        b[y].y = pack_bf2(__float_as_uint(p[y][0][2]), __float_as_uint(p[y][0][3]));
-        b[y].z = pack_bf2(__float_as_uint(p[y][1][0]), __float_as_uint(p[y][1][1]));
-        b[y].w = pack_bf2(__float_as_uint(p[y][1][2]), __float_as_uint(p[y][1][3]));
+        b[y].x = first(p[y][0][0], p[y][0][1]);
+        b[y].y = first(p[y][0][2], p[y][0][3]);
+        b[y].z = first(p[y][1][0], p[y][1][1]);
+        b[y].w = first(p[y][1][2], p[y][1][3]);
         b2[y].x = rest(b[y].x, p[y][0][0], p[y][0][1]);
         b2[y].y = rest(b[y].y, p[y][0][2], p[y][0][3]);
         b2[y].z = rest(b[y].z, p[y][1][0], p[y][1][1]);
@@ -768,10 +778,13 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
       const int i = !SHARED ? 0 : g / wide;
       if constexpr (FORM == ATT_SUFFIX) {
         // the sums over the row's shared positions, a slot after the other
-        const AttRowFrom& F = A.from[row + i];
-        const int parts = ldg(&F.parts), c = ldg(&F.col0) + h0 + g - i * wide - kvh * A.group, x = c / A.seed_cols;
-        const float* p = A.seeds + (ldg(&F.slot0) + ((int64_t)kvh * ldg(&F.tiles) + x) * parts) * A.seed_cols * (DP + 4) +
-                         (c - x * A.seed_cols) * (DP + 4);
+        const u32x4 f0 = ldg((const u32x4*)(A.from + row + i)), f1 = ldg((const u32x4*)(A.from + row + i) + 1);
+        const AttRowFrom F{(int)f0.x, (int)f0.y, (int)f0.z, (int)f0.w, f1.x, f1.y, f1.z, 0};
+        const int c = F.col0 + h0 + g - i * wide - kvh * A.group, tile = c / A.seed_cols;
+        const uint32_t x = (uint32_t)(kvh * F.tiles + tile), u = F.u0 + x * F.units;
+        const uint32_t w0 = F.units ? u / F.each : 0;
+        const int parts = F.units ? (int)((u + F.units - 1) / F.each - w0) + 1 : 0;
+        const float* p = A.seeds + ((int64_t)(w0 + F.x0 + x) * A.seed_cols + c - tile * A.seed_cols) * (DP + 4);
         for (int j0 = 0; j0 < parts; j0 += 4) {  // (four slots' loads in flight)
           f32x4 ml[4], v[4];
 #pragma unroll

@@ -172,6 +172,10 @@ SIGNATURES = {
     "scute_sink_attention": (C.c_int32, [C.POINTER(KVCacheDesc), _P, C.c_int64, C.c_int32, _P,
                                          C.c_int64, C.c_int32, C.c_int32, _P, _P, C.c_int32,
                                          C.c_float, C.c_int32, C.c_int32, _P, C.c_int64, _P, C.c_int64, _P]),
+    "scute_shared_attention_workspace": (C.c_int32, [C.c_int32] * 7 + [C.POINTER(C.c_int64)]),
+    "scute_shared_attention": (C.c_int32, [C.POINTER(KVCacheDesc), _P, C.c_int64, C.c_int32, _P, C.c_int64,
+                                           C.c_int32, C.c_int32, _P, _P, C.c_int32, _P, _P, C.c_int32,
+                                           C.c_float, _P, C.c_int64, _P, C.c_int64, _P]),
     "scute_residual_norm": (C.c_int32, [C.POINTER(NormDesc), _P, C.c_int32, C.c_int64, _P, C.c_int32,
                                         C.c_int64, _P, C.c_int64, _P, C.c_int64, _P, C.c_int32,
                                         C.c_int64, C.c_int32, _P]),
@@ -364,6 +368,23 @@ def scute_sink_attention(cache: KVCacheDesc, q, q_stride, n_heads, table, table_
     _check(lib.scute_sink_attention(cache, _ptr(q), q_stride, n_heads, _ptr(table), table_stride, n_requests,
                                     table_width, _ptr(len), _ptr(req), n_rows, scale, window, sinks, _ptr(out),
                                     out_stride, _ptr(workspace), workspace_bytes, _stream_ptr(stream)))
+
+
+def scute_shared_attention_workspace(device: int, dtype: int, head_dim: int, n_heads: int, n_kv_heads: int,
+                                     max_rows: int, max_groups: int) -> int:
+    out = C.c_int64(0)
+    _check(lib.scute_shared_attention_workspace(device, dtype, head_dim, n_heads, n_kv_heads, max_rows,
+                                                max_groups, C.byref(out)))
+    return out.value
+
+
+def scute_shared_attention(cache: KVCacheDesc, q, q_stride, n_heads, table, table_stride, n_requests, table_width,
+                           len, req, n_rows, group, shared_len, n_groups, scale, out, out_stride, workspace,
+                           workspace_bytes, stream=None) -> None:
+    _check(lib.scute_shared_attention(cache, _ptr(q), q_stride, n_heads, _ptr(table), table_stride, n_requests,
+                                      table_width, _ptr(len), _ptr(req), n_rows, _ptr(group), _ptr(shared_len),
+                                      n_groups, scale, _ptr(out), out_stride, _ptr(workspace), workspace_bytes,
+                                      _stream_ptr(stream)))
 
 
 def scute_residual_norm(norm: NormDesc, y, y_dtype, y_stride, h, h_dtype, h_stride, gate, gate_stride,

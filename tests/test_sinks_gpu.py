@@ -21,10 +21,10 @@ def _need_gpu():
         pytest.skip("no GPU")
 
 
-def attend_ref(q, kc, vc, table, lens, req, seen, scale):
+def attend_ref(q, kc, vc, table, lens, req, seen, scale, weight=U[BF16] ** 2):
     """(out, its bound) in 64 bits; seen(i, n): the positions of row i, of length
     n; those whose page is not in the cache are not seen. The bound is that of
-    test_block_gpu._attend_ref."""
+    test_block_gpu._attend_ref; weight: how far off a weight of a bf16 cache is."""
     q, kc, vc, table = q.cpu().double(), kc.cpu(), vc.cpu(), table.cpu()
     dt = kc.dtype
     N, H, D = q.shape
@@ -47,7 +47,7 @@ def attend_ref(q, kc, vc, table, lens, req, seen, scale):
         o, mag = p @ V, p @ V.abs()
         off = (qi.abs() @ K.transpose(1, 2).abs()).amax(-1, keepdim=True) * abs(scale) * (D + 3) * U[F32]
         rel = 4 * off + (2 * len(t) + 16) * U[F32]
-        b = (rel + (U[dt] ** 2 if dt == BF16 else 0.0)) * mag + U[dt] * (o.abs() + 2 * rel * mag)
+        b = (rel + (weight if dt == BF16 else 0.0)) * mag + U[dt] * (o.abs() + 2 * rel * mag)
         out[i], tol[i] = o.reshape(H, D), b.reshape(H, D)
     return out, tol
 
