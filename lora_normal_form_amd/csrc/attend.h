@@ -272,7 +272,8 @@ struct AttTile {
   // columns of the lanes that `keep`. POS: both parts of a weight are positive (the
   // first cut off instead of rounded, the second 2^-20 of the weight more than the
   // rest), so that an infinite V stays infinite; the weight is off by 2^-15 at most.
-  template <int QT, bool SOME = false, bool POS = false>
+  // Y0 .. Y1 - 1: the query tiles it is done for
+  template <int QT, bool SOME = false, bool POS = false, int Y0 = 0, int Y1 = QT>
   __device__ __forceinline__ void weigh(const f32x4 (&p)[QT][G::SUB], f32x4 (&acc)[QT][G::NG][G::VD],
                                         const uint32_t (*mask)[4] = nullptr, bool keep = true) {
     const auto val = [&](int s, int j, int ng, int i) { return SOME ? v[s][j][ng][i] & mask[s][j] : v[s][j][ng][i]; };
@@ -297,7 +298,7 @@ struct AttTile {
         return pack_bf2(__float_as_uint(x - __uint_as_float(hi << 16)), __float_as_uint(y - __uint_as_float(hi & 0xFFFF0000u)));
       };
 #pragma unroll
-      for (int y = 0; y < QT; ++y) {
+      for (int y = Y0; y < Y1; ++y) {
         b[y].x = first(p[y][0][0], p[y][0][1]);
         b[y].y = first(p[y][0][2], p[y][0][3]);
         b[y].z = first(p[y][1][0], p[y][1][1]);
@@ -318,7 +319,7 @@ struct AttTile {
           a.z = __builtin_amdgcn_perm(val(1, 1, ng, i / 2), val(1, 0, ng, i / 2), sel);
           a.w = __builtin_amdgcn_perm(val(1, 3, ng, i / 2), val(1, 2, ng, i / 2), sel);
 #pragma unroll
-          for (int y = 0; y < QT; ++y) put(acc[y][ng][i], mfma16(a, b2[y], mfma16(a, b[y], acc[y][ng][i])));
+          for (int y = Y0; y < Y1; ++y) put(acc[y][ng][i], mfma16(a, b2[y], mfma16(a, b[y], acc[y][ng][i])));
         }
     } else {
 #pragma unroll
@@ -326,7 +327,7 @@ struct AttTile {
 #pragma unroll
         for (int i = 0; i < G::VD; ++i)
 #pragma unroll
-          for (int y = 0; y < QT; ++y) {
+          for (int y = Y0; y < Y1; ++y) {
             f32x4 x = acc[y][ng][i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) x = mfma4(val(0, j, ng, i), __float_as_uint(p[y][0][j]), x);

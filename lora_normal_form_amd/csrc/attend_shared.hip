@@ -18,20 +18,78 @@ struct SharedArgs {
   int64_t q_stride, page_stride, token_stride, head_stride, table_stride, n_pages;
   uint32_t ps_mul;
   int32_t n_rows, n_groups, n_kv, heads, head_dim, page_size, ps_shift, reach, n_requests, max_tiles;
-  float scale_log2;
+  int32_t negate;    // the scale is below 0
+  float scale_log2;  // its magnitude times log2(e), above 0 (so that what is masked stays at -inf)
 };
 
 // Geometry of one instantiation.
+constexpr int sh_stage(int es, int dp) {
+  return 8192 / (dp * es) > 32 / (es / 2) ? 8192 / (dp * es) : 32 / (es / 2);  // (a tile at least)
+}
 template <typename T, int DP>
 struct ShGeo {
   using G = AttGeo<T, DP>;
   static constexpr int QT = DP * G::ES >= 1024 ? 1 : 2;  // query tiles a wave (one where two would not fit the registers)
   static constexpr int COLS = 4 * 16 * QT;               // columns of a work-group
-  static constexpr int ROW = DP * G::ES;                 // bytes of a position in LDS, without its padding
-  static constexpr int STAGE = 16384 / ROW > 64 ? 64 : 16384 / ROW;  // positions staged at once: a unit
-  static constexpr int PIECES = ROW / 16, PASS = STAGE * PIECES / 256;  // 16-byte pieces; passes of all threads
-  static constexpr int PAD = ROW + 16;
+  static constexpr int ROW = DP * G::ES;                 // bytes of a position in LDS
+  static constexpr int STAGE = sh_stage(G::ES, DP);      // positions staged at once: a unit
+  static constexpr int RING = 4, BYTES = STAGE * ROW;    // stages of K (and of V) in LDS
+  static constexpr int PIECES = ROW / 16;                // 16-byte pieces of a position
+  static constexpr int LOADS = BYTES / 4096;             // a wave's loads of 1 KB a stage (of K, and of V)
 };
+// where LDS holds piece p of a stage's position: rows that are read together are
+// spread over the banks
+template <int ROW>
+__device__ __forceinline__ int sh_slot(int row, int p) {
+  return ROW >= 256 ? (p & ~15) | ((p ^ row) & 15) : p ^ ((row >> 1) & 7);
+}
+// Vectors of W dwords from LDS at a[0 .. 3] + O0 (out[0 .. 3]) and, where O1 is not
+// 0, + O1 (out[4 .. 7]), there when it returns. In assembly because the compiler
+// makes its own reads of LDS wait for every load to LDS that is under way (each
+// stage would wait for the three behind it).
+template <int W, int O0, int O1>
+__device__ __forceinline__ void lds_read(const uint32_t (&a)[4], uint32_t (*const (&out)[8])) {
+  typedef uint32_t vec __attribute__((ext_vector_type(W)));
+  vec v[8];
+  if constexpr (W == 4 && O1 != 0) {
+    asm volatile(
+        "ds_read_b128 %0, %8 offset:%12\n\tds_read_b128 %1, %9 offset:%12\n\t"
+        "ds_read_b128 %2, %10 offset:%12\n\tds_read_b128 %3, %11 offset:%12\n\t"
+        "ds_read_b128 %4, %8 offset:%13\n\tds_read_b128 %5, %9 offset:%13\n\t"
+        "ds_read_b128 %6, %10 offset:%13\n\tds_read_b128 %7, %11 offset:%13\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7])
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0), "n"(O1)
+        : "memory");
+  } else if constexpr (W == 2 && O1 != 0) {
+    asm volatile(
+        "ds_read_b64 %0, %8 offset:%12\n\tds_read_b64 %1, %9 offset:%12\n\t"
+        "ds_read_b64 %2, %10 offset:%12\n\tds_read_b64 %3, %11 offset:%12\n\t"
+        "ds_read_b64 %4, %8 offset:%13\n\tds_read_b64 %5, %9 offset:%13\n\t"
+        "ds_read_b64 %6, %10 offset:%13\n\tds_read_b64 %7, %11 offset:%13\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7])
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0), "n"(O1)
+        : "memory");
+  } else {
+    static_assert(W == 4 && O1 == 0);
+    asm volatile(
+        "ds_read_b128 %0, %4 offset:%8\n\tds_read_b128 %1, %5 offset:%8\n\t"
+        "ds_read_b128 %2, %6 offset:%8\n\tds_read_b128 %3, %7 offset:%8\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+        : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0)
+        : "memory");
+  }
+#pragma unroll
+  for (int i = 0; i < (O1 != 0 ? 8 : 4); ++i)
+#pragma unroll
+    for (int e = 0; e < W; ++e) out[i][e] = v[i][e];
+}
+__device__ __forceinline__ float max_over_rows(float v) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  const u32x2 a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a.x), __uint_as_float(a.y));
+  const u32x2 b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b.x), __uint_as_float(b.y));
+}
 
 constexpr int SH_TILES = 1 << 22;  // (group, key head, tile)s stay below it
 
@@ -66,13 +124,11 @@ __device__ __forceinline__ int sh_len(const SharedArgs& A, int row) {
 // side. Lengths and groups are on the device; every work-group numbers them by
 // itself.
 template <typename T, int DP, bool EXACT>
-__global__ __launch_bounds__(256) void k_shared_prefix(SharedArgs A) {
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_prefix(SharedArgs A) {
   using G = AttGeo<T, DP>;
   using S = ShGeo<T, DP>;
   constexpr int TILE = G::TILE, SUB = G::SUB, QT = S::QT, COLS = S::COLS;
-  __shared__ __align__(16) char s_k[2][S::STAGE][S::PAD];
-  __shared__ __align__(16) char s_v[2][S::STAGE][S::PAD];
-  __shared__ uint32_t s_away[2][S::STAGE];  // positions whose page is outside the cache
+  __shared__ __align__(1024) char s_kv[S::RING][2 * S::BYTES];
   __shared__ uint32_t s_u[257], s_x[257];   // units and (group, key head, tile)s before each thread's groups
   __shared__ int s_row[257];                // their first row
   __shared__ uint32_t s_sum[2][4];
@@ -181,7 +237,8 @@ __global__ __launch_bounds__(256) void k_shared_prefix(SharedArgs A) {
       for (int k = 0; k < G::NC; ++k) {
         const int at = 64 * k + 16 * gq;
         const uint4 v = ldg_b16<false>(qp, EXACT ? at : min(at, row_bytes - 16));
-        qf[y][k] = my_n[y] > 0 && (EXACT || at < row_bytes) ? v : make_uint4(0, 0, 0, 0);
+        const uint32_t s = A.negate ? (G::ES == 2 ? 0x80008000u : 0x80000000u) : 0u;  // (a scale below 0 turns q's sign)
+        qf[y][k] = my_n[y] > 0 && (EXACT || at < row_bytes) ? make_uint4(v.x ^ s, v.y ^ s, v.z ^ s, v.w ^ s) : make_uint4(0, 0, 0, 0);
       }
       if (my_n[y] > 0) n_min = min(n_min, my_n[y]), n_max = max(n_max, my_n[y]);
     }
@@ -202,88 +259,102 @@ __global__ __launch_bounds__(256) void k_shared_prefix(SharedArgs A) {
         for (int e = 0; e < G::VD; ++e) acc[y][ng][e] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    // ---- staging: this thread's piece of PASS positions a unit ----
-    const int piece = tid % S::PIECES, p0 = tid / S::PIECES;
-    constexpr int STEP = 256 / S::PIECES;
-    const int req = A.req ? ldg(A.req + lead) : lead;
-    const int32_t* tab = A.table + (int64_t)(reach > 0 ? uni(req) : 0) * A.table_stride;
+    // ---- staging: loads of 1 KB straight to LDS, three stages ahead ----
+    constexpr int ROWS = 1024 / S::ROW;  // positions of a load
+    const int32_t* tab = A.table + (int64_t)(reach > 0 ? uni(A.req ? ldg(A.req + lead) : lead) : 0) * A.table_stride;
     const int64_t head = (int64_t)kvh * A.head_stride * G::ES;
-    const uint32_t at16 = EXACT ? 16 * piece : min(16 * piece, row_bytes - 16);
-    const bool in_row = EXACT || 16 * piece < row_bytes;
     const auto page_of = [&](int t) { return (int)(((uint64_t)(uint32_t)t * A.ps_mul) >> (31 + A.ps_shift)); };
-    int page[S::PASS];
-    uint4 rk[S::PASS], rv[S::PASS];
-    uint32_t away = 0;  // bit j: pass j's position has no page
-    const auto look_up = [&](int s) {
+    const auto row_of = [&](int j) { return (w + 4 * j) * ROWS + lane / S::PIECES; };  // of this lane's piece, load j
+    const auto position = [&](int s) { return min((first + s) * S::STAGE + lane % S::STAGE, reach - 1); };
+    const auto look_up = [&](int s) { return ldg(tab + page_of(position(min(s, units - 1)))); };
+    // stage s, whose pages are `page` (a position a lane); returns those of its
+    // positions that are on no page
+    const auto load = [&](int s, int page) {
+      const int t = position(s);
+      const bool ok = page >= 0 && page < A.n_pages;
+      const int64_t off =
+          (ok ? (int64_t)page * A.page_stride + (int64_t)(t - page_of(t) * A.page_size) * A.token_stride : 0) * G::ES + head;
+      char* to = s_kv[s % S::RING];
 #pragma unroll
-      for (int j = 0; j < S::PASS; ++j)
-        page[j] = ldg(tab + page_of(min((first + s) * S::STAGE + p0 + j * STEP, reach - 1)));
-    };
-    const auto load = [&](int s) {
-      away = 0;
-#pragma unroll
-      for (int j = 0; j < S::PASS; ++j) {
-        const int t = min((first + s) * S::STAGE + p0 + j * STEP, reach - 1);
-        const bool ok = page[j] >= 0 && page[j] < A.n_pages;
-        const int64_t off =
-            (ok ? (int64_t)page[j] * A.page_stride + (int64_t)(t - page_of(t) * A.page_size) * A.token_stride : 0) * G::ES + head;
-        rk[j] = ldg_b16<false>((const char*)A.k + off, at16);
-        rv[j] = ldg_b16<false>((const char*)A.v + off, at16);
-        away |= ok ? 0u : 1u << j;
+      for (int j = 0; j < S::LOADS; ++j) {
+        const int row = row_of(j), at = 16 * sh_slot<S::ROW>(row, lane % S::PIECES);
+        const uint32_t lo = __shfl((int)(uint32_t)off, row, 64), hi = __shfl((int)(off >> 32), row, 64);
+        const int64_t o = (int64_t)((uint64_t)hi << 32 | lo) + (EXACT ? at : min(at, row_bytes - 16));
+        __builtin_amdgcn_global_load_lds((const GLOBAL void*)((const char*)A.k + o), (lds_void*)(to + (w + 4 * j) * 1024), 16,
+                                         0, 0);
+        __builtin_amdgcn_global_load_lds((const GLOBAL void*)((const char*)A.v + o),
+                                         (lds_void*)(to + S::BYTES + (w + 4 * j) * 1024), 16, 0, 0);
       }
+      return (uint64_t)__ballot(!ok);
     };
-    const auto put = [&](int b) {
-#pragma unroll
-      for (int j = 0; j < S::PASS; ++j) {
-        const int p = p0 + j * STEP;
-        const bool keep = in_row && !(away >> j & 1);
-        *(uint4*)&s_k[b][p][16 * piece] = keep ? rk[j] : make_uint4(0, 0, 0, 0);
-        *(uint4*)&s_v[b][p][16 * piece] = keep ? rv[j] : make_uint4(0, 0, 0, 0);
-        if (piece == 0) s_away[b][p] = away >> j & 1;
-      }
-    };
+    int page3 = 0, page4 = 0;                  // of stages s + 3, s + 4
+    uint64_t away0 = 0, away1 = 0, away2 = 0;  // of stages s, s + 1, s + 2
     if (units > 0) {
-      look_up(0);
-      load(0);
-      look_up(min(1, units - 1));
+      const int p0 = look_up(0), p1 = look_up(1), p2 = look_up(2);
+      page3 = look_up(3), page4 = look_up(4);
+      away0 = load(0, p0);
+      if (units > 1) away1 = load(1, p1);
+      if (units > 2) away2 = load(2, p2);
+    }
+    const uint32_t lds = (uint32_t)(uintptr_t)(lds_void*)&s_kv[0][0];
+    const uint32_t k_at = m16 * S::ROW + 16 * sh_slot<S::ROW>(m16, gq);  // (chunk c: ^ 64 c, 16 positions on: + 16 ROW)
+    uint32_t v_at[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = 4 * gq + j, b = m16 * G::VB;
+      v_at[j] = S::BYTES + row * S::ROW + 16 * sh_slot<S::ROW>(row, b / 16) + b % 16;
     }
     for (int s = 0; s < units; ++s) {
-      const int b = s & 1;
-      put(b);
-      if (s + 1 < units) {
-        load(s + 1);
-        look_up(min(s + 2, units - 1));
+      // this wave's part of stage s is there when those of the two behind it are
+      // the only loads that are out; then all waves' parts are
+      if (s + 2 < units)
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(4 * S::LOADS));
+      else
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+      lds_barrier();
+      const uint64_t away = away0;
+      away0 = away1, away1 = away2;
+      if (s + 3 < units) {
+        const int page = page3;
+        page3 = page4;
+        page4 = look_up(s + 5);
+        away2 = load(s + 3, page);
       }
-      __syncthreads();
       if (n_max == 0) continue;
 #pragma unroll 1
       for (int tt = 0; tt < S::STAGE / TILE; ++tt) {
         const int t = (first + s) * S::STAGE + tt * TILE;
         if (t >= n_max) break;
         AttTile<T, DP, EXACT> tile;
-        const char *kp = s_k[b][tt * TILE], *vp = s_v[b][tt * TILE];
+        const uint32_t base = lds + (s % S::RING) * 2 * S::BYTES + tt * TILE * S::ROW;
+        if constexpr (G::NC == 2) {  // (two chunks of 32 positions, as four rows)
+          static_assert(SUB == 2);
+          const uint32_t a[4] = {base + k_at, base + (k_at ^ 64), base + k_at + 16 * S::ROW, base + (k_at ^ 64) + 16 * S::ROW};
+          uint32_t* const o[8] = {&tile.k[0][0].x, &tile.k[0][1].x, &tile.k[1][0].x, &tile.k[1][1].x};
+          lds_read<4, 0, 0>(a, o);
+        } else {
 #pragma unroll
-        for (int sb = 0; sb < SUB; ++sb)
-#pragma unroll
-          for (int c = 0; c < G::NC; ++c) tile.k[sb][c] = *(const uint4*)(kp + (16 * sb + m16) * S::PAD + 64 * c + 16 * gq);
+          for (int c = 0; c < G::NC; c += 4) {
+            const uint32_t a[4] = {base + (k_at ^ (64 * c)), base + (k_at ^ (64 * c + 64)), base + (k_at ^ (64 * c + 128)),
+                                   base + (k_at ^ (64 * c + 192))};
+            uint32_t* const o[8] = {&tile.k[0][c].x, &tile.k[0][c + 1].x, &tile.k[0][c + 2].x, &tile.k[0][c + 3].x,
+                                    &tile.k[SUB - 1][c].x, &tile.k[SUB - 1][c + 1].x, &tile.k[SUB - 1][c + 2].x,
+                                    &tile.k[SUB - 1][c + 3].x};
+            lds_read<4, 0, SUB == 2 ? 16 * S::ROW : 0>(a, o);
+          }
+        }
         f32x4 sc[QT][SUB];
         tile.template scores<QT>([&](int y, int c) { return qf[y][c]; }, sc, gq, row_bytes);
-        const uint32_t gone = (uint32_t)__ballot(lane < TILE && s_away[b][tt * TILE + (lane & (TILE - 1))] != 0);
-#pragma unroll
-        for (int sb = 0; sb < SUB; ++sb)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int ng = 0; ng < G::NG; ++ng) {
-              typedef uint32_t vec __attribute__((ext_vector_type(G::VB / 4)));
-              const vec x4 = *(const vec*)(vp + (16 * sb + 4 * gq + j) * S::PAD + (16 * ng + m16) * G::VB);
-#pragma unroll
-              for (int e = 0; e < G::VB / 4; ++e) tile.v[sb][j][ng][e] = x4[e];
-            }
-#pragma unroll
-        for (int y = 0; y < QT; ++y)
-#pragma unroll
-          for (int sb = 0; sb < SUB; ++sb) sc[y][sb] *= A.scale_log2;
+        const uint32_t gone = (uint32_t)(away >> (tt * TILE)) & (uint32_t)((1ull << TILE) - 1);
+        const uint32_t va[4] = {base + v_at[0], base + v_at[1], base + v_at[2], base + v_at[3]};
+        const auto read_v = [&](auto ng) {
+          uint32_t* const o[8] = {tile.v[0][0][ng], tile.v[0][1][ng], tile.v[0][2][ng], tile.v[0][3][ng],
+                                  tile.v[SUB - 1][0][ng], tile.v[SUB - 1][1][ng], tile.v[SUB - 1][2][ng], tile.v[SUB - 1][3][ng]};
+          lds_read<G::VB / 4, 16 * G::VB * ng, SUB == 2 ? 16 * G::VB * ng + 16 * S::ROW : 0>(va, o);
+        };
+        read_v(std::integral_constant<int, 0>{});
+        if constexpr (G::NG > 1) read_v(std::integral_constant<int, 1>{});
+        if constexpr (G::NG > 2) read_v(std::integral_constant<int, 2>{}), read_v(std::integral_constant<int, 3>{});
         // positions that not all columns see
         const bool cut = t + TILE > n_min || gone;
         bool odd = false;  // some of what only some columns see is not finite
@@ -303,8 +374,10 @@ __global__ __launch_bounds__(256) void k_shared_prefix(SharedArgs A) {
                 for (int ng = 0; ng < G::NG; ++ng)
 #pragma unroll
                   for (int e = 0; e < G::VB / 4; ++e) {
-                    const uint32_t v = tile.v[sb][j][ng][e];
-                    odd |= (v & 0x7F800000u) == 0x7F800000u || (G::ES == 2 && (v & 0x7F80u) == 0x7F80u);
+                    uint32_t& v = tile.v[sb][j][ng][e];
+                    const bool hi = (v & 0x7F800000u) == 0x7F800000u, lo = G::ES == 2 && (v & 0x7F80u) == 0x7F80u;
+                    odd |= hi || lo;
+                    v = G::ES == 4 ? (hi ? 0u : v) : (hi ? v & 0xFFFFu : v) & (lo ? 0xFFFF0000u : ~0u);
                   }
               }
             }
@@ -317,8 +390,11 @@ __global__ __launch_bounds__(256) void k_shared_prefix(SharedArgs A) {
           for (int sb = 0; sb < SUB; ++sb)
 #pragma unroll
             for (int j = 0; j < 4; ++j) tm = fmaxf(tm, sc[y][sb][j]);
-          const float mn = fmaxf(mx[y], max_over_quarters(tm));
-          if (__any(mn > mx[y])) {
+          // The reference of a column's powers of two moves where a score passes it
+          // by 2^8: until then the powers stay far inside fp32, and nothing has to
+          // cross lanes.
+          if (__any(fmaf(tm, A.scale_log2, -mx[y]) > 8.f)) {
+            const float mn = fmaxf(mx[y], max_over_rows(tm) * A.scale_log2);
             const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mx[y] - mn);
             l[y] *= f;
 #pragma unroll
@@ -332,35 +408,31 @@ __global__ __launch_bounds__(256) void k_shared_prefix(SharedArgs A) {
           for (int sb = 0; sb < SUB; ++sb)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              sc[y][sb][j] = __builtin_amdgcn_exp2f(sc[y][sb][j] - ref);
+              sc[y][sb][j] = __builtin_amdgcn_exp2f(fmaf(sc[y][sb][j], A.scale_log2, -ref));
               l[y] += sc[y][sb][j];
             }
         }
-        if (!odd) {
-          tile.template weigh<QT, false, true>(sc, acc);
-        } else {  // a column after the other, with V cleared where it does not see it
-          for (int c = 0; c < 16; ++c) {
+        tile.template weigh<QT, false, true>(sc, acc);
+        const char* vp = s_kv[s % S::RING] + S::BYTES + tt * TILE * S::ROW;
+        if (odd) {  // what was left out, for those who see it: the sum is not finite there, whatever the weight
+#pragma unroll 1
+          for (int p = max(0, n_min - t); p < min(TILE, n_max - t); ++p) {
+            if (gone >> p & 1) continue;
 #pragma unroll
-            for (int y = 0; y < QT; ++y) {
-              const int n = lane_of(my_n[y], c);
-              uint32_t mask[SUB][4];
+            for (int ng = 0; ng < G::NG; ++ng)
 #pragma unroll
-              for (int sb = 0; sb < SUB; ++sb)
+              for (int r = 0; r < 4; ++r) {
+                typedef uint32_t vec __attribute__((ext_vector_type(G::VB / 4)));
+                const int b16 = (16 * ng + 4 * gq + r) * G::VB;  // (bytes of the row)
+                const vec x4 = *(const vec*)(vp + p * S::ROW + 16 * sh_slot<S::ROW>(p, b16 / 16) + b16 % 16);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) mask[sb][j] = t + 16 * sb + 4 * gq + j >= n ? 0u : ~0u;
-              f32x4 p1[1][SUB], a1[1][G::NG][G::VD];
+                for (int i = 0; i < G::VD; ++i) {
+                  const float v = __uint_as_float(G::ES == 4 ? x4[i % (G::VB / 4)] : i & 1 ? x4[i / 2] & 0xFFFF0000u : x4[i / 2] << 16);
 #pragma unroll
-              for (int sb = 0; sb < SUB; ++sb) p1[0][sb] = sc[y][sb];
-#pragma unroll
-              for (int ng = 0; ng < G::NG; ++ng)
-#pragma unroll
-                for (int e = 0; e < G::VD; ++e) a1[0][ng][e] = acc[y][ng][e];
-              tile.template weigh<1, true, true>(p1, a1, mask, m16 == c);
-#pragma unroll
-              for (int ng = 0; ng < G::NG; ++ng)
-#pragma unroll
-                for (int e = 0; e < G::VD; ++e) acc[y][ng][e] = a1[0][ng][e];
-            }
+                  for (int y = 0; y < QT; ++y)
+                    if (!isfinite(v) && t + p < my_n[y]) acc[y][ng][i][r] += v;
+                }
+              }
           }
         }
       }
@@ -407,7 +479,6 @@ void sh_dim(const SharedArgs& A, int dp, int blocks, hipStream_t s) {
 
 // columns of a work-group, positions of a unit
 int sh_cols(int es, int dp) { return dp * es >= 1024 ? 64 : 128; }
-int sh_stage(int es, int dp) { return std::min(64, 16384 / (dp * es)); }
 int sh_blocks(int units) { return 2 * units; }
 // (group, key head, tile)s of up to n_rows rows in up to n_groups groups
 int64_t sh_tiles(int64_t n_rows, int64_t n_groups, int64_t group, int64_t n_kv, int cols) {
@@ -481,7 +552,7 @@ extern "C" scute_status scute_shared_attention(const scute_kv_cache* C, const vo
   const SharedArgs A{q, C->k, C->v, table, len, req, group, shared_len, from, seeds, q_stride, C->page_stride,
                      C->token_stride, C->head_stride, table_stride, C->n_pages, (uint32_t)mul, n_rows, n_groups,
                      C->n_kv_heads, group_heads, C->head_dim, C->page_size, shift, (int32_t)reach, n_requests, (int32_t)tiles,
-                     scale * 1.4426950408889634f};
+                     scale < 0.f, std::max(fabsf(scale * 1.4426950408889634f), 1e-37f)};
   const hipStream_t s = (hipStream_t)stream;
   if (es == 4) sh_dim<float>(A, dp, sh_blocks(units), s);
   else sh_dim<uint16_t>(A, dp, sh_blocks(units), s);
