@@ -32,8 +32,8 @@ ARCH = "gfx950"
 
 HOST_SRCS = ["layer.cpp", "plan.cpp", "plan_decode.cpp", "plan_prefill.cpp", "plan_fdecode.cpp"]
 HIP_SRCS = ["forward.hip", "decode.hip", "prefill.hip", "fdecode.hip", "rotate.hip", "routes.hip",
-            "block.hip", "attend.hip", "attend_sinks.hip", "attend_suffix.hip",
-            "attend_shared.hip", "pages.hip"]
+            "block.hip", "attend.hip", "attend_sinks.hip", "attend_shared.hip",
+            "pages.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
           "-I" + os.path.join(ROOT, "include")]

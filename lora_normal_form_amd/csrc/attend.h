@@ -1,5 +1,5 @@
-// The kernel of attention over the paged cache, for its three forms (attend.hip,
-// attend_sinks.hip, attend_suffix.hip).
+// The kernel of attention over the paged cache, for its forms (attend.hip,
+// attend_sinks.hip), and its tiles' products (attend_shared.hip too).
 #pragma once
 
 #include <math.h>
@@ -14,19 +14,7 @@ namespace scute {
 // What a row's positions are:
 //   ATT_PLAIN   the last `window` below its length (0: all)
 //   ATT_SINKS   those, and the first `sinks`
-//   ATT_SUFFIX  those from AttRowFrom::from on; the sums of what lies before have
-//               been taken by k_shared_prefix and are added at the end
-enum : int { ATT_PLAIN = 0, ATT_SINKS = 1, ATT_SUFFIX = 2 };
-
-// A row's shared positions and where their partial results lie: the row's group
-// has `tiles` tiles of columns (row of the group times heads of a key head, and
-// head of it; the row's first is col0) for each key head, the x0-th on, of `units`
-// units from the u0-th on; work-group u / each of k_shared_prefix took unit u, and
-// its part of the x-th tile is in slot u / each + x.
-struct alignas(16) AttRowFrom {
-  int32_t from, tiles, col0, units;
-  uint32_t u0, x0, each, pad;
-};
+enum : int { ATT_PLAIN = 0, ATT_SINKS = 1 };
 
 struct AttArgs {
   const void *q, *k, *v;
@@ -39,10 +27,7 @@ struct AttArgs {
   uint32_t part_bytes, ps_mul;  // t / page_size = t ps_mul >> 31 + ps_shift
   int32_t n_rows, n_kv, q_tiles, group, together, head_dim, page_size, ps_shift, reach, n_requests, window;
   float scale_log2;  // scale log2(e): the softmax runs on powers of two
-  int32_t sinks;           // ATT_SINKS
-  const AttRowFrom* from;  // ATT_SUFFIX, of each row
-  const float* seeds;      // slots of `seed_cols` columns of (head size, rounded up, values, m, l, two unused)
-  int32_t seed_cols;
+  int32_t sinks;     // ATT_SINKS
 };
 
 // out[h] = sum_t softmax_t(scale q[h] . K[t]) V[t] with a running maximum and
@@ -94,16 +79,9 @@ struct AttRow {
 __device__ __forceinline__ int att_len(const AttArgs& A, int len, int req) {
   return (uint32_t)req < (uint32_t)A.n_requests ? min(max(len, 0), A.reach) : 0;
 }
-// and the first of them (ATT_SINKS: behind the sinks), `from` its shared positions
-template <int FORM>
-__device__ __forceinline__ int att_first(const AttArgs& A, int n, int from) {
-  if constexpr (FORM == ATT_SUFFIX) return min(from, n);
+// and the first of them (ATT_SINKS: behind the sinks)
+__device__ __forceinline__ int att_first(const AttArgs& A, int n) {
   return A.window > 0 && n > A.window ? n - A.window : 0;
-}
-template <int FORM>
-__device__ __forceinline__ int att_from(const AttArgs& A, int row) {
-  if constexpr (FORM == ATT_SUFFIX) return ldg(&A.from[row].from);
-  return 0;
 }
 // whether a row whose positions begin at lo sees none at `at` (below its length)
 template <int FORM>
@@ -116,20 +94,19 @@ __device__ __forceinline__ AttRow att_row(const AttArgs& A, int row) {
   AttRow r;
   bool leads = true;
   if (!SHARED || A.together == 1) {
-    const int len = ldg(A.len + row), from = att_from<FORM>(A, row);  // (asked for before req is known: one trip to memory, not two)
+    const int len = ldg(A.len + row);  // (asked for before req is known: one trip to memory, not two)
     r.req = A.req ? ldg(A.req + row) : A.row0 + row;
     r.n = att_len(A, len, r.req);
-    r.lo = att_first<FORM>(A, r.n, from);
+    r.lo = att_first(A, r.n);
     r.rows = 1, r.every_lo = r.lo, r.every_n = r.n;
   } else {
     const int base = row / A.together * A.together, me = row - base;
-    int q[4], l[4], f[4];
+    int q[4], l[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int at = min(base + j, A.n_rows - 1);
       q[j] = ldg(A.req + at);
       l[j] = ldg(A.len + at);
-      f[j] = att_from<FORM>(A, at);
     }
     const int own = me == 0 ? q[0] : me == 1 ? q[1] : me == 2 ? q[2] : q[3];
     leads = me == 0 || own != (me == 1 ? q[0] : me == 2 ? q[1] : q[2]);
@@ -138,7 +115,7 @@ __device__ __forceinline__ AttRow att_row(const AttArgs& A, int row) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       on = on && (j < me || (j < A.together && base + j < A.n_rows && q[j] == own));
-      const int n = att_len(A, l[j], own), lo = att_first<FORM>(A, n, f[j]);
+      const int n = att_len(A, l[j], own), lo = att_first(A, n);
       if (on && j >= me) {
         r.n = max(r.n, n);
         if (n > 0) r.lo = min(r.lo, lo);
@@ -272,8 +249,7 @@ struct AttTile {
   // columns of the lanes that `keep`. POS: both parts of a weight are positive (the
   // first cut off instead of rounded, the second 2^-20 of the weight more than the
   // rest), so that an infinite V stays infinite; the weight is off by 2^-15 at most.
-  // Y0 .. Y1 - 1: the query tiles it is done for
-  template <int QT, bool SOME = false, bool POS = false, int Y0 = 0, int Y1 = QT>
+  template <int QT, bool SOME = false, bool POS = false>
   __device__ __forceinline__ void weigh(const f32x4 (&p)[QT][G::SUB], f32x4 (&acc)[QT][G::NG][G::VD],
                                         const uint32_t (*mask)[4] = nullptr, bool keep = true) {
     const auto val = [&](int s, int j, int ng, int i) { return SOME ? v[s][j][ng][i] & mask[s][j] : v[s][j][ng][i]; };
@@ -298,7 +274,7 @@ struct AttTile {
         return pack_bf2(__float_as_uint(x - __uint_as_float(hi << 16)), __float_as_uint(y - __uint_as_float(hi & 0xFFFF0000u)));
       };
 #pragma unroll
-      for (int y = Y0; y < Y1; ++y) {
+      for (int y = 0; y < QT; ++y) {
         b[y].x = first(p[y][0][0], p[y][0][1]);
         b[y].y = first(p[y][0][2], p[y][0][3]);
         b[y].z = first(p[y][1][0], p[y][1][1]);
@@ -319,7 +295,7 @@ struct AttTile {
           a.z = __builtin_amdgcn_perm(val(1, 1, ng, i / 2), val(1, 0, ng, i / 2), sel);
           a.w = __builtin_amdgcn_perm(val(1, 3, ng, i / 2), val(1, 2, ng, i / 2), sel);
 #pragma unroll
-          for (int y = Y0; y < Y1; ++y) put(acc[y][ng][i], mfma16(a, b2[y], mfma16(a, b[y], acc[y][ng][i])));
+          for (int y = 0; y < QT; ++y) put(acc[y][ng][i], mfma16(a, b2[y], mfma16(a, b[y], acc[y][ng][i])));
         }
     } else {
 #pragma unroll
@@ -327,7 +303,7 @@ struct AttTile {
 #pragma unroll
         for (int i = 0; i < G::VD; ++i)
 #pragma unroll
-          for (int y = Y0; y < Y1; ++y) {
+          for (int y = 0; y < QT; ++y) {
             f32x4 x = acc[y][ng][i];
 #pragma unroll
             for (int j = 0; j < 4; ++j) x = mfma4(val(0, j, ng, i), __float_as_uint(p[y][0][j]), x);
@@ -524,7 +500,7 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
     int my_n = R.n, my_lo = R.lo;  // what this lane's column sees
     if (shared && R.rows > 1) {
       my_n = att_len(A, ldg(A.len + row + my_row), R.req);
-      my_lo = att_first<FORM>(A, my_n, att_from<FORM>(A, row + my_row));
+      my_lo = att_first(A, my_n);
     }
 
     // ---- the wave's tiles t0 + w, t0 + w + 4, ... ----
@@ -775,37 +751,9 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
     __syncthreads();
     const bool whole = units == (uint32_t)R.units;
     const int E = nq * D / 4;  // groups of four elements of the piece's output
-    const auto put = [&](int g, int d, f32x4 o, float L, float m) {
-      const int i = !SHARED ? 0 : g / wide;
-      if constexpr (FORM == ATT_SUFFIX) {
-        // the sums over the row's shared positions, a slot after the other
-        const u32x4 f0 = ldg((const u32x4*)(A.from + row + i)), f1 = ldg((const u32x4*)(A.from + row + i) + 1);
-        const AttRowFrom F{(int)f0.x, (int)f0.y, (int)f0.z, (int)f0.w, f1.x, f1.y, f1.z, 0};
-        const int c = F.col0 + h0 + g - i * wide - kvh * A.group, tile = c / A.seed_cols;
-        const uint32_t x = (uint32_t)(kvh * F.tiles + tile), u = F.u0 + x * F.units;
-        const uint32_t w0 = F.units ? u / F.each : 0;
-        const int parts = F.units ? (int)((u + F.units - 1) / F.each - w0) + 1 : 0;
-        const float* p = A.seeds + ((int64_t)(w0 + F.x0 + x) * A.seed_cols + c - tile * A.seed_cols) * (DP + 4);
-        for (int j0 = 0; j0 < parts; j0 += 4) {  // (four slots' loads in flight)
-          f32x4 ml[4], v[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float* a = p + (int64_t)min(j0 + j, parts - 1) * A.seed_cols * (DP + 4);
-            ml[j] = ldg4(a + DP);
-            v[j] = ldg4(a + d);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (j0 + j >= parts) break;
-            const float mn = fmaxf(m, ml[j].x), ref = mn == -INFINITY ? 0.f : mn;
-            const float fa = __builtin_amdgcn_exp2f(m - ref), fb = __builtin_amdgcn_exp2f(ml[j].x - ref);
-            o = o * fa + v[j] * fb;
-            L = L * fa + ml[j].y * fb;
-            m = mn;
-          }
-        }
-      }
+    const auto put = [&](int g, int d, f32x4 o, float L) {
       const f32x4 x = L == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : o / L;
+      const int i = !SHARED ? 0 : g / wide;
       const int64_t at = (int64_t)(row + i) * A.out_stride + (int64_t)(h0 + g - i * wide) * D + d;
       if constexpr (G::ES == 4) {
         stg4((float*)A.out + at, x);
@@ -846,7 +794,7 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
           typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
           const int i = SHARED ? g / wide : 0;
           const int n = shared ? att_len(A, ldg(A.len + row + i), R.req) : R.n;
-          const int lo = att_first<FORM>(A, n, shared ? att_from<FORM>(A, row + i) : R.lo);
+          const int lo = att_first(A, n);
           const int32_t* tab = A.table + (int64_t)R.req * A.table_stride;
           const char* vp = (const char*)A.v + ((int64_t)kvh * A.head_stride + d) * G::ES;
           f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -885,7 +833,7 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
         }
       }
       if (whole) {
-        put(g, d, o, L, gm);
+        put(g, d, o, L);
       } else {
         const uint32_t at = slot * SLOT + g * (DP + 4) * 4;
         st_sys4(part, at + d * 4, o);
@@ -982,7 +930,7 @@ __global__ __launch_bounds__(256) void k_paged_attention(AttArgs A) {
             for (int y = 0; y < Y; ++y)
               if (on[y] && set == 0) {
                 if (level) {
-                  put(g[y], d[y], o[y], L[y], gm[y]);
+                  put(g[y], d[y], o[y], L[y]);
                 } else {  // (in the group's first place, whose elements only this thread reads, m and l beside its own)
                   const uint32_t at = first * SLOT + g[y] * (DP + 4) * 4;
                   st_sys4(part, at + d[y] * 4, o[y]);

@@ -83,7 +83,7 @@ scute_status att_run(const char* fn, const AttCall& c, int form, hipStream_t s) 
             c.q_stride, c.out_stride, C->page_stride, C->token_stride, C->head_stride, c.table_stride, C->n_pages, 0,
             (uint32_t)(need - counters), (uint32_t)mul, c.n_rows, C->n_kv_heads,
             (group + columns - 1) / columns, group, together, C->head_dim, C->page_size, shift, (int32_t)reach,
-            c.n_requests, c.window, c.scale * 1.4426950408889634f, c.sinks, c.from, c.seeds, c.seed_cols};
+            c.n_requests, c.window, c.scale * 1.4426950408889634f, c.sinks};
   // rows of one launch: their units, at the table's whole width, stay below 2^31
   // (sinks: one tile more)
   const int64_t most = (((int64_t)1 << 31) - 1) /
@@ -96,8 +96,7 @@ scute_status att_run(const char* fn, const AttCall& c, int form, hipStream_t s) 
     A.out = (char*)c.out + r * c.out_stride * es;
     A.len = c.len + r;
     A.req = c.req ? c.req + r : nullptr;
-    A.from = c.from ? c.from + r : nullptr;
-    (form == ATT_PLAIN ? att_plain : form == ATT_SINKS ? att_sinks : att_suffix)(A, (int)es, dp, units, s);
+    (form == ATT_PLAIN ? att_plain : att_sinks)(A, (int)es, dp, units, s);
   }
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SCUTE_OK : hip_fail(e, fn);
@@ -138,7 +137,7 @@ extern "C" scute_status scute_paged_attention(const scute_kv_cache* C, const voi
                                               int64_t workspace_bytes, void* stream) {
   return attention("scute_paged_attention",
                    AttCall{C, q, q_stride, n_heads, table, table_stride, n_requests, table_width, len, req, n_rows, scale,
-                           window, 0, out, out_stride, workspace, workspace_bytes, nullptr, nullptr, 1},
+                           window, 0, out, out_stride, workspace, workspace_bytes},
                    ATT_PLAIN, stream);
 }
 
@@ -151,6 +150,6 @@ extern "C" scute_status scute_sink_attention(const scute_kv_cache* C, const void
   // (without a window every position is seen already)
   return attention("scute_sink_attention",
                    AttCall{C, q, q_stride, n_heads, table, table_stride, n_requests, table_width, len, req, n_rows, scale,
-                           window, sinks, out, out_stride, workspace, workspace_bytes, nullptr, nullptr, 1},
+                           window, sinks, out, out_stride, workspace, workspace_bytes},
                    window > 0 && sinks > 0 ? ATT_SINKS : ATT_PLAIN, stream);
 }

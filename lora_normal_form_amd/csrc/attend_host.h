@@ -6,10 +6,8 @@
 namespace scute {
 
 struct AttArgs;
-struct AttRowFrom;
 
-// Arguments of a call, as of scute_paged_attention; sinks and the rows' shared
-// positions where the form has them.
+// Arguments of a call, as of scute_paged_attention, and sinks where it has them.
 struct AttCall {
   const scute_kv_cache* C;
   const void* q;
@@ -26,12 +24,8 @@ struct AttCall {
   int64_t out_stride;
   void* workspace;
   int64_t workspace_bytes;
-  const AttRowFrom* from;
-  const float* seeds;
-  int32_t seed_cols;
 };
-// the checks of a call's arguments (`need`: bytes of workspace, asked for last);
-// nothing touches the device
+// the checks of a call's arguments (not the workspace's size); nothing touches the device
 scute_status att_check(const char* fn, const AttCall& c);
 // its launches, with the cache's device current
 scute_status att_run(const char* fn, const AttCall& c, int form, hipStream_t s);
@@ -43,6 +37,5 @@ int64_t att_workspace(int units, int head_dim);
 
 void att_plain(const AttArgs& A, int es, int dp, int blocks, hipStream_t s);
 void att_sinks(const AttArgs& A, int es, int dp, int blocks, hipStream_t s);
-void att_suffix(const AttArgs& A, int es, int dp, int blocks, hipStream_t s);
 
 }  // namespace scute

@@ -1,7 +1,5 @@
 // Attention of rows whose contexts begin with the same positions
-// (scute_shared_attention): the shared positions once for all rows of a group,
-// here; what each row has beside them by the kernel of attend.h, which joins
-// the two.
+// (scute_shared_attention).
 
 #include <algorithm>
 
@@ -10,14 +8,34 @@
 
 namespace scute {
 
+// Where a row's partial results lie.
+struct alignas(16) ShRow {
+  // shared positions: the row's group has `tiles` tiles of columns (row of the group
+  // times heads of a key head, and head of it; the row's first is col0) for each
+  // key head, the x0-th on, of `units` units from the u0-th on (0: nothing shared)
+  int32_t units, tiles, col0;
+  uint32_t u0, x0;
+  // its own: `own` tiles a head behind `before` of the rows before it, of row
+  // `lead`'s run, whose column `at` is the row's first
+  int32_t own;
+  uint32_t before;
+  int32_t lead, at, pad[3];
+};
+struct ShPlan {
+  uint32_t each_shared, each_own;  // units of a work-group, tiles of a wave
+};
+
 struct SharedArgs {
   const void *q, *k, *v;
+  void* out;
   const int32_t *table, *len, *req, *group, *shared;
-  AttRowFrom* from;
-  float* seeds;
-  int64_t q_stride, page_stride, token_stride, head_stride, table_stride, n_pages;
+  ShRow* rows;
+  ShPlan* plan;
+  float *seeds, *own;  // partial results of shared and of own positions
+  int64_t q_stride, out_stride, page_stride, token_stride, head_stride, table_stride, n_pages;
   uint32_t ps_mul;
   int32_t n_rows, n_groups, n_kv, heads, head_dim, page_size, ps_shift, reach, n_requests, max_tiles;
+  int32_t together, q_tiles, own_cols;  // rows of a run at most; query tiles of a key head; columns of an own slot
   int32_t negate;    // the scale is below 0
   float scale_log2;  // its magnitude times log2(e), above 0 (so that what is masked stays at -inf)
 };
@@ -103,7 +121,7 @@ __device__ __forceinline__ ShGroup sh_group(const SharedArgs& A, int g) {
   q.row = a, q.rows = max(b - a, 0);
   q.n = min(max(ldg(A.shared + g), 0), A.reach);
   q.tiles = (int)(((int64_t)q.rows * A.heads + S::COLS - 1) / S::COLS);
-  q.units = (q.n + S::STAGE - 1) / S::STAGE;
+  q.units = q.tiles ? (q.n + S::STAGE - 1) / S::STAGE : 0;
   return q;
 }
 __device__ __forceinline__ int sh_len(const SharedArgs& A, int row) {
@@ -111,87 +129,179 @@ __device__ __forceinline__ int sh_len(const SharedArgs& A, int row) {
   return (uint32_t)req < (uint32_t)A.n_requests ? min(max(len, 0), A.reach) : 0;
 }
 
+// What a work-group knows of the call's groups and rows: in LDS, for each thread's
+// groups and rows.
+struct ShShared {
+  uint32_t u[257], x[257];   // units and (group, key head, tile)s of the groups before the thread's
+  int row[257];              // its groups' first row
+  int end[256], n[256];      // the first of its groups: the row behind it, shared positions
+  uint32_t t[257];           // tiles a head of the rows before the thread's
+  uint32_t sum[2][4];
+  unsigned long long lead[4];
+};
+struct ShCall {
+  int per_g, per_r;  // groups and rows a thread
+  bool fits;
+};
+
+// index of the last border (of 256, the first 0) that is <= x
+template <typename B>
+__device__ __forceinline__ int sh_find(const B* b, B x) {
+  int lo = 0;
+#pragma unroll
+  for (int step = 128; step > 0; step >>= 1)
+    if (b[lo + step] <= x) lo += step;
+  return lo;
+}
+// the group of a row: f(group, units before it, tiles before it); whether it has one
+template <typename S, typename F>
+__device__ __forceinline__ bool sh_group_of(const SharedArgs& A, const ShCall& c, const ShShared& L, int row, F f) {
+  if (!c.fits) return false;
+  const int lo = sh_find(L.row, row);
+  uint32_t u = L.u[lo], x = L.x[lo];
+  for (int g = lo * c.per_g; g < min(A.n_groups, (lo + 1) * c.per_g); ++g) {
+    const ShGroup q = sh_group<S>(A, g);
+    if (row >= q.row && row < q.row + q.rows) {
+      f(q, u, x);
+      return true;
+    }
+    u += (uint32_t)q.units * q.tiles * A.n_kv;
+    x += (uint32_t)(q.units ? q.tiles : 0) * A.n_kv;
+  }
+  return false;
+}
+// positions that a row shares
+template <typename S>
+__device__ __forceinline__ int sh_from(const SharedArgs& A, const ShCall& c, const ShShared& L, int row) {
+  if (c.per_g == 1) {
+    const int lo = sh_find(L.row, row);
+    return c.fits && row >= L.row[lo] && row < L.end[lo] ? L.n[lo] : 0;
+  }
+  int n = 0;
+  sh_group_of<S>(A, c, L, row, [&](const ShGroup& q, uint32_t, uint32_t) { n = q.n; });
+  return n;
+}
+
+// A run: up to `together` rows of one request that follow each other (as many as
+// fit 16 columns with all heads of a key head, from multiples of `together` on),
+// which are read for together. Its positions lo .. n - 1, those that every row of
+// it with any sees every_lo .. every_n - 1.
+struct ShRun {
+  int row, rows, req, lo, n, every_lo, every_n, tiles;
+};
+// f(run) for the runs of rows base .. base + together - 1
+template <typename S, int TILE, typename F>
+__device__ __forceinline__ void sh_runs(const SharedArgs& A, const ShCall& c, const ShShared& L, int base, F f) {
+  int q[4], n[4], lo[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int row = min(base + j, A.n_rows - 1);
+    n[j] = 0, q[j] = -1;
+    if (j < A.together) {
+      n[j] = ldg(A.len + row);
+      q[j] = A.req ? ldg(A.req + row) : row;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    lo[j] = 0;
+    if (j < A.together && base + j < A.n_rows) {
+      n[j] = (uint32_t)q[j] < (uint32_t)A.n_requests ? min(max(n[j], 0), A.reach) : 0;
+      lo[j] = min(n[j], sh_from<S>(A, c, L, base + j));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i >= A.together || base + i >= A.n_rows || (i > 0 && q[i] == q[i > 0 ? i - 1 : 0])) continue;
+    ShRun r{base + i, 0, q[i], 0x7FFFFFFF, 0, 0, 0x7FFFFFFF, 0};
+    bool on = true;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j < i) continue;
+      on = on && j < A.together && base + j < A.n_rows && q[j] == q[i];
+      if (!on) continue;
+      ++r.rows;
+      if (n[j] > lo[j]) {
+        r.lo = min(r.lo, lo[j]), r.n = max(r.n, n[j]);
+        r.every_lo = max(r.every_lo, lo[j]), r.every_n = min(r.every_n, n[j]);
+      }
+    }
+    r.lo = min(r.lo, r.n);
+    r.tiles = r.n > r.lo ? (r.n + TILE - 1) / TILE - r.lo / TILE : 0;
+    f(r);
+  }
+}
+
+// The weights of a tile's scores, in their place: the column's sum, and its sums of
+// values where the reference of its powers of two moves. It moves where a score
+// passes it by 2^8: until then the powers stay far inside fp32, and nothing has to
+// cross lanes.
+template <typename G>
+__device__ __forceinline__ void sh_weights(const SharedArgs& A, f32x4 (&sc)[G::SUB], float& mx, float& l,
+                                           f32x4 (&acc)[G::NG][G::VD]) {
+  float tm = sc[0][0];
+#pragma unroll
+  for (int sb = 0; sb < G::SUB; ++sb)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) tm = fmaxf(tm, sc[sb][j]);
+  if (__any(fmaf(tm, A.scale_log2, -mx) > 8.f)) {
+    const float mn = fmaxf(mx, max_over_rows(tm) * A.scale_log2);
+    const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mx - mn);
+    l *= f;
+#pragma unroll
+    for (int ng = 0; ng < G::NG; ++ng)
+#pragma unroll
+      for (int e = 0; e < G::VD; ++e) acc[ng][e] *= f;
+    mx = mn;
+  }
+  const float ref = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+  for (int sb = 0; sb < G::SUB; ++sb)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      sc[sb][j] = __builtin_amdgcn_exp2f(fmaf(sc[sb][j], A.scale_log2, -ref));
+      l += sc[sb][j];
+    }
+}
+// Elements of a dword of V that are not finite become 0; whether there are any.
+template <int ES>
+__device__ __forceinline__ bool sh_finite(uint32_t& v) {
+  const bool hi = (v & 0x7F800000u) == 0x7F800000u, lo = ES == 2 && (v & 0x7F80u) == 0x7F80u;
+  v = ES == 4 ? (hi ? 0u : v) : (hi ? v & 0xFFFFu : v) & (lo ? 0xFFFF0000u : ~0u);
+  return hi || lo;
+}
+// What is not finite of the elements at p (one load of a lane) to row r of the sums
+// of a column that sees it: they are not finite then, whatever the weight.
+template <typename G>
+__device__ __forceinline__ void sh_add_odd(const char* p, bool seen, f32x4 (&acc)[G::VD], int r) {
+  typedef uint32_t vec __attribute__((ext_vector_type(G::VB / 4)));
+  const vec x = *(const vec*)p;
+#pragma unroll
+  for (int i = 0; i < G::VD; ++i) {
+    const float v = __uint_as_float(G::ES == 4 ? x[i % (G::VB / 4)] : i & 1 ? x[i / 2] & 0xFFFF0000u : x[i / 2] << 16);
+    if (!isfinite(v) && seen) acc[i][r] += v;
+  }
+}
+
 // Sums of the softmax over a group's shared positions for all its rows: a
 // product of tall matrices, so K and V go through LDS once for 128 columns (rows
 // times the heads of a key head), 32 columns a wave, and a wave's columns are
 // its own: nothing is joined between waves.
-//
-// How the work is cut. A unit is one stage of positions of one (group, key head,
-// tile of columns); the units are numbered in that order and every work-group
-// takes the same number of consecutive ones. Work-group w's part of the x-th
-// (group, key head, tile) is a piece, in slot w + x: both grow from piece to
-// piece, so slots are not shared and a (group, key head, tile)'s lie side by
-// side. Lengths and groups are on the device; every work-group numbers them by
-// itself.
 template <typename T, int DP, bool EXACT>
-__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_prefix(SharedArgs A) {
+__device__ __forceinline__ void sh_prefix(const SharedArgs& A, const ShCall& call, ShShared& L,
+                                          char (*s_kv)[2 * ShGeo<T, DP>::BYTES], uint32_t group_of_units, uint32_t each) {
   using G = AttGeo<T, DP>;
   using S = ShGeo<T, DP>;
   constexpr int TILE = G::TILE, SUB = G::SUB, QT = S::QT, COLS = S::COLS;
-  __shared__ __align__(1024) char s_kv[S::RING][2 * S::BYTES];
-  __shared__ uint32_t s_u[257], s_x[257];   // units and (group, key head, tile)s before each thread's groups
-  __shared__ int s_row[257];                // their first row
-  __shared__ uint32_t s_sum[2][4];
-  __shared__ unsigned long long s_lead[4];
   const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6), m16 = lane & 15, gq = lane >> 4;
   const int D = EXACT ? DP : A.head_dim, row_bytes = D * G::ES;
-
-  // ---- the numbering ----
-  const int per = (A.n_groups + 255) / 256, g0 = min(A.n_groups, tid * per), g1 = min(A.n_groups, g0 + per);
-  {
-    uint32_t u = 0, x = 0;
-    for (int g = g0; g < g1; ++g) {
-      const ShGroup q = sh_group<S>(A, g);
-      if (g == g0) s_row[tid] = q.row;
-      u += (uint32_t)q.units * q.tiles * A.n_kv;
-      x = (uint32_t)min((int64_t)SH_TILES, x + (int64_t)(q.units ? q.tiles : 0) * A.n_kv);
-    }
-    if (g0 >= g1) s_row[tid] = A.n_rows;
-    const uint32_t iu = wave_scan(u), ix = wave_scan(x);
-    if (lane == 63) s_sum[0][w] = iu, s_sum[1][w] = ix;
-    __syncthreads();
-    uint32_t bu = 0, bx = 0;
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (i < w) bu += s_sum[0][i], bx += s_sum[1][i];
-    s_u[tid + 1] = bu + iu, s_x[tid + 1] = bx + ix;
-    if (tid == 0) s_u[0] = s_x[0] = 0;
-    __syncthreads();
-  }
-  // groups that overlap may be more tiles than the workspace has room for: then
-  // nothing is shared (below that the units are under 2^31)
-  const bool fits = s_x[256] <= (uint32_t)A.max_tiles;
-  const uint32_t total = fits ? s_u[256] : 0, each = total ? (total + gridDim.x - 1) / gridDim.x : 1;
-
-  // ---- where each row's partial results will lie ----
-  for (int row = blockIdx.x * 256 + tid; row < A.n_rows; row += gridDim.x * 256) {
-    int lo = 0;  // the last thread whose groups begin at or before the row
-    for (int step = 128; step > 0; step >>= 1)
-      if (s_row[lo + step] <= row) lo += step;
-    uint32_t u = s_u[lo], x = s_x[lo];
-    AttRowFrom F{0, 0, 0, 0, 0, 0, 0, 0};
-    for (int g = lo * per; fits && g < min(A.n_groups, lo * per + per); ++g) {
-      const ShGroup q = sh_group<S>(A, g);
-      if (row >= q.row && row < q.row + q.rows) {
-        F.from = q.n, F.tiles = q.tiles, F.col0 = (row - q.row) * A.heads;
-        F.u0 = u, F.x0 = x, F.units = q.units, F.each = each;
-        break;
-      }
-      u += (uint32_t)q.units * q.tiles * A.n_kv;
-      x += (uint32_t)(q.units ? q.tiles : 0) * A.n_kv;
-    }
-    A.from[row] = F;
-  }
-
-  // ---- this work-group's units ----
-  const uint32_t u_end = min((uint64_t)total, (uint64_t)(blockIdx.x + 1) * each);
-  for (uint32_t u = min((uint64_t)total, (uint64_t)blockIdx.x * each); u < u_end;) {
-    int lo = 0;
-    for (int step = 128; step > 0; step >>= 1)
-      if (s_u[lo + step] <= u) lo += step;
-    uint32_t u0 = s_u[lo], x = s_x[lo];
-    ShGroup q;
-    for (int g = lo * per;; ++g) {  // (the next border is past u)
+  const uint32_t total = L.u[256];
+  const uint32_t u_end = (uint32_t)min((uint64_t)total, (uint64_t)(group_of_units + 1) * each);
+  for (uint32_t u = (uint32_t)min((uint64_t)total, (uint64_t)group_of_units * each); u < u_end;) {
+    const int lo = sh_find(L.u, u);
+    uint32_t u0 = L.u[lo], x = L.x[lo];
+    ShGroup q{};
+    for (int g = lo * call.per_g; g < A.n_groups; ++g) {  // (the next border is past u)
       q = sh_group<S>(A, g);
       const uint32_t n = (uint32_t)q.units * q.tiles * A.n_kv;
       if (u - u0 < n) break;
@@ -199,6 +309,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_prefix(Shared
     }
     q = {uni(q.row), uni(q.rows), uni(q.n), uni(q.tiles), uni(q.units)};
     u0 = (uint32_t)uni((int)u0), x = (uint32_t)uni((int)x);
+    if (q.units == 0) return;  // (only if the lengths change while the call runs)
     const uint32_t i = (u - u0) / in_place(q.units);
     const int kvh = i / in_place(q.tiles), ct = i - kvh * q.tiles, first = u - u0 - i * q.units;
     const int last = min((uint32_t)q.units, first + (u_end - u));  // units first .. last - 1 of the group's
@@ -216,10 +327,10 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_prefix(Shared
       best = v > best ? v : best;
     }
     __syncthreads();  // (the previous piece is done with LDS)
-    if (lane == 0) s_lead[w] = best;
+    if (lane == 0) L.lead[w] = best;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) best = s_lead[k] > best ? s_lead[k] : best;
+    for (int k = 0; k < 4; ++k) best = L.lead[k] > best ? L.lead[k] : best;
     const int reach = uni((int)(best >> 32));  // positions that some row sees
     const int lead = q.row + uni((int)(0xFFFFFFFFu - (uint32_t)best));
     const int units = min(last, (reach + S::STAGE - 1) / S::STAGE) - first;
@@ -374,44 +485,14 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_prefix(Shared
                 for (int ng = 0; ng < G::NG; ++ng)
 #pragma unroll
                   for (int e = 0; e < G::VB / 4; ++e) {
-                    uint32_t& v = tile.v[sb][j][ng][e];
-                    const bool hi = (v & 0x7F800000u) == 0x7F800000u, lo = G::ES == 2 && (v & 0x7F80u) == 0x7F80u;
-                    odd |= hi || lo;
-                    v = G::ES == 4 ? (hi ? 0u : v) : (hi ? v & 0xFFFFu : v) & (lo ? 0xFFFF0000u : ~0u);
+                    odd |= sh_finite<G::ES>(tile.v[sb][j][ng][e]);
                   }
               }
             }
           odd = __any(odd);
         }
 #pragma unroll
-        for (int y = 0; y < QT; ++y) {
-          float tm = sc[y][0][0];
-#pragma unroll
-          for (int sb = 0; sb < SUB; ++sb)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) tm = fmaxf(tm, sc[y][sb][j]);
-          // The reference of a column's powers of two moves where a score passes it
-          // by 2^8: until then the powers stay far inside fp32, and nothing has to
-          // cross lanes.
-          if (__any(fmaf(tm, A.scale_log2, -mx[y]) > 8.f)) {
-            const float mn = fmaxf(mx[y], max_over_rows(tm) * A.scale_log2);
-            const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mx[y] - mn);
-            l[y] *= f;
-#pragma unroll
-            for (int ng = 0; ng < G::NG; ++ng)
-#pragma unroll
-              for (int e = 0; e < G::VD; ++e) acc[y][ng][e] *= f;
-            mx[y] = mn;
-          }
-          const float ref = mx[y] == -INFINITY ? 0.f : mx[y];
-#pragma unroll
-          for (int sb = 0; sb < SUB; ++sb)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              sc[y][sb][j] = __builtin_amdgcn_exp2f(fmaf(sc[y][sb][j], A.scale_log2, -ref));
-              l[y] += sc[y][sb][j];
-            }
-        }
+        for (int y = 0; y < QT; ++y) sh_weights<G>(A, sc[y], mx[y], l[y], acc[y]);
         tile.template weigh<QT, false, true>(sc, acc);
         const char* vp = s_kv[s % S::RING] + S::BYTES + tt * TILE * S::ROW;
         if (odd) {  // what was left out, for those who see it: the sum is not finite there, whatever the weight
@@ -422,16 +503,10 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_prefix(Shared
             for (int ng = 0; ng < G::NG; ++ng)
 #pragma unroll
               for (int r = 0; r < 4; ++r) {
-                typedef uint32_t vec __attribute__((ext_vector_type(G::VB / 4)));
                 const int b16 = (16 * ng + 4 * gq + r) * G::VB;  // (bytes of the row)
-                const vec x4 = *(const vec*)(vp + p * S::ROW + 16 * sh_slot<S::ROW>(p, b16 / 16) + b16 % 16);
+                const char* v = vp + p * S::ROW + 16 * sh_slot<S::ROW>(p, b16 / 16) + b16 % 16;
 #pragma unroll
-                for (int i = 0; i < G::VD; ++i) {
-                  const float v = __uint_as_float(G::ES == 4 ? x4[i % (G::VB / 4)] : i & 1 ? x4[i / 2] & 0xFFFF0000u : x4[i / 2] << 16);
-#pragma unroll
-                  for (int y = 0; y < QT; ++y)
-                    if (!isfinite(v) && t + p < my_n[y]) acc[y][ng][i][r] += v;
-                }
+                for (int y = 0; y < QT; ++y) sh_add_odd<G>(v, t + p < my_n[y], acc[y][ng], r);
               }
           }
         }
@@ -439,7 +514,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_prefix(Shared
     }
 
     // ---- the piece's sums to its slot ----
-    float* out = A.seeds + (int64_t)(blockIdx.x + x) * COLS * (DP + 4);
+    float* out = A.seeds + (int64_t)(group_of_units + x) * COLS * (DP + 4);
 #pragma unroll
     for (int y = 0; y < QT; ++y) {
       float sum = l[y];
@@ -463,12 +538,386 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_prefix(Shared
   }
 }
 
+// Sums over what the rows of a run hold of their own: a wave a piece, as K and V
+// stream by; few columns, so bound by the memory.
+template <typename T, int DP, bool PAGE16, bool EXACT>
+__device__ __forceinline__ void sh_own(const SharedArgs& A, const ShCall& call, const ShShared& L, uint32_t wave, uint32_t each) {
+  using G = AttGeo<T, DP>;
+  using S = ShGeo<T, DP>;
+  constexpr int TILE = G::TILE, SUB = G::SUB;
+  const int lane = threadIdx.x & 63, m16 = lane & 15, gq = lane >> 4;
+  const int D = EXACT ? DP : A.head_dim, row_bytes = D * G::ES, H = A.n_kv * A.q_tiles;
+  const uint32_t total = L.t[256] * H;
+  const uint32_t u_end = (uint32_t)min((uint64_t)total, (uint64_t)(wave + 1) * each);
+  const uint32_t neg = A.negate ? (G::ES == 2 ? 0x80008000u : 0x80000000u) : 0u;
+  const uint32_t tok = (uint32_t)A.token_stride * G::ES;
+  const auto page_of = [&](int t) { return (int)(((uint64_t)(uint32_t)t * A.ps_mul) >> (31 + A.ps_shift)); };
+  for (uint32_t u = (uint32_t)min((uint64_t)total, (uint64_t)wave * each); u < u_end;) {
+    // the run that holds unit u
+    const int lo = sh_find(L.t, u / in_place(H));
+    uint32_t before = L.t[lo];
+    ShRun R{};
+    for (int base = lo * call.per_r; base < A.n_rows && R.tiles == 0; base += A.together)  // (the next border is past u)
+      sh_runs<S, TILE>(A, call, L, base, [&](const ShRun& r) {
+        if (R.tiles == 0) {
+          if (u < (before + r.tiles) * H)
+            R = r;
+          else
+            before += r.tiles;
+        }
+      });
+    R = {uni(R.row), uni(R.rows), uni(R.req), uni(R.lo), uni(R.n), uni(R.every_lo), uni(R.every_n), uni(R.tiles)};
+    before = (uint32_t)uni((int)before);
+    if (R.tiles == 0) return;  // (only if the lengths change while the call runs)
+    const uint32_t in = u - before * H;
+    const int hh = in / in_place(R.tiles), ta = in - hh * R.tiles, cnt = min((uint32_t)(R.tiles - ta), u_end - u);
+    const int kvh = A.q_tiles == 1 ? hh : hh / in_place(A.q_tiles), qt = hh - kvh * A.q_tiles;
+    u += cnt;
+    // columns: c is head h0 + c % wide of row c / wide
+    const bool several = A.together > 1;
+    const int wide = several ? A.heads : 16, nq = several ? R.rows * A.heads : min(16, A.heads - 16 * qt);
+    const int h0 = kvh * A.heads + 16 * qt, col = min(m16, nq - 1), my_row = several ? col / in_place(wide) : 0;
+    int my_n = R.n, my_lo = R.lo;
+    if (R.rows > 1) {
+      my_n = sh_len(A, R.row + my_row);
+      my_lo = min(my_n, sh_from<S>(A, call, L, R.row + my_row));
+    }
+    const char* qp = (const char*)A.q + ((int64_t)(R.row + my_row) * A.q_stride + (int64_t)(h0 + col - my_row * wide) * D) * G::ES;
+    uint4 q[G::NC];
+#pragma unroll
+    for (int c = 0; c < G::NC; ++c) {
+      const int at = 64 * c + 16 * gq;
+      const uint4 x = ldg_b16<false>(qp, EXACT ? at : min(at, row_bytes - 16));
+      q[c] = m16 < nq && (EXACT || at < row_bytes) ? make_uint4(x.x ^ neg, x.y ^ neg, x.z ^ neg, x.w ^ neg) : make_uint4(0, 0, 0, 0);
+    }
+    const char *kb = (const char*)A.k, *vb = (const char*)A.v;
+    const int32_t* tab = A.table + (int64_t)R.req * A.table_stride;
+    const int64_t head = (int64_t)kvh * A.head_stride * G::ES;
+    const int tb = R.lo / TILE + ta;
+
+    AttTile<T, DP, EXACT> tile;
+    int32_t place_lo[SUB], place_hi[SUB], page_next[SUB];
+    const auto look_up = [&](int i) {
+#pragma unroll
+      for (int s = 0; s < SUB; ++s) {
+        if constexpr (PAGE16) {  // the next 64 tiles' blocks, a tile a lane
+          const int t = min((tb + i + lane) * TILE + 16 * s, (R.n - 1) & ~15);
+          const int at = page_of(t), page = ldg(tab + at);
+          const int64_t off = ((int64_t)page * A.page_stride + (int64_t)(t - at * A.page_size) * A.token_stride) * G::ES + head;
+          const bool ok = page >= 0 && page < A.n_pages;
+          place_lo[s] = ok ? (int32_t)(uint32_t)off : -1;
+          place_hi[s] = ok ? (int32_t)(off >> 32) : -1;
+        } else {  // the tile's positions, one a lane
+          page_next[s] = ldg(tab + page_of(min((tb + i) * TILE + 16 * s + m16, R.n - 1)));
+        }
+      }
+    };
+    int64_t off[SUB];
+    uint32_t bad[SUB];
+    const auto locate = [&](int i) {
+#pragma unroll
+      for (int s = 0; s < SUB; ++s) {
+        if constexpr (PAGE16) {
+          const int src = i & 63;
+          const int64_t o = (int64_t)(((uint64_t)(uint32_t)lane_of(place_hi[s], src) << 32) | (uint32_t)lane_of(place_lo[s], src));
+          bad[s] = o < 0 ? 0xFFFFu : 0u;
+          off[s] = o < 0 ? head : o;
+        } else {
+          const int t = min((tb + i) * TILE + 16 * s + m16, R.n - 1), page = page_next[s];
+          const bool ok = page >= 0 && page < A.n_pages;
+          off[s] = (ok ? ((int64_t)page * A.page_stride + (int64_t)(t - page_of(t) * A.page_size) * A.token_stride) * G::ES : 0) + head;
+          bad[s] = (uint32_t)(__ballot(!ok) & 0xFFFFu);
+        }
+      }
+    };
+    const auto load_k = [&]() {
+#pragma unroll
+      for (int s = 0; s < SUB; ++s)
+#pragma unroll
+        for (int c = 0; c < G::NC; ++c) {
+          if (!EXACT && DP > 64 && 64 * c >= row_bytes) continue;  // (uniform)
+          const uint32_t at = EXACT ? 64 * c + 16 * gq : min(64 * c + 16 * gq, row_bytes - 16);
+          tile.k[s][c] = ldg_b16<true>(kb + off[s], PAGE16 ? m16 * tok + at : at);
+        }
+    };
+    const auto load_v = [&]() {
+#pragma unroll
+      for (int s = 0; s < SUB; ++s)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const char* p = vb + off[s];
+          uint32_t o = (4 * gq + j) * tok;
+          if constexpr (!PAGE16) {
+            const int src = 4 * gq + j;
+            const uint32_t lo32 = __shfl((int)(uint32_t)off[s], src, 64), hi32 = __shfl((int)(off[s] >> 32), src, 64);
+            p = vb + (int64_t)(((uint64_t)hi32 << 32) | lo32);
+            o = 0;
+          }
+#pragma unroll
+          for (int ng = 0; ng < G::NG; ++ng) {
+            const int at = (16 * ng + m16) * G::VB;
+            tile.template load_v<true>(p, o + (EXACT ? at : min(at, row_bytes - G::VB)), s, j, ng);
+          }
+        }
+    };
+
+    float mx[1] = {-INFINITY}, l = 0.f;
+    f32x4 acc[1][G::NG][G::VD];
+#pragma unroll
+    for (int ng = 0; ng < G::NG; ++ng)
+#pragma unroll
+      for (int e = 0; e < G::VD; ++e) acc[0][ng][e] = f32x4{0.f, 0.f, 0.f, 0.f};
+    look_up(0);
+    locate(0);
+    load_k();
+    load_v();
+    if constexpr (!PAGE16) look_up(min(1, cnt - 1));
+    // (the next tile's loads run under this one's products)
+    const auto trip = [&](int i, auto more) {
+      const int t = (tb + i) * TILE;
+      uint32_t gone[SUB];
+      bool cut = t < R.every_lo || t + TILE > R.every_n;
+#pragma unroll
+      for (int s = 0; s < SUB; ++s) {
+        gone[s] = bad[s];
+        cut = cut || bad[s] != 0;
+      }
+      f32x4 sc[1][SUB];
+      tile.template scores<1>([&](int, int c) { return q[c]; }, sc, gq, row_bytes);
+      if constexpr (more) {
+        if constexpr (PAGE16) {
+          if (((i + 1) & 63) == 0) look_up(i + 1);
+        }
+        locate(i + 1);
+        load_k();
+        if constexpr (!PAGE16) look_up(min(i + 2, cnt - 1));
+      }
+      bool odd = false;
+      if (cut) {
+        // a position that is not seen has no weight; what is not finite where only
+        // some rows see it is left out and added for those below
+#pragma unroll
+        for (int s = 0; s < SUB; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int at = t + 16 * s + 4 * gq + j;
+            const bool away = gone[s] >> (4 * gq + j) & 1;
+            if (at < my_lo || at >= my_n || away) sc[0][s][j] = -INFINITY;
+            if (at < R.lo || at >= R.n || away) tile.clear_v(s, j);
+            if (at < R.every_lo || at >= R.every_n) {
+#pragma unroll
+              for (int ng = 0; ng < G::NG; ++ng)
+#pragma unroll
+                for (int e = 0; e < G::VB / 4; ++e) odd |= sh_finite<G::ES>(tile.v[s][j][ng][e]);
+            }
+          }
+        odd = __any(odd);
+      }
+      sh_weights<G>(A, sc[0], mx[0], l, acc[0]);
+      tile.template weigh<1, false, true>(sc, acc);
+      if (odd) {
+        for (int p = 0; p < TILE; ++p) {
+          const int at = t + p, sub = SUB == 2 ? p >> 4 : 0;
+          if ((at >= R.every_lo && at < R.every_n) || at < R.lo || at >= R.n || (gone[sub] >> (p & 15) & 1)) continue;
+          const int c = page_of(at), page = ldg(tab + c);
+          const char* row = vb + ((int64_t)page * A.page_stride + (int64_t)(at - c * A.page_size) * A.token_stride) * G::ES + head;
+#pragma unroll
+          for (int ng = 0; ng < G::NG; ++ng)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int b = (16 * ng + 4 * gq + r) * G::VB;
+              sh_add_odd<G>(row + (EXACT ? b : min(b, row_bytes - G::VB)), at >= my_lo && at < my_n, acc[0][ng], r);
+            }
+        }
+      }
+      if constexpr (more) load_v();
+    };
+    for (int i = 0; i + 1 < cnt; ++i) trip(i, std::true_type());
+    trip(cnt - 1, std::false_type());
+
+    // ---- the piece's sums to its slot ----
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    float* o = A.own + ((int64_t)wave + (int64_t)R.row * H + hh) * A.own_cols * (DP + 4) + m16 * (DP + 4);
+    if (m16 < nq) {
+      const bool sees = my_n > my_lo;  // (others: sums of nothing)
+#pragma unroll
+      for (int ng = 0; ng < G::NG; ++ng)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int e = 0; e < G::VD; e += 4)
+            stg4(o + 16 * G::VD * ng + G::VD * (4 * gq + r) + e,
+                 sees ? f32x4{acc[0][ng][e][r], acc[0][ng][e + 1][r], acc[0][ng][e + 2][r], acc[0][ng][e + 3][r]}
+                      : f32x4{0.f, 0.f, 0.f, 0.f});
+      if (gq == 0) stg4(o + DP, f32x4{sees ? mx[0] : -INFINITY, sees ? l : 0.f, 0.f, 0.f});
+    }
+  }
+}
+
+// Both kinds of work at once: products over shared positions keep the matrix
+// units busy while what the rows have of their own streams from memory. Units of
+// each kind are numbered (group, key head, tile of columns, stage of positions;
+// row, head, tile of positions), and every work-group, or wave, takes the same
+// number of consecutive ones. Work-group or wave w's part of the x-th (group, key
+// head, tile) or (row, head) is a piece, in slot w + x: both grow from piece to
+// piece, so slots are not shared and those of one x lie side by side. Lengths and
+// groups are on the device; every work-group numbers them by itself, and the
+// partial results are joined by the next launch.
+constexpr uint32_t SH_COST_SHARED = 5, SH_COST_OWN = 4;  // of a unit and of a tile
+
+template <typename T, int DP, bool PAGE16, bool EXACT>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_attention(SharedArgs A) {
+  using G = AttGeo<T, DP>;
+  using S = ShGeo<T, DP>;
+  __shared__ __align__(1024) char s_kv[S::RING][2 * S::BYTES];
+  __shared__ ShShared L;
+  const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6);
+  ShCall call;
+  call.per_g = (A.n_groups + 255) / 256;
+  call.per_r = ((A.n_rows + 255) / 256 + A.together - 1) / A.together * A.together;
+  // ---- the groups ----
+  {
+    uint32_t u = 0, x = 0;
+    L.row[tid] = A.n_rows, L.end[tid] = 0, L.n[tid] = 0;
+    const int g0 = min(A.n_groups, tid * call.per_g), g1 = min(A.n_groups, g0 + call.per_g);
+    for (int g = g0; g < g1; ++g) {
+      const ShGroup q = sh_group<S>(A, g);
+      if (g == g0) L.row[tid] = q.row, L.end[tid] = q.row + q.rows, L.n[tid] = q.n;
+      u += (uint32_t)q.units * q.tiles * A.n_kv;
+      x = (uint32_t)min((int64_t)SH_TILES, x + (int64_t)(q.units ? q.tiles : 0) * A.n_kv);
+    }
+    const uint32_t iu = wave_scan(u), ix = wave_scan(x);
+    if (lane == 63) L.sum[0][w] = iu, L.sum[1][w] = ix;
+    __syncthreads();
+    uint32_t bu = 0, bx = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (i < w) bu += L.sum[0][i], bx += L.sum[1][i];
+    L.u[tid + 1] = bu + iu, L.x[tid + 1] = bx + ix;
+    if (tid == 0) L.u[0] = L.x[0] = 0;
+    __syncthreads();
+  }
+  // groups that overlap may be more tiles than the workspace has room for: then
+  // nothing is shared (below that the units are under 2^31)
+  call.fits = L.x[256] <= (uint32_t)A.max_tiles;
+  // ---- the rows ----
+  {
+    uint32_t t = 0;
+    const int r0 = min(A.n_rows, tid * call.per_r), r1 = min(A.n_rows, r0 + call.per_r);
+    for (int r = r0; r < r1; r += A.together) sh_runs<S, G::TILE>(A, call, L, r, [&](const ShRun& q) { t += q.tiles; });
+    const uint32_t it = wave_scan(t);
+    if (lane == 63) L.sum[0][w] = it;
+    __syncthreads();
+    uint32_t bt = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (i < w) bt += L.sum[0][i];
+    L.t[tid + 1] = bt + it;
+    if (tid == 0) L.t[0] = 0;
+    __syncthreads();
+  }
+  const int H = A.n_kv * A.q_tiles;
+  const uint32_t units = call.fits ? L.u[256] : 0, tiles = L.t[256] * H;
+  // ---- shares of the work-groups ----
+  const float cs = (float)units * SH_COST_SHARED, co = (float)tiles * SH_COST_OWN;
+  uint32_t ws = units == 0 ? 0 : (uint32_t)(gridDim.x * (cs / (cs + co)) + 0.5f);
+  ws = units == 0 ? 0 : min(max(ws, 1u), tiles ? gridDim.x - 1 : gridDim.x);
+  const uint32_t wo = gridDim.x - ws;
+  const uint32_t each_s = ws ? (units + ws - 1) / ws : 1, each_o = wo && tiles ? (tiles + 4 * wo - 1) / (4 * wo) : 1;
+  // ---- where each row's partial results will lie ----
+  if (blockIdx.x == 0 && tid == 0) *A.plan = ShPlan{each_s, each_o};
+  for (int base = (blockIdx.x * 256 + tid) * A.together; base < A.n_rows; base += gridDim.x * 256 * A.together) {
+    const int chunk = base / call.per_r;
+    uint32_t before = L.t[chunk];
+    for (int b = chunk * call.per_r; b < base; b += A.together)
+      sh_runs<S, G::TILE>(A, call, L, b, [&](const ShRun& q) { before += q.tiles; });
+    sh_runs<S, G::TILE>(A, call, L, base, [&](const ShRun& q) {
+      for (int i = 0; i < q.rows; ++i) {
+        ShRow R{0, 0, 0, 0, 0, q.tiles, before, q.row, A.together > 1 ? i * A.heads : 0, {0, 0, 0}};
+        sh_group_of<S>(A, call, L, q.row + i, [&](const ShGroup& g, uint32_t u, uint32_t x) {
+          R.units = g.units, R.tiles = g.tiles, R.col0 = (q.row + i - g.row) * A.heads, R.u0 = u, R.x0 = x;
+        });
+        A.rows[q.row + i] = R;
+      }
+      before += q.tiles;
+    });
+  }
+  // ---- the work-groups' kinds, spread evenly ----
+  const uint32_t upto = (uint32_t)((uint64_t)blockIdx.x * ws / gridDim.x), next = (uint32_t)((uint64_t)(blockIdx.x + 1) * ws / gridDim.x);
+  if (next > upto)
+    sh_prefix<T, DP, EXACT>(A, call, L, s_kv, upto, each_s);
+  else if (tiles)
+    sh_own<T, DP, PAGE16, EXACT>(A, call, L, 4 * (blockIdx.x - upto) + w, each_o);
+}
+
+// The slots of a (row, head), DP / 4 lanes for its elements, eight slots' loads in
+// flight: shared positions' first, each in the work's order, so the result does
+// not depend on who was done when.
+template <typename T, int DP>
+__global__ __launch_bounds__(256) void k_shared_join(SharedArgs A) {
+  using S = ShGeo<T, DP>;
+  constexpr int LP = DP / 4;
+  const int64_t pair = (int64_t)blockIdx.x * (256 / LP) + threadIdx.x / LP;
+  const int n_heads = A.n_kv * A.heads, row = (int)(pair / n_heads), h = (int)(pair - (int64_t)row * n_heads);
+  const int d = 4 * (threadIdx.x % LP);
+  if (row >= A.n_rows || d >= A.head_dim) return;
+  const ShRow R = A.rows[row];
+  const ShPlan P = *A.plan;
+  const int kvh = h / A.heads, hg = h - kvh * A.heads, H = A.n_kv * A.q_tiles;
+  // shared
+  const int c = R.col0 + hg, ct = c / S::COLS;
+  const uint32_t x = (uint32_t)(kvh * R.tiles + ct), u = R.u0 + x * R.units, w0 = u / P.each_shared;
+  const int n0 = R.units ? (int)((u + R.units - 1) / P.each_shared - w0) + 1 : 0;
+  const float* p0 = A.seeds + ((int64_t)(w0 + R.x0 + x) * S::COLS + c - ct * S::COLS) * (DP + 4);
+  // own
+  const int qt = A.together > 1 ? 0 : hg / 16, hh = kvh * A.q_tiles + qt, col = R.at + hg - 16 * qt;
+  const uint32_t v = R.before * H + (uint32_t)hh * R.own, w1 = v / P.each_own;
+  const int n1 = R.own ? (int)((v + R.own - 1) / P.each_own - w1) + 1 : 0;
+  const float* p1 = A.own + ((int64_t)w1 + (int64_t)R.lead * H + hh) * A.own_cols * (DP + 4) + col * (DP + 4);
+  const int64_t s0 = S::COLS * (DP + 4), s1 = (int64_t)A.own_cols * (DP + 4);
+  float m = -INFINITY, l = 0.f;
+  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 < n0 + n1; j0 += 8) {
+    f32x4 ml[8], z[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = min(j0 + j, n0 + n1 - 1);
+      const float* p = i < n0 ? p0 + i * s0 : p1 + (i - n0) * s1;
+      ml[j] = ldg4(p + DP);
+      z[j] = ldg4(p + d);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j0 + j >= n0 + n1) break;
+      const float mn = fmaxf(m, ml[j].x), ref = mn == -INFINITY ? 0.f : mn;
+      const float fa = __builtin_amdgcn_exp2f(m - ref), fb = __builtin_amdgcn_exp2f(ml[j].x - ref);
+      o = o * fa + z[j] * fb;
+      l = l * fa + ml[j].y * fb;
+      m = mn;
+    }
+  }
+  const f32x4 y = l == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : o / l;
+  const int64_t at = (int64_t)row * A.out_stride + (int64_t)h * A.head_dim + d;
+  if constexpr (sizeof(T) == 4) {
+    stg4((float*)A.out + at, y);
+  } else {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    *(GLOBAL u32x2*)((uint16_t*)A.out + at) = u32x2{pack_bf2(__float_as_uint(y.x), __float_as_uint(y.y)),
+                                                   pack_bf2(__float_as_uint(y.z), __float_as_uint(y.w))};
+  }
+}
+
 template <typename T, int DP>
 void sh_launch(const SharedArgs& A, int blocks, hipStream_t s) {
-  if (A.head_dim == DP)
-    hipLaunchKernelGGL((k_shared_prefix<T, DP, true>), dim3(blocks), dim3(256), 0, s, A);
+  if (A.page_size % 16)
+    hipLaunchKernelGGL((k_shared_attention<T, DP, false, false>), dim3(blocks), dim3(256), 0, s, A);
+  else if (A.head_dim == DP)
+    hipLaunchKernelGGL((k_shared_attention<T, DP, true, true>), dim3(blocks), dim3(256), 0, s, A);
   else
-    hipLaunchKernelGGL((k_shared_prefix<T, DP, false>), dim3(blocks), dim3(256), 0, s, A);
+    hipLaunchKernelGGL((k_shared_attention<T, DP, true, false>), dim3(blocks), dim3(256), 0, s, A);
+  const int64_t pairs = (int64_t)A.n_rows * A.n_kv * A.heads, each = 256 / (DP / 4);
+  hipLaunchKernelGGL((k_shared_join<T, DP>), dim3((unsigned)((pairs + each - 1) / each)), dim3(256), 0, s, A);
 }
 template <typename T>
 void sh_dim(const SharedArgs& A, int dp, int blocks, hipStream_t s) {
@@ -477,12 +926,27 @@ void sh_dim(const SharedArgs& A, int dp, int blocks, hipStream_t s) {
   else sh_launch<T, 256>(A, blocks, s);
 }
 
-// columns of a work-group, positions of a unit
-int sh_cols(int es, int dp) { return dp * es >= 1024 ? 64 : 128; }
-int sh_blocks(int units) { return 2 * units; }
-// (group, key head, tile)s of up to n_rows rows in up to n_groups groups
-int64_t sh_tiles(int64_t n_rows, int64_t n_groups, int64_t group, int64_t n_kv, int cols) {
-  return n_kv * (n_rows * group / cols + n_groups);
+// What a call of these sizes needs.
+struct ShSizes {
+  int es, dp, group, cols, together, q_tiles, own_cols, blocks;
+  int64_t tiles;                  // (group, key head, tile)s at most
+  int64_t rows, seeds, own, bytes;  // places in the workspace, and its bytes
+};
+ShSizes sh_sizes(int dtype, int head_dim, int n_heads, int n_kv, bool runs, int64_t n_rows, int64_t n_groups, int units) {
+  const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+  ShSizes z;
+  z.es = dtype == SCUTE_F32 ? 4 : 2, z.dp = att_dim(head_dim), z.group = n_heads / n_kv;
+  z.cols = z.dp * z.es >= 1024 ? 64 : 128;
+  z.together = runs && z.group <= 8 ? std::min(4, 16 / z.group) : 1;
+  z.q_tiles = (z.group + 15) / 16;
+  z.own_cols = z.together > 1 ? z.together * z.group : std::min(16, z.group);
+  z.blocks = z.dp <= 128 ? 2 * units : units;  // (as many as are resident at once)
+  z.tiles = n_kv * (n_rows * z.group / z.cols + n_groups);
+  z.rows = 256;  // (the plan's)
+  z.seeds = z.rows + up(n_rows * sizeof(ShRow));
+  z.own = z.seeds + (z.blocks + z.tiles) * z.cols * (z.dp + 4) * 4;
+  z.bytes = z.own + (4 * z.blocks + n_rows * n_kv * z.q_tiles) * z.own_cols * (z.dp + 4) * 4;
+  return z;
 }
 
 }  // namespace scute
@@ -504,10 +968,8 @@ extern "C" scute_status scute_shared_attention_workspace(int32_t device, int32_t
     return bad(SCUTE_E_SHAPE, "max_rows must be in [0, 2^20] and max_groups in [0, 65536]");
   const int units = device_units(device);
   if (units < 0) return bad(SCUTE_E_INVALID, "no such HIP device");
-  const int es = dtype == SCUTE_F32 ? 4 : 2, dp = att_dim(head_dim), cols = sh_cols(es, dp);
-  const int64_t slots = sh_blocks(units) + sh_tiles(max_rows, max_groups, n_heads / n_kv_heads, n_kv_heads, cols);
-  const int64_t rows = ((int64_t)max_rows * sizeof(AttRowFrom) + 255) / 256 * 256;
-  *bytes = (att_workspace(units, head_dim) + 255) / 256 * 256 + rows + slots * cols * (dp + 4) * 4;
+  *bytes = std::max(sh_sizes(dtype, head_dim, n_heads, n_kv_heads, false, max_rows, max_groups, units).bytes,
+                    sh_sizes(dtype, head_dim, n_heads, n_kv_heads, true, max_rows, max_groups, units).bytes);
   return SCUTE_OK;
 }
 
@@ -520,9 +982,8 @@ extern "C" scute_status scute_shared_attention(const scute_kv_cache* C, const vo
                                                void* stream) {
   const char* fn = "scute_shared_attention";
   const auto bad = [&](scute_status code, const char* what) { return fail(code, std::string(fn) + ": " + what); };
-  AttCall c{C, q, q_stride, n_heads, table, table_stride, n_requests, table_width, len, req, n_rows, scale,
-            0, 0, out, out_stride, workspace, workspace_bytes, nullptr, nullptr, 1};
-  scute_status st = att_check(fn, c);
+  const scute_status st = att_check(fn, AttCall{C, q, q_stride, n_heads, table, table_stride, n_requests, table_width, len,
+                                                req, n_rows, scale, 0, 0, out, out_stride, workspace, workspace_bytes});
   if (st != SCUTE_OK) return st;
   if (n_groups < 0 || n_groups > 65536) return bad(SCUTE_E_SHAPE, "n_groups must be in [0, 65536]");
   if (n_rows == 0) return SCUTE_OK;
@@ -530,34 +991,28 @@ extern "C" scute_status scute_shared_attention(const scute_kv_cache* C, const vo
   if (((uintptr_t)group | (uintptr_t)shared_len) & 3) return bad(SCUTE_E_INVALID, "misaligned pointer");
   OnDevice g(C->device);
   if (!g.ok()) return hip_fail(g.err, fn);
-  int64_t need = 0;
-  if ((st = scute_shared_attention_workspace(C->device, C->dtype, C->head_dim, n_heads, C->n_kv_heads, n_rows, n_groups,
-                                             &need)) != SCUTE_OK)
-    return st;
-  if (workspace_bytes < need) return bad(SCUTE_E_INVALID, "the workspace is too small");
-  const int units = device_units(C->device), es = C->dtype == SCUTE_F32 ? 4 : 2, dp = att_dim(C->head_dim);
-  const int group_heads = n_heads / C->n_kv_heads, cols = sh_cols(es, dp);
+  const int units = device_units(C->device);
+  if (units < 0) return bad(SCUTE_E_INVALID, "no such HIP device");
+  const ShSizes z = sh_sizes(C->dtype, C->head_dim, n_heads, C->n_kv_heads, req != nullptr, n_rows, n_groups, units);
+  if (workspace_bytes < z.bytes) return bad(SCUTE_E_INVALID, "the workspace is too small");
   const int64_t reach = std::min<int64_t>((int64_t)table_width * C->page_size, (int64_t)1 << 29);
-  // (units are counted in 31 bits)
-  const int64_t tiles = sh_tiles(n_rows, n_groups, group_heads, C->n_kv_heads, cols);
-  if (tiles >= SH_TILES || tiles * (reach / sh_stage(es, dp) + 1) >= ((int64_t)1 << 31))
+  // (units and tiles are counted in 31 bits)
+  const int64_t stage = z.es == 4 ? 16 : 32, most = ((int64_t)1 << 31) - 1;
+  if (z.tiles >= SH_TILES || z.tiles * (reach / stage + 1) > most ||
+      (int64_t)n_rows * C->n_kv_heads * z.q_tiles * (reach / stage + 2) > most)
     return bad(SCUTE_E_SHAPE, "too many rows and heads for a table this wide");
-  const int64_t own = (att_workspace(units, C->head_dim) + 255) / 256 * 256;
   char* ws = (char*)workspace;
-  AttRowFrom* from = (AttRowFrom*)(ws + own);
-  float* seeds = (float*)(ws + own + ((int64_t)n_rows * sizeof(AttRowFrom) + 255) / 256 * 256);
   int shift = 0;
   while ((1 << shift) < C->page_size) ++shift;
   const uint64_t mul = (((uint64_t)1 << (31 + shift)) + C->page_size - 1) / C->page_size;
-  const SharedArgs A{q, C->k, C->v, table, len, req, group, shared_len, from, seeds, q_stride, C->page_stride,
-                     C->token_stride, C->head_stride, table_stride, C->n_pages, (uint32_t)mul, n_rows, n_groups,
-                     C->n_kv_heads, group_heads, C->head_dim, C->page_size, shift, (int32_t)reach, n_requests, (int32_t)tiles,
-                     scale < 0.f, std::max(fabsf(scale * 1.4426950408889634f), 1e-37f)};
+  const SharedArgs A{q, C->k, C->v, out, table, len, req, group, shared_len, (ShRow*)(ws + z.rows), (ShPlan*)ws,
+                     (float*)(ws + z.seeds), (float*)(ws + z.own), q_stride, out_stride, C->page_stride, C->token_stride,
+                     C->head_stride, table_stride, C->n_pages, (uint32_t)mul, n_rows, n_groups, C->n_kv_heads, z.group,
+                     C->head_dim, C->page_size, shift, (int32_t)reach, n_requests, (int32_t)z.tiles, z.together, z.q_tiles,
+                     z.own_cols, scale < 0.f, std::max(fabsf(scale * 1.4426950408889634f), 1e-37f)};
   const hipStream_t s = (hipStream_t)stream;
-  if (es == 4) sh_dim<float>(A, dp, sh_blocks(units), s);
-  else sh_dim<uint16_t>(A, dp, sh_blocks(units), s);
+  if (z.es == 4) sh_dim<float>(A, z.dp, z.blocks, s);
+  else sh_dim<uint16_t>(A, z.dp, z.blocks, s);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return hip_fail(e, fn);
-  c.from = from, c.seeds = seeds, c.seed_cols = cols;
-  return att_run(fn, c, ATT_SUFFIX, s);
+  return e == hipSuccess ? SCUTE_OK : hip_fail(e, fn);
 }

@@ -238,13 +238,10 @@ def test_captured_steps():
         assert torch.equal(out, other)
 
 
-def test_without_groups_it_is_paged_attention():
+def test_without_groups_nothing_is_shared():
     kc, vc, table, q, lens = make(8, [(5, 96)], 16, 8, 2, 64, BF16)
-    want = block.PagedAttention(block.KVCache(kc, vc), 8).forward(q, _int(table), _int(lens), torch.empty_like(q))
-    for offs, shared in (([0], []), ([0, 5], [0]), ([0, 5], [-7]), ([2, 2], [96])):
-        att = block.SharedAttention(block.KVCache(kc, vc), 8, 5, 1)
-        out = att.forward(q, _int(table), _int(lens), _int(offs), _int(shared), torch.empty_like(q))
-        assert torch.equal(out, want)
+    outs = [run(kc, vc, table, q, lens, offs, shared) for offs, shared in (([0], []), ([0, 5], [0]), ([0, 5], [-7]), ([2, 2], [96]))]
+    assert all(torch.equal(o, outs[0]) for o in outs)
 
 
 def test_refusals():
