@@ -608,6 +608,10 @@ scute_status scute_sink_attention(const scute_kv_cache* cache, const void* q, in
                                   int32_t sinks, void* out, int64_t out_stride, void* workspace,
                                   int64_t workspace_bytes, void* stream);
 
+typedef enum scute_shared_flag {
+  SCUTE_SHARED_ALWAYS = 1 /* shares however little that saves */
+} scute_shared_flag;
+
 /* Bytes of workspace that scute_shared_attention may use for calls of up to
  * max_rows rows in up to max_groups groups. Errors as for the call's sizes. */
 scute_status scute_shared_attention_workspace(int32_t device, int32_t dtype, int32_t head_dim,
@@ -622,20 +626,26 @@ scute_status scute_shared_attention_workspace(int32_t device, int32_t dtype, int
  * of them. A row sees its positions below len as there, shared or its own,
  * rows of no request or of length 0 nothing; rows of no group share nothing,
  * and shared_len may be 0. Results are those of scute_paged_attention but for
- * the order of the sums (an infinite V that a bf16 row sees with a weight under 2^-100
- * may give NaN).
+ * the order of the sums and a bf16 cache's weights, the sums of a value cut off to
+ * bf16 and of the rest rounded to it (off by 2^-15 at most; an infinite V that a
+ * row sees with a weight under 2^-100 may give NaN). Where sharing cannot save the
+ * reads of 256 MiB (rows past one a group, at the table's whole width) the call is
+ * scute_paged_attention's, unless flags says otherwise.
  * group and shared_len are device arrays; group is not checked: offsets that
  * do not ascend give rows whose output is not defined, no access out of bounds.
  * workspace as there, of at least what scute_shared_attention_workspace says
- * for n_rows and n_groups. Errors as there, SCUTE_E_SHAPE for n_groups outside
- * 0 .. 65536 or, at the table's whole width, 2^31 units of 16 positions and 64 columns. */
+ * for n_rows and n_groups. flags: a bitwise or of scute_shared_flag. Errors as
+ * there, SCUTE_E_INVALID for an unknown flag, SCUTE_E_SHAPE for n_groups outside
+ * 0 .. 65536 or more rows and heads than can be numbered at the table's whole width
+ * (rows x key heads x tiles of 16 query heads x table positions / 32, or / 16 in
+ * float32, stay under 2^31). */
 scute_status scute_shared_attention(const scute_kv_cache* cache, const void* q, int64_t q_stride,
                                     int32_t n_heads, const int32_t* table, int64_t table_stride,
                                     int32_t n_requests, int32_t table_width, const int32_t* len,
                                     const int32_t* req, int32_t n_rows, const int32_t* group,
                                     const int32_t* shared_len, int32_t n_groups, float scale, void* out,
                                     int64_t out_stride, void* workspace, int64_t workspace_bytes,
-                                    void* stream);
+                                    uint32_t flags, void* stream);
 
 /* The norms around a block's residual:
  *   h' = h_scale h + y_scale (gate (.) N_post(y))     x = N_pre(h')

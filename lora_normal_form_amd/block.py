@@ -443,13 +443,15 @@ class SharedAttention:
     positions (samples of a prompt, users of a system prompt): those are read
     once for all rows of a group. Up to max_rows rows in up to max_groups groups
     a call; scale as in PagedAttention, and as there the handle owns the
-    workspace of one call at a time."""
+    workspace of one call at a time. Calls that sharing could not save the reads of
+    256 MiB are PagedAttention's (the library's rule), with `always` none."""
 
-    def __init__(self, cache, n_heads, max_rows, max_groups, scale=None):
+    def __init__(self, cache, n_heads, max_rows, max_groups, scale=None, always=False):
         if n_heads < 1 or n_heads % cache.n_kv_heads:
             _bad("n_heads must be a multiple of the cache's n_kv_heads")
         self.cache, self.n_heads = cache, int(n_heads)
         self.max_rows, self.max_groups = int(max_rows), int(max_groups)
+        self.flags = scute.SHARED_ALWAYS if always else 0
         self.scale = 1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale)
         nbytes = scute.scute_shared_attention_workspace(cache.device.index, _DTYPES[cache.dtype], cache.head_dim,
                                                         self.n_heads, cache.n_kv_heads, max_rows, max_groups)
@@ -484,7 +486,7 @@ class SharedAttention:
         ws = self.workspace
         scute._check(scute.lib.scute_shared_attention(
             c.desc, q.data_ptr(), qs if N > 1 else 0, H, table.data_ptr(), ts if R > 1 else P, R, P, lp, rp, N, gp, sp,
-            n_groups, self.scale, out.data_ptr(), os if N > 1 else 0, ws.data_ptr(), ws.shape[0],
+            n_groups, self.scale, out.data_ptr(), os if N > 1 else 0, ws.data_ptr(), ws.shape[0], self.flags,
             _stream(stream, c.index)))
         return out
 

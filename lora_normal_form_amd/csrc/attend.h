@@ -245,24 +245,21 @@ struct AttTile {
 #pragma unroll
       for (int e = 0; e < G::VB / 4; ++e) v[s][j][ng][e] = 0;
   }
-  // SOME: of the positions that `mask` (ones or zeros for each) leaves, for the
-  // columns of the lanes that `keep`. POS: both parts of a weight are positive (the
-  // first cut off instead of rounded, the second 2^-20 of the weight more than the
-  // rest), so that an infinite V stays infinite; the weight is off by 2^-15 at most.
-  template <int QT, bool SOME = false, bool POS = false>
-  __device__ __forceinline__ void weigh(const f32x4 (&p)[QT][G::SUB], f32x4 (&acc)[QT][G::NG][G::VD],
-                                        const uint32_t (*mask)[4] = nullptr, bool keep = true) {
-    const auto val = [&](int s, int j, int ng, int i) { return SOME ? v[s][j][ng][i] & mask[s][j] : v[s][j][ng][i]; };
-    const auto put = [&](f32x4& to, f32x4 x) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) to[r] = !SOME || keep ? x[r] : to[r];
-    };
+  // a tile's weights as operands
+  template <int QT>
+  struct Weights {
+    uint4 b[QT], b2[G::ES == 2 ? QT : 1];
+  };
+  // bf16: the weights as sums of two bf16 (one alone would add an error of the
+  // output's own rounding, 2^-8; the second products cost no time). The second is 0
+  // or of either sign, so an infinite V gives a sum of any kind, which is put right
+  // where the waves' results are joined. POS: both parts are positive (the first cut
+  // off instead of rounded, the second 2^-20 of the weight more than the rest), so
+  // that an infinite V stays infinite; the weight is off by 2^-15 at most.
+  template <int QT, bool POS = false>
+  static __device__ __forceinline__ Weights<QT> pack(const f32x4 (&p)[QT][G::SUB]) {
+    Weights<QT> W;
     if constexpr (G::ES == 2) {
-      // the weights as sums of two bf16 (one alone would add an error of the
-      // output's own rounding, 2^-8; the second products cost no time). The
-      // second is 0 or of either sign, so an infinite V gives a sum of any kind,
-      // which is put right where the waves' results are joined.
-      uint4 b[QT], b2[QT];
       const auto first = [](float x, float y) {
         return POS ? __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u)
                    : pack_bf2(__float_as_uint(x), __float_as_uint(y));
@@ -275,19 +272,38 @@ struct AttTile {
       };
 #pragma unroll
       for (int y = 0; y < QT; ++y) {
-        b[y].x = first(p[y][0][0], p[y][0][1]);
-        b[y].y = first(p[y][0][2], p[y][0][3]);
-        b[y].z = first(p[y][1][0], p[y][1][1]);
-        b[y].w = first(p[y][1][2], p[y][1][3]);
-        b2[y].x = rest(b[y].x, p[y][0][0], p[y][0][1]);
-        b2[y].y = rest(b[y].y, p[y][0][2], p[y][0][3]);
-        b2[y].z = rest(b[y].z, p[y][1][0], p[y][1][1]);
-        b2[y].w = rest(b[y].w, p[y][1][2], p[y][1][3]);
+        W.b[y].x = first(p[y][0][0], p[y][0][1]);
+        W.b[y].y = first(p[y][0][2], p[y][0][3]);
+        W.b[y].z = first(p[y][1][0], p[y][1][1]);
+        W.b[y].w = first(p[y][1][2], p[y][1][3]);
+        W.b2[y].x = rest(W.b[y].x, p[y][0][0], p[y][0][1]);
+        W.b2[y].y = rest(W.b[y].y, p[y][0][2], p[y][0][3]);
+        W.b2[y].z = rest(W.b[y].z, p[y][1][0], p[y][1][1]);
+        W.b2[y].w = rest(W.b[y].w, p[y][1][2], p[y][1][3]);
       }
+    } else {
 #pragma unroll
-      for (int ng = 0; ng < G::NG; ++ng)
+      for (int y = 0; y < QT; ++y)
+        W.b[y] = make_uint4(__float_as_uint(p[y][0][0]), __float_as_uint(p[y][0][1]), __float_as_uint(p[y][0][2]),
+                            __float_as_uint(p[y][0][3]));
+    }
+    return W;
+  }
+  // V times them. SOME: of the positions that `mask` (ones or zeros for each) leaves,
+  // for the columns of the lanes that `keep`
+  template <int QT, bool SOME = false>
+  __device__ __forceinline__ void products(const Weights<QT>& W, f32x4 (&acc)[QT][G::NG][G::VD],
+                                           const uint32_t (*mask)[4] = nullptr, bool keep = true) {
+    const auto val = [&](int s, int j, int ng, int i) { return SOME ? v[s][j][ng][i] & mask[s][j] : v[s][j][ng][i]; };
+    const auto put = [&](f32x4& to, f32x4 x) {
 #pragma unroll
-        for (int i = 0; i < G::VD; ++i) {
+      for (int r = 0; r < 4; ++r) to[r] = !SOME || keep ? x[r] : to[r];
+    };
+#pragma unroll
+    for (int ng = 0; ng < G::NG; ++ng)
+#pragma unroll
+      for (int i = 0; i < G::VD; ++i) {
+        if constexpr (G::ES == 2) {
           const uint32_t sel = i & 1 ? 0x07060302u : 0x05040100u;
           uint4 a;
           a.x = __builtin_amdgcn_perm(val(0, 1, ng, i / 2), val(0, 0, ng, i / 2), sel);
@@ -295,21 +311,22 @@ struct AttTile {
           a.z = __builtin_amdgcn_perm(val(1, 1, ng, i / 2), val(1, 0, ng, i / 2), sel);
           a.w = __builtin_amdgcn_perm(val(1, 3, ng, i / 2), val(1, 2, ng, i / 2), sel);
 #pragma unroll
-          for (int y = 0; y < QT; ++y) put(acc[y][ng][i], mfma16(a, b2[y], mfma16(a, b[y], acc[y][ng][i])));
-        }
-    } else {
-#pragma unroll
-      for (int ng = 0; ng < G::NG; ++ng)
-#pragma unroll
-        for (int i = 0; i < G::VD; ++i)
+          for (int y = 0; y < QT; ++y) put(acc[y][ng][i], mfma16(a, W.b2[y], mfma16(a, W.b[y], acc[y][ng][i])));
+        } else {
 #pragma unroll
           for (int y = 0; y < QT; ++y) {
             f32x4 x = acc[y][ng][i];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x = mfma4(val(0, j, ng, i), __float_as_uint(p[y][0][j]), x);
+            for (int j = 0; j < 4; ++j) x = mfma4(val(0, j, ng, i), dword(W.b[y], j), x);
             put(acc[y][ng][i], x);
           }
-    }
+        }
+      }
+  }
+  template <int QT, bool SOME = false, bool POS = false>
+  __device__ __forceinline__ void weigh(const f32x4 (&p)[QT][G::SUB], f32x4 (&acc)[QT][G::NG][G::VD],
+                                        const uint32_t (*mask)[4] = nullptr, bool keep = true) {
+    products<QT, SOME>(pack<QT, POS>(p), acc, mask, keep);
   }
 };
 

@@ -10,9 +10,10 @@ namespace scute {
 
 // Where a row's partial results lie.
 struct alignas(16) ShRow {
-  // shared positions: the row's group has `tiles` tiles of columns (row of the group
-  // times heads of a key head, and head of it; the row's first is col0) for each
-  // key head, the x0-th on, of `units` units from the u0-th on (0: nothing shared)
+  // shared positions: the row's group has `tiles` wide tiles of columns (row of the
+  // group times heads of a key head, and head of it; the row's first is col0) for
+  // each key head, the x0-th on, of `units` units from the u0-th on (0: nothing
+  // shared)
   int32_t units, tiles, col0;
   uint32_t u0, x0;
   // its own: `own` tiles a head behind `before` of the rows before it, of row
@@ -22,7 +23,8 @@ struct alignas(16) ShRow {
   int32_t lead, at, pad[3];
 };
 struct ShPlan {
-  uint32_t each_shared, each_own;  // units of a work-group, tiles of a wave
+  uint32_t each_shared, each_own;  // units of a gang, tiles of a chunk
+  int32_t taken;                   // chunks taken behind the waves' first; 0 between calls
 };
 
 struct SharedArgs {
@@ -35,6 +37,8 @@ struct SharedArgs {
   int64_t q_stride, out_stride, page_stride, token_stride, head_stride, table_stride, n_pages;
   uint32_t ps_mul;
   int32_t n_rows, n_groups, n_kv, heads, head_dim, page_size, ps_shift, reach, n_requests, max_tiles;
+  int32_t cw, pw;                       // waves side by side in a work-group's columns, and one after the other in positions
+  int32_t gang;                         // work-groups of a wide tile of columns
   int32_t together, q_tiles, own_cols;  // rows of a run at most; query tiles of a key head; columns of an own slot
   int32_t negate;    // the scale is below 0
   float scale_log2;  // its magnitude times log2(e), above 0 (so that what is masked stays at -inf)
@@ -48,12 +52,13 @@ template <typename T, int DP>
 struct ShGeo {
   using G = AttGeo<T, DP>;
   static constexpr int QT = DP * G::ES >= 1024 ? 1 : 2;  // query tiles a wave (one where two would not fit the registers)
-  static constexpr int COLS = 4 * 16 * QT;               // columns of a work-group
+  static constexpr int NW = 4;                           // waves of a work-group
+  static constexpr int WCOLS = 16 * QT;                  // columns of a wave
   static constexpr int ROW = DP * G::ES;                 // bytes of a position in LDS
   static constexpr int STAGE = sh_stage(G::ES, DP);      // positions staged at once: a unit
-  static constexpr int RING = 4, BYTES = STAGE * ROW;    // stages of K (and of V) in LDS
+  static constexpr int BYTES = STAGE * ROW, RING = (DP <= 128 ? 32768 : 65536) / BYTES;  // bytes of a stage of K (of V), stages in LDS
   static constexpr int PIECES = ROW / 16;                // 16-byte pieces of a position
-  static constexpr int LOADS = BYTES / 4096;             // a wave's loads of 1 KB a stage (of K, and of V)
+  static constexpr int LOADS = BYTES / 1024 / NW;        // a wave's loads of 1 KB a stage (of K, and of V)
 };
 // where LDS holds piece p of a stage's position: rows that are read together are
 // spread over the banks
@@ -109,10 +114,12 @@ __device__ __forceinline__ float max_over_rows(float v) {
   return fmaxf(__uint_as_float(b.x), __uint_as_float(b.y));
 }
 
+constexpr int SH_CHUNKS = 9;        // chunks a wave at most (eight, and one more)
+constexpr int64_t SH_SAVED = 256 << 20;  // bytes
 constexpr int SH_TILES = 1 << 22;  // (group, key head, tile)s stay below it
 
 struct ShGroup {
-  int row, rows, n, tiles, units;  // first row, rows, shared positions, column tiles, units of positions
+  int row, rows, n, tiles, units;  // first row, rows, shared positions, wide tiles of columns, units of positions
 };
 template <typename S>
 __device__ __forceinline__ ShGroup sh_group(const SharedArgs& A, int g) {
@@ -120,7 +127,8 @@ __device__ __forceinline__ ShGroup sh_group(const SharedArgs& A, int g) {
   const int a = min(max(ldg(A.group + g), 0), A.n_rows), b = min(max(ldg(A.group + g + 1), 0), A.n_rows);
   q.row = a, q.rows = max(b - a, 0);
   q.n = min(max(ldg(A.shared + g), 0), A.reach);
-  q.tiles = (int)(((int64_t)q.rows * A.heads + S::COLS - 1) / S::COLS);
+  const int wide = S::WCOLS * A.cw * A.gang;
+  q.tiles = (int)(((int64_t)q.rows * A.heads + wide - 1) / wide);
   q.units = q.tiles ? (q.n + S::STAGE - 1) / S::STAGE : 0;
   return q;
 }
@@ -137,7 +145,7 @@ struct ShShared {
   int end[256], n[256];      // the first of its groups: the row behind it, shared positions
   uint32_t t[257];           // tiles a head of the rows before the thread's
   uint32_t sum[2][4];
-  unsigned long long lead[4];
+  unsigned long long lead[8];
 };
 struct ShCall {
   int per_g, per_r;  // groups and rows a thread
@@ -263,6 +271,21 @@ __device__ __forceinline__ void sh_weights(const SharedArgs& A, f32x4 (&sc)[G::S
       l += sc[sb][j];
     }
 }
+// waits until at most n vector memory operations are out (n rounded down to what
+// there is an instruction for)
+__device__ __forceinline__ void sh_wait(int n) {
+#define WAIT(x) \
+  else if (n >= x) __builtin_amdgcn_s_waitcnt(vmcnt_imm(x))
+  if (n >= 16) __builtin_amdgcn_s_waitcnt(vmcnt_imm(16));
+  WAIT(12);
+  WAIT(10);
+  WAIT(8);
+  WAIT(6);
+  WAIT(4);
+  WAIT(2);
+  else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+#undef WAIT
+}
 // Elements of a dword of V that are not finite become 0; whether there are any.
 template <int ES>
 __device__ __forceinline__ bool sh_finite(uint32_t& v) {
@@ -284,20 +307,23 @@ __device__ __forceinline__ void sh_add_odd(const char* p, bool seen, f32x4 (&acc
 }
 
 // Sums of the softmax over a group's shared positions for all its rows: a
-// product of tall matrices, so K and V go through LDS once for 128 columns (rows
-// times the heads of a key head), 32 columns a wave, and a wave's columns are
-// its own: nothing is joined between waves.
-template <typename T, int DP, bool EXACT>
+// product of tall matrices, so K and V go through LDS once for up to 128 columns
+// (rows times the heads of a key head), 32 columns a wave: nothing is joined
+// between waves. Where the columns do not fill the waves, the waves of a column
+// take stages in turn.
+template <typename T, int DP, bool PAGE16, bool EXACT>
 __device__ __forceinline__ void sh_prefix(const SharedArgs& A, const ShCall& call, ShShared& L,
-                                          char (*s_kv)[2 * ShGeo<T, DP>::BYTES], uint32_t group_of_units, uint32_t each) {
+                                          char (*s_kv)[2 * ShGeo<T, DP>::BYTES], uint32_t gang, int member,
+                                          uint32_t each) {
   using G = AttGeo<T, DP>;
   using S = ShGeo<T, DP>;
-  constexpr int TILE = G::TILE, SUB = G::SUB, QT = S::QT, COLS = S::COLS;
+  constexpr int TILE = G::TILE, SUB = G::SUB, QT = S::QT, NW = S::NW;
   const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6), m16 = lane & 15, gq = lane >> 4;
   const int D = EXACT ? DP : A.head_dim, row_bytes = D * G::ES;
+  const int COLS = S::WCOLS * A.cw, pw = A.pw, wc = w % A.cw, wp = w / A.cw;  // the wave's columns and turn
   const uint32_t total = L.u[256];
-  const uint32_t u_end = (uint32_t)min((uint64_t)total, (uint64_t)(group_of_units + 1) * each);
-  for (uint32_t u = (uint32_t)min((uint64_t)total, (uint64_t)group_of_units * each); u < u_end;) {
+  const uint32_t u_end = (uint32_t)min((uint64_t)total, (uint64_t)(gang + 1) * each);
+  for (uint32_t u = (uint32_t)min((uint64_t)total, (uint64_t)gang * each); u < u_end;) {
     const int lo = sh_find(L.u, u);
     uint32_t u0 = L.u[lo], x = L.x[lo];
     ShGroup q{};
@@ -311,14 +337,14 @@ __device__ __forceinline__ void sh_prefix(const SharedArgs& A, const ShCall& cal
     u0 = (uint32_t)uni((int)u0), x = (uint32_t)uni((int)x);
     if (q.units == 0) return;  // (only if the lengths change while the call runs)
     const uint32_t i = (u - u0) / in_place(q.units);
-    const int kvh = i / in_place(q.tiles), ct = i - kvh * q.tiles, first = u - u0 - i * q.units;
+    const int kvh = i / in_place(q.tiles), ct = (i - kvh * q.tiles) * A.gang + member, first = u - u0 - i * q.units;
     const int last = min((uint32_t)q.units, first + (u_end - u));  // units first .. last - 1 of the group's
     x += i;
     u += last - first;
 
     // the row that sees most of the shared positions, the first of those: its pages are read
     unsigned long long best = 0;
-    for (int r = tid; r < q.rows; r += 256) {
+    for (int r = tid; r < q.rows; r += 64 * NW) {
       const unsigned long long v = (unsigned long long)min(sh_len(A, q.row + r), q.n) << 32 | (0xFFFFFFFFu - (uint32_t)r);
       best = v > best ? v : best;
     }
@@ -330,7 +356,7 @@ __device__ __forceinline__ void sh_prefix(const SharedArgs& A, const ShCall& cal
     if (lane == 0) L.lead[w] = best;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) best = L.lead[k] > best ? L.lead[k] : best;
+    for (int k = 0; k < NW; ++k) best = L.lead[k] > best ? L.lead[k] : best;
     const int reach = uni((int)(best >> 32));  // positions that some row sees
     const int lead = q.row + uni((int)(0xFFFFFFFFu - (uint32_t)best));
     const int units = min(last, (reach + S::STAGE - 1) / S::STAGE) - first;
@@ -341,7 +367,7 @@ __device__ __forceinline__ void sh_prefix(const SharedArgs& A, const ShCall& cal
     int n_min = 0x7FFFFFFF, n_max = 0;
 #pragma unroll
     for (int y = 0; y < QT; ++y) {
-      const int c = ct * COLS + (w * QT + y) * 16 + m16, r = c / A.heads, h = kvh * A.heads + (c - r * A.heads);
+      const int c = ct * COLS + (wc * QT + y) * 16 + m16, r = c / A.heads, h = kvh * A.heads + (c - r * A.heads);
       my_n[y] = r < q.rows ? min(sh_len(A, q.row + r), q.n) : 0;
       const char* qp = (const char*)A.q + ((int64_t)(q.row + (r < q.rows ? r : 0)) * A.q_stride + (int64_t)h * D) * G::ES;
 #pragma unroll
@@ -370,42 +396,80 @@ __device__ __forceinline__ void sh_prefix(const SharedArgs& A, const ShCall& cal
         for (int e = 0; e < G::VD; ++e) acc[y][ng][e] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    // ---- staging: loads of 1 KB straight to LDS, three stages ahead ----
-    constexpr int ROWS = 1024 / S::ROW;  // positions of a load
+    // ---- staging: loads of 1 KB straight to LDS, a step (pw stages) a time,
+    // `ahead` steps before it is used ----
+    constexpr int ROWS = 1024 / S::ROW;                  // positions of a load
+    constexpr int NB = S::STAGE / 16, REACH = 64 / NB;   // blocks of 16 positions of a stage; stages of 64 blocks
+    const int steps = (units + pw - 1) / pw, ahead = S::RING / pw - 1;
     const int32_t* tab = A.table + (int64_t)(reach > 0 ? uni(A.req ? ldg(A.req + lead) : lead) : 0) * A.table_stride;
     const int64_t head = (int64_t)kvh * A.head_stride * G::ES;
+    const uint32_t tok = (uint32_t)A.token_stride * G::ES;
     const auto page_of = [&](int t) { return (int)(((uint64_t)(uint32_t)t * A.ps_mul) >> (31 + A.ps_shift)); };
-    const auto row_of = [&](int j) { return (w + 4 * j) * ROWS + lane / S::PIECES; };  // of this lane's piece, load j
-    const auto position = [&](int s) { return min((first + s) * S::STAGE + lane % S::STAGE, reach - 1); };
-    const auto look_up = [&](int s) { return ldg(tab + page_of(position(min(s, units - 1)))); };
-    // stage s, whose pages are `page` (a position a lane); returns those of its
-    // positions that are on no page
-    const auto load = [&](int s, int page) {
-      const int t = position(s);
-      const bool ok = page >= 0 && page < A.n_pages;
-      const int64_t off =
-          (ok ? (int64_t)page * A.page_stride + (int64_t)(t - page_of(t) * A.page_size) * A.token_stride : 0) * G::ES + head;
-      char* to = s_kv[s % S::RING];
-#pragma unroll
-      for (int j = 0; j < S::LOADS; ++j) {
-        const int row = row_of(j), at = 16 * sh_slot<S::ROW>(row, lane % S::PIECES);
-        const uint32_t lo = __shfl((int)(uint32_t)off, row, 64), hi = __shfl((int)(off >> 32), row, 64);
-        const int64_t o = (int64_t)((uint64_t)hi << 32 | lo) + (EXACT ? at : min(at, row_bytes - 16));
-        __builtin_amdgcn_global_load_lds((const GLOBAL void*)((const char*)A.k + o), (lds_void*)(to + (w + 4 * j) * 1024), 16,
-                                         0, 0);
-        __builtin_amdgcn_global_load_lds((const GLOBAL void*)((const char*)A.v + o),
-                                         (lds_void*)(to + S::BYTES + (w + 4 * j) * 1024), 16, 0, 0);
-      }
-      return (uint64_t)__ballot(!ok);
+    const auto row0 = [&](int j) { return (w + NW * j) * ROWS; };  // the first row of load j
+    const auto to_lds = [&](const char* k, const char* v, int s, int j) {
+      char* to = s_kv[s % S::RING] + (w + NW * j) * 1024;
+      __builtin_amdgcn_global_load_lds((const GLOBAL void*)k, (lds_void*)to, 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((const GLOBAL void*)v, (lds_void*)(to + S::BYTES), 16, 0, 0);
     };
-    int page3 = 0, page4 = 0;                  // of stages s + 3, s + 4
-    uint64_t away0 = 0, away1 = 0, away2 = 0;  // of stages s, s + 1, s + 2
+    // pages of multiples of 16 positions: where 64 blocks lie, one a lane, and the
+    // pages of the next 64; otherwise the pages of a stage's positions, one a lane,
+    // of the two stages that are loaded next
+    int32_t place_lo = 0, place_hi = 0, raw = 0, raw2 = 0;
+    uint64_t bad[2] = {0, 0};                           // blocks on no page, by turns of 64
+    uint64_t gone_at[PAGE16 ? 1 : S::RING] = {};        // positions on no page, of stages s, s + 1, ...
+    const auto block = [&](int g) { return 16 * min(first * NB + 64 * g + lane, (reach - 1) >> 4); };
+    const auto position = [&](int s) { return min((first + min(s, units - 1)) * S::STAGE + lane % S::STAGE, reach - 1); };
+    const auto refill = [&](int g) {
+      const int t = block(g), at = page_of(t);
+      const bool ok = raw >= 0 && raw < A.n_pages;
+      const int64_t off = ((int64_t)raw * A.page_stride + (int64_t)(t - at * A.page_size) * A.token_stride) * G::ES + head;
+      place_lo = ok ? (int32_t)(uint32_t)off : (int32_t)(uint32_t)head, place_hi = ok ? (int32_t)(off >> 32) : (int32_t)(head >> 32);
+      const uint64_t no = __ballot(!ok);
+      if (g & 1) bad[1] = no;
+      else bad[0] = no;
+      raw = ldg(tab + page_of(block(g + 1)));
+    };
+    const auto load = [&](int s) {  // stage s, or the last again behind it
+      if constexpr (PAGE16) {
+        if (s % REACH == 0) refill(s / REACH);
+#pragma unroll
+        for (int j = 0; j < S::LOADS; ++j) {
+          const int r = row0(j), b = s % REACH * NB + r / 16;
+          const int64_t base = (int64_t)((uint64_t)(uint32_t)lane_of(place_hi, b) << 32 | (uint32_t)lane_of(place_lo, b));
+          const int in = r % 16 + lane / S::PIECES, at = 16 * sh_slot<S::ROW>(r + lane / S::PIECES, lane % S::PIECES);
+          const uint32_t off = in * tok + (EXACT ? at : min(at, row_bytes - 16));
+          to_lds((const char*)A.k + base + off, (const char*)A.v + base + off, s, j);
+        }
+      } else {
+        const int t = position(s);
+        const bool ok = raw >= 0 && raw < A.n_pages;
+        const int64_t off =
+            (ok ? (int64_t)raw * A.page_stride + (int64_t)(t - page_of(t) * A.page_size) * A.token_stride : 0) * G::ES + head;
+        raw = raw2;
+        raw2 = ldg(tab + page_of(position(s + 2)));
+#pragma unroll
+        for (int j = 0; j < S::LOADS; ++j) {
+          const int r = row0(j) + lane / S::PIECES, at = 16 * sh_slot<S::ROW>(r, lane % S::PIECES);
+          const uint32_t lo = __shfl((int)(uint32_t)off, r, 64), hi = __shfl((int)(off >> 32), r, 64);
+          const int64_t o = (int64_t)((uint64_t)hi << 32 | lo) + (EXACT ? at : min(at, row_bytes - 16));
+          to_lds((const char*)A.k + o, (const char*)A.v + o, s, j);
+        }
+        gone_at[S::RING - 1] = __ballot(!ok);
+      }
+    };
     if (units > 0) {
-      const int p0 = look_up(0), p1 = look_up(1), p2 = look_up(2);
-      page3 = look_up(3), page4 = look_up(4);
-      away0 = load(0, p0);
-      if (units > 1) away1 = load(1, p1);
-      if (units > 2) away2 = load(2, p2);
+      raw = ldg(tab + page_of(PAGE16 ? block(0) : position(0)));
+      if constexpr (!PAGE16) raw2 = ldg(tab + page_of(position(1)));
+      if constexpr (PAGE16) {
+        for (int s = 0; s < min(ahead, steps) * pw; ++s) load(s);
+      } else {
+#pragma unroll
+        for (int s = 0; s < S::RING - 1; ++s)  // (pw is 1)
+          if (s < steps) {
+            load(s);
+            gone_at[s] = gone_at[S::RING - 1];
+          }
+      }
     }
     const uint32_t lds = (uint32_t)(uintptr_t)(lds_void*)&s_kv[0][0];
     const uint32_t k_at = m16 * S::ROW + 16 * sh_slot<S::ROW>(m16, gq);  // (chunk c: ^ 64 c, 16 positions on: + 16 ROW)
@@ -415,27 +479,36 @@ __device__ __forceinline__ void sh_prefix(const SharedArgs& A, const ShCall& cal
       const int row = 4 * gq + j, b = m16 * G::VB;
       v_at[j] = S::BYTES + row * S::ROW + 16 * sh_slot<S::ROW>(row, b / 16) + b % 16;
     }
-    for (int s = 0; s < units; ++s) {
-      // this wave's part of stage s is there when those of the two behind it are
-      // the only loads that are out; then all waves' parts are
-      if (s + 2 < units)
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm(4 * S::LOADS));
-      else
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
+    for (int i = 0; i < steps; ++i) {
+      // this wave's part of step i is there when those of the steps behind it are the
+      // only loads that are out; then all waves' parts are
+      sh_wait(min(steps - 1 - i, ahead - 1) * pw * 2 * S::LOADS);
       lds_barrier();
-      const uint64_t away = away0;
-      away0 = away1, away1 = away2;
-      if (s + 3 < units) {
-        const int page = page3;
-        page3 = page4;
-        page4 = look_up(s + 5);
-        away2 = load(s + 3, page);
+      const int s = i * pw + wp;  // the wave's stage of the step
+      uint64_t gone_s = 0;
+      if constexpr (PAGE16) {
+        const uint64_t b = (s / REACH & 1 ? bad[1] : bad[0]) >> (s % REACH * NB);
+#pragma unroll
+        for (int x = 0; x < NB; ++x) gone_s |= b >> x & 1 ? 0xFFFFull << (16 * x) : 0ull;
+      } else {
+        gone_s = gone_at[0];
+#pragma unroll
+        for (int x = 0; x + 1 < S::RING; ++x) gone_at[x] = gone_at[x + 1];
       }
-      if (n_max == 0) continue;
+      const auto next = [&]() {
+        if (i + ahead < steps) {
+          for (int x = 0; x < pw; ++x) load((i + ahead) * pw + x);
+          if constexpr (!PAGE16) gone_at[S::RING - 2] = gone_at[S::RING - 1];
+        }
+      };
+      if (s >= units || (first + s) * S::STAGE >= n_max) {  // (no column of the wave sees any of it)
+        next();
+        continue;
+      }
 #pragma unroll 1
       for (int tt = 0; tt < S::STAGE / TILE; ++tt) {
         const int t = (first + s) * S::STAGE + tt * TILE;
-        if (t >= n_max) break;
+        if (tt > 0 && t >= n_max) break;
         AttTile<T, DP, EXACT> tile;
         const uint32_t base = lds + (s % S::RING) * 2 * S::BYTES + tt * TILE * S::ROW;
         if constexpr (G::NC == 2) {  // (two chunks of 32 positions, as four rows)
@@ -456,7 +529,8 @@ __device__ __forceinline__ void sh_prefix(const SharedArgs& A, const ShCall& cal
         }
         f32x4 sc[QT][SUB];
         tile.template scores<QT>([&](int y, int c) { return qf[y][c]; }, sc, gq, row_bytes);
-        const uint32_t gone = (uint32_t)(away >> (tt * TILE)) & (uint32_t)((1ull << TILE) - 1);
+        if (tt == 0) next();  // (under the products)
+        const uint32_t gone = (uint32_t)(gone_s >> (tt * TILE)) & (uint32_t)((1ull << TILE) - 1);
         const uint32_t va[4] = {base + v_at[0], base + v_at[1], base + v_at[2], base + v_at[3]};
         const auto read_v = [&](auto ng) {
           uint32_t* const o[8] = {tile.v[0][0][ng], tile.v[0][1][ng], tile.v[0][2][ng], tile.v[0][3][ng],
@@ -514,13 +588,13 @@ __device__ __forceinline__ void sh_prefix(const SharedArgs& A, const ShCall& cal
     }
 
     // ---- the piece's sums to its slot ----
-    float* out = A.seeds + (int64_t)(group_of_units + x) * COLS * (DP + 4);
+    float* out = A.seeds + (((int64_t)(gang + x) * A.gang + member) * pw + wp) * COLS * (DP + 4);
 #pragma unroll
     for (int y = 0; y < QT; ++y) {
       float sum = l[y];
       sum += __shfl_xor(sum, 16, 64);
       sum += __shfl_xor(sum, 32, 64);
-      const int c = (w * QT + y) * 16 + m16;
+      const int c = (wc * QT + y) * 16 + m16;
       float* o = out + (int64_t)c * (DP + 4);
       const bool sees = my_n[y] > 0;  // (others: sums of nothing)
       if (ct * COLS + c >= q.rows * A.heads) continue;
@@ -538,21 +612,21 @@ __device__ __forceinline__ void sh_prefix(const SharedArgs& A, const ShCall& cal
   }
 }
 
-// Sums over what the rows of a run hold of their own: a wave a piece, as K and V
-// stream by; few columns, so bound by the memory.
+// Sums over what the rows of a run hold of their own, for a chunk of their tiles: a
+// wave a piece, as K and V stream by; few columns, so bound by the memory.
 template <typename T, int DP, bool PAGE16, bool EXACT>
-__device__ __forceinline__ void sh_own(const SharedArgs& A, const ShCall& call, const ShShared& L, uint32_t wave, uint32_t each) {
+__device__ __forceinline__ void sh_own(const SharedArgs& A, const ShCall& call, const ShShared& L, uint32_t chunk, uint32_t each) {
   using G = AttGeo<T, DP>;
   using S = ShGeo<T, DP>;
   constexpr int TILE = G::TILE, SUB = G::SUB;
   const int lane = threadIdx.x & 63, m16 = lane & 15, gq = lane >> 4;
   const int D = EXACT ? DP : A.head_dim, row_bytes = D * G::ES, H = A.n_kv * A.q_tiles;
   const uint32_t total = L.t[256] * H;
-  const uint32_t u_end = (uint32_t)min((uint64_t)total, (uint64_t)(wave + 1) * each);
+  const uint32_t u_end = (uint32_t)min((uint64_t)total, (uint64_t)(chunk + 1) * each);
   const uint32_t neg = A.negate ? (G::ES == 2 ? 0x80008000u : 0x80000000u) : 0u;
   const uint32_t tok = (uint32_t)A.token_stride * G::ES;
   const auto page_of = [&](int t) { return (int)(((uint64_t)(uint32_t)t * A.ps_mul) >> (31 + A.ps_shift)); };
-  for (uint32_t u = (uint32_t)min((uint64_t)total, (uint64_t)wave * each); u < u_end;) {
+  for (uint32_t u = (uint32_t)min((uint64_t)total, (uint64_t)chunk * each); u < u_end;) {
     // the run that holds unit u
     const int lo = sh_find(L.t, u / in_place(H));
     uint32_t before = L.t[lo];
@@ -738,7 +812,7 @@ __device__ __forceinline__ void sh_own(const SharedArgs& A, const ShCall& call, 
     // ---- the piece's sums to its slot ----
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
-    float* o = A.own + ((int64_t)wave + (int64_t)R.row * H + hh) * A.own_cols * (DP + 4) + m16 * (DP + 4);
+    float* o = A.own + ((int64_t)chunk + (int64_t)R.row * H + hh) * A.own_cols * (DP + 4) + m16 * (DP + 4);
     if (m16 < nq) {
       const bool sees = my_n > my_lo;  // (others: sums of nothing)
 #pragma unroll
@@ -756,15 +830,19 @@ __device__ __forceinline__ void sh_own(const SharedArgs& A, const ShCall& call, 
 }
 
 // Both kinds of work at once: products over shared positions keep the matrix
-// units busy while what the rows have of their own streams from memory. Units of
-// each kind are numbered (group, key head, tile of columns, stage of positions;
-// row, head, tile of positions), and every work-group, or wave, takes the same
-// number of consecutive ones. Work-group or wave w's part of the x-th (group, key
-// head, tile) or (row, head) is a piece, in slot w + x: both grow from piece to
-// piece, so slots are not shared and those of one x lie side by side. Lengths and
-// groups are on the device; every work-group numbers them by itself, and the
-// partial results are joined by the next launch.
-constexpr uint32_t SH_COST_SHARED = 5, SH_COST_OWN = 4;  // of a unit and of a tile
+// units busy while what the rows have of their own streams from memory.
+//
+// How the work is cut. A unit is one stage of positions of one (group, key head,
+// wide tile of columns): as many tiles of 128 columns as a gang has work-groups,
+// which lie on one die and walk the positions side by side, so that all but the
+// first find them in its L2. The units, numbered in that order, are cut into
+// equal ranges for the gangs; so are the tiles of positions of all (row, head)s
+// for the waves of the other work-groups. Gang or wave w's part of the x-th
+// (group, key head, wide tile) or (row, head) is a piece, in slot w + x: both grow
+// from piece to piece, so slots are not shared and those of one x lie side by
+// side. Lengths and groups are on the device; every work-group numbers them by
+// itself, and the partial results are joined by the next launch.
+constexpr float SH_COST_SHARED = 10.f, SH_COST_OWN = 7.f;  // of a unit and of a tile
 
 template <typename T, int DP, bool PAGE16, bool EXACT>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_attention(SharedArgs A) {
@@ -779,7 +857,8 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_attention(Sha
   // ---- the groups ----
   {
     uint32_t u = 0, x = 0;
-    L.row[tid] = A.n_rows, L.end[tid] = 0, L.n[tid] = 0;
+    // (the first 256 threads' groups, and rows below)
+    if (tid < 256) L.row[tid] = A.n_rows, L.end[tid] = 0, L.n[tid] = 0;
     const int g0 = min(A.n_groups, tid * call.per_g), g1 = min(A.n_groups, g0 + call.per_g);
     for (int g = g0; g < g1; ++g) {
       const ShGroup q = sh_group<S>(A, g);
@@ -788,13 +867,13 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_attention(Sha
       x = (uint32_t)min((int64_t)SH_TILES, x + (int64_t)(q.units ? q.tiles : 0) * A.n_kv);
     }
     const uint32_t iu = wave_scan(u), ix = wave_scan(x);
-    if (lane == 63) L.sum[0][w] = iu, L.sum[1][w] = ix;
+    if (lane == 63 && w < 4) L.sum[0][w] = iu, L.sum[1][w] = ix;
     __syncthreads();
     uint32_t bu = 0, bx = 0;
 #pragma unroll
     for (int i = 0; i < 3; ++i)
       if (i < w) bu += L.sum[0][i], bx += L.sum[1][i];
-    L.u[tid + 1] = bu + iu, L.x[tid + 1] = bx + ix;
+    if (tid < 256) L.u[tid + 1] = bu + iu, L.x[tid + 1] = bx + ix;
     if (tid == 0) L.u[0] = L.x[0] = 0;
     __syncthreads();
   }
@@ -807,27 +886,38 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_attention(Sha
     const int r0 = min(A.n_rows, tid * call.per_r), r1 = min(A.n_rows, r0 + call.per_r);
     for (int r = r0; r < r1; r += A.together) sh_runs<S, G::TILE>(A, call, L, r, [&](const ShRun& q) { t += q.tiles; });
     const uint32_t it = wave_scan(t);
-    if (lane == 63) L.sum[0][w] = it;
+    if (lane == 63 && w < 4) L.sum[0][w] = it;
     __syncthreads();
     uint32_t bt = 0;
 #pragma unroll
     for (int i = 0; i < 3; ++i)
       if (i < w) bt += L.sum[0][i];
-    L.t[tid + 1] = bt + it;
+    if (tid < 256) L.t[tid + 1] = bt + it;
     if (tid == 0) L.t[0] = 0;
     __syncthreads();
   }
   const int H = A.n_kv * A.q_tiles;
   const uint32_t units = call.fits ? L.u[256] : 0, tiles = L.t[256] * H;
   // ---- shares of the work-groups ----
-  const float cs = (float)units * SH_COST_SHARED, co = (float)tiles * SH_COST_OWN;
-  uint32_t ws = units == 0 ? 0 : (uint32_t)(gridDim.x * (cs / (cs + co)) + 0.5f);
-  ws = units == 0 ? 0 : min(max(ws, 1u), tiles ? gridDim.x - 1 : gridDim.x);
-  const uint32_t wo = gridDim.x - ws;
-  const uint32_t each_s = ws ? (units + ws - 1) / ws : 1, each_o = wo && tiles ? (tiles + 4 * wo - 1) / (4 * wo) : 1;
+  const float cs = (float)units * A.gang * SH_COST_SHARED / A.pw, co = (float)tiles * SH_COST_OWN;
+  // (whole gangs on each of the dies, to which work-groups go in turn)
+  const uint32_t dies = gridDim.x % 8 == 0 ? 8 : 1, here = gridDim.x / dies, die = blockIdx.x % dies, k = blockIdx.x / dies;
+  uint32_t ws = 0;  // work-groups of a die for shared positions
+  if (units) {
+    const uint32_t gangs = (uint32_t)((float)here * (cs / (cs + co)) / (float)A.gang + 0.5f);
+    ws = min(max(gangs, 1u), (here - (tiles ? 1 : 0)) / A.gang) * A.gang;
+  }
+  const uint32_t wo = here - ws;
+  const uint32_t n_gangs = dies * (ws / A.gang), waves = dies * wo * S::NW;
+  // (four units at least: fewer pieces to join; four rows behind 1000 positions, one unit: 39 us, four: 34)
+  const uint32_t each_s = n_gangs ? max((units + n_gangs - 1) / n_gangs, 4u) : 1;
+  // own tiles: chunks of an eighth of a wave's share (8 tiles at least), taken from
+  // a counter after each wave's first: waves with equal work differ by half in time
+  const uint32_t share = tiles ? (tiles + waves - 1) / waves : 1, each_o = max(min(share, 8u), (share + 7) / 8);
+  const uint32_t chunks = (tiles + each_o - 1) / each_o;
   // ---- where each row's partial results will lie ----
-  if (blockIdx.x == 0 && tid == 0) *A.plan = ShPlan{each_s, each_o};
-  for (int base = (blockIdx.x * 256 + tid) * A.together; base < A.n_rows; base += gridDim.x * 256 * A.together) {
+  if (blockIdx.x == 0 && tid == 0) A.plan->each_shared = each_s, A.plan->each_own = each_o;
+  for (int base = (blockIdx.x * 64 * S::NW + tid) * A.together; base < A.n_rows; base += gridDim.x * 64 * S::NW * A.together) {
     const int chunk = base / call.per_r;
     uint32_t before = L.t[chunk];
     for (int b = chunk * call.per_r; b < base; b += A.together)
@@ -844,11 +934,17 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_attention(Sha
     });
   }
   // ---- the work-groups' kinds, spread evenly ----
-  const uint32_t upto = (uint32_t)((uint64_t)blockIdx.x * ws / gridDim.x), next = (uint32_t)((uint64_t)(blockIdx.x + 1) * ws / gridDim.x);
-  if (next > upto)
-    sh_prefix<T, DP, EXACT>(A, call, L, s_kv, upto, each_s);
-  else if (tiles)
-    sh_own<T, DP, PAGE16, EXACT>(A, call, L, 4 * (blockIdx.x - upto) + w, each_o);
+  const uint32_t upto = k * ws / here, next = (k + 1) * ws / here;
+  if (next > upto) {
+    sh_prefix<T, DP, PAGE16, EXACT>(A, call, L, s_kv, die * (ws / A.gang) + upto / A.gang, (int)(upto % A.gang), each_s);
+  } else {
+    for (uint32_t chunk = S::NW * (die * wo + k - upto) + w; chunk < chunks;) {
+      sh_own<T, DP, PAGE16, EXACT>(A, call, L, chunk, each_o);
+      int taken = 0;
+      if (lane == 0) taken = arrive(&A.plan->taken);
+      chunk = waves + (uint32_t)uni(taken);
+    }
+  }
 }
 
 // The slots of a (row, head), DP / 4 lanes for its elements, eight slots' loads in
@@ -866,16 +962,18 @@ __global__ __launch_bounds__(256) void k_shared_join(SharedArgs A) {
   const ShPlan P = *A.plan;
   const int kvh = h / A.heads, hg = h - kvh * A.heads, H = A.n_kv * A.q_tiles;
   // shared
-  const int c = R.col0 + hg, ct = c / S::COLS;
-  const uint32_t x = (uint32_t)(kvh * R.tiles + ct), u = R.u0 + x * R.units, w0 = u / P.each_shared;
-  const int n0 = R.units ? (int)((u + R.units - 1) / P.each_shared - w0) + 1 : 0;
-  const float* p0 = A.seeds + ((int64_t)(w0 + R.x0 + x) * S::COLS + c - ct * S::COLS) * (DP + 4);
+  if (blockIdx.x == 0 && threadIdx.x == 0) A.plan->taken = 0;
+  const int COLS = S::WCOLS * A.cw, c = R.col0 + hg, ct = c / COLS;
+  const uint32_t x = (uint32_t)(kvh * R.tiles + ct / A.gang), u = R.u0 + x * R.units, w0 = u / P.each_shared;
+  const int n0 = R.units ? ((int)((u + R.units - 1) / P.each_shared - w0) + 1) * A.pw : 0;
+  const float* p0 = A.seeds + (((int64_t)(w0 + R.x0 + x) * A.gang + ct % A.gang) * A.pw * COLS + c % COLS) * (DP + 4);
   // own
   const int qt = A.together > 1 ? 0 : hg / 16, hh = kvh * A.q_tiles + qt, col = R.at + hg - 16 * qt;
   const uint32_t v = R.before * H + (uint32_t)hh * R.own, w1 = v / P.each_own;
   const int n1 = R.own ? (int)((v + R.own - 1) / P.each_own - w1) + 1 : 0;
   const float* p1 = A.own + ((int64_t)w1 + (int64_t)R.lead * H + hh) * A.own_cols * (DP + 4) + col * (DP + 4);
-  const int64_t s0 = S::COLS * (DP + 4), s1 = (int64_t)A.own_cols * (DP + 4);
+  // (slots of one x: its turns lie side by side, its pieces a gang's slots apart)
+  const int64_t turn = (int64_t)COLS * (DP + 4), s0 = A.gang * A.pw * turn, s1 = (int64_t)A.own_cols * (DP + 4);
   float m = -INFINITY, l = 0.f;
   f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int j0 = 0; j0 < n0 + n1; j0 += 8) {
@@ -883,7 +981,7 @@ __global__ __launch_bounds__(256) void k_shared_join(SharedArgs A) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int i = min(j0 + j, n0 + n1 - 1);
-      const float* p = i < n0 ? p0 + i * s0 : p1 + (i - n0) * s1;
+      const float* p = i < n0 ? p0 + i / A.pw * s0 + i % A.pw * turn : p1 + (i - n0) * s1;
       ml[j] = ldg4(p + DP);
       z[j] = ldg4(p + d);
     }
@@ -910,12 +1008,13 @@ __global__ __launch_bounds__(256) void k_shared_join(SharedArgs A) {
 
 template <typename T, int DP>
 void sh_launch(const SharedArgs& A, int blocks, hipStream_t s) {
+  const dim3 threads(256);
   if (A.page_size % 16)
-    hipLaunchKernelGGL((k_shared_attention<T, DP, false, false>), dim3(blocks), dim3(256), 0, s, A);
+    hipLaunchKernelGGL((k_shared_attention<T, DP, false, false>), dim3(blocks), threads, 0, s, A);
   else if (A.head_dim == DP)
-    hipLaunchKernelGGL((k_shared_attention<T, DP, true, true>), dim3(blocks), dim3(256), 0, s, A);
+    hipLaunchKernelGGL((k_shared_attention<T, DP, true, true>), dim3(blocks), threads, 0, s, A);
   else
-    hipLaunchKernelGGL((k_shared_attention<T, DP, true, false>), dim3(blocks), dim3(256), 0, s, A);
+    hipLaunchKernelGGL((k_shared_attention<T, DP, true, false>), dim3(blocks), threads, 0, s, A);
   const int64_t pairs = (int64_t)A.n_rows * A.n_kv * A.heads, each = 256 / (DP / 4);
   hipLaunchKernelGGL((k_shared_join<T, DP>), dim3((unsigned)((pairs + each - 1) / each)), dim3(256), 0, s, A);
 }
@@ -928,24 +1027,36 @@ void sh_dim(const SharedArgs& A, int dp, int blocks, hipStream_t s) {
 
 // What a call of these sizes needs.
 struct ShSizes {
-  int es, dp, group, cols, together, q_tiles, own_cols, blocks;
-  int64_t tiles;                  // (group, key head, tile)s at most
-  int64_t rows, seeds, own, bytes;  // places in the workspace, and its bytes
+  int es, dp, group, cols, cw, pw, gang, together, q_tiles, own_cols, blocks, waves;
+  int64_t tiles;                  // (group, key head, wide tile)s at most
+  int64_t plan, rows, seeds, own, bytes;  // places in the workspace, and its bytes
 };
-ShSizes sh_sizes(int dtype, int head_dim, int n_heads, int n_kv, bool runs, int64_t n_rows, int64_t n_groups, int units) {
+ShSizes sh_sizes(int dtype, int head_dim, int page_size, int n_heads, int n_kv, bool runs, int64_t n_rows, int64_t n_groups,
+                 int units) {
   const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   ShSizes z;
   z.es = dtype == SCUTE_F32 ? 4 : 2, z.dp = att_dim(head_dim), z.group = n_heads / n_kv;
-  z.cols = z.dp * z.es >= 1024 ? 64 : 128;
+  z.waves = 4;
+  // waves side by side: as many as the columns of a group of the mean size fill,
+  // half of them at least; then as many work-groups as it has tiles, up to 4
+  const int64_t mean = n_groups > 0 ? n_rows * z.group / n_groups : 0;
+  const int wave_cols = z.dp * z.es >= 1024 ? 16 : 32;
+  z.cw = z.waves;
+  if (page_size % 16 == 0)
+    while (z.cw > 2 && z.cw / 2 * wave_cols >= mean) z.cw /= 2;
+  z.pw = z.waves / z.cw, z.cols = wave_cols * z.cw;
+  z.gang = mean > 2 * z.cols ? 4 : mean > z.cols ? 2 : 1;
   z.together = runs && z.group <= 8 ? std::min(4, 16 / z.group) : 1;
   z.q_tiles = (z.group + 15) / 16;
   z.own_cols = z.together > 1 ? z.together * z.group : std::min(16, z.group);
   z.blocks = z.dp <= 128 ? 2 * units : units;  // (as many as are resident at once)
-  z.tiles = n_kv * (n_rows * z.group / z.cols + n_groups);
-  z.rows = 256;  // (the plan's)
+  z.tiles = n_kv * (n_rows * z.group / (z.cols * z.gang) + n_groups);
+  // paged attention's workspace, for calls that share nothing; the same for all calls
+  z.plan = up(att_workspace(units, head_dim));
+  z.rows = z.plan + 256;
   z.seeds = z.rows + up(n_rows * sizeof(ShRow));
-  z.own = z.seeds + (z.blocks + z.tiles) * z.cols * (z.dp + 4) * 4;
-  z.bytes = z.own + (4 * z.blocks + n_rows * n_kv * z.q_tiles) * z.own_cols * (z.dp + 4) * 4;
+  z.own = z.seeds + (z.blocks + z.tiles * z.gang) * z.waves * wave_cols * (z.dp + 4) * 4;
+  z.bytes = z.own + (SH_CHUNKS * z.waves * z.blocks + n_rows * n_kv * z.q_tiles) * z.own_cols * (z.dp + 4) * 4;
   return z;
 }
 
@@ -968,8 +1079,15 @@ extern "C" scute_status scute_shared_attention_workspace(int32_t device, int32_t
     return bad(SCUTE_E_SHAPE, "max_rows must be in [0, 2^20] and max_groups in [0, 65536]");
   const int units = device_units(device);
   if (units < 0) return bad(SCUTE_E_INVALID, "no such HIP device");
-  *bytes = std::max(sh_sizes(dtype, head_dim, n_heads, n_kv_heads, false, max_rows, max_groups, units).bytes,
-                    sh_sizes(dtype, head_dim, n_heads, n_kv_heads, true, max_rows, max_groups, units).bytes);
+  // (room for calls of fewer rows or groups too, whose waves stand in other ways:
+  // a tile and its gang's and turns' take 4 work-groups' columns at most)
+  *bytes = 0;
+  for (const bool runs : {false, true}) {
+    const ShSizes z = sh_sizes(dtype, head_dim, 16, n_heads, n_kv_heads, runs, max_rows, max_groups, units);
+    const int64_t wave_cols = z.cols / z.cw, all = z.waves * wave_cols;
+    const int64_t tiles = (int64_t)n_kv_heads * ((int64_t)max_rows * z.group / (2 * wave_cols) + 4ll * max_groups);
+    *bytes = std::max(*bytes, z.bytes + (tiles - z.tiles * z.gang) * all * (z.dp + 4) * 4);
+  }
   return SCUTE_OK;
 }
 
@@ -979,12 +1097,14 @@ extern "C" scute_status scute_shared_attention(const scute_kv_cache* C, const vo
                                                const int32_t* req, int32_t n_rows, const int32_t* group,
                                                const int32_t* shared_len, int32_t n_groups, float scale, void* out,
                                                int64_t out_stride, void* workspace, int64_t workspace_bytes,
-                                               void* stream) {
+                                               uint32_t flags, void* stream) {
   const char* fn = "scute_shared_attention";
   const auto bad = [&](scute_status code, const char* what) { return fail(code, std::string(fn) + ": " + what); };
-  const scute_status st = att_check(fn, AttCall{C, q, q_stride, n_heads, table, table_stride, n_requests, table_width, len,
-                                                req, n_rows, scale, 0, 0, out, out_stride, workspace, workspace_bytes});
+  const AttCall call{C, q, q_stride, n_heads, table, table_stride, n_requests, table_width, len, req, n_rows, scale,
+                     0, 0, out, out_stride, workspace, workspace_bytes};
+  const scute_status st = att_check(fn, call);
   if (st != SCUTE_OK) return st;
+  if (flags & ~(uint32_t)SCUTE_SHARED_ALWAYS) return bad(SCUTE_E_INVALID, "unknown flag");
   if (n_groups < 0 || n_groups > 65536) return bad(SCUTE_E_SHAPE, "n_groups must be in [0, 65536]");
   if (n_rows == 0) return SCUTE_OK;
   if (n_groups > 0 && (!group || !shared_len)) return bad(SCUTE_E_INVALID, "null pointer");
@@ -993,9 +1113,17 @@ extern "C" scute_status scute_shared_attention(const scute_kv_cache* C, const vo
   if (!g.ok()) return hip_fail(g.err, fn);
   const int units = device_units(C->device);
   if (units < 0) return bad(SCUTE_E_INVALID, "no such HIP device");
-  const ShSizes z = sh_sizes(C->dtype, C->head_dim, n_heads, C->n_kv_heads, req != nullptr, n_rows, n_groups, units);
+  const ShSizes z = sh_sizes(C->dtype, C->head_dim, C->page_size, n_heads, C->n_kv_heads, req != nullptr, n_rows, n_groups, units);
   if (workspace_bytes < z.bytes) return bad(SCUTE_E_INVALID, "the workspace is too small");
   const int64_t reach = std::min<int64_t>((int64_t)table_width * C->page_size, (int64_t)1 << 29);
+  // Sharing has more to do before and after than paged attention of few rows, whose
+  // reads it saves. Where it cannot save as much, at the table's whole width, the rows
+  // are read for one by one (captured calls, shared and one by one: 4 rows behind 8000
+  // positions, 97 MB, 51 and 29 us; 32 behind 1000, 130 MB, 44 and 21; 4 behind 32000,
+  // 390 MB, 74 and 80).
+  const int64_t saved = std::max<int64_t>(0, (int64_t)n_rows - n_groups) * reach * 2 * C->n_kv_heads * C->head_dim * z.es;
+  if (!(flags & SCUTE_SHARED_ALWAYS) && (n_groups == 0 || saved < SH_SAVED))
+    return att_run(fn, call, ATT_PLAIN, (hipStream_t)stream);
   // (units and tiles are counted in 31 bits)
   const int64_t stage = z.es == 4 ? 16 : 32, most = ((int64_t)1 << 31) - 1;
   if (z.tiles >= SH_TILES || z.tiles * (reach / stage + 1) > most ||
@@ -1005,10 +1133,10 @@ extern "C" scute_status scute_shared_attention(const scute_kv_cache* C, const vo
   int shift = 0;
   while ((1 << shift) < C->page_size) ++shift;
   const uint64_t mul = (((uint64_t)1 << (31 + shift)) + C->page_size - 1) / C->page_size;
-  const SharedArgs A{q, C->k, C->v, out, table, len, req, group, shared_len, (ShRow*)(ws + z.rows), (ShPlan*)ws,
+  const SharedArgs A{q, C->k, C->v, out, table, len, req, group, shared_len, (ShRow*)(ws + z.rows), (ShPlan*)(ws + z.plan),
                      (float*)(ws + z.seeds), (float*)(ws + z.own), q_stride, out_stride, C->page_stride, C->token_stride,
                      C->head_stride, table_stride, C->n_pages, (uint32_t)mul, n_rows, n_groups, C->n_kv_heads, z.group,
-                     C->head_dim, C->page_size, shift, (int32_t)reach, n_requests, (int32_t)z.tiles, z.together, z.q_tiles,
+                     C->head_dim, C->page_size, shift, (int32_t)reach, n_requests, (int32_t)z.tiles, z.cw, z.pw, z.gang, z.together, z.q_tiles,
                      z.own_cols, scale < 0.f, std::max(fabsf(scale * 1.4426950408889634f), 1e-37f)};
   const hipStream_t s = (hipStream_t)stream;
   if (z.es == 4) sh_dim<float>(A, z.dp, z.blocks, s);

@@ -119,6 +119,9 @@ class NormDesc(C.Structure):
 NORM_RMS, NORM_LAYER = 0, 1
 
 
+SHARED_ALWAYS = 1
+
+
 class HeadNormDesc(C.Structure):
     """scute_head_norm"""
     _fields_ = [("kind", C.c_int32), ("eps", C.c_float), ("q_w", C.c_void_p), ("q_b", C.c_void_p),
@@ -175,7 +178,7 @@ SIGNATURES = {
     "scute_shared_attention_workspace": (C.c_int32, [C.c_int32] * 7 + [C.POINTER(C.c_int64)]),
     "scute_shared_attention": (C.c_int32, [C.POINTER(KVCacheDesc), _P, C.c_int64, C.c_int32, _P, C.c_int64,
                                            C.c_int32, C.c_int32, _P, _P, C.c_int32, _P, _P, C.c_int32,
-                                           C.c_float, _P, C.c_int64, _P, C.c_int64, _P]),
+                                           C.c_float, _P, C.c_int64, _P, C.c_int64, C.c_uint32, _P]),
     "scute_residual_norm": (C.c_int32, [C.POINTER(NormDesc), _P, C.c_int32, C.c_int64, _P, C.c_int32,
                                         C.c_int64, _P, C.c_int64, _P, C.c_int64, _P, C.c_int32,
                                         C.c_int64, C.c_int32, _P]),
@@ -380,11 +383,11 @@ def scute_shared_attention_workspace(device: int, dtype: int, head_dim: int, n_h
 
 def scute_shared_attention(cache: KVCacheDesc, q, q_stride, n_heads, table, table_stride, n_requests, table_width,
                            len, req, n_rows, group, shared_len, n_groups, scale, out, out_stride, workspace,
-                           workspace_bytes, stream=None) -> None:
+                           workspace_bytes, flags=0, stream=None) -> None:
     _check(lib.scute_shared_attention(cache, _ptr(q), q_stride, n_heads, _ptr(table), table_stride, n_requests,
                                       table_width, _ptr(len), _ptr(req), n_rows, _ptr(group), _ptr(shared_len),
                                       n_groups, scale, _ptr(out), out_stride, _ptr(workspace), workspace_bytes,
-                                      _stream_ptr(stream)))
+                                      flags, _stream_ptr(stream)))
 
 
 def scute_residual_norm(norm: NormDesc, y, y_dtype, y_stride, h, h_dtype, h_stride, gate, gate_stride,

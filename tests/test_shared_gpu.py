@@ -57,8 +57,9 @@ def make(seed, groups, ps, Hq, Hk, D, dt, by_head=False, outside=0, suffix=40):
     return kc, vc, table, q, lens
 
 
-def run(kc, vc, table, q, lens, offsets, shared, req=None, scale=None, again=True):
-    att = block.SharedAttention(block.KVCache(kc, vc), q.shape[1], q.shape[0], max(1, len(shared)), scale=scale)
+def run(kc, vc, table, q, lens, offsets, shared, req=None, scale=None, again=True, always=True):
+    att = block.SharedAttention(block.KVCache(kc, vc), q.shape[1], q.shape[0], max(1, len(shared)), scale=scale,
+                                always=always)
     buf = torch.full((q.shape[0] + 1, q.shape[1], q.shape[2]), 55.0, dtype=q.dtype, device=DEV)
     tab, rl = _int(table), _int(lens)
     rr = None if req is None else _int(req)
@@ -193,7 +194,7 @@ def test_offsets_that_do_not_ascend_stay_in_bounds(offsets):
     """What such rows give is not said; nothing else is written, and the next
     call is right."""
     kc, vc, table, q, lens = make(6, [(12, 400)], 8, 8, 2, 64, BF16)
-    att = block.SharedAttention(block.KVCache(kc, vc), 8, 12, 5)
+    att = block.SharedAttention(block.KVCache(kc, vc), 8, 12, 5, always=True)
     n = att.workspace.shape[0]
     wide = torch.full((n + (1 << 20),), 77, dtype=torch.uint8, device=DEV)
     wide[:n] = 0
@@ -218,7 +219,7 @@ def test_captured_steps():
     rng = np.random.default_rng(1)
     free = np.setdiff1d(np.arange(kc.shape[0]), table)
     table[:, 20:] = rng.choice(free, size=table[:, 20:].shape)
-    att = block.SharedAttention(block.KVCache(kc, vc), 8, N, 3)
+    att = block.SharedAttention(block.KVCache(kc, vc), 8, N, 3, always=True)
     tab, lens, offs, shared = _int(table), _int(np.zeros(N)), _int([0] * 4), _int([0] * 3)
     out, s, g = torch.empty_like(q), torch.cuda.Stream(), torch.cuda.CUDAGraph()
     with torch.cuda.graph(g, stream=s):
@@ -242,6 +243,31 @@ def test_without_groups_nothing_is_shared():
     kc, vc, table, q, lens = make(8, [(5, 96)], 16, 8, 2, 64, BF16)
     outs = [run(kc, vc, table, q, lens, offs, shared) for offs, shared in (([0], []), ([0, 5], [0]), ([0, 5], [-7]), ([2, 2], [96]))]
     assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+def test_calls_that_share_little():
+    """Without `always` the rows are read one by one: paged attention's bits. Calls
+    of both kinds may follow each other with one workspace."""
+    kc, vc, table, q, lens = make(9, [(30, 160)], 16, 8, 2, 64, BF16)
+    paged = block.PagedAttention(block.KVCache(kc, vc), 8).forward(q, _int(table), _int(lens), torch.empty_like(q))
+    assert torch.equal(run(kc, vc, table, q, lens, [0, 30], [160], always=False), paged)
+    att = block.SharedAttention(block.KVCache(kc, vc), 8, 30, 1)
+    outs = []
+    for flags in (0, 1, 0, 1, 1, 0):
+        att.flags = flags
+        outs.append(att.forward(q, _int(table), _int(lens), _int([0, 30]), _int([160]), torch.empty_like(q)))
+    assert torch.equal(outs[2], paged) and torch.equal(outs[5], paged)
+    assert torch.equal(outs[1], outs[3]) and torch.equal(outs[1], outs[4])
+
+
+def test_a_table_wide_enough_shares():
+    """The rule itself takes the shared path: a wide table, 60 rows past one a group."""
+    kc, vc, table, q, lens = make(10, [(61, 480)], 16, 8, 2, 64, BF16)
+    wide = np.full((61, 560), -1)
+    wide[:, :table.shape[1]] = table
+    assert 60 * 560 * 16 * 2 * 2 * 64 * 2 > 256 << 20
+    shares = run(kc, vc, wide, q, lens, [0, 61], [480], always=False)
+    assert torch.equal(shares, run(kc, vc, wide, q, lens, [0, 61], [480]))
 
 
 def test_refusals():

@@ -13,13 +13,13 @@ from test_block_host import BAD_CACHES, FAKE, _cache  # noqa: E402
 def _attend(cache=None, **kw):
     d = dict(q=FAKE, q_stride=512, n_heads=8, table=FAKE, table_stride=8, n_requests=5, table_width=8, len=FAKE,
              req=None, n_rows=5, group=FAKE, shared_len=FAKE, n_groups=2, scale=0.125, out=FAKE + (1 << 14),
-             out_stride=512, workspace=FAKE, workspace_bytes=1 << 30)
+             out_stride=512, workspace=FAKE, workspace_bytes=1 << 30, flags=0)
     d.update(kw)
     scute.scute_shared_attention(_cache(**(cache or {})), *d.values(), 0)
 
 
 @pytest.mark.parametrize("kw, code", [
-    (dict(n_groups=-1), scute.E_SHAPE), (dict(n_groups=65537), scute.E_SHAPE), (dict(group=None), scute.E_INVALID),
+    (dict(flags=2), scute.E_INVALID), (dict(n_groups=-1), scute.E_SHAPE), (dict(n_groups=65537), scute.E_SHAPE), (dict(group=None), scute.E_INVALID),
     (dict(shared_len=None), scute.E_INVALID), (dict(group=FAKE + 1), scute.E_INVALID), (dict(shared_len=FAKE + 2), scute.E_INVALID),
     (dict(n_heads=7), scute.E_SHAPE), (dict(n_rows=6), scute.E_SHAPE), (dict(n_rows=-1), scute.E_SHAPE),
     (dict(table_width=0), scute.E_SHAPE), (dict(table_stride=7), scute.E_SHAPE), (dict(scale=math.inf), scute.E_INVALID),
