@@ -297,56 +297,98 @@ __global__ __launch_bounds__(256) void k_cache_copy(MoveArgs A, int n_copies) {
 }
 
 // A wave moves one request's column of LP 16-byte pieces of one head of K or of
-// V, 64 positions at a time: a position only moves down, so what a later trip
-// reads is not what an earlier one writes, and a trip's loads are waited for
-// before its stores.
+// V, 16 loads a trip. A position only moves down, so what a later trip reads is
+// not what an earlier one writes: a trip's loads are asked for before the last
+// one's stores, which wait for all of their own trip's loads. Which positions move
+// is known three trips ahead, their pages two.
 template <int LP>
-__global__ __launch_bounds__(256) void k_cache_compact(MoveArgs A) {
-  constexpr int ROWS = 64 / LP, U = LP;  // positions of a load, loads of 64 positions
-  const int lane = threadIdx.x & 63, cols = (A.pieces + LP - 1) / LP;
+__global__ __launch_bounds__(64) void k_cache_compact(MoveArgs A) {
+  constexpr int U = 16, ROWS = 64 / LP, TRIP = U * ROWS, PL = TRIP / 64;  // positions of a load, of a trip, of a trip a lane
+  const int lane = threadIdx.x, cols = (A.pieces + LP - 1) / LP;
   const int64_t per = 2ll * A.n_heads * cols, units = per * A.n_requests;
-  for (int64_t unit = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); unit < units; unit += (int64_t)gridDim.x * 4) {
+  for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
     const int r = (int)(unit / per);
     const int x = (int)(unit - r * per), col = x % cols, h = x / cols % A.n_heads;
     char* base = (x / cols < A.n_heads ? A.k : A.v) + h * A.head_stride;
     const int piece = col * LP + lane % LP;
+    const bool mine = piece < A.pieces;
+    base += 16 * (mine ? piece : 0);
     const uint32_t a = (uint32_t)max(ldg(A.start + r), 0);
     const int n = min(max(ldg(A.n_kept + r), 0), A.kept_width);
     if (A.new_len && x == 0 && lane == 0) A.new_len[r] = (int32_t)min(a + (uint32_t)n, 1u << 30);
     const int32_t *tab = A.table + r * A.table_stride, *kept = A.kept + r * A.kept_stride;
-    const auto place = [&](uint32_t t) -> int64_t {  // of a position, -1: none
-      if (t >= (uint32_t)A.reach) return -1;
-      const uint32_t c = (uint32_t)(((uint64_t)t * A.mul) >> (31 + A.shift));
-      const int p = ldg(tab + c);
-      return p >= 0 && p < A.n_pages ? p * A.page_stride + (int64_t)(t - c * A.page_size) * A.token_stride : -1;
+    const auto column = [&](uint32_t t) { return (uint32_t)(((uint64_t)t * A.mul) >> (31 + A.shift)); };
+    struct Moves {  // of a trip, PL positions a lane: where from (-1: it stays), and the two pages
+      int32_t from[PL], page_from[PL], page_to[PL];
     };
-    for (int j0 = 0; j0 < n; j0 += 64) {
-      // places of 64 positions, one a lane
-      int64_t from = -1, to = -1;
-      if (j0 + lane < n) {
-        const int s = ldg(kept + j0 + lane);
-        const uint32_t d = a + j0 + lane;
-        if (s >= 0 && (uint32_t)s > d) from = place(s), to = place(d);
+    const auto listed = [&](int i, Moves& m) {
+#pragma unroll
+      for (int k = 0; k < PL; ++k) {
+        const int j = i * TRIP + 64 * k + lane;
+        m.from[k] = ldg(kept + min(j, n - 1));
+        if (j >= n) m.from[k] = -1;
       }
-      const int go = from >= 0 && to >= 0;
-      if (!__any(go)) continue;
-      u32x4 v[U];
-  #pragma unroll
+    };
+    const auto look_up = [&](int i, Moves& m) {
+#pragma unroll
+      for (int k = 0; k < PL; ++k) {
+        const uint32_t to = a + (uint32_t)(i * TRIP + 64 * k + lane);
+        const bool moves = m.from[k] >= 0 && (uint32_t)m.from[k] > to && m.from[k] < A.reach;  // (so `to` is in reach too)
+        if (!moves) m.from[k] = -1;
+        m.page_from[k] = ldg(tab + (moves ? column((uint32_t)m.from[k]) : 0));
+        m.page_to[k] = ldg(tab + (moves ? column(to) : 0));
+      }
+    };
+    const int trips = (n + TRIP - 1) / TRIP;
+    if (trips == 0) continue;
+    Moves m0, m1, m2;  // of this trip, and the next two
+    listed(0, m0);
+    listed(1, m1);
+    look_up(0, m0);
+    u32x4 old[U];
+    int64_t old_to[PL];
+#pragma unroll
+    for (int k = 0; k < PL; ++k) old_to[k] = -1;
+    const auto store = [&]() {
+#pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int src = u * ROWS + lane / LP;
-        const int64_t f = __shfl(from, src, 64);
-        if (__shfl(go, src, 64) && piece < A.pieces) v[u] = ld_piece(base + f + 16 * piece);
+        const int64_t t = __shfl(old_to[u * ROWS / 64], u * ROWS % 64 + lane / LP, 64);
+        if (t >= 0 && mine) st_piece(base + t, old[u]);
       }
-      wait_vm_all();
-  #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int src = u * ROWS + lane / LP;
-        const int64_t t = __shfl(to, src, 64);
-        if (__shfl(go, src, 64) && piece < A.pieces) st_piece(base + t + 16 * piece, v[u]);
+    };
+    for (int i = 0; i < trips; ++i) {
+      listed(i + 2, m2);
+      look_up(i + 1, m1);
+      int64_t from[PL], to[PL];
+#pragma unroll
+      for (int k = 0; k < PL; ++k) {
+        const uint32_t s = (uint32_t)m0.from[k], d = a + (uint32_t)(i * TRIP + 64 * k + lane);
+        const bool go = m0.from[k] >= 0 && (uint32_t)m0.page_from[k] < (uint64_t)A.n_pages && (uint32_t)m0.page_to[k] < (uint64_t)A.n_pages;
+        from[k] = go ? m0.page_from[k] * A.page_stride + (int64_t)(s - column(s) * A.page_size) * A.token_stride : 0;
+        to[k] = go ? m0.page_to[k] * A.page_stride + (int64_t)(d - column(d) * A.page_size) * A.token_stride : -1;
       }
+      u32x4 v[U];  // (of a position that stays: some other, so that the loads can be counted)
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[u] = ld_piece(base + __shfl(from[u * ROWS / 64], u * ROWS % 64 + lane / LP, 64));
+      // the last trip's loads are done when these 16 are the only operations out
+      asm volatile("s_waitcnt vmcnt(16)" ::: "memory");
+      store();
+#pragma unroll
+      for (int u = 0; u < U; ++u) old[u] = v[u];
+#pragma unroll
+      for (int k = 0; k < PL; ++k) old_to[k] = to[k];
+      m0 = m1, m1 = m2;
     }
+    wait_vm_all();
+    store();
   }
 }
+
+// Waves from which on a compaction's columns are 256 bytes; with fewer they are
+// 128 (a line of the L2): 256 waves of 256 bytes, half of 16 x 16000 positions,
+// 265 us, 512 of 128 190, 1024 of 64 240; 1024 waves of 256, trees of 24 tokens of 64
+// requests, 5.2 us, of 128 6.8. (Bound by the memory: 787 MB, 4.1 TB/s.)
+constexpr int64_t COMPACT_WAVES = 1024;
 
 struct Parts {
   int64_t first, whole, before, need, need_sum, free_sum, bytes;
@@ -525,7 +567,12 @@ extern "C" scute_status scute_cache_compact(const scute_kv_cache* C, const int32
   A.new_len = new_len, A.n_requests = n_requests;
   A.reach = (int32_t)std::min<int64_t>((int64_t)table_width * C->page_size, (int64_t)1 << 30);
   division(C->page_size, A.mul, A.shift);
-  const int64_t waves = 2 * R * A.n_heads * ((A.pieces + 15) / 16), most = 1 << 20;
-  hipLaunchKernelGGL(k_cache_compact<16>, dim3((unsigned)std::min(most, (waves + 3) / 4)), dim3(256), 0, (hipStream_t)stream, A);
+  const int64_t columns = 2 * R * A.n_heads, most = 1 << 22;
+  const hipStream_t s = (hipStream_t)stream;
+  const auto blocks = [&](int lp) { return dim3((unsigned)std::min(most, columns * ((A.pieces + lp - 1) / lp))); };
+  if (columns * ((A.pieces + 15) / 16) >= COMPACT_WAVES)
+    hipLaunchKernelGGL(k_cache_compact<16>, blocks(16), dim3(64), 0, s, A);
+  else
+    hipLaunchKernelGGL(k_cache_compact<8>, blocks(8), dim3(64), 0, s, A);
   return done(fn);
 }
