@@ -415,9 +415,16 @@ struct HeadNormArgs {
   RotArgs r;
   const float *q_w, *q_b, *k_w, *k_b;
   int64_t q_stride, k_stride;  // of the weights' heads
+  int64_t n_tokens;
   int32_t layer;
   float eps, inv_d;
 };
+
+// tokens of a work-group of the norms, from how many on
+// (8191 tokens of 40 heads of 128, a weight a head: one 77 us, two 69, four 73,
+// eight 66; the same weights for all heads: 62, 59, 65, 62; 4096 tokens of these:
+// 38, 38, 36, 49; up to 2048 tokens they are equal)
+constexpr int HEAD_BLOCK = 2, HEAD_TOKENS = 4096;
 
 // sum over groups of LP lanes, in each of them
 template <int LP>
@@ -434,137 +441,146 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 
 // A head's rotation needs its norm, and its norm the whole head: LP lanes hold a
-// head (N units each, a unit as in k_rotary_store: V pairs of the halves, V / 2
-// adjacent pairs, or V elements that are not rotated), so q, k and v are read
-// once and written once and nothing but two sums crosses lanes. A work-group's
-// groups of lanes take a token's heads in turn, q's, k's, then v's.
-template <typename S, typename D, int V, int LP, int N>
+// head, each N times 2 V elements that are V pairs where they are rotated (V of
+// each half, or 2 V adjacent ones), so q, k and v are read once and written once
+// and nothing but two sums crosses lanes. A work-group's groups of lanes take the
+// heads in turn, q's, k's, then v's, each for TB tokens, so that a head's weights
+// are read once for them. All lanes of a head of 64 or 128 elements are busy,
+// whatever part of it is rotated: with a unit of V elements where it is not, half
+// of them idle, 8191 tokens with 64 of 128 rotated took 94 us, so 61, which is
+// what their 302 MB take at a copy's rate.
+template <typename S, typename D, int V, int LP, int N, int TB>
 __global__ __launch_bounds__(256) void k_norm_rotary_store(HeadNormArgs G) {
   const RotArgs& A = G.r;
-  __shared__ float cs[128], sn[128];
-  const int64_t t = blockIdx.x;
-  const int n = A.n_pairs, hd = A.head_dim, rd = 2 * n, tid = threadIdx.x, lane = tid % LP;
-  const int64_t slot = A.slot[t];
-  const bool store = slot >= 0 && slot < A.n_slots;
-  int64_t crow = 0;
-  if (store) {
-    const int64_t page = slot / A.page_size;
-    crow = page * A.page_stride + (slot - page * A.page_size) * A.token_stride;
-  }
-  const bool joined = V == 4 && A.interleaved;  // a unit's pairs lie side by side
-  const int ur = joined ? rd / V : n / V, per = ur + (hd - rd) / V;
+  __shared__ float cs[TB][128], sn[TB][128];
+  __shared__ int64_t s_row[TB];  // where the token lies in the cache, -1: nowhere
+  const int64_t t0 = (int64_t)blockIdx.x * TB;
+  const int nt = TB == 1 ? 1 : (int)min((int64_t)TB, G.n_tokens - t0);
+  const int n = A.n_pairs, hd = A.head_dim, per = hd / (2 * V), tid = threadIdx.x, lane = tid % LP;
   const int nq = A.n_heads, nk = nq + A.n_kv_heads, all = nk + A.n_kv_heads;
-  // elements of unit u: V from e0 on and, where it is rotated in halves (or one
-  // pair), V from e1 on
-  const auto two = [&](int u) { return u < ur && !joined; };
-  const auto e0 = [&](int u) { return u >= ur ? rd + (u - ur) * V : A.interleaved && V == 1 ? 2 * u : V * u; };
-  const auto e1 = [&](int u) { return A.interleaved ? 2 * u + 1 : n + V * u; };
-  const auto load = [&](int h, float (&a)[N][V], float (&b)[N][V]) {
+  // unit u holds V elements from e0 on, V from e1 on, and pairs V u .. V u + V - 1
+  const bool halves = !A.interleaved;
+  const auto e0 = [&](int u) { return halves && V * u < n ? V * u : 2 * V * u; };
+  const auto e1 = [&](int u) { return halves && V * u < n ? V * u + n : 2 * V * u + V; };
+  const auto load = [&](int h, int i, float (&a)[N][V], float (&b)[N][V]) {
     const void* src = h < nq ? A.q : A.k;
-    const int64_t at = h < nq ? t * A.q_stride + (int64_t)h * hd : t * A.k_stride + (int64_t)(h - nq) * hd;
+    const int64_t t = t0 + i, at = h < nq ? t * A.q_stride + (int64_t)h * hd : t * A.k_stride + (int64_t)(h - nq) * hd;
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int u = lane + k * LP;
 #pragma unroll
-      for (int i = 0; i < V; ++i) a[k][i] = b[k][i] = 0.f;
+      for (int j = 0; j < V; ++j) a[k][j] = b[k][j] = 0.f;
       if (h < nk && u < per) {
         ld_vec<S, V, true>(src, at + e0(u), a[k]);
-        if (two(u)) ld_vec<S, V, true>(src, at + e1(u), b[k]);
+        ld_vec<S, V, true>(src, at + e1(u), b[k]);
       }
     }
   };
   const int step = gridDim.y * (256 / LP);
   int h = blockIdx.y * (256 / LP) + tid / LP;
   float a[N][V], b[N][V];
-  load(h, a, b);
-  for (int i = tid; i < n; i += 256) {
-    const int ax = A.axis ? A.axis[i] : 0;
-    const int p = A.pos[(ax > 0 && ax < A.n_axes ? ax : 0) * A.pos_stride + t];
-    const double turns = (double)p * (A.freq[i] * 0.15915494309189533577);
+  load(h, 0, a, b);
+  if (tid < nt) {
+    const int64_t slot = A.slot[t0 + tid];
+    int64_t row = -1;
+    if (slot >= 0 && slot < A.n_slots) {
+      const int64_t page = slot / A.page_size;
+      row = page * A.page_stride + (slot - page * A.page_size) * A.token_stride;
+    }
+    s_row[tid] = row;
+  }
+  for (int i = tid; i < n * nt; i += 256) {
+    const int tt = TB == 1 ? 0 : i / n, p = i - tt * n;
+    const int ax = A.axis ? A.axis[p] : 0;
+    const int at = A.pos[(ax > 0 && ax < A.n_axes ? ax : 0) * A.pos_stride + t0 + tt];
+    const double turns = (double)at * (A.freq[p] * 0.15915494309189533577);
     float s, c;
     sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-    cs[i] = c;
-    sn[i] = s;
+    cs[tt][p] = c;
+    sn[tt][p] = s;
   }
   __syncthreads();
   for (; h < nk; h += step) {
-    // the next head's loads under this one's sums
-    float na[N][V], nb[N][V];
-    load(h + step, na, nb);
     const bool of_q = h < nq;
-    if (of_q || store) {
-      float mu = 0.f, s = 0.f;
-      if (G.layer) {
+    float wa[N][V], wb[N][V], ca[N][V], cb[N][V];  // weights and biases of the lane's elements
+    {
+      const float *w = of_q ? G.q_w : G.k_w, *c = of_q ? G.q_b : G.k_b;
+      const int64_t at = of_q ? h * G.q_stride : (h - nq) * G.k_stride;
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const int u = lane + k * LP;
+#pragma unroll
+        for (int j = 0; j < V; ++j) wa[k][j] = wb[k][j] = 1.f, ca[k][j] = cb[k][j] = 0.f;
+        if (u >= per) continue;
+        if (w) ld_vec<float, V>(w, at + e0(u), wa[k]), ld_vec<float, V>(w, at + e1(u), wb[k]);
+        if (c) ld_vec<float, V>(c, at + e0(u), ca[k]), ld_vec<float, V>(c, at + e1(u), cb[k]);
+      }
+    }
+    for (int i = 0; i < nt; ++i) {
+      // the next token's loads, or the next head's, under this one's sums
+      float na[N][V], nb[N][V];
+      const bool more = i + 1 < nt;
+      load(more ? h : h + step, more ? i + 1 : 0, na, nb);
+      const int64_t row = s_row[i];
+      if (of_q || row >= 0) {
+        float mu = 0.f, s = 0.f;
+        if (G.layer) {
+#pragma unroll
+          for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int j = 0; j < V; ++j) s += a[k][j] + b[k][j];
+          mu = lanes_sum<LP>(s) * G.inv_d;
+          s = 0.f;
+        }
 #pragma unroll
         for (int k = 0; k < N; ++k)
 #pragma unroll
-          for (int i = 0; i < V; ++i) s += a[k][i] + b[k][i];
-        mu = lanes_sum<LP>(s) * G.inv_d;
-        s = 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int u = lane + k * LP;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if (u < per) a[k][i] -= mu, s += a[k][i] * a[k][i];
-          if (u < per && two(u)) b[k][i] -= mu, s += b[k][i] * b[k][i];
-        }
-      }
-      const float r = rsqrtf(lanes_sum<LP>(s) * G.inv_d + G.eps);
-      const float *w = of_q ? G.q_w : G.k_w, *c = of_q ? G.q_b : G.k_b;
-      const int64_t wat = of_q ? h * G.q_stride : (h - nq) * G.k_stride;
-      void* dst = of_q ? A.q_out : A.kc;
-      const int64_t di = of_q ? t * A.q_out_stride + (int64_t)h * hd : crow + (h - nq) * A.head_stride;
-#pragma unroll
-      for (int k = 0; k < N; ++k) {
-        const int u = lane + k * LP;
-        if (u >= per) continue;
-        const auto scaled = [&](float (&x)[V], int e) {
-          float g[V], o[V];
-#pragma unroll
-          for (int i = 0; i < V; ++i) g[i] = 1.f, o[i] = 0.f;
-          if (w) ld_vec<float, V>(w, wat + e, g);
-          if (c) ld_vec<float, V>(c, wat + e, o);
-#pragma unroll
-          for (int i = 0; i < V; ++i) x[i] = x[i] * r * g[i] + o[i];
-        };
-        scaled(a[k], e0(u));
-        if (u >= ur) {
-          st_vec<D, V>(dst, di + e0(u), a[k]);
-        } else if (joined) {
-          if constexpr (V == 4) {
-            const float c0 = cs[2 * u], s0 = sn[2 * u], c1 = cs[2 * u + 1], s1 = sn[2 * u + 1];
-            const float o[4] = {a[k][0] * c0 - a[k][1] * s0, a[k][0] * s0 + a[k][1] * c0,
-                                a[k][2] * c1 - a[k][3] * s1, a[k][2] * s1 + a[k][3] * c1};
-            st_vec<D, V>(dst, di + 4 * u, o);
+          for (int j = 0; j < V; ++j) {
+            a[k][j] -= mu, b[k][j] -= mu;
+            if (lane + k * LP < per) s += a[k][j] * a[k][j] + b[k][j] * b[k][j];
           }
-        } else {
-          scaled(b[k], e1(u));
+        const float r = rsqrtf(lanes_sum<LP>(s) * G.inv_d + G.eps);
+        void* dst = of_q ? A.q_out : A.kc;
+        const int64_t di = of_q ? (t0 + i) * A.q_out_stride + (int64_t)h * hd : row + (h - nq) * A.head_stride;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const int u = lane + k * LP;
+          if (u >= per) continue;
           float x[V], y[V];
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const float cc = cs[V * u + i], ss = sn[V * u + i];
-            x[i] = a[k][i] * cc - b[k][i] * ss;
-            y[i] = a[k][i] * ss + b[k][i] * cc;
+          for (int j = 0; j < V; ++j) x[j] = a[k][j] * r * wa[k][j] + ca[k][j], y[j] = b[k][j] * r * wb[k][j] + cb[k][j];
+          const auto turn = [&](float& p, float& q, int j) {
+            if (V * u + j >= n) return;
+            const float c = cs[i][V * u + j], s = sn[i][V * u + j], p0 = p;
+            p = p0 * c - q * s;
+            q = p0 * s + q * c;
+          };
+          if (V == 1 || halves) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) turn(x[j], y[j], j);
+          } else if constexpr (V == 4) {
+            turn(x[0], x[1], 0), turn(x[2], x[3], 1), turn(y[0], y[1], 2), turn(y[2], y[3], 3);
           }
           st_vec<D, V>(dst, di + e0(u), x);
           st_vec<D, V>(dst, di + e1(u), y);
         }
       }
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) a[k][j] = na[k][j], b[k][j] = nb[k][j];
     }
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-#pragma unroll
-      for (int i = 0; i < V; ++i) a[k][i] = na[k][i], b[k][i] = nb[k][i];
   }
-  if (store)
-    for (; h < all; h += step)
+  for (; h < all; h += step)
+    for (int i = 0; i < nt; ++i) {
+      const int64_t row = s_row[i];
+      if (row < 0) continue;
       for (int e = lane * V; e < hd; e += LP * V) {
         float x[V];
-        ld_vec<S, V, true>(A.v, t * A.v_stride + (int64_t)(h - nk) * hd + e, x);
-        st_vec<D, V>(A.vc, crow + (h - nk) * A.head_stride + e, x);
+        ld_vec<S, V, true>(A.v, (t0 + i) * A.v_stride + (int64_t)(h - nk) * hd + e, x);
+        st_vec<D, V>(A.vc, row + (h - nk) * A.head_stride + e, x);
       }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -963,35 +979,44 @@ scute_status rotary_store(const char* fn, const scute_rotary* Ro, const scute_he
   const int64_t units = (n_heads + C->n_kv_heads) * per + C->n_kv_heads * (hd / V);
   // few tokens: their units spread over more work-groups, one unit a thread
   // (norms: one head a group of lanes)
-  const int lanes = !vec || per > 32 ? 64 : per > 16 ? 32 : per > 8 ? 16 : 8;
+  const int lanes = !vec ? 64 : hd > 128 ? 32 : hd > 64 ? 16 : 8;
   const int64_t rounds = norm ? ((int64_t)n_heads + 2 * C->n_kv_heads) * lanes : units;
   const int64_t parts = std::min<int64_t>(std::min<int64_t>((rounds + 255) / 256, 4096),
                                           std::max<int64_t>(1, 1024 / n_tokens));
   const hipStream_t s = (hipStream_t)stream;
-  for (int64_t t = 0; t < n_tokens; t += most_groups(256)) {
-    const dim3 grid((unsigned)std::min(most_groups(256), n_tokens - t), (unsigned)parts);
+  // many tokens: several a work-group
+  const bool block = norm && vec && n_tokens >= HEAD_TOKENS;
+  const int64_t most = most_groups(256) * (block ? HEAD_BLOCK : 1);
+  for (int64_t t = 0; t < n_tokens; t += most) {
+    const int64_t here = std::min<int64_t>(most, n_tokens - t);
+    const dim3 grid((unsigned)(block ? (here + HEAD_BLOCK - 1) / HEAD_BLOCK : here), (unsigned)parts);
     A.q = (const char*)q + t * q_stride * (int64_t)es;
     A.k = (const char*)k + t * k_stride * (int64_t)es;
     A.v = (const char*)v + t * v_stride * (int64_t)es;
     A.q_out = (char*)q_out + t * q_out_stride * (int64_t)ed;
     A.pos = pos ? pos + t : nullptr;
     A.slot = slot + t;
+#define NORMED(S, D, LP)                                                                       \
+  do {                                                                                         \
+    if (block)                                                                                 \
+      hipLaunchKernelGGL((k_norm_rotary_store<S, D, 4, LP, 1, HEAD_BLOCK>), grid, dim3(256), 0, s, H); \
+    else                                                                                       \
+      hipLaunchKernelGGL((k_norm_rotary_store<S, D, 4, LP, 1, 1>), grid, dim3(256), 0, s, H);  \
+  } while (0)
 #define ROT(S, D)                                                                              \
   do {                                                                                         \
     if (norm) {                                                                                \
       const HeadNormArgs H{A, norm->q_w, norm->q_b, norm->k_w, norm->k_b, norm->q_stride,      \
-                           norm->k_stride, norm->kind == SCUTE_NORM_LAYER, norm->eps,          \
+                           norm->k_stride, here, norm->kind == SCUTE_NORM_LAYER, norm->eps,    \
                            1.f / (float)hd};                                                   \
       if (!vec)                                                                                \
-        hipLaunchKernelGGL((k_norm_rotary_store<S, D, 1, 64, 4>), grid, dim3(256), 0, s, H);   \
+        hipLaunchKernelGGL((k_norm_rotary_store<S, D, 1, 64, 2, 1>), grid, dim3(256), 0, s, H); \
       else if (lanes == 8)                                                                     \
-        hipLaunchKernelGGL((k_norm_rotary_store<S, D, 4, 8, 1>), grid, dim3(256), 0, s, H);    \
+        NORMED(S, D, 8);                                                                       \
       else if (lanes == 16)                                                                    \
-        hipLaunchKernelGGL((k_norm_rotary_store<S, D, 4, 16, 1>), grid, dim3(256), 0, s, H);   \
-      else if (lanes == 32)                                                                    \
-        hipLaunchKernelGGL((k_norm_rotary_store<S, D, 4, 32, 1>), grid, dim3(256), 0, s, H);   \
+        NORMED(S, D, 16);                                                                      \
       else                                                                                     \
-        hipLaunchKernelGGL((k_norm_rotary_store<S, D, 4, 64, 1>), grid, dim3(256), 0, s, H);   \
+        NORMED(S, D, 32);                                                                      \
     } else if (vec) {                                                                          \
       hipLaunchKernelGGL((k_rotary_store<S, D, 4>), grid, dim3(256), 0, s, A);                 \
     } else {                                                                                   \
@@ -1007,6 +1032,7 @@ scute_status rotary_store(const char* fn, const scute_rotary* Ro, const scute_he
     else
       ROT(uint16_t, uint16_t);
 #undef ROT
+#undef NORMED
     const scute_status ls = launched(fn);
     if (ls != SCUTE_OK) return ls;
   }
