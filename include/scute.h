@@ -270,6 +270,8 @@ scute_status scute_batch_destroy(scute_batch* batch);
  * rotation output are rounded to the activation dtype once as MFMA
  * operands), so any input scale whose products and sums stay inside the
  * float32 range is served; there is no fixed-point stage.
+ * May be captured into a graph, and replayed between other forwards of the
+ * plan; a plan's workspaces serve one forward at a time.
  * Errors: SCUTE_E_STATE if the plan is stale or from another layer,
  * SCUTE_E_UNSUPPORTED on a host-only layer, SCUTE_E_INVALID for null or
  * misaligned pointers (16-byte alignment required). */

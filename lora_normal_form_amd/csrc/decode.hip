@@ -976,9 +976,15 @@ scute_status launch_decode(scute_layer* L, const scute_batch* B, const void* x, 
                            float* y, hipStream_t st, int32_t* launches) {
   const DecodePlan& D = B->dp;
   // the shrink sums of this forward and the buffer cleared for the next
+  const bool captured = in_capture(st, &D.captured);
+  if (captured) D.fwd = 0;
   float* acc = D.acc32[D.fwd & 1];
   float* acc_next = D.acc32[(D.fwd + 1) & 1];
   int nl = 0;
+  if (captured) {
+    clear_words(acc, D.acc_bytes / 4, nullptr, 0, st);
+    ++nl;
+  }
   if (D.route) {  // route variant: the rotation as a pass of its own
     scute_status rs = launch_route_rotate(L, B, x, st, &nl);
     if (rs != SCUTE_OK) return rs;

@@ -671,6 +671,12 @@ scute_status launch_fdecode(scute_layer* L, const scute_batch* B, const void* x,
                             float* y, hipStream_t st, int32_t* launches) {
   const FdPlan& P = B->fp;
   int nl = 0;
+  if (in_capture(st, &P.captured)) {
+    P.fwd = 0;
+    // (xdone lies behind xcnt)
+    clear_words(P.xcnt, (int64_t)((int32_t*)P.xdone - P.xcnt) + P.n_xb, P.cnt, (int64_t)P.C * P.MG * 4, st);
+    ++nl;
+  }
   if (P.n_rot_items > 0) {
     if (!B->delta || !P.rot) return fail(SCUTE_E_STATE, "fused decode: rotation tables missing");
     ProfScope ps(L, st, "fd_rotate");

@@ -355,6 +355,24 @@ static bool trace_on() {
   return on;
 }
 
+bool in_capture(hipStream_t st, bool* captured) {
+  hipStreamCaptureStatus now = hipStreamCaptureStatusNone;
+  if (!*captured && hipStreamIsCapturing(st, &now) == hipSuccess && now == hipStreamCaptureStatusActive)
+    *captured = true;
+  return *captured;
+}
+
+static __global__ void __launch_bounds__(256) k_clear_words(uint32_t* a, int64_t n_a, uint32_t* b, int64_t n_b) {
+  const int64_t step = (int64_t)gridDim.x * 256;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n_a + n_b; i += step) (i < n_a ? a[i] : b[i - n_a]) = 0;
+}
+
+void clear_words(void* a, int64_t n_a, void* b, int64_t n_b, hipStream_t st) {
+  const int64_t blocks = std::min<int64_t>((n_a + n_b + 255) / 256, 1024);
+  if (blocks > 0)
+    hipLaunchKernelGGL(k_clear_words, dim3((unsigned)blocks), dim3(256), 0, st, (uint32_t*)a, n_a, (uint32_t*)b, n_b);
+}
+
 static scute_status launch_path(scute_layer* L, const scute_batch* B, const void* x, const void* W, float* y,
                                 hipStream_t st, int32_t* launches) {
   if (B->fp.enabled) return launch_fdecode(L, B, x, W, y, st, launches);

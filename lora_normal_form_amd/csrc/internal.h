@@ -188,6 +188,7 @@ struct DecodePlan {
   // forwards launched with this plan; the shrink sums alternate between the
   // two acc32 buffers, and each forward's prologue clears the other one
   mutable uint32_t fwd = 0;
+  mutable bool captured = false;  // (in_capture)
   // route variant (SCUTE_PLAN_ROUTE_* bits; 0: everything fused)
   uint32_t route = 0;
   const FdRotItem* rot = nullptr;  // rotation pass items (ROTATE_PASS)
@@ -270,6 +271,7 @@ struct FdPlan {
   uint32_t wait_bias = 0;          // 1: the waits look for a forward that never comes (tests)
   uint32_t acc_bytes = 0, part_bytes = 0, xpart_bytes = 0;
   mutable uint32_t fwd = 0;        // forwards launched with this plan
+  mutable bool captured = false;   // (in_capture)
 };
 
 // Chunk of a prefill batch: the rows of one adapter segment (or of rows
@@ -413,6 +415,13 @@ int32_t forward_launch_count(const scute_layer* L, const scute_batch* B);
 // against 91 us at 11008; 256 LoRA rows: 95 against 83 us).
 constexpr int DECODE_DEFAULT = 2;
 constexpr int FUSED_MIN_GROUPS = 7;
+
+// Whether `st` is being captured, or `captured` says that this plan was: a graph
+// replays the forward with the numbers it was captured with, so from its first
+// capture on every forward of a plan clears its counts and sums itself
+// (clear_words, a launch) and counts as the first.
+bool in_capture(hipStream_t st, bool* captured);
+void clear_words(void* a, int64_t n_a, void* b, int64_t n_b, hipStream_t st);
 
 // decode path (decode.hip / plan.cpp)
 scute_status build_decode_plan(const scute_layer* L, scute_batch* B, hipStream_t st);
