@@ -303,12 +303,23 @@ class AttentionStep:
     none, ends or finds no page, empty (n is n_requests; more tokens are
     refused); the attention then streams the cache. freq (float64 [pairs]), axis, n_axes
     and interleaved as in block.Rotary; norm_in, norm_post, norm_out: float32
-    weights [d] (norm_post None: no norm on o)."""
+    weights [d] (norm_post None: no norm on o). head_norm: a block.HeadNorm of q's
+    and k's heads before they are rotated. window, sinks: as in block.PagedAttention.
+
+    groups > 0: rows whose contexts begin with the same pages read those
+    positions once (block.SharedAttention, without a window): `group`
+    [groups + 1] and `shared_len` [groups] say which, by row, zero at first and
+    to be written by the caller. forks: requests may go on from others, be cut
+    back or keep some of their positions (fork, keep_only); they then end by
+    fork, and a negative new_len is a request without tokens."""
+
+    head_norm = group = shared_len = None
+    forks = False
 
     def __init__(self, qkv, wl_out, n_heads, n_kv_heads, head_dim, n_requests, pages_per_request, page_size,
                  n_pages, freq, axis=None, n_axes=1, interleaved=False, norm_in=None, norm_post=None, norm_out=None,
                  kind="rms", eps=1e-5, h_scale=1.0, y_scale=1.0, window=0, one_each=False, device=0,
-                 tenants=None, like=None):
+                 tenants=None, like=None, head_norm=None, sinks=0, groups=0, forks=False):
         import torch
         from . import block
         from . import workload as glue
@@ -324,6 +335,10 @@ class AttentionStep:
         if like is not None and (like.cache.k.shape, like.table.shape, like.cache.dtype, like.cache.device) != (
                 shape, (n_requests, pages_per_request), dt, dev):
             raise ValueError("like: a step whose requests, pages, heads, type or device are others")
+        if like is not None and like.forks != bool(forks):
+            raise ValueError("like: requests end by fork in both steps or in none")
+        if groups and (window or sinks):
+            raise ValueError("groups: rows that share positions see all of theirs, without a window")
         if tenants is not None and (tenants.dtype != torch.int32 or tenants.shape != (2, n_requests)):
             raise ValueError("tenants must be int32 [2][n_requests]")
         self.qkv, self.out = qkv, glue.load(wl_out, device=device)
@@ -341,7 +356,18 @@ class AttentionStep:
             self.cache, self.table, self.ring, self.state = like.cache, like.table, like.ring, like.state
             self.rows.state.copy_(self.state)
         self.rotary = block.Rotary(freq, head_dim, axis=axis, n_axes=n_axes, interleaved=interleaved)
-        self.attention = block.PagedAttention(self.cache, n_heads, window=window)
+        self.head_norm, self.window, self.sinks = head_norm, window, sinks
+        if groups:
+            self.attention = block.SharedAttention(self.cache, n_heads, n, groups)
+            self.group = torch.zeros(groups + 1, dtype=torch.int32, device=dev)
+            self.shared_len = torch.zeros(groups, dtype=torch.int32, device=dev)
+        else:
+            self.attention = block.PagedAttention(self.cache, n_heads, window=window, sinks=sinks)
+        self.forks = bool(forks)
+        if forks:
+            self._fork = block.Fork(n_requests, pages_per_request, n_pages, dev)
+            self._new_len, self._keep = (torch.zeros(n_requests, dtype=torch.int32, device=dev) for _ in range(2))
+            self._same = torch.arange(n_requests, dtype=torch.int32, device=dev)
         self.norm_in = block.ResidualNorm(d, kind, pre_weight=norm_in, eps=eps, device=dev)
         self.norm_out = block.ResidualNorm(d, kind, post=norm_post is not None, post_weight=norm_post,
                                            pre_weight=norm_out, h_scale=h_scale, y_scale=y_scale, eps=eps, device=dev)
@@ -368,6 +394,9 @@ class AttentionStep:
         if plans is not None and [p.info()["n"] for p in plans] != 2 * [rows.max_tokens]:
             raise ValueError(f"plans must be two plans of {rows.max_tokens} rows")
         cursor, seq_len = block.split_state(self.state, rows.n_requests)
+        if self.forks:
+            block._vector(new_len, rows.n_requests, torch.int32, "new_len")
+            new_len = torch.clamp(new_len, min=0, out=self._new_len)
         block.assign_pages(seq_len, new_len, self.table, self.ring, cursor, self.cache.page_size, rows, stream=s,
                            fit_rows=True, one_each=self.one_each)
         qkv, out = self.qkv, self.out
@@ -380,14 +409,51 @@ class AttentionStep:
         self._layer(qkv, plans[0], ids[0], s)
         if pos is None:
             pos = rows.pos if self.rotary.n_axes == 1 else rows.pos.expand(self.rotary.n_axes, -1)
-        self.rotary.store(self.q, self.k, self.v, pos, rows.slot, self.cache, self.q_rot, stream=s)
-        self.attention.forward(self.q_rot, self.table, rows.len, self.a, row_req=None if self.one_each else rows.req,
-                               stream=s)
+        self.rotary.store(self.q, self.k, self.v, pos, rows.slot, self.cache, self.q_rot, stream=s,
+                          norm=self.head_norm)
+        req = None if self.one_each else rows.req
+        if self.group is None:
+            self.attention.forward(self.q_rot, self.table, rows.len, self.a, row_req=req, stream=s)
+        else:
+            self.attention.forward(self.q_rot, self.table, rows.len, self.group, self.shared_len, self.a, row_req=req,
+                                   stream=s)
         self._layer(out, plans[1], ids[1], s)
         self.norm_out.forward(out.y, h, h_out, x_out, gate=gate, stream=s)
         # (last, so that a call that was refused on its way may be made again)
         torch.add(rows.state, 0, out=self.state)
         return h_out, x_out
+
+    def fork(self, parent, keep=None, drop=False):
+        """Between two steps: request r goes on from the first keep[r] positions
+        (None: all) of request parent[r], as in block.fork_pages (outside the
+        requests: it ends). drop: pages that rows from here on do not see
+        through the window go back, so the request cannot be cut back past them
+        later. Returns the block.Fork that says what came of it."""
+        import torch
+        from . import block
+        if not self.forks:
+            raise ValueError("a step made without forks")
+        f, s = self._fork, block.current_stream(self.cache.index)
+        cursor, seq_len = block.split_state(self.state, self.rows.n_requests)
+        block.fork_pages(seq_len, parent, self.table, self.ring, cursor, self.cache.page_size, f, keep=keep,
+                         window=self.window if drop else 0, sinks=self.sinks if drop else 0, stream=s)
+        block.copy_pages(self.cache, f.src, f.dst, f.n, stream=s)
+        torch.add(f.table, 0, out=self.table)
+        torch.add(f.state, 0, out=self.state)
+        return f
+
+    def keep_only(self, start, kept, n_kept, drop=False):
+        """Between two steps: of its positions from start[r] on request r keeps
+        n_kept[r], those in kept[r] (ascending), moved together (block.compact: the
+        drafts that were accepted, a cache with positions evicted), and gives back
+        the pages behind. The pages from start[r] on must be the request's alone.
+        Returns the block.Fork of that."""
+        from . import block
+        if not self.forks:
+            raise ValueError("a step made without forks")
+        s = block.current_stream(self.cache.index)
+        block.compact(self.cache, self.table, start, kept, n_kept, new_len=self._keep, stream=s)
+        return self.fork(self._same, self._keep, drop=drop)
 
     @staticmethod
     def _layer(ld, plan, ids, stream):
