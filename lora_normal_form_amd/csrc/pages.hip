@@ -17,7 +17,8 @@ namespace scute {
 // counted between steps: every entry marks its page (held before; held wholly
 // after; the first request that holds it partly), the marks say which last pages
 // are to be copied and which pages are free, and two prefix sums number those.
-// Three launches: marks, sums of blocks, and the tables and the ring. Marks are
+// Three launches: marks, sums of blocks, and the tables and the ring, each a chain
+// of four to six reads that wait for one another, which is what bounds them. Marks are
 // plain stores of one value, but for the first partial holder, an atomic maximum
 // of n_requests - r, so the order of the stores does not matter.
 constexpr int FORK_THREADS = 1024, FORK_PAGES = 4 * FORK_THREADS;  // pages a block
@@ -47,14 +48,11 @@ struct ForkReq {
   uint32_t n, whole, part, cols;      // positions, whole pages, positions on the last, columns of the table
   uint32_t drop_from, drop_to;        // columns that are dropped
 };
-__device__ __forceinline__ ForkReq fork_req(const ForkArgs& G, int r) {
+// of the request that goes on from the first n positions of `parent`
+__device__ __forceinline__ ForkReq fork_req(const ForkArgs& G, int parent, uint32_t n) {
   const scute_cache_fork_args& A = G.a;
   ForkReq q;
-  q.parent = ldg(A.parent + r);
-  const bool lives = (uint32_t)q.parent < (uint32_t)A.n_requests;
-  if (!lives) q.parent = r;
-  q.n = lives ? fork_len(G, ldg(A.len + q.parent)) : 0u;
-  if (A.keep) q.n = min(q.n, (uint32_t)max(ldg(A.keep + r), 0));
+  q.parent = parent, q.n = n;
   q.whole = fork_div(G, q.n);
   q.part = q.n - q.whole * A.page_size;
   q.cols = q.whole + (q.part ? 1u : 0u);
@@ -65,6 +63,15 @@ __device__ __forceinline__ ForkReq fork_req(const ForkArgs& G, int r) {
     q.drop_to = fork_div(G, q.n - (uint32_t)A.window);
   }
   return q;
+}
+__device__ __forceinline__ ForkReq fork_req(const ForkArgs& G, int r) {
+  const scute_cache_fork_args& A = G.a;
+  int parent = ldg(A.parent + r);
+  const bool lives = (uint32_t)parent < (uint32_t)A.n_requests;
+  if (!lives) parent = r;
+  uint32_t n = lives ? fork_len(G, ldg(A.len + parent)) : 0u;
+  if (A.keep) n = min(n, (uint32_t)max(ldg(A.keep + r), 0));
+  return fork_req(G, parent, n);
 }
 // the page of a column of the request after the step, before copies (-1: none)
 __device__ __forceinline__ int fork_page(const ForkArgs& G, const ForkReq& q, uint32_t c) {
@@ -245,6 +252,96 @@ __global__ __launch_bounds__(FORK_THREADS) void k_fork_apply(ForkArgs G) {
       if (last != -2 && c == q.whole) p = last == -3 ? -1 : last;
       A.table_out[(int64_t)r * A.table_out_stride + c] = p;
     }
+  }
+}
+
+// Few requests and pages: one work-group does it in one launch, marks in LDS, a
+// thread a request, eight pages a thread, a wave a row. In a graph, with the copies:
+// 8 requests of 13 pages 13.3 us (three launches 19.4), 32 of 128 16.8 (22.0), 128
+// of 32 20.0 (21.8), 256 of 32, the most pieces, 22.1 (22.3).
+constexpr int FORK_ONE_PAGES = 8 * FORK_THREADS, FORK_ONE_PIECES = 256;  // (pieces: of 64 entries of the table)
+
+__global__ __launch_bounds__(FORK_THREADS) void k_fork_one(ForkArgs G) {
+  const scute_cache_fork_args& A = G.a;
+  __shared__ uint32_t s_before[FORK_ONE_PAGES / 32], s_whole[FORK_ONE_PAGES / 32], s_sum[FORK_THREADS / 64];
+  __shared__ int32_t s_first[FORK_ONE_PAGES], s_parent[FORK_ONE_PIECES], s_last[FORK_ONE_PIECES];
+  __shared__ uint32_t s_n[FORK_ONE_PIECES], s_held[FORK_ONE_PIECES];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, R = A.n_requests;
+  const uint32_t n_pages = (uint32_t)A.n_pages;
+  const int64_t head = A.cursor[0], tail = A.cursor[1];
+  ForkReq q{};
+  if (tid < R) {
+    q = fork_req(G, tid);
+    s_parent[tid] = q.parent, s_n[tid] = q.n;
+    s_held[tid] = fork_div(G, fork_len(G, ldg(A.len + tid)) + A.page_size - 1);
+  }
+  for (int i = tid; i < FORK_ONE_PAGES; i += FORK_THREADS) s_first[i] = 0;
+  if (tid < FORK_ONE_PAGES / 32) s_before[tid] = s_whole[tid] = 0;
+  __syncthreads();
+  for (int r = w; r < R; r += FORK_THREADS / 64) {
+    const ForkReq o = fork_req(G, s_parent[r], s_n[r]);
+    const uint32_t held = s_held[r];
+    for (uint32_t c = lane; c < max(held, o.cols); c += 64) {
+      const int was = c < held ? ldg(A.table + (int64_t)r * A.table_stride + c) : -1, p = fork_page(G, o, c);
+      if ((uint32_t)was < n_pages) atomicOr(s_before + was / 32, 1u << (was % 32));
+      if (p >= 0) {
+        if (c < o.whole)
+          atomicOr(s_whole + p / 32, 1u << (p % 32));
+        else
+          atomicMax(s_first + p, R - r);
+      }
+    }
+  }
+  __syncthreads();
+  const uint32_t cap = (uint32_t)A.ring_size;
+  const int64_t free64 = tail - head;
+  const uint32_t avail = free64 <= 0 ? 0u : free64 < (int64_t)cap ? (uint32_t)free64 : cap;
+  const uint32_t h0 = (uint32_t)((uint64_t)head % cap), t0 = (uint32_t)((uint64_t)tail % cap);
+  uint32_t wants = 0, gone = 0, all_wants, all_gone, live;
+  int from = -1;
+  if (tid < R && q.part) {
+    from = fork_page(G, q, q.whole);
+    wants = from >= 0 && ((s_whole[from / 32] >> (from % 32) & 1) || s_first[from] != R - tid);
+  }
+  uint32_t at = fork_scan(wants, s_sum, all_wants);
+  const bool copied = wants && at < avail, refused = wants && !copied;
+  if (tid < R) {
+    const uint32_t c = h0 + at;
+    const int last = copied ? ldg(A.ring + (c < cap ? c : c - cap)) : refused ? -1 : -2;  // (-2: the parent's)
+    s_last[tid] = last;
+    A.src[tid] = copied ? from : -1;
+    A.dst[tid] = copied ? last : -1;
+    A.n[tid] = copied ? (int32_t)q.part : 0;
+    A.seq_len[tid] = (int32_t)(refused ? q.n - q.part : q.n);
+  }
+  fork_scan(tid < R && (refused ? q.whole : q.n) > 0, s_sum, live);
+  bool goes[8];
+  const uint32_t p0 = tid * 8;
+  const uint32_t freed = s_before[p0 / 32] & ~s_whole[p0 / 32];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) gone += goes[i] = (freed >> ((p0 + i) % 32) & 1) && s_first[p0 + i] == 0;
+  at = fork_scan(gone, s_sum, all_gone);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (goes[i]) {
+      const uint32_t c = t0 + at;
+      if (at < cap) A.ring[c < cap ? c : c - cap] = (int32_t)(p0 + i);  // (no more than the ring holds)
+      ++at;
+    }
+  if (tid == 0) {
+    const uint32_t taken = min(all_wants, avail);
+    A.cursor_out[0] = head + taken;
+    A.cursor_out[1] = tail + all_gone;
+    A.counts[0] = (int32_t)live;
+    A.counts[1] = (int32_t)taken;
+    A.counts[2] = (int32_t)(all_wants - taken);
+    A.counts[3] = (int32_t)all_gone;
+  }
+  for (int r = w; r < R; r += FORK_THREADS / 64) {
+    const ForkReq o = fork_req(G, s_parent[r], s_n[r]);
+    const int last = s_last[r];
+    for (uint32_t c = lane; c < (uint32_t)A.table_width; c += 64)
+      A.table_out[(int64_t)r * A.table_out_stride + c] = last != -2 && c == o.whole ? last : fork_page(G, o, c);
   }
 }
 
@@ -503,6 +600,10 @@ extern "C" scute_status scute_cache_fork(const scute_cache_fork_args* A, void* s
   G.req_blocks = (int)((R + FORK_THREADS - 1) / FORK_THREADS);
   G.page_blocks = (A->n_pages + FORK_PAGES - 1) / FORK_PAGES;
   const hipStream_t s = (hipStream_t)stream;
+  if (A->n_pages <= FORK_ONE_PAGES && R * ((A->table_width + 63) / 64) <= FORK_ONE_PIECES) {
+    hipLaunchKernelGGL(k_fork_one, dim3(1), dim3(FORK_THREADS), 0, s, G);
+    return done(fn);
+  }
   // several work-groups a row where the rows are few
   const int64_t rows = std::min<int64_t>(R, 4096);
   const auto parts = [&](int64_t each) {

@@ -113,7 +113,9 @@ FORKS = [
     (64, 300, 5, dict(beams=3), 200, 7), (64, 300, 5, dict(beams=3, bad=True), 31, 0),
     (63, 40, 16, dict(beams=9, bad=True, share_free=0.0), 0, 0), (300, 12, 1, dict(beams=2), 4, 3),
     (1023, 9, 16, dict(beams=4, share_free=0.1), 40, 16), (1025, 9, 16, dict(beams=4), 16, 100000),
-    (2500, 5, 128, dict(beams=6, share_free=0.05), 0, 0), (3, 2500, 2, dict(beams=3), 1, 0)]
+    (2500, 5, 128, dict(beams=6, share_free=0.05), 0, 0), (3, 2500, 2, dict(beams=3), 1, 0),
+    (17, 300, 5, dict(beams=3, bad=True), 31, 0), (256, 30, 4, dict(beams=4, share_free=0.1), 40, 3), (257, 30, 4, dict(beams=4), 40, 3),
+    (2, 4093, 1, dict(beams=2), 0, 0), (2, 4092, 1, dict(beams=2), 1000, 70)]
 
 
 @pytest.mark.parametrize("R, P, ps, kw, window, sinks", FORKS)
