@@ -481,11 +481,14 @@ __global__ __launch_bounds__(64) void k_cache_compact(MoveArgs A) {
   }
 }
 
-// Waves from which on a compaction's columns are 256 bytes; with fewer they are
-// 128 (a line of the L2): 256 waves of 256 bytes, half of 16 x 16000 positions,
-// 265 us, 512 of 128 190, 1024 of 64 240; 1024 waves of 256, trees of 24 tokens of 64
-// requests, 5.2 us, of 128 6.8. (Bound by the memory: 787 MB, 4.1 TB/s.)
-constexpr int64_t COMPACT_WAVES = 1024;
+// Waves from which on a compaction's columns are 256 bytes, and from which on 128 (a
+// line of the L2); with fewer they are 64, so that more waves each make fewer trips.
+// Half of r x 16000 positions of 8 heads of 256 bytes, times in a graph: r = 16, 256
+// waves of 256 bytes 280 us, 512 of 128 204, 1024 of 64 252; r = 8, 128 bytes 177, 64
+// 192; r = 4, 151 and 120; r = 1, 130 and 87 (32 bytes: 73, but 161 for r = 4). 1024
+// waves of 256, trees of 24 tokens of 64 requests, 5.2 us of the kernel, of 128 6.8.
+// (Bound by the memory where waves are many: r = 16, 787 MB, 4.1 TB/s.)
+constexpr int64_t COMPACT_WAVES = 1024, COMPACT_FEW = 256;
 
 struct Parts {
   int64_t first, whole, before, need, need_sum, free_sum, bytes;
@@ -673,7 +676,9 @@ extern "C" scute_status scute_cache_compact(const scute_kv_cache* C, const int32
   const auto blocks = [&](int lp) { return dim3((unsigned)std::min(most, columns * ((A.pieces + lp - 1) / lp))); };
   if (columns * ((A.pieces + 15) / 16) >= COMPACT_WAVES)
     hipLaunchKernelGGL(k_cache_compact<16>, blocks(16), dim3(64), 0, s, A);
-  else
+  else if (columns * ((A.pieces + 7) / 8) >= COMPACT_FEW)
     hipLaunchKernelGGL(k_cache_compact<8>, blocks(8), dim3(64), 0, s, A);
+  else
+    hipLaunchKernelGGL(k_cache_compact<4>, blocks(4), dim3(64), 0, s, A);
   return done(fn);
 }
