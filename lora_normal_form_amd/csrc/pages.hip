@@ -482,13 +482,15 @@ __global__ __launch_bounds__(64) void k_cache_compact(MoveArgs A) {
 }
 
 // Waves from which on a compaction's columns are 256 bytes, and from which on 128 (a
-// line of the L2); with fewer they are 64, so that more waves each make fewer trips.
+// line of the L2); with fewer they are 64, or 32 where those are below the last, so
+// that more waves each make fewer trips.
 // Half of r x 16000 positions of 8 heads of 256 bytes, times in a graph: r = 16, 256
 // waves of 256 bytes 280 us, 512 of 128 204, 1024 of 64 252; r = 8, 128 bytes 177, 64
-// 192; r = 4, 151 and 120; r = 1, 130 and 87 (32 bytes: 73, but 161 for r = 4). 1024
+// 192; r = 4, 151 and 120, of 32 161; r = 1, 130, 87 and 72; 8 x 9304 of one head of 128
+// bytes, of 64 58, of 32 45 (lists of up to 2000: equal). 1024
 // waves of 256, trees of 24 tokens of 64 requests, 5.2 us of the kernel, of 128 6.8.
 // (Bound by the memory where waves are many: r = 16, 787 MB, 4.1 TB/s.)
-constexpr int64_t COMPACT_WAVES = 1024, COMPACT_FEW = 256;
+constexpr int64_t COMPACT_WAVES = 1024, COMPACT_FEW = 256, COMPACT_FEWER = 144;
 
 struct Parts {
   int64_t first, whole, before, need, need_sum, free_sum, bytes;
@@ -678,7 +680,9 @@ extern "C" scute_status scute_cache_compact(const scute_kv_cache* C, const int32
     hipLaunchKernelGGL(k_cache_compact<16>, blocks(16), dim3(64), 0, s, A);
   else if (columns * ((A.pieces + 7) / 8) >= COMPACT_FEW)
     hipLaunchKernelGGL(k_cache_compact<8>, blocks(8), dim3(64), 0, s, A);
-  else
+  else if (columns * ((A.pieces + 3) / 4) >= COMPACT_FEWER)
     hipLaunchKernelGGL(k_cache_compact<4>, blocks(4), dim3(64), 0, s, A);
+  else
+    hipLaunchKernelGGL(k_cache_compact<2>, blocks(2), dim3(64), 0, s, A);
   return done(fn);
 }
