@@ -305,6 +305,29 @@ def test_compact_matches_loops(ps, heads, dim, dt, by_head, R, P, share):
     assert new_len.tolist() == [max(0, int(a)) + min(int(n), W) for a, n in zip(start, n_kept)]
 
 
+@pytest.mark.parametrize("R, heads, dim, dt", [(2, 1, 8, F32), (9, 2, 128, BF16), (40, 4, 128, F32), (70, 8, 128, BF16)])
+def test_compact_columns_of_each_width(R, heads, dim, dt):
+    """32, 64, 128 and 256 bytes, lists of several trips of each."""
+    rng, P, ps, W = np.random.default_rng(R), 80, 16, 1100
+    table = rng.permutation(R * P).reshape(R, P)
+    k, v = _cache(R * P, ps, heads, dim, dt, False, seed=R)
+    kd, vd = k.to(DEV), v.to(DEV)
+    start = rng.integers(0, 9, size=R)
+    kept = np.stack([np.sort(rng.choice(np.arange(10, P * ps), W, replace=False)) for _ in range(R)])
+    n_kept = rng.integers(W - 60, W + 1, size=R)
+    block.compact(block.KVCache(kd, vd), _int(table), _int(start), _int(kept), _int(n_kept))
+    for z, got in ((k, kd), (v, vd)):
+        want = z.clone()
+        for r in range(R):
+            n, src = n_kept[r], torch.as_tensor(kept[r][:n_kept[r]])
+            to, t = start[r] + torch.arange(n), torch.as_tensor(table[r])
+            at = src > to
+            src, to = src[at], to[at]
+            want[t[to // ps], to % ps] = z[t[src // ps], src % ps]
+        same = torch.equal(got.cpu(), want)
+        assert same
+
+
 def test_compact_nothing_kept():
     k, v = _cache(4, 2, 1, 8, F32, False)
     kd, vd, new_len = k.to(DEV), v.to(DEV), _int([7, 7])
