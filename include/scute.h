@@ -636,7 +636,8 @@ scute_status scute_shared_attention_workspace(int32_t device, int32_t dtype, int
  * group and shared_len are device arrays; group is not checked: offsets that
  * do not ascend give rows whose output is not defined, no access out of bounds.
  * workspace as there, of at least what scute_shared_attention_workspace says
- * for n_rows and n_groups. flags: a bitwise or of scute_shared_flag. Errors as
+ * for n_rows and n_groups; one that is large enough may serve calls of any sizes
+ * and caches of any head_dim in turn, scute_paged_attention's too. flags: a bitwise or of scute_shared_flag. Errors as
  * there, SCUTE_E_INVALID for an unknown flag, SCUTE_E_SHAPE for n_groups outside
  * 0 .. 65536 or more rows and heads than can be numbered at the table's whole width
  * (rows x key heads x tiles of 16 query heads x table positions / 32, or / 16 in

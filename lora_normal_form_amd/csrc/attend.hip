@@ -25,7 +25,10 @@ int device_units(int device) {
 
 int att_dim(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 int64_t att_places(int units) { return (int64_t)units * ATT_PLACES; }
-int64_t att_counter_bytes(int units) { return (4 * (ATT_ARRIVALS + 2 * att_places(units)) + 255) / 256 * 256; }
+// the counters, and behind them the plan of calls over shared positions: the same
+// place for heads of any size, so that nothing else is written to either
+int64_t att_plan_place(int units) { return (4 * (ATT_ARRIVALS + 2 * att_places(units)) + 255) / 256 * 256; }
+int64_t att_counter_bytes(int units) { return att_plan_place(units) + ATT_PLAN_BYTES; }
 int64_t att_workspace(int units, int head_dim) {
   return att_counter_bytes(units) + att_places(units) * ATT_COLS * (att_dim(head_dim) + 4) * 4;
 }

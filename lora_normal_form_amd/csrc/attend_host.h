@@ -34,6 +34,8 @@ scute_status att_run(const char* fn, const AttCall& c, int form, hipStream_t s);
 int device_units(int device);
 int att_dim(int head_dim);
 int64_t att_workspace(int units, int head_dim);
+constexpr int64_t ATT_PLAN_BYTES = 256;
+int64_t att_plan_place(int units);
 
 void att_plain(const AttArgs& A, int es, int dp, int blocks, hipStream_t s);
 void att_sinks(const AttArgs& A, int es, int dp, int blocks, hipStream_t s);

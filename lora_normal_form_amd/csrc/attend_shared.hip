@@ -26,6 +26,7 @@ struct ShPlan {
   uint32_t each_shared, each_own;  // units of a gang, tiles of a chunk
   int32_t taken;                   // chunks taken behind the waves' first; 0 between calls
 };
+static_assert(sizeof(ShPlan) <= ATT_PLAN_BYTES);
 
 struct SharedArgs {
   const void *q, *k, *v;
@@ -1057,9 +1058,10 @@ ShSizes sh_sizes(int dtype, int head_dim, int page_size, int n_heads, int n_kv, 
   z.own_cols = z.together > 1 ? z.together * z.group : std::min(16, z.group);
   z.blocks = z.dp <= 128 ? 2 * units : units;  // (as many as are resident at once)
   z.tiles = n_kv * (n_rows * z.group / (z.cols * z.gang) + n_groups);
-  // paged attention's workspace, for calls that share nothing; the same for all calls
-  z.plan = up(att_workspace(units, head_dim));
-  z.rows = z.plan + 256;
+  // paged attention's workspace, for calls that share nothing; its counters hold the
+  // plan, which has to stay as the last call left it
+  z.plan = att_plan_place(units);
+  z.rows = up(att_workspace(units, head_dim));
   z.seeds = z.rows + up(n_rows * sizeof(ShRow));
   z.own = z.seeds + (z.blocks + z.tiles * z.gang) * z.waves * wave_cols * (z.dp + 4) * 4;
   z.bytes = z.own + (SH_CHUNKS * z.waves * z.blocks + n_rows * n_kv * z.q_tiles) * z.own_cols * (z.dp + 4) * 4;

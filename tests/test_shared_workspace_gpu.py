@@ -1,0 +1,65 @@
+"""Workspaces of attention over shared positions: one for caches of several head
+sizes, paged calls between."""
+
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from lora_normal_form_amd import block  # noqa: E402
+from test_block_gpu import BF16, DEV, F32, _int  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def _same(a, b):
+    return torch.equal(a.view(torch.int16 if a.dtype == BF16 else torch.int32), b.view(torch.int16 if b.dtype == BF16 else torch.int32))
+
+
+def _workspace(n):
+    w = torch.zeros(n, dtype=torch.uint8, device=DEV)
+    assert w.data_ptr() % 256 == 0
+    return w
+
+
+def test_one_workspace_for_heads_of_several_sizes():
+    """A workspace zeroed once serves caches of 64, 128 and 256 elements and paged
+    calls in turn: the bits of handles of their own. The rows' own positions are
+    more chunks than waves, so the counter of chunks is used."""
+    N, H, Hq, L, ps = 64, 8, 128, 6000, 16
+    g = torch.Generator().manual_seed(5)
+    rng = np.random.default_rng(5)
+    P = -(-L // ps) + 4
+    table = _int(rng.integers(0, 300, size=(N, P)))  # (read only: pages may repeat)
+    lens, none = _int(rng.integers(L - 200, L + 1, size=N)), _int([0, 3])
+    calls = {}
+    for D, dt in ((64, BF16), (128, BF16), (256, BF16), (64, F32), (256, F32)):
+        kc, vc = (torch.randn((300, ps, H, D), generator=g).to(DEV, dt) for _ in range(2))
+        q = torch.randn((N, Hq, D), generator=g).to(DEV, dt)
+        cache = block.KVCache(kc, vc)
+        shared, paged = block.SharedAttention(cache, Hq, N, 1, always=True), block.PagedAttention(cache, Hq)
+        args = (q, table, lens, none, _int([32]))
+        want = shared.forward(*args, torch.empty_like(q)), paged.forward(q, table, lens, torch.empty_like(q))
+        calls[D, dt] = shared, paged, args, want
+    torch.cuda.synchronize()
+    one = _workspace(max(h.workspace.shape[0] for c in calls.values() for h in c[:2]))
+    for shared, paged, *_ in calls.values():
+        shared.workspace = paged.workspace = one
+    keys = list(calls)
+    for i in range(40):
+        key = keys[int(rng.integers(0, len(keys)))]
+        shared, paged, args, want = calls[key]
+        q = args[0]
+        if i % 3 == 2:
+            same = _same(paged.forward(q, table, lens, torch.full_like(q, math.nan)), want[1])
+        else:
+            same = _same(shared.forward(*args, torch.full_like(q, math.nan)), want[0])
+        assert same, (i, key)
