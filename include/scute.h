@@ -441,7 +441,7 @@ scute_status scute_cache_assign(const scute_cache_assign_args* args, void* strea
  * entry of a request that ends there.
  * Lengths and cursors as in scute_cache_assign. workspace: at least what
  * scute_cache_fork_workspace says, 256-byte aligned, zeroed once before its
- * first use; calls that may overlap in time need workspaces of their own.
+ * first use (calls of any sizes may use it in turn); calls that may overlap in time need workspaces of their own.
  * Errors: as scute_cache_assign's; SCUTE_E_INVALID for a workspace that is too
  * small. */
 typedef struct scute_cache_fork_args {

@@ -492,19 +492,23 @@ __global__ __launch_bounds__(64) void k_cache_compact(MoveArgs A) {
 // (Bound by the memory where waves are many: r = 16, 787 MB, 4.1 TB/s.)
 constexpr int64_t COMPACT_WAVES = 1024, COMPACT_FEW = 256, COMPACT_FEWER = 144;
 
+// The workspace of a fork. What a call leaves behind comes first, with room for the
+// most requests and pages, and the marks, which are zero between calls, behind it:
+// calls of any sizes may use one workspace in turn.
+constexpr int64_t FORK_MOST = 65536, FORK_MOST_PAGES = 1 << 24;
 struct Parts {
-  int64_t first, whole, before, need, need_sum, free_sum, bytes;
+  int64_t need, need_sum, free_sum, first, whole, before, bytes;
 };
-Parts fork_parts(int64_t R, int64_t n_pages) {
+Parts fork_parts(int64_t n_pages) {
   const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   Parts p;
-  p.first = 0;
-  p.whole = up(4 * n_pages);
+  p.need = 0;
+  p.need_sum = p.need + 4 * FORK_MOST;
+  p.free_sum = p.need_sum + 4 * FORK_MOST / FORK_THREADS;
+  p.first = p.free_sum + 4 * FORK_MOST_PAGES / FORK_PAGES;
+  p.whole = p.first + up(4 * n_pages);
   p.before = p.whole + up(n_pages);
-  p.need = p.before + up(n_pages);
-  p.need_sum = p.need + up(4 * R);
-  p.free_sum = p.need_sum + up(4 * ((R + FORK_THREADS - 1) / FORK_THREADS));
-  p.bytes = p.free_sum + up(4 * ((n_pages + FORK_PAGES - 1) / FORK_PAGES));
+  p.bytes = p.before + up(n_pages);
   return p;
 }
 
@@ -542,9 +546,9 @@ using namespace scute;
 
 extern "C" scute_status scute_cache_fork_workspace(int32_t n_requests, int32_t n_pages, int64_t* bytes) {
   if (!bytes) return fail(SCUTE_E_INVALID, "scute_cache_fork_workspace: bytes is null");
-  if (n_requests < 0 || n_requests > 65536 || n_pages < 1 || n_pages > (1 << 24))
+  if (n_requests < 0 || n_requests > FORK_MOST || n_pages < 1 || n_pages > FORK_MOST_PAGES)
     return fail(SCUTE_E_SHAPE, "scute_cache_fork_workspace: n_requests must be in [0, 65536] and n_pages in [1, 2^24]");
-  *bytes = fork_parts(n_requests, n_pages).bytes;
+  *bytes = fork_parts(n_pages).bytes;
   return SCUTE_OK;
 }
 
@@ -552,7 +556,7 @@ extern "C" scute_status scute_cache_fork(const scute_cache_fork_args* A, void* s
   const char* fn = "scute_cache_fork";
   if (!A) return fail(SCUTE_E_INVALID, "scute_cache_fork: args is null");
   if (A->device < 0) return fail(SCUTE_E_INVALID, "scute_cache_fork: device must be >= 0");
-  if (A->n_requests < 0 || A->n_requests > 65536)
+  if (A->n_requests < 0 || A->n_requests > FORK_MOST)
     return fail(SCUTE_E_SHAPE, "scute_cache_fork: n_requests must be in [0, 65536]");
   if (A->page_size < 1 || A->page_size > 65536)
     return fail(SCUTE_E_SHAPE, "scute_cache_fork: page_size must be in [1, 65536]");
@@ -562,7 +566,7 @@ extern "C" scute_status scute_cache_fork(const scute_cache_fork_args* A, void* s
     return fail(SCUTE_E_SHAPE, "scute_cache_fork: table_width must be in [1, 2^24] and at most the tables' strides");
   if (A->ring_size < 1 || A->ring_size > (1 << 30))
     return fail(SCUTE_E_SHAPE, "scute_cache_fork: ring_size must be in [1, 2^30]");
-  if (A->n_pages < 1 || A->n_pages > (1 << 24))
+  if (A->n_pages < 1 || A->n_pages > FORK_MOST_PAGES)
     return fail(SCUTE_E_SHAPE, "scute_cache_fork: n_pages must be in [1, 2^24]");
   if (A->window < 0 || A->sinks < 0) return fail(SCUTE_E_SHAPE, "scute_cache_fork: window and sinks must be >= 0");
   const bool some = A->n_requests > 0;
@@ -577,7 +581,7 @@ extern "C" scute_status scute_cache_fork(const scute_cache_fork_args* A, void* s
     return fail(SCUTE_E_INVALID, "scute_cache_fork: misaligned pointer");
   if ((uintptr_t)A->workspace & 255) return fail(SCUTE_E_INVALID, "scute_cache_fork: workspace must be 256-byte aligned");
   const int64_t R = A->n_requests;
-  const Parts P = fork_parts(R, A->n_pages);
+  const Parts P = fork_parts(A->n_pages);
   if (A->workspace_bytes < P.bytes) return fail(SCUTE_E_INVALID, "scute_cache_fork: the workspace is too small");
   // work-groups read the inputs while others write the outputs
   const int64_t extent = some ? 4 * ((R - 1) * A->table_stride + A->table_width) : 0;

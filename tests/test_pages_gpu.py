@@ -367,3 +367,25 @@ def test_compact_in_a_graph():
         torch.cuda.synchronize()
         k, v = _compact_ref(k, table, start, kept, n, ps), _compact_ref(v, table, start, kept, n, ps)
         assert torch.equal(kd.cpu(), k) and torch.equal(vd.cpu(), v)
+
+
+def test_one_workspace_for_forks_of_several_sizes():
+    """A workspace zeroed once serves calls of other requests and pages in turn."""
+    sizes = [(64, 9, 16, 7), (700, 40, 5, 900), (2500, 5, 16, 0), (1, 5, 4, 9000), (300, 60, 2, 5000), (4100, 3, 8, 1)]
+    forks = [block.Fork(R, P, R * P + spare, DEV) for R, P, _, spare in sizes]
+    one = torch.zeros(max(f._workspace.shape[0] for f in forks), dtype=torch.uint8, device=DEV)
+    for f in forks:
+        f.args.workspace, f.args.workspace_bytes = one.data_ptr(), one.shape[0]
+    for i in (1, 2, 1, 4, 0, 3, 5, 4, 2, 3, 1, 5, 0, 4):
+        (R, P, ps, spare), f = sizes[i], forks[i]
+        length, parent, keep, table, ring, head, tail, n_pages = _case(R + P, R, P, ps, beams=4, spare=spare, share_free=0.3)
+        want, ring_want = fork_ref(length, parent, keep, table, ring, head, tail, ps, n_pages)
+        ring_d = _int(ring)
+        block.fork_pages(_int(length), _int(parent), _int(table), ring_d, torch.tensor([head, tail], device=DEV), ps, f,
+                         keep=_int(keep))
+        torch.cuda.synchronize()
+        for name, v in want.items():
+            same = np.array_equal(getattr(f, name).cpu().numpy(), v)
+            assert same, (i, name)
+        same = np.array_equal(ring_d.cpu().numpy(), ring_want)
+        assert same, i
