@@ -5,6 +5,7 @@
 
 #include "attend.h"
 #include "attend_host.h"
+#include "shared_cut.h"
 
 namespace scute {
 
@@ -53,7 +54,7 @@ template <typename T, int DP>
 struct ShGeo {
   using G = AttGeo<T, DP>;
   static constexpr int QT = DP * G::ES >= 1024 ? 1 : 2;  // query tiles a wave (one where two would not fit the registers)
-  static constexpr int NW = 4;                           // waves of a work-group
+  static constexpr int NW = SH_WAVES;                    // waves of a work-group
   static constexpr int WCOLS = 16 * QT;                  // columns of a wave
   static constexpr int ROW = DP * G::ES;                 // bytes of a position in LDS
   static constexpr int STAGE = sh_stage(G::ES, DP);      // positions staged at once: a unit
@@ -115,7 +116,6 @@ __device__ __forceinline__ float max_over_rows(float v) {
   return fmaxf(__uint_as_float(b.x), __uint_as_float(b.y));
 }
 
-constexpr int SH_CHUNKS = 9;        // chunks a wave at most (eight, and one more)
 constexpr int64_t SH_SAVED = 256 << 20;  // bytes
 constexpr int SH_TILES = 1 << 22;  // (group, key head, tile)s stay below it
 
@@ -849,8 +849,6 @@ __device__ __forceinline__ void sh_own(const SharedArgs& A, const ShCall& call, 
 // units' cycles); 128 rows of one group behind 8192: 76 and 7. What bounds it: the
 // softmax of a score costs as many cycles as its products, and both wait for LDS;
 // the prefix alone takes 740 us, without the softmax 630, without V's products 536.
-constexpr float SH_COST_SHARED = 10.f, SH_COST_OWN = 7.f;  // of a unit and of a tile
-
 template <typename T, int DP, bool PAGE16, bool EXACT>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_attention(SharedArgs A) {
   using G = AttGeo<T, DP>;
@@ -906,24 +904,11 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_attention(Sha
   const int H = A.n_kv * A.q_tiles;
   const uint32_t units = call.fits ? L.u[256] : 0, tiles = L.t[256] * H;
   // ---- shares of the work-groups ----
-  const float cs = (float)units * A.gang * SH_COST_SHARED / A.pw, co = (float)tiles * SH_COST_OWN;
+  const ShCut cut = sh_cut(gridDim.x, units, tiles, A.gang, A.pw);
   // (whole gangs on each of the dies, to which work-groups go in turn)
-  const uint32_t dies = gridDim.x % 8 == 0 ? 8 : 1, here = gridDim.x / dies, die = blockIdx.x % dies, k = blockIdx.x / dies;
-  uint32_t ws = 0;  // work-groups of a die for shared positions
-  if (units) {
-    const uint32_t gangs = (uint32_t)((float)here * (cs / (cs + co)) / (float)A.gang + 0.5f);
-    ws = min(max(gangs, 1u), (here - (tiles ? 1 : 0)) / A.gang) * A.gang;
-  }
-  const uint32_t wo = here - ws;
-  const uint32_t n_gangs = dies * (ws / A.gang), waves = dies * wo * S::NW;
-  // (four units at least: fewer pieces to join; four rows behind 1000 positions, one unit: 39 us, four: 34)
-  const uint32_t each_s = n_gangs ? max((units + n_gangs - 1) / n_gangs, 4u) : 1;
-  // own tiles: chunks of an eighth of a wave's share (8 tiles at least), taken from
-  // a counter after each wave's first: waves with equal work differ by half in time
-  const uint32_t share = tiles ? (tiles + waves - 1) / waves : 1, each_o = max(min(share, 8u), (share + 7) / 8);
-  const uint32_t chunks = (tiles + each_o - 1) / each_o;
+  const uint32_t die = blockIdx.x % cut.dies, k = blockIdx.x / cut.dies;
   // ---- where each row's partial results will lie ----
-  if (blockIdx.x == 0 && tid == 0) A.plan->each_shared = each_s, A.plan->each_own = each_o;
+  if (blockIdx.x == 0 && tid == 0) A.plan->each_shared = cut.each_s, A.plan->each_own = cut.each_o;
   for (int base = (blockIdx.x * 64 * S::NW + tid) * A.together; base < A.n_rows; base += gridDim.x * 64 * S::NW * A.together) {
     const int chunk = base / call.per_r;
     uint32_t before = L.t[chunk];
@@ -941,15 +926,15 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void k_shared_attention(Sha
     });
   }
   // ---- the work-groups' kinds, spread evenly ----
-  const uint32_t upto = k * ws / here, next = (k + 1) * ws / here;
+  const uint32_t upto = k * cut.ws / cut.here, next = (k + 1) * cut.ws / cut.here;
   if (next > upto) {
-    sh_prefix<T, DP, PAGE16, EXACT>(A, call, L, s_kv, die * (ws / A.gang) + upto / A.gang, (int)(upto % A.gang), each_s);
+    sh_prefix<T, DP, PAGE16, EXACT>(A, call, L, s_kv, die * (cut.ws / A.gang) + upto / A.gang, (int)(upto % A.gang), cut.each_s);
   } else {
-    for (uint32_t chunk = S::NW * (die * wo + k - upto) + w; chunk < chunks;) {
-      sh_own<T, DP, PAGE16, EXACT>(A, call, L, chunk, each_o);
+    for (uint32_t chunk = S::NW * (die * cut.wo + k - upto) + w; chunk < cut.chunks;) {
+      sh_own<T, DP, PAGE16, EXACT>(A, call, L, chunk, cut.each_o);
       int taken = 0;
       if (lane == 0) taken = arrive(&A.plan->taken);
-      chunk = waves + (uint32_t)uni(taken);
+      chunk = cut.waves + (uint32_t)uni(taken);
     }
   }
 }
@@ -1032,42 +1017,6 @@ void sh_dim(const SharedArgs& A, int dp, int blocks, hipStream_t s) {
   else sh_launch<T, 256>(A, blocks, s);
 }
 
-// What a call of these sizes needs.
-struct ShSizes {
-  int es, dp, group, cols, cw, pw, gang, together, q_tiles, own_cols, blocks, waves;
-  int64_t tiles;                  // (group, key head, wide tile)s at most
-  int64_t plan, rows, seeds, own, bytes;  // places in the workspace, and its bytes
-};
-ShSizes sh_sizes(int dtype, int head_dim, int page_size, int n_heads, int n_kv, bool runs, int64_t n_rows, int64_t n_groups,
-                 int units) {
-  const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
-  ShSizes z;
-  z.es = dtype == SCUTE_F32 ? 4 : 2, z.dp = att_dim(head_dim), z.group = n_heads / n_kv;
-  z.waves = 4;
-  // waves side by side: as many as the columns of a group of the mean size fill,
-  // half of them at least; then as many work-groups as it has tiles, up to 4
-  const int64_t mean = n_groups > 0 ? n_rows * z.group / n_groups : 0;
-  const int wave_cols = z.dp * z.es >= 1024 ? 16 : 32;
-  z.cw = z.waves;
-  if (page_size % 16 == 0)
-    while (z.cw > 2 && z.cw / 2 * wave_cols >= mean) z.cw /= 2;
-  z.pw = z.waves / z.cw, z.cols = wave_cols * z.cw;
-  z.gang = mean > 2 * z.cols ? 4 : mean > z.cols ? 2 : 1;
-  z.together = runs && z.group <= 8 ? std::min(4, 16 / z.group) : 1;
-  z.q_tiles = (z.group + 15) / 16;
-  z.own_cols = z.together > 1 ? z.together * z.group : std::min(16, z.group);
-  z.blocks = z.dp <= 128 ? 2 * units : units;  // (as many as are resident at once)
-  z.tiles = n_kv * (n_rows * z.group / (z.cols * z.gang) + n_groups);
-  // paged attention's workspace, for calls that share nothing; its counters hold the
-  // plan, which has to stay as the last call left it
-  z.plan = att_plan_place(units);
-  z.rows = up(att_workspace(units, head_dim));
-  z.seeds = z.rows + up(n_rows * sizeof(ShRow));
-  z.own = z.seeds + (z.blocks + z.tiles * z.gang) * z.waves * wave_cols * (z.dp + 4) * 4;
-  z.bytes = z.own + (SH_CHUNKS * z.waves * z.blocks + n_rows * n_kv * z.q_tiles) * z.own_cols * (z.dp + 4) * 4;
-  return z;
-}
-
 }  // namespace scute
 
 using namespace scute;
@@ -1087,15 +1036,8 @@ extern "C" scute_status scute_shared_attention_workspace(int32_t device, int32_t
     return bad(SCUTE_E_SHAPE, "max_rows must be in [0, 2^20] and max_groups in [0, 65536]");
   const int units = device_units(device);
   if (units < 0) return bad(SCUTE_E_INVALID, "no such HIP device");
-  // (room for calls of fewer rows or groups too, whose waves stand in other ways:
-  // a tile and its gang's and turns' take 4 work-groups' columns at most)
-  *bytes = 0;
-  for (const bool runs : {false, true}) {
-    const ShSizes z = sh_sizes(dtype, head_dim, 16, n_heads, n_kv_heads, runs, max_rows, max_groups, units);
-    const int64_t wave_cols = z.cols / z.cw, all = z.waves * wave_cols;
-    const int64_t tiles = (int64_t)n_kv_heads * ((int64_t)max_rows * z.group / (2 * wave_cols) + 4ll * max_groups);
-    *bytes = std::max(*bytes, z.bytes + (tiles - z.tiles * z.gang) * all * (z.dp + 4) * 4);
-  }
+  *bytes = sh_workspace(dtype == SCUTE_F32 ? 4 : 2, att_dim(head_dim), att_workspace(units, head_dim), sizeof(ShRow), n_heads,
+                        n_kv_heads, max_rows, max_groups, units);
   return SCUTE_OK;
 }
 
@@ -1121,7 +1063,11 @@ extern "C" scute_status scute_shared_attention(const scute_kv_cache* C, const vo
   if (!g.ok()) return hip_fail(g.err, fn);
   const int units = device_units(C->device);
   if (units < 0) return bad(SCUTE_E_INVALID, "no such HIP device");
-  const ShSizes z = sh_sizes(C->dtype, C->head_dim, C->page_size, n_heads, C->n_kv_heads, req != nullptr, n_rows, n_groups, units);
+  const int es = C->dtype == SCUTE_F32 ? 4 : 2, dp = att_dim(C->head_dim);
+  // (paged attention's workspace comes first, for calls that share nothing; its
+  // counters hold the plan, which has to stay as the last call left it)
+  const ShSizes z = sh_sizes(es, dp, att_workspace(units, C->head_dim), sizeof(ShRow), C->page_size, n_heads, C->n_kv_heads,
+                             req != nullptr, n_rows, n_groups, units);
   if (workspace_bytes < z.bytes) return bad(SCUTE_E_INVALID, "the workspace is too small");
   const int64_t reach = std::min<int64_t>((int64_t)table_width * C->page_size, (int64_t)1 << 29);
   // Sharing has more to do before and after than paged attention of few rows, whose
@@ -1129,11 +1075,11 @@ extern "C" scute_status scute_shared_attention(const scute_kv_cache* C, const vo
   // are read for one by one (captured calls, shared and one by one: 4 rows behind 8000
   // positions, 97 MB, 51 and 29 us; 32 behind 1000, 130 MB, 44 and 21; 4 behind 32000,
   // 390 MB, 74 and 80).
-  const int64_t saved = std::max<int64_t>(0, (int64_t)n_rows - n_groups) * reach * 2 * C->n_kv_heads * C->head_dim * z.es;
-  if (!(flags & SCUTE_SHARED_ALWAYS) && (n_groups == 0 || saved < SH_SAVED))
+  const int64_t saved = std::max<int64_t>(0, (int64_t)n_rows - n_groups) * reach * 2 * C->n_kv_heads * C->head_dim * es;
+  if ((!(flags & SCUTE_SHARED_ALWAYS) && (n_groups == 0 || saved < SH_SAVED)) || !sh_can_share(z))
     return att_run(fn, call, ATT_PLAIN, (hipStream_t)stream);
   // (units and tiles are counted in 31 bits)
-  const int64_t stage = z.es == 4 ? 16 : 32, most = ((int64_t)1 << 31) - 1;
+  const int64_t stage = es == 4 ? 16 : 32, most = ((int64_t)1 << 31) - 1;
   if (z.tiles >= SH_TILES || z.tiles * (reach / stage + 1) > most ||
       (int64_t)n_rows * C->n_kv_heads * z.q_tiles * (reach / stage + 2) > most)
     return bad(SCUTE_E_SHAPE, "too many rows and heads for a table this wide");
@@ -1141,14 +1087,14 @@ extern "C" scute_status scute_shared_attention(const scute_kv_cache* C, const vo
   int shift = 0;
   while ((1 << shift) < C->page_size) ++shift;
   const uint64_t mul = (((uint64_t)1 << (31 + shift)) + C->page_size - 1) / C->page_size;
-  const SharedArgs A{q, C->k, C->v, out, table, len, req, group, shared_len, (ShRow*)(ws + z.rows), (ShPlan*)(ws + z.plan),
+  const SharedArgs A{q, C->k, C->v, out, table, len, req, group, shared_len, (ShRow*)(ws + z.rows), (ShPlan*)(ws + att_plan_place(units)),
                      (float*)(ws + z.seeds), (float*)(ws + z.own), q_stride, out_stride, C->page_stride, C->token_stride,
                      C->head_stride, table_stride, C->n_pages, (uint32_t)mul, n_rows, n_groups, C->n_kv_heads, z.group,
                      C->head_dim, C->page_size, shift, (int32_t)reach, n_requests, (int32_t)z.tiles, z.cw, z.pw, z.gang, z.together, z.q_tiles,
                      z.own_cols, scale < 0.f, std::max(fabsf(scale * 1.4426950408889634f), 1e-37f)};
   const hipStream_t s = (hipStream_t)stream;
-  if (z.es == 4) sh_dim<float>(A, z.dp, z.blocks, s);
-  else sh_dim<uint16_t>(A, z.dp, z.blocks, s);
+  if (es == 4) sh_dim<float>(A, dp, z.blocks, s);
+  else sh_dim<uint16_t>(A, dp, z.blocks, s);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SCUTE_OK : hip_fail(e, fn);
 }

@@ -37,7 +37,7 @@ def kernel_sources():
 
 # the operators between the layers, which the layer's kernels do not use
 NOT_THE_LAYER = ("block.hip", "block.h", "attend.hip", "attend.h", "attend_host.h", "attend_sinks.hip",
-                 "attend_shared.hip", "pages.hip")
+                 "attend_shared.hip", "shared_cut.h", "pages.hip")
 
 COPY_KERNEL = "__amd_rocclr_copyBuffer"
 
