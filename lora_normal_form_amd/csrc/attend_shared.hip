@@ -946,55 +946,57 @@ template <typename T, int DP>
 __global__ __launch_bounds__(256) void k_shared_join(SharedArgs A) {
   using S = ShGeo<T, DP>;
   constexpr int LP = DP / 4;
-  const int64_t pair = (int64_t)blockIdx.x * (256 / LP) + threadIdx.x / LP;
-  const int n_heads = A.n_kv * A.heads, row = (int)(pair / n_heads), h = (int)(pair - (int64_t)row * n_heads);
-  const int d = 4 * (threadIdx.x % LP);
-  if (row >= A.n_rows || d >= A.head_dim) return;
-  const ShRow R = A.rows[row];
+  const int n_heads = A.n_kv * A.heads, H = A.n_kv * A.q_tiles, d = 4 * (threadIdx.x % LP);
   const ShPlan P = *A.plan;
-  const int kvh = h / A.heads, hg = h - kvh * A.heads, H = A.n_kv * A.q_tiles;
-  // shared
   if (blockIdx.x == 0 && threadIdx.x == 0) A.plan->taken = 0;
-  const int COLS = S::WCOLS * A.cw, c = R.col0 + hg, ct = c / COLS;
-  const uint32_t x = (uint32_t)(kvh * R.tiles + ct / A.gang), u = R.u0 + x * R.units, w0 = u / P.each_shared;
-  const int n0 = R.units ? ((int)((u + R.units - 1) / P.each_shared - w0) + 1) * A.pw : 0;
-  const float* p0 = A.seeds + (((int64_t)(w0 + R.x0 + x) * A.gang + ct % A.gang) * A.pw * COLS + c % COLS) * (DP + 4);
-  // own
-  const int qt = A.together > 1 ? 0 : hg / 16, hh = kvh * A.q_tiles + qt, col = R.at + hg - 16 * qt;
-  const uint32_t v = R.before * H + (uint32_t)hh * R.own, w1 = v / P.each_own;
-  const int n1 = R.own ? (int)((v + R.own - 1) / P.each_own - w1) + 1 : 0;
-  const float* p1 = A.own + ((int64_t)w1 + (int64_t)R.lead * H + hh) * A.own_cols * (DP + 4) + col * (DP + 4);
-  // (slots of one x: its turns lie side by side, its pieces a gang's slots apart)
-  const int64_t turn = (int64_t)COLS * (DP + 4), s0 = A.gang * A.pw * turn, s1 = (int64_t)A.own_cols * (DP + 4);
-  float m = -INFINITY, l = 0.f;
-  f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int j0 = 0; j0 < n0 + n1; j0 += 8) {
-    f32x4 ml[8], z[8];
+  if (d >= A.head_dim) return;
+  for (int64_t pair = (int64_t)blockIdx.x * (256 / LP) + threadIdx.x / LP; pair < (int64_t)A.n_rows * n_heads;
+       pair += (int64_t)gridDim.x * (256 / LP)) {
+    const int row = (int)(pair / n_heads), h = (int)(pair - (int64_t)row * n_heads);
+    const ShRow R = A.rows[row];
+    const int kvh = h / A.heads, hg = h - kvh * A.heads;
+    // shared
+    const int COLS = S::WCOLS * A.cw, c = R.col0 + hg, ct = c / COLS;
+    const uint32_t x = (uint32_t)(kvh * R.tiles + ct / A.gang), u = R.u0 + x * R.units, w0 = u / P.each_shared;
+    const int n0 = R.units ? ((int)((u + R.units - 1) / P.each_shared - w0) + 1) * A.pw : 0;
+    const float* p0 = A.seeds + (((int64_t)(w0 + R.x0 + x) * A.gang + ct % A.gang) * A.pw * COLS + c % COLS) * (DP + 4);
+    // own
+    const int qt = A.together > 1 ? 0 : hg / 16, hh = kvh * A.q_tiles + qt, col = R.at + hg - 16 * qt;
+    const uint32_t v = R.before * H + (uint32_t)hh * R.own, w1 = v / P.each_own;
+    const int n1 = R.own ? (int)((v + R.own - 1) / P.each_own - w1) + 1 : 0;
+    const float* p1 = A.own + ((int64_t)w1 + (int64_t)R.lead * H + hh) * A.own_cols * (DP + 4) + col * (DP + 4);
+    // (slots of one x: its turns lie side by side, its pieces a gang's slots apart)
+    const int64_t turn = (int64_t)COLS * (DP + 4), s0 = A.gang * A.pw * turn, s1 = (int64_t)A.own_cols * (DP + 4);
+    float m = -INFINITY, l = 0.f;
+    f32x4 o = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < n0 + n1; j0 += 8) {
+      f32x4 ml[8], z[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = min(j0 + j, n0 + n1 - 1);
-      const float* p = i < n0 ? p0 + i / A.pw * s0 + i % A.pw * turn : p1 + (i - n0) * s1;
-      ml[j] = ldg4(p + DP);
-      z[j] = ldg4(p + d);
-    }
+      for (int j = 0; j < 8; ++j) {
+        const int i = min(j0 + j, n0 + n1 - 1);
+        const float* p = i < n0 ? p0 + i / A.pw * s0 + i % A.pw * turn : p1 + (i - n0) * s1;
+        ml[j] = ldg4(p + DP);
+        z[j] = ldg4(p + d);
+      }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j0 + j >= n0 + n1) break;
-      const float mn = fmaxf(m, ml[j].x), ref = mn == -INFINITY ? 0.f : mn;
-      const float fa = __builtin_amdgcn_exp2f(m - ref), fb = __builtin_amdgcn_exp2f(ml[j].x - ref);
-      o = o * fa + z[j] * fb;
-      l = l * fa + ml[j].y * fb;
-      m = mn;
+      for (int j = 0; j < 8; ++j) {
+        if (j0 + j >= n0 + n1) break;
+        const float mn = fmaxf(m, ml[j].x), ref = mn == -INFINITY ? 0.f : mn;
+        const float fa = __builtin_amdgcn_exp2f(m - ref), fb = __builtin_amdgcn_exp2f(ml[j].x - ref);
+        o = o * fa + z[j] * fb;
+        l = l * fa + ml[j].y * fb;
+        m = mn;
+      }
     }
-  }
-  const f32x4 y = l == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : o / l;
-  const int64_t at = (int64_t)row * A.out_stride + (int64_t)h * A.head_dim + d;
-  if constexpr (sizeof(T) == 4) {
-    stg4((float*)A.out + at, y);
-  } else {
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    *(GLOBAL u32x2*)((uint16_t*)A.out + at) = u32x2{pack_bf2(__float_as_uint(y.x), __float_as_uint(y.y)),
-                                                   pack_bf2(__float_as_uint(y.z), __float_as_uint(y.w))};
+    const f32x4 y = l == 0.f ? f32x4{0.f, 0.f, 0.f, 0.f} : o / l;
+    const int64_t at = (int64_t)row * A.out_stride + (int64_t)h * A.head_dim + d;
+    if constexpr (sizeof(T) == 4) {
+      stg4((float*)A.out + at, y);
+    } else {
+      typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+      *(GLOBAL u32x2*)((uint16_t*)A.out + at) = u32x2{pack_bf2(__float_as_uint(y.x), __float_as_uint(y.y)),
+                                                     pack_bf2(__float_as_uint(y.z), __float_as_uint(y.w))};
+    }
   }
 }
 
@@ -1007,8 +1009,8 @@ void sh_launch(const SharedArgs& A, int blocks, hipStream_t s) {
     hipLaunchKernelGGL((k_shared_attention<T, DP, true, true>), dim3(blocks), threads, 0, s, A);
   else
     hipLaunchKernelGGL((k_shared_attention<T, DP, true, false>), dim3(blocks), threads, 0, s, A);
-  const int64_t pairs = (int64_t)A.n_rows * A.n_kv * A.heads, each = 256 / (DP / 4);
-  hipLaunchKernelGGL((k_shared_join<T, DP>), dim3((unsigned)((pairs + each - 1) / each)), dim3(256), 0, s, A);
+  const int64_t pairs = (int64_t)A.n_rows * A.n_kv * A.heads;
+  hipLaunchKernelGGL((k_shared_join<T, DP>), dim3((unsigned)sh_join_blocks(pairs, DP)), dim3(256), 0, s, A);
 }
 template <typename T>
 void sh_dim(const SharedArgs& A, int dp, int blocks, hipStream_t s) {

@@ -44,6 +44,14 @@ constexpr ShCut sh_cut(uint32_t grid, uint32_t units, uint32_t tiles, uint32_t g
   return c;
 }
 
+// Work-groups of 256 threads that join the partial results of `pairs` (row, head)s,
+// dp / 4 threads each, in turns where there are more: a launch takes 2^32 threads.
+constexpr int64_t SH_JOIN_MOST = 65536;
+constexpr int64_t sh_join_blocks(int64_t pairs, int dp) {
+  const int64_t all = (pairs + 1024 / dp - 1) / (1024 / dp);
+  return all < SH_JOIN_MOST ? all : SH_JOIN_MOST;
+}
+
 // What a call of these sizes needs.
 struct ShSizes {
   int group, cols, cw, pw, gang, together, q_tiles, own_cols, blocks;

@@ -67,6 +67,12 @@ int main() {
               for (uint32_t t : amounts)
                 if (cu % 16 == 0 || (u + t) % 3 == 0) walk(z, u, t, page == 16 ? "pages of 16" : "pages of 5", cu);
           }
+  // work-groups of a join: at most 2^32 threads in a launch, and enough of them
+  for (int64_t pairs = 1; pairs <= (int64_t)1 << 34; pairs = pairs * 3 / 2 + 1)
+    for (int dp : {64, 128, 256}) {
+      const int64_t b = sh_join_blocks(pairs, dp);
+      CHECK(b > 0 && b * 256 < (int64_t)1 << 32, "%ld pairs of %d: %ld work-groups", (long)pairs, dp, (long)b);
+    }
   srand(7);
   for (int i = 0; i < 200000; ++i) {
     const int64_t rows = rand() % (i % 3 ? 300 : 5000), groups = rand() % (i % 5 ? 40 : 6000);

@@ -10,6 +10,8 @@ torch = pytest.importorskip("torch")
 
 from lora_normal_form_amd import block  # noqa: E402
 from test_block_gpu import BF16, DEV, F32, _int  # noqa: E402
+from test_shared_gpu import WEIGHT  # noqa: E402
+from test_sinks_gpu import attend_ref, close  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -63,3 +65,22 @@ def test_one_workspace_for_heads_of_several_sizes():
         else:
             same = _same(shared.forward(*args, torch.full_like(q, math.nan)), want[0])
         assert same, (i, key)
+
+
+def test_more_rows_and_heads_than_the_join_has_threads():
+    """4500 rows of 64 heads of 256: the join's work-groups take several each."""
+    N, H, D, ps = 4500, 64, 256, 16
+    g = torch.Generator().manual_seed(6)
+    rng = np.random.default_rng(6)
+    kc, vc = (torch.randn((200, ps, 1, D), generator=g).to(DEV, BF16) for _ in range(2))
+    q = torch.randn((N, H, D), device=DEV).to(BF16)
+    table = rng.integers(0, 200, size=(N, 4))
+    table[:, :2] = table[0, :2]
+    lens = rng.integers(0, 65, size=N)
+    att = block.SharedAttention(block.KVCache(kc, vc), H, N, 2, always=True)
+    out = att.forward(q, _int(table), _int(lens), _int([0, 2000, N - 3]), _int([32, 30]), torch.full_like(q, math.nan))
+    some = np.unique(np.concatenate([rng.integers(0, N, size=200), [0, 1999, 2000, N - 4, N - 3, N - 1]]))
+    ref, tol = attend_ref(q[some], kc, vc, _int(table[some]), lens[some], range(len(some)), lambda i, n: torch.arange(n),
+                          1 / math.sqrt(D), weight=WEIGHT)
+    close(out[some], ref, tol, "rows")
+    assert not bool(torch.isnan(out).any())
