@@ -271,7 +271,9 @@ scute_status scute_batch_destroy(scute_batch* batch);
  * operands), so any input scale whose products and sums stay inside the
  * float32 range is served; there is no fixed-point stage.
  * May be captured into a graph, and replayed between other forwards of the
- * plan; a plan's workspaces serve one forward at a time.
+ * plan; a plan's workspaces serve one forward at a time. From a decode plan's
+ * first capture on each of its forwards, captured or not, makes one launch more,
+ * which clears what the last one left (scute_cost.launches counts it).
  * Errors: SCUTE_E_STATE if the plan is stale or from another layer,
  * SCUTE_E_UNSUPPORTED on a host-only layer, SCUTE_E_INVALID for null or
  * misaligned pointers (16-byte alignment required). */

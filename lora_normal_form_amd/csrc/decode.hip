@@ -981,7 +981,8 @@ scute_status launch_decode(scute_layer* L, const scute_batch* B, const void* x, 
   float* acc = D.acc32[D.fwd & 1];
   float* acc_next = D.acc32[(D.fwd + 1) & 1];
   int nl = 0;
-  if (captured) {
+  if (captured && D.acc_bytes > 0) {
+    ProfScope ps(L, st, "clear");
     clear_words(acc, D.acc_bytes / 4, nullptr, 0, st);
     ++nl;
   }

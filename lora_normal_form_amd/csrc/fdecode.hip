@@ -673,6 +673,7 @@ scute_status launch_fdecode(scute_layer* L, const scute_batch* B, const void* x,
   int nl = 0;
   if (in_capture(st, &P.captured)) {
     P.fwd = 0;
+    ProfScope ps(L, st, "clear");
     // (xdone lies behind xcnt)
     clear_words(P.xcnt, (int64_t)((int32_t*)P.xdone - P.xcnt) + P.n_xb, P.cnt, (int64_t)P.C * P.MG * 4, st);
     ++nl;

@@ -338,8 +338,9 @@ static scute_status launch_ref(scute_layer* L, const scute_batch* B, const T* x,
 int32_t forward_launch_count(const scute_layer* L, const scute_batch* B) {
   (void)L;
   if (B->n == 0) return 0;
-  if (B->fp.enabled) return (B->fp.n_rot_items > 0) + 1;  // rotation + fused main
-  if (B->dp.enabled) return 2 + decode_route_launches(B);  // prologue (gather, rotation, shrinks) + main
+  if (B->fp.enabled) return B->fp.captured + (B->fp.n_rot_items > 0) + 1;  // clear + rotation + fused main
+  if (B->dp.enabled)  // clear + prologue (gather, rotation, shrinks) + main
+    return (B->dp.captured && B->dp.acc_bytes > 0) + 2 + decode_route_launches(B);
   if (B->pp.enabled) return (B->pp.n_pro > 0) + 1;  // prologue (rotation, shrinks) + main
   return (B->n_rot > 0) + (B->max_rank > 0) + (B->n_vera > 0) + 1 +
          (B->max_rank > 0 || B->n_vera > 0);
