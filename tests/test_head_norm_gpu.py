@@ -191,3 +191,40 @@ def test_norms_of_other_heads_refused():
                  block.HeadNorm(D, "rms", None, torch.ones((4, D), device=DEV))):
         with pytest.raises(ValueError):
             rot.store(q, k, k, pos, slot, block.KVCache(kc, kc.clone()), torch.empty_like(q), norm=norm)
+
+
+PROMPTS = [  # (as CASES) two tokens a work-group, the last one odd or not: every pair of types and size of head
+    (4096, 3, 1, 64, 64, 2, False, "rms", False, False, F32, BF16, False, 0),
+    (4097, 3, 2, 64, 32, 1, True, "layer", True, True, BF16, F32, False, 0),
+    (8191, 2, 1, 64, 64, 1, False, "layer", False, True, BF16, BF16, True, 0),
+    (4097, 5, 1, 32, 16, 1, False, "rms", True, False, F32, F32, False, 0),
+    (4096, 3, 1, 128, 64, 3, False, "layer", True, True, F32, BF16, False, 0),
+    (8191, 2, 2, 128, 128, 1, True, "rms", False, True, BF16, BF16, False, 0),
+    (4097, 2, 1, 96, 96, 2, False, "rms", True, False, F32, F32, True, 0),
+    (4097, 2, 1, 104, 40, 2, False, "layer", False, False, BF16, F32, False, 0),
+    (4097, 2, 1, 256, 256, 1, False, "rms", True, True, F32, BF16, False, 0),
+    (4096, 1, 1, 256, 100, 2, True, "layer", False, False, F32, F32, False, 0),
+    (8191, 1, 1, 200, 0, 1, False, "layer", True, True, BF16, BF16, False, 0),
+    (4097, 3, 1, 136, 64, 4, False, "rms", False, False, BF16, F32, False, 0),
+    (4097, 3, 1, 136, 66, 1, False, "rms", True, True, F32, BF16, False, 1)]  # (one element an access)
+
+
+@pytest.mark.parametrize("T, Hq, Hk, D, rd, axes, inter, kind, own, bias, src, dt, by_head, off", PROMPTS)
+def test_prompts(T, Hq, Hk, D, rd, axes, inter, kind, own, bias, src, dt, by_head, off):
+    test_norm_rotary_store(T, Hq, Hk, D, rd, axes, inter, kind, own, bias, src, dt, by_head, off)
+
+
+def test_prompts_in_place():
+    """q rotated where it lies: what the two tokens of a work-group ask for early is not what it writes."""
+    g = torch.Generator().manual_seed(3)
+    T, H, D = 4097, 6, 128
+    q = torch.randn((T, H, D), generator=g).to(DEV)
+    k, v = (torch.randn((T, 1, D), generator=g).to(DEV) for _ in range(2))
+    kc, vc = (torch.zeros((T, 1, 1, D), device=DEV) for _ in range(2))
+    rot = block.Rotary(torch.ones(D // 2, dtype=torch.float64, device=DEV), D)
+    pos, slot = torch.arange(T, dtype=torch.int32, device=DEV), torch.arange(T, device=DEV)
+    norm, out = block.HeadNorm(D), torch.empty_like(q)
+    rot.store(q, k, v, pos, slot, block.KVCache(kc, vc), out, norm=norm)
+    k0 = kc.clone()
+    rot.store(q, k, v, pos, slot, block.KVCache(kc, vc), q, norm=norm)
+    assert torch.equal(q, out) and torch.equal(kc, k0)

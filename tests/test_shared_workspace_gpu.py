@@ -84,3 +84,40 @@ def test_more_rows_and_heads_than_the_join_has_threads():
                           1 / math.sqrt(D), weight=WEIGHT)
     close(out[some], ref, tol, "rows")
     assert not bool(torch.isnan(out).any())
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("ps", [16, 5])
+@pytest.mark.parametrize("by_request", [False, True])
+def test_calls_smaller_than_their_handle(dt, ps, by_request):
+    """One handle for 512 rows in 64 groups, in turn for calls of fewer, whose waves
+    stand in other ways; nothing behind its workspace is written."""
+    H, Hk, D = 8, 2, 64
+    g = torch.Generator().manual_seed(ps)
+    rng = np.random.default_rng(ps)
+    kc, vc = (torch.randn((900, ps, Hk, D), generator=g).to(DEV, dt) for _ in range(2))
+    att = block.SharedAttention(block.KVCache(kc, vc), H, 512, 64, always=True)
+    n = att.workspace.shape[0]
+    wide = torch.full((n + (1 << 20),), 77, dtype=torch.uint8, device=DEV)
+    wide[:n] = 0
+    assert wide.data_ptr() % 256 == 0
+    att.workspace = wide[:n]
+    for rows, groups in ((512, 1), (512, 64), (7, 1), (33, 20), (1, 64), (512, 3), (40, 1), (3, 0), (512, 64)):
+        offsets = np.sort(np.concatenate([[0], rng.integers(0, rows + 1, size=groups)]))
+        table = rng.integers(0, 900, size=(rows, 70))
+        shared = rng.integers(0, 50, size=groups) * ps
+        for x in range(groups):
+            table[offsets[x]:offsets[x + 1], :50] = table[offsets[x] if offsets[x] < rows else 0, :50]
+        lens = rng.integers(0, 70 * ps + 1, size=rows) if rows < 100 else rng.integers(0, 20 * ps, size=rows)
+        req = rng.permutation(rows) if by_request else np.arange(rows)
+        q = torch.randn((rows, H, D), generator=g).to(DEV, dt)
+        tab = np.empty_like(table)
+        tab[req] = table
+        out = att.forward(q, _int(tab), _int(lens), _int(offsets), _int(shared), torch.full_like(q, math.nan),
+                          row_req=_int(req) if by_request else None)
+        torch.cuda.synchronize()
+        some = np.arange(rows) if rows < 100 else np.sort(rng.permutation(rows)[:60])
+        ref, tol = attend_ref(q[some], kc, vc, _int(table[some]), lens[some], range(len(some)), lambda i, n: torch.arange(n),
+                              1 / math.sqrt(D), weight=WEIGHT)
+        close(out[some], ref, tol, f"{rows} rows in {groups}")
+        assert not bool(torch.isnan(out).any()) and bool((wide[n:] == 77).all()), (rows, groups)
