@@ -311,7 +311,8 @@ class AttentionStep:
     [groups + 1] and `shared_len` [groups] say which, by row, zero at first and
     to be written by the caller. forks: requests may go on from others, be cut
     back or keep some of their positions (fork, keep_only); they then end by
-    fork, and a negative new_len is a request without tokens."""
+    fork, and a negative new_len is a request without tokens. Steps with forks that
+    share a cache (like) have one window and the same sinks."""
 
     head_norm = group = shared_len = None
     forks = False
@@ -337,6 +338,8 @@ class AttentionStep:
             raise ValueError("like: a step whose requests, pages, heads, type or device are others")
         if like is not None and like.forks != bool(forks):
             raise ValueError("like: requests end by fork in both steps or in none")
+        if like is not None and forks and (like.window, like.window and like.sinks) != (window, window and sinks):
+            raise ValueError("like: forks give back pages behind the window, which has to be the same in both steps")
         if groups and (window or sinks):
             raise ValueError("groups: rows that share positions see all of theirs, without a window")
         if tenants is not None and (tenants.dtype != torch.int32 or tenants.shape != (2, n_requests)):

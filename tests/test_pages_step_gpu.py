@@ -209,3 +209,18 @@ def test_steps_refuse():
     plain.close()
     plain.qkv.close()
     s.close()
+
+
+def test_steps_that_share_a_cache_have_one_window():
+    """fork(drop=True) gives back pages that its own window does not see, so another
+    step on the same requests may not see more."""
+    from lora_normal_form_amd import multiproj
+    s = Steps(46, window=6, sinks=3)
+    st = s.st
+    same = _step(46, window=6, sinks=3, forks=True, like=st)[0]
+    for window, sinks, groups in ((0, 0, 0), (7, 3, 0), (6, 2, 0), (0, 0, 2)):
+        with pytest.raises(ValueError, match="window"):
+            _step(46, window=window, sinks=sinks, groups=groups, forks=True, like=st)
+    same.close()
+    same.qkv.close()
+    s.close()
