@@ -285,3 +285,13 @@ def test_refusals():
     with pytest.raises(ValueError):
         small = block.SharedAttention(cache, 8, 4, 1)
         small.forward(**ok)
+
+
+@pytest.mark.parametrize("dt, D, ps", [(BF16, 128, 16), (F32, 64, 16), (BF16, 40, 5)])
+def test_prompts_behind_what_they_share(dt, D, ps):
+    """Hundreds of new tokens a request, part of a prompt each."""
+    kc, vc, table, _, lens_r = make(D, [(3, 40 * ps)], ps, 8, 2, D, dt, suffix=260)
+    req = np.repeat([0, 1, 2], 250)
+    lens = np.concatenate([np.maximum(0, n - 249 + np.arange(250)) for n in lens_r])
+    q = torch.randn((750, 8, D), generator=torch.Generator().manual_seed(4)).to(DEV, dt)
+    run(kc, vc, table, q, lens, [0, 750], [40 * ps], req=req)

@@ -217,3 +217,15 @@ def test_refusals():
     with pytest.raises(scute.ScuteError) as e:
         att.forward(q, table, _int([4]), torch.empty_like(q))
     assert e.value.code == scute.E_SHAPE
+
+
+@pytest.mark.parametrize("dt, D, ps", [(BF16, 128, 16), (F32, 64, 16), (BF16, 40, 5)])
+def test_prompts(dt, D, ps):
+    """Hundreds of new tokens a request, from its first on and behind others."""
+    g, P = torch.Generator().manual_seed(D), -(-1100 // ps)
+    kc, vc = (torch.randn((2 * P, ps, 2, D), generator=g).to(DEV, dt) for _ in range(2))
+    table = torch.randperm(2 * P, generator=g).view(2, P)
+    req = np.repeat([0, 1], 400)
+    lens = np.concatenate([1 + np.arange(400), 700 + np.arange(400)])
+    q = torch.randn((800, 8, D), generator=g).to(DEV, dt)
+    run(kc, vc, _int(table), q, lens, 130, 21, req=req)
