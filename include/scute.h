@@ -434,7 +434,10 @@ scute_status scute_cache_assign(const scute_cache_assign_args* args, void* strea
  *     request is refused: it keeps its whole pages, and seq_len[r] says so.
  *   - window > 0: a page whose positions all lie in [sinks, n - window) is
  *     dropped (table_out -1), as rows from n on do not see it
- *     (scute_sink_attention with this window and these sinks).
+ *     (scute_sink_attention with this window and these sinks). A refused
+ *     request's pages are dropped by the n it did not get: where the window is
+ *     not whole pages, rows from its seq_len[r] on may see the end of one that is
+ *     gone, so such a request ends, or is read again from its start.
  *   - Pages that some request held and none holds any more go to the tail of
  *     the ring in ascending order, and may be taken from the next step on.
  * Entries of table_out past a request's pages are -1. The table that is handed

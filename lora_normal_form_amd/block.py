@@ -239,7 +239,9 @@ def fork_pages(seq_len, parent, table, ring, cursor, page_size, fork, keep=None,
     another, or outside the requests: it ends). Whole pages are shared; a last
     page that others hold too is to be copied (copy_pages, in each layer's
     cache); pages that nobody holds any more go back to the ring; window > 0
-    drops the pages between sinks and the last `window` positions. seq_len,
+    drops the pages between sinks and the last `window` positions (of a request
+    that is refused, too: where the window is not whole pages its next rows may
+    see one of them, so it is ended or read again). seq_len,
     parent, keep int32 [R]; table [R][P] is left as it is, the new one is
     fork.table. Everything but the ring goes into fork, which is returned."""
     R, P, a = fork.n_requests, fork.pages, fork.args
@@ -443,8 +445,13 @@ class SharedAttention:
     positions (samples of a prompt, users of a system prompt): those are read
     once for all rows of a group. Up to max_rows rows in up to max_groups groups
     a call; scale as in PagedAttention, and as there the handle owns the
-    workspace of one call at a time. Calls that sharing could not save the reads of
-    256 MiB are PagedAttention's (the library's rule), with `always` none."""
+    workspace of one call at a time (for 32 query and 8 key heads of 128
+    227 MB for 4 rows of one group, 240 for 128 rows). Calls that sharing could not save the reads of
+    256 MiB, if all rows past one a group shared the table's whole width, are
+    PagedAttention's (the library's rule: the shared lengths are on the GPU), with
+    `always` none. So with a table much wider than what is shared (AttentionStep's
+    is as wide as its requests may get) rows that share little take longer than
+    PagedAttention's."""
 
     def __init__(self, cache, n_heads, max_rows, max_groups, scale=None, always=False):
         if n_heads < 1 or n_heads % cache.n_kv_heads:

@@ -431,7 +431,9 @@ class AttentionStep:
         (None: all) of request parent[r], as in block.fork_pages (outside the
         requests: it ends). drop: pages that rows from here on do not see
         through the window go back, so the request cannot be cut back past them
-        later. Returns the block.Fork that says what came of it."""
+        later, and one that is refused (its length says so) is ended or read again
+        from its start where the window is not whole pages. Returns the block.Fork
+        that says what came of it."""
         import torch
         from . import block
         if not self.forks:
